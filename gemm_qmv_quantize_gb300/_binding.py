@@ -48,6 +48,13 @@ SIGNATURES = {
     "qmv_q4_k_q8_1_fused_group": (_i32, [_i32, ctypes.POINTER(_vp), ctypes.POINTER(_vp), ctypes.POINTER(_vp),
                                          ctypes.POINTER(_i64), _i32, _i64, _vp]),
     "qmv_debug_q4_k_block_dots": (_i32, [_vp, _vp, _vp, _i32, _i64, _i64, _vp]),
+    "qmv_lora_add_workspace": (_i64, [_i32, _i32, _i64]),
+    "qmv_lora_add": (_i32, [_vp, _i32, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _i64, _i32, _i64, _i64, _i32, _i32, _vp]),
+    "qmv_rope_append": (_i32, [_vp, _vp, _vp, ctypes.c_char_p, _vp, _vp, _vp, _vp] + [_i32] * 9 + [_i64, _vp]),
+    "qmv_prefix_attention_workspace": (_i64, [_i32] * 5 + [_i64, _i64]),
+    "qmv_prefix_attention": (_i32, [_vp, _vp, _vp, _i32, _i64, _i32, _vp, _i64, _vp, _i32, _vp, _i64, _f32, _vp, _vp,
+                                    _i64] + [_i32] * 5 + [_vp]),
+    "qmv_penalize_logits": (_i32, [_vp, _vp, _i32] + [_vp] * 7 + [_i32, _vp, _vp, _i32, _vp, _i32, _i32, _vp]),
     "qmv_set_launch_overlap": (None, [_i32]),
     "qmv_get_launch_overlap": (_i32, []),
     "qmv_route_count": (_i32, []),

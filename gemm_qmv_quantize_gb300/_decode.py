@@ -1,0 +1,213 @@
+"""Binding of the operators beside the matmuls in a batched decode step (include/qmv.h):
+low-rank adapters, rotary positions with the append to a paged cache, attention over a
+shared prefix, and penalties, biases and masks on logits.
+
+As in ``_binding``: tensors are checked for type, shape and contiguity, pointers and
+sizes go to the C entry point of the same name, and all arithmetic runs in the library.
+A workspace that is not given is allocated for the call; a program that repeats calls
+keeps one of the bytes that the ``_workspace`` function names.
+"""
+from __future__ import annotations
+
+import math
+
+import torch
+
+from ._binding import QmvError, _check, _need, _stream, lib
+
+_TYPE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}   # QMV_F32, QMV_F16, QMV_BF16
+
+
+def _type(t: torch.Tensor, name: str, allowed) -> int:
+    if t.dtype not in allowed:
+        raise TypeError(f"{name}: expected {' or '.join(map(str, allowed))}, got {t.dtype}")
+    return _TYPE[t.dtype]
+
+
+def _workspace(buffer, need: int, device, stream):
+    """`buffer`, or a new one of `need` bytes that stays valid for the call's stream."""
+    if buffer is None:
+        buffer = torch.empty((need,), dtype=torch.uint8, device=device)
+        if stream is not None:
+            buffer.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
+                                 torch.cuda.ExternalStream(_stream(stream)))
+    else:
+        _need(buffer, "workspace", torch.uint8)
+        if buffer.numel() < need:
+            raise ValueError(f"workspace: {buffer.numel()} bytes, the call needs {need}")
+    return buffer
+
+
+def _bytes(fn: str, n: int) -> int:
+    if n < 0:
+        raise QmvError(fn, n)
+    return n
+
+
+def qmv_lora_add_workspace(M: int, R: int, K: int) -> int:
+    """Bytes of workspace of qmv_lora_add on M rows of K with adapters of rank R."""
+    return _bytes("qmv_lora_add_workspace", lib().qmv_lora_add_workspace(M, R, K))
+
+
+def qmv_lora_add(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, adapter: torch.Tensor, scale: torch.Tensor,
+                 base: torch.Tensor, out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                 stream=None) -> torch.Tensor:
+    """base fp32 [M, N] + scale[l] (x[m] A[l]^T) B[l]^T with l = adapter[m] (none where it
+    is outside 0..L-1): x fp32 or fp16 [M, K], a [L, R, K] and b [L, N, R] fp16 or bf16,
+    adapter int32 [M], scale fp32 [L]. out may be base."""
+    M, K = x.shape
+    L, R, _ = a.shape
+    N = base.shape[1]
+    _need(x, "x", x.dtype)
+    xt = _type(x, "x", (torch.float32, torch.float16))
+    wt = _type(a, "a", (torch.float16, torch.bfloat16))
+    _need(a, "a", a.dtype, (L, R, K))
+    _need(b, "b", a.dtype, (L, N, R))
+    _need(adapter, "adapter", torch.int32, (M,))
+    _need(scale, "scale", torch.float32, (L,))
+    _need(base, "base", torch.float32, (M, N))
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.float32, device=base.device)
+    else:
+        _need(out, "out", torch.float32, (M, N))
+    ws = _workspace(workspace, qmv_lora_add_workspace(M, R, K), x.device, stream)
+    _check("qmv_lora_add", lib().qmv_lora_add(
+        x.data_ptr(), xt, a.data_ptr(), b.data_ptr(), wt, adapter.data_ptr(), scale.data_ptr(), base.data_ptr(),
+        out.data_ptr(), ws.data_ptr(), ws.numel(), M, N, K, R, L, _stream(stream)))
+    return out
+
+
+def qmv_rope_table(n_positions: int, rot: int, base: float = 10000.0, device=None) -> torch.Tensor:
+    """fp32 [n_positions, rot/2, 2]: (cos, sin) of position * base^(-2i/rot), computed in
+    64 bits and rounded once."""
+    pairs = rot // 2
+    inv = base ** -(torch.arange(pairs, dtype=torch.float64, device=device) / max(pairs, 1))
+    angle = torch.arange(n_positions, dtype=torch.float64, device=device)[:, None] * inv
+    return torch.stack([angle.cos(), angle.sin()], -1).to(torch.float32).contiguous()
+
+
+def qmv_rope_append(qkv: torch.Tensor, positions: torch.Tensor, table: torch.Tensor, axis_of_pair, slots: torch.Tensor,
+                    k_cache: torch.Tensor, v_cache: torch.Tensor, interleaved: bool = False,
+                    out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Turns q and k of qkv fp32 [M, (Hq + 2 Hkv) D] by their positions, int32 [axes, M],
+    and writes k and v to slots int64 [M] of k_cache and v_cache [pages, page, Hkv, D]
+    (negative slots are skipped); returns q [M, Hq, D] in the caches' type. table: fp32
+    [n_positions, rot/2, 2] as of qmv_rope_table; axis_of_pair: rot/2 numbers (bytes, or a
+    sequence), the axis of each pair. interleaved: pairs (2i, 2i+1), not (i, i + rot/2)."""
+    pages, page, Hkv, D = k_cache.shape
+    M, width = qkv.shape
+    axes = positions.shape[0]
+    n_positions, pairs, _ = table.shape
+    heads, odd = divmod(width, D)
+    if odd or heads <= 2 * Hkv:
+        raise ValueError(f"qkv: rows of {width} are not q heads and 2 x {Hkv} heads of {D}")
+    Hq = heads - 2 * Hkv
+    if not isinstance(axis_of_pair, bytes):
+        axis_of_pair = bytes(axis_of_pair)
+    if len(axis_of_pair) != pairs:
+        raise ValueError(f"axis_of_pair: expected {pairs} entries, got {len(axis_of_pair)}")
+    t = _type(k_cache, "k_cache", (torch.float16, torch.bfloat16))
+    _need(qkv, "qkv", torch.float32)
+    _need(positions, "positions", torch.int32, (axes, M))
+    _need(table, "table", torch.float32, (n_positions, pairs, 2))
+    _need(slots, "slots", torch.int64, (M,))
+    _need(k_cache, "k_cache", k_cache.dtype)
+    _need(v_cache, "v_cache", k_cache.dtype, (pages, page, Hkv, D))
+    if out is None:
+        out = torch.empty((M, Hq, D), dtype=k_cache.dtype, device=qkv.device)
+    else:
+        _need(out, "out", k_cache.dtype, (M, Hq, D))
+    _check("qmv_rope_append", lib().qmv_rope_append(
+        qkv.data_ptr(), positions.data_ptr(), table.data_ptr(), axis_of_pair, slots.data_ptr(), out.data_ptr(),
+        k_cache.data_ptr(), v_cache.data_ptr(), t, int(bool(interleaved)), M, Hq, Hkv, D, 2 * pairs, axes,
+        n_positions, pages * page, _stream(stream)))
+    return out
+
+
+def qmv_prefix_attention_workspace(B: int, T: int, Hq: int, Hkv: int, D: int, prefix_len: int, max_own: int) -> int:
+    """Bytes of workspace of qmv_prefix_attention at these sizes."""
+    return _bytes("qmv_prefix_attention_workspace",
+                  lib().qmv_prefix_attention_workspace(B, T, Hq, Hkv, D, prefix_len, max_own))
+
+
+def qmv_prefix_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, prefix_table: torch.Tensor,
+                         prefix_len: int, own_table: torch.Tensor, own_len: torch.Tensor, scale: float | None = None,
+                         max_own: int | None = None, out: torch.Tensor | None = None,
+                         workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Attention of q [B, T, Hq, D] over a prefix that all requests share (prefix_len keys
+    in the pages prefix_table int32 [n]) and each request's own_len[b] own keys (int32 [B],
+    in the pages own_table[b] int32 [B, own_pages]), its T tokens being the last of them;
+    k_cache, v_cache [pages, page, Hkv, D]. scale: 1 / sqrt(D) unless given. max_own: a
+    bound of own_len that the caller knows (the table's width unless given; the work is
+    split by it)."""
+    B, T, Hq, D = q.shape
+    pages, page, Hkv, _ = k_cache.shape
+    own_pages = own_table.shape[1]
+    t = _type(q, "q", (torch.float16, torch.bfloat16))
+    _need(q, "q", q.dtype)
+    _need(k_cache, "k_cache", q.dtype, (pages, page, Hkv, D))
+    _need(v_cache, "v_cache", q.dtype, (pages, page, Hkv, D))
+    _need(prefix_table, "prefix_table", torch.int32)
+    _need(own_table, "own_table", torch.int32, (B, own_pages))
+    _need(own_len, "own_len", torch.int32, (B,))
+    if prefix_table.numel() * page < prefix_len:
+        raise ValueError(f"prefix_table: {prefix_table.numel()} pages of {page} hold no {prefix_len} keys")
+    if max_own is None:
+        max_own = own_pages * page
+    if out is None:
+        out = torch.empty((B, T, Hq, D), dtype=q.dtype, device=q.device)
+    else:
+        _need(out, "out", q.dtype, (B, T, Hq, D))
+    need = qmv_prefix_attention_workspace(B, T, Hq, Hkv, D, prefix_len, max_own)
+    ws = _workspace(workspace, need, q.device, stream)
+    _check("qmv_prefix_attention", lib().qmv_prefix_attention(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), t, pages, page, prefix_table.data_ptr(), prefix_len,
+        own_table.data_ptr(), own_pages, own_len.data_ptr(), max_own, 1.0 / math.sqrt(D) if scale is None else scale,
+        out.data_ptr(), ws.data_ptr(), ws.numel(), B, T, Hq, Hkv, D, _stream(stream)))
+    return out
+
+
+def qmv_penalize_logits(logits: torch.Tensor, tokens: torch.Tensor, prompt_len: torch.Tensor, total_len: torch.Tensor,
+                        repetition: torch.Tensor | None = None, presence: torch.Tensor | None = None,
+                        frequency: torch.Tensor | None = None, bias_tokens: torch.Tensor | None = None,
+                        bias_values: torch.Tensor | None = None, mask: torch.Tensor | None = None,
+                        mask_row: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                        stream=None) -> torch.Tensor:
+    """Penalties for the tokens of each row's history, biases and masks on logits fp32
+    [M, V]: tokens int32 [M, H], of which the first total_len[m] count (the first
+    prompt_len[m] are the prompt's); repetition, presence, frequency fp32 [M] or None;
+    bias_tokens int32 and bias_values fp32 [M, n]; mask int32 [n_masks, ceil(V/32)], bit
+    set = allowed, with mask_row int32 [M] (negative: none). out may be logits."""
+    M, V = logits.shape
+    H = tokens.shape[1]
+    _need(logits, "logits", torch.float32)
+    _need(tokens, "tokens", torch.int32, (M, H))
+    _need(prompt_len, "prompt_len", torch.int32, (M,))
+    _need(total_len, "total_len", torch.int32, (M,))
+    rows = []
+    for name, t in (("repetition", repetition), ("presence", presence), ("frequency", frequency)):
+        if t is not None:
+            _need(t, name, torch.float32, (M,))
+        rows.append(None if t is None else t.data_ptr())
+    n_bias = n_masks = 0
+    if (bias_tokens is None) != (bias_values is None):
+        raise ValueError("bias_tokens and bias_values come together")
+    if bias_tokens is not None:
+        n_bias = bias_tokens.shape[1]
+        _need(bias_tokens, "bias_tokens", torch.int32, (M, n_bias))
+        _need(bias_values, "bias_values", torch.float32, (M, n_bias))
+    if mask is not None:
+        n_masks = mask.shape[0]
+        _need(mask, "mask", torch.int32, (n_masks, (V + 31) // 32))
+    if mask_row is not None:
+        _need(mask_row, "mask_row", torch.int32, (M,))
+    if out is None:
+        out = torch.empty((M, V), dtype=torch.float32, device=logits.device)
+    else:
+        _need(out, "out", torch.float32, (M, V))
+    _check("qmv_penalize_logits", lib().qmv_penalize_logits(
+        logits.data_ptr(), tokens.data_ptr(), H, prompt_len.data_ptr(), total_len.data_ptr(), *rows,
+        None if bias_tokens is None else bias_tokens.data_ptr(), None if bias_values is None else bias_values.data_ptr(),
+        n_bias, None if mask is None else mask.data_ptr(), None if mask_row is None else mask_row.data_ptr(), n_masks,
+        out.data_ptr(), M, V, _stream(stream)))
+    return out

@@ -8,6 +8,7 @@
 namespace qmv {
 
 constexpr uint32_t kErrWaitTimeout = 1u;   // error-word bit: an mbarrier wait gave up
+constexpr uint32_t kErrIndex = 2u;         // error-word bit: an index read from device memory lies outside its array
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p)
 {

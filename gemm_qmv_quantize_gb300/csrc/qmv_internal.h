@@ -27,6 +27,10 @@ enum Route : int {
     kRouteQ4KMmaFused,    // ... with the Q8_1 quantize in the prologue
     kRouteNvfp4Umma,      // NVFP4: tcgen05.mma (TMEM accumulators), M <= 96 in one weight pass
     kRouteFp8Umma,        // FP8: the same kernel with a byte-wide decode
+    kRouteLora,           // low-rank adapters added to a projection's output
+    kRouteRopeAppend,     // rotary positions and the append to a paged cache
+    kRoutePrefixAttention,  // attention over a shared prefix and the requests' own tokens
+    kRouteLogits,         // penalties, biases and masks on logits
     kRouteCount
 };
 

@@ -49,7 +49,8 @@ typedef struct CUstream_st *qmv_stream_t;
 typedef int qmv_status;
 #define QMV_OK                0
 #define QMV_ERR_NULL         -1  /* a required pointer is NULL */
-#define QMV_ERR_SHAPE        -2  /* M outside 0..8 (0..96 NVFP4 / FP8), N or K negative, K not a multiple of the format's block */
+#define QMV_ERR_SHAPE        -2  /* M outside 0..8 (0..96 NVFP4 / FP8), N or K negative, K not a multiple of the format's block
+                                    (the decode-step operators: a size, type or workspace outside what each call names) */
 #define QMV_ERR_ALIGN        -3  /* a pointer is not aligned to its element type (see each call) */
 #define QMV_ERR_CUDA         -4  /* a CUDA runtime call failed (launch, attribute, device query) */
 #define QMV_ERR_TIMEOUT      -5  /* qmv_error_flags: a bounded device-side wait gave up */
@@ -253,6 +254,120 @@ QMV_API void qmv_set_launch_overlap(int enable);
 QMV_API int qmv_get_launch_overlap(void);
 
 /* ---------------------------------------------------------------------------
+ * Operators of a batched decode step, beside the matmuls: the adapters of a
+ * projection's rows, rotary positions with the append to a paged cache, attention
+ * over a shared prefix, and penalties, biases and masks on the logits.
+ *
+ * 16-bit tensors are IEEE binary16 or bfloat16, named by a type argument. Sums,
+ * softmax statistics and products are fp32; an output is rounded once. A workspace is
+ * device memory of the caller, 16-byte aligned, of at least the bytes that the call's
+ * _workspace function names; its contents need no initialisation and hold nothing
+ * between calls. Calls in flight at the same time need workspaces of their own.
+ * Indices that the kernels read from device memory are checked against their arrays:
+ * one outside sets bit 2 of qmv_error_flags and is handled as each call says, never
+ * followed.
+ * ------------------------------------------------------------------------- */
+#define QMV_F32  0
+#define QMV_F16  1
+#define QMV_BF16 2
+
+/*
+ * Low-rank adapters of many requests at once, beside a shared projection:
+ *   y[m] = base[m] + scale[a] * B[a] (A[a] x[m]),  a = adapter[m].
+ *   x        [M][K], QMV_F32 or QMV_F16: the projection's own input, M = 0..96.
+ *   a, b     [L][R][K] and [L][N][R], QMV_F16 or QMV_BF16 (w_type); R a multiple of 8,
+ *            8..256 (an adapter of a smaller rank is padded with zeros), K a multiple
+ *            of 8. scale fp32 [L].
+ *   adapter  int32 [M]; outside 0..L-1: the row has none and y = base.
+ *   base, y  fp32 [M][N]; y may be base (the projection's output in place), with no
+ *            other overlap.
+ *   x, a, b 16-byte aligned, the others to their element type. Rows that share an
+ *   adapter read its weights together. L == 0 or K == 0 copies base.
+ *   Workspace: qmv_lora_add_workspace(M, R, K) bytes (negative: QMV_ERR_SHAPE).
+ */
+QMV_API int64_t qmv_lora_add_workspace(int M, int R, int64_t K);
+QMV_API qmv_status qmv_lora_add(const void *x, int x_type, const void *a, const void *b, int w_type,
+                                const int32_t *adapter, const float *scale, const float *base, float *y,
+                                void *workspace, int64_t workspace_bytes, int M, int64_t N, int64_t K, int R, int L,
+                                qmv_stream_t stream);
+
+/*
+ * Rotary positions on a projection's q and k, and the append of k and v to a cache.
+ *   qkv       fp32 [M][Hq + 2 Hkv][D], the projection's output: q heads, k heads, v
+ *             heads. D a multiple of 8, 8..256.
+ *   positions int32 [axes][M], 1..4 axes (text: one; images and video: time, height,
+ *             width); table fp32 [n_positions][rot / 2][2] of (cos, sin) pairs, 16-byte
+ *             aligned; axis_of_pair HOST array [rot / 2]: the axis whose position turns
+ *             each pair. A position outside the table takes its nearest end (bit 2).
+ *   Pair i of a head's first `rot` elements (a multiple of 8, 0..D) is (i, i + rot/2),
+ *   or (2i, 2i + 1) where interleaved is nonzero: (a, b) -> (a c - b s, b c + a s) with
+ *   (c, s) = table[position][i]. The other elements and v are copied.
+ *   slots     int64 [M], 8-byte aligned: the token's place in the caches, page * page
+ *             size + offset; negative: not appended (padding), and so is one of n_slots
+ *             or more (bit 2). Two tokens of a call must not name the same slot.
+ *   q         [M][Hq][D]; k_cache, v_cache [n_slots][Hkv][D] = [pages][page][Hkv][D];
+ *             QMV_F16 or QMV_BF16 (type). Only the named slots are written.
+ *   qkv, q and the caches 16-byte aligned.
+ */
+QMV_API qmv_status qmv_rope_append(const float *qkv, const int32_t *positions, const float *table,
+                                   const uint8_t *axis_of_pair, const int64_t *slots, void *q, void *k_cache,
+                                   void *v_cache, int type, int interleaved, int M, int Hq, int Hkv, int D, int rot,
+                                   int axes, int n_positions, int64_t n_slots, qmv_stream_t stream);
+
+/*
+ * Attention of a batch whose requests share a prefix: T tokens of each of B requests see
+ * the prefix's keys (all of them) and their request's own keys up to themselves.
+ *   out[b][t][h] = sum_j p_j V_j,  p = softmax_j(scale * q[b][t][h] . K_j)
+ * over the keys j of the prefix and the first own_len[b] - T + 1 + t own ones; head h
+ * reads key head h / (Hq / Hkv). The T tokens are the last of own_len[b], so their keys
+ * are in the cache before the call. A row without any key gives zeros.
+ *   q, out   [B][T][Hq][D], D = 64 or 128, Hkv dividing Hq.
+ *   k_cache, v_cache [n_pages][page][Hkv][D], page a power of two, 16..256. All of the
+ *            type `type` (QMV_F16 or QMV_BF16), 16-byte aligned.
+ *   prefix_table int32 [ceil(prefix_len / page)]: the pages of the shared prefix, read
+ *            once for all rows; prefix_len 0 is allowed.
+ *   own_table int32 [B][own_pages], own_len int32 [B] (at most max_own, a bound the
+ *            caller knows, itself at most own_pages * page; a longer one is cut to
+ *            max_own and sets bit 2). A page outside the cache reads as zeros (bit 2).
+ *            Whatever lies in the cache past a request's length or the prefix's is not
+ *            used, NaN included.
+ *   scale    finite and positive.
+ *   Workspace: qmv_prefix_attention_workspace(...) bytes (negative: QMV_ERR_SHAPE).
+ */
+QMV_API int64_t qmv_prefix_attention_workspace(int B, int T, int Hq, int Hkv, int D, int64_t prefix_len,
+                                               int64_t max_own);
+QMV_API qmv_status qmv_prefix_attention(const void *q, const void *k_cache, const void *v_cache, int type,
+                                        int64_t n_pages, int page, const int32_t *prefix_table, int64_t prefix_len,
+                                        const int32_t *own_table, int own_pages, const int32_t *own_len,
+                                        int64_t max_own, float scale, void *out, void *workspace,
+                                        int64_t workspace_bytes, int B, int T, int Hq, int Hkv, int D,
+                                        qmv_stream_t stream);
+
+/*
+ * Penalties for repeated tokens, biases and grammar masks on logits, a row a request:
+ *   x = logits[m][v];  n = how often v is among tokens[m][prompt_len[m] .. total_len[m])
+ *   if v is among tokens[m][0 .. total_len[m]): x = x > 0 ? x / repetition[m] : x * repetition[m]
+ *   if n > 0: x = x - (frequency[m] * n + presence[m])
+ *   x = x + the biases that name v, in their order;  y[m][v] = mask bit v ? x : -inf
+ *   logits, y  fp32 [M][V], M = 0..65535; y may be logits.
+ *   tokens     int32 [M][max_history], the prompt's tokens before the answer's; negative
+ *              ones are skipped, those of V or more too (bit 2). total_len above
+ *              max_history is cut to it (bit 2). prompt_len, total_len int32 [M].
+ *   repetition, presence, frequency fp32 [M], each NULL for none (1, 0, 0).
+ *   bias_tokens int32, bias_values fp32 [M][max_bias]; negative tokens are unused
+ *              entries. max_bias 0: none.
+ *   mask       uint32 [n_masks][ceil(V / 32)], bit v % 32 of word v / 32 set = allowed;
+ *              NULL for none. mask_row int32 [M]: the row's mask, negative for none, one
+ *              of n_masks or more counts as none (bit 2); NULL: row m has mask m.
+ */
+QMV_API qmv_status qmv_penalize_logits(const float *logits, const int32_t *tokens, int max_history,
+                                       const int32_t *prompt_len, const int32_t *total_len, const float *repetition,
+                                       const float *presence, const float *frequency, const int32_t *bias_tokens,
+                                       const float *bias_values, int max_bias, const uint32_t *mask,
+                                       const int32_t *mask_row, int n_masks, float *y, int M, int V,
+                                       qmv_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Introspection (tests and benchmarks)
  * ------------------------------------------------------------------------- */
 
@@ -348,7 +463,9 @@ QMV_API void qmv_route_reset(void);
 
 /*
  * Device-side error word of the current device: bit flags set by kernels whose
- * bounded waits gave up (they skip their work instead of hanging). Synchronizes
+ * bounded waits gave up (bit 1; they skip their work instead of hanging) or that met
+ * an index in device memory outside its array (bit 2; see the decode-step operators,
+ * which say what such an index does). Synchronizes
  * the device. Returns QMV_OK and writes the word to *flags; clear=1 resets it.
  */
 QMV_API qmv_status qmv_error_flags(uint32_t *flags, int clear);

@@ -1,0 +1,130 @@
+"""GPU tests of qmv_lora_add against its definition in 64 bits.
+
+Tolerance, from the arithmetic: weights and fp16 activations are exact in every product;
+what is held in pieces (fp32 activations, A x) keeps at least 21 bits, 2^-21 each; fp32
+sums of at most 2^14 terms are taken over at most 64 dependent steps per chain (2^-23
+each where a step truncates). Together below 2e-5 of the sum over absolute values, and
+one rounding (2^-23) of base and of the output.
+"""
+import pytest
+import torch
+
+import decode_ref
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+
+
+def inputs(M, N, K, R, L, x="f16", w="f16", seed=0, adapter=None):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    if adapter is None:
+        adapter = torch.randint(-1, L, (M,), generator=g, device="cuda", dtype=torch.int32)
+    else:
+        adapter = torch.tensor(adapter, dtype=torch.int32, device="cuda")
+    return dict(x=r(M, K).to(TYPES[x]), a=(r(L, R, K) / max(K, 1) ** 0.5).to(TYPES[w]), b=r(L, N, R).to(TYPES[w]),
+                adapter=adapter, scale=torch.rand((L,), generator=g, device="cuda") + 0.5, base=r(M, N))
+
+
+def check(args, **kw):
+    import gemm_qmv_quantize_gb300 as q
+    y, bound = decode_ref.lora(**args)
+    got = q.qmv_lora_add(**args, **kw)
+    tol = 2e-5 * bound + 2.0 ** -22 * (args["base"].double().abs() + y.abs()) + 1e-30
+    err = (got.double() - y).abs()
+    assert bool((err <= tol).all()), float((err / tol).max())
+    return got
+
+
+@pytest.mark.parametrize("x,w", [("f16", "f16"), ("f16", "bf16"), ("f32", "f16"), ("f32", "bf16")])
+@pytest.mark.parametrize("M,N,K,R,L", [
+    (1, 1, 8, 8, 1), (1, 17, 40, 8, 3), (2, 130, 264, 16, 2), (5, 1000, 520, 24, 3), (7, 257, 1032, 40, 2),
+    (9, 333, 4096, 64, 4), (33, 129, 512, 136, 5), (96, 260, 768, 32, 7), (3, 64, 2056, 256, 2), (8, 100, 17408, 16, 2)])
+def test_sizes_and_types(M, N, K, R, L, x, w):
+    check(inputs(M, N, K, R, L, x, w, seed=M * 1000 + N))
+
+
+@pytest.mark.parametrize("adapter", [
+    [0] * 40,                                             # all rows one adapter
+    list(range(40)),                                      # each its own
+    [-1] * 40,                                            # none at all
+    [39, -1, 0, 0, 39, 40, 1000, -7] * 5,                 # shared, none, outside 0..L-1
+    [1] * 17 + [0] * 9 + [-1] + [1] * 13])                # groups of odd sizes, apart
+def test_who_shares_what(adapter):
+    check(inputs(40, 300, 1024, 16, 40, "f16", "bf16", seed=3, adapter=adapter))
+
+
+def test_in_place_and_rows_without_adapter():
+    args = inputs(6, 500, 512, 16, 2, seed=5, adapter=[0, -1, 1, 0, 5, -1])
+    y, bound = decode_ref.lora(**args)
+    base = args["base"].clone()
+    got = check(args, out=args["base"])
+    assert got.data_ptr() == args["base"].data_ptr()
+    for m in (1, 4, 5):
+        assert torch.equal(got[m], base[m])
+
+
+def test_large_fp32_activations_keep_their_range():
+    args = inputs(3, 64, 256, 8, 2, "f32", "f16", seed=6)
+    args["x"] *= 1e6                                       # beyond fp16's range
+    check(args)
+
+
+def test_no_adapters_and_empty_sum():
+    import gemm_qmv_quantize_gb300 as q
+    for args in (inputs(3, 50, 64, 8, 0, adapter=[0, 1, -1]), inputs(3, 50, 0, 8, 2)):
+        assert torch.equal(q.qmv_lora_add(**args), args["base"])
+    args = inputs(0, 50, 64, 8, 2)
+    assert q.qmv_lora_add(**args).shape == (0, 50)
+
+
+def test_same_call_same_bits_and_other_streams():
+    import gemm_qmv_quantize_gb300 as q
+    args = inputs(20, 700, 2048, 32, 4, "f16", "bf16", seed=8)
+    first = q.qmv_lora_add(**args)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        second = q.qmv_lora_add(**args)
+    third = torch.empty_like(first)
+    q.qmv_lora_add(**args, out=third, stream=s)
+    s.synchronize()
+    assert torch.equal(first, second) and torch.equal(first, third)
+
+
+def test_chained_calls_with_launch_overlap():
+    """The output of one call is the next one's base, launches overlapping."""
+    import gemm_qmv_quantize_gb300 as q
+    args = inputs(4, 256, 256, 8, 3, seed=9)
+    plain = args["base"]
+    for _ in range(6):
+        plain = q.qmv_lora_add(**{**args, "base": plain})
+    try:
+        q.set_launch_overlap(True)
+        y = args["base"]
+        for _ in range(6):
+            y = q.qmv_lora_add(**{**args, "base": y})
+        torch.cuda.synchronize()
+    finally:
+        q.set_launch_overlap(False)
+    assert torch.equal(y, plain)
+
+
+def test_refusals():
+    import gemm_qmv_quantize_gb300 as q
+    args = inputs(2, 32, 64, 8, 2)
+    with pytest.raises(TypeError):
+        q.qmv_lora_add(**{**args, "x": args["x"].bfloat16()})
+    with pytest.raises(TypeError):
+        q.qmv_lora_add(**{**args, "b": args["b"].bfloat16()})
+    with pytest.raises(ValueError):
+        q.qmv_lora_add(**{**args, "b": args["b"][:, :-1].contiguous()})
+    with pytest.raises(ValueError):
+        q.qmv_lora_add(**{**args, "a": args["a"].transpose(1, 2).contiguous().transpose(1, 2)})
+    with pytest.raises(ValueError):
+        q.qmv_lora_add(**args, workspace=torch.empty((4,), dtype=torch.uint8, device="cuda"))
+    with pytest.raises(q.QmvError):
+        q.qmv_lora_add(**inputs(2, 32, 64, 12, 2))         # rank not a multiple of 8
+    with pytest.raises(q.QmvError):
+        q.qmv_lora_add(**inputs(97, 32, 64, 8, 2))         # more rows than a projection takes
