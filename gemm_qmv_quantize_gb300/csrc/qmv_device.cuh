@@ -167,6 +167,16 @@ __device__ __forceinline__ void tma_load_2d(void *dst, const void *tmap, int x, 
         : "memory");
 }
 
+// The same for a 4-D tensor map, coordinates in elements, innermost first.
+__device__ __forceinline__ void tma_load_4d(void *dst, const void *tmap, int c0, int c1, int c2, int c3, uint64_t *bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_addr(dst)),
+        "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_addr(bar))
+        : "memory");
+}
+
 // Order this thread's earlier generic-proxy shared-memory accesses (and, after a
 // warp or CTA barrier, those of the threads it synchronized with) before its later
 // async-proxy (bulk copy / TMA) accesses: a slot the warp has just read is refilled

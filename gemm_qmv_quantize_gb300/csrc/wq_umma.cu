@@ -45,6 +45,7 @@
 
 #include "qmv_device.cuh"
 #include "qmv_internal.h"
+#include "umma_device.cuh"
 
 namespace qmv {
 namespace {
@@ -118,95 +119,6 @@ struct UmmaParams {
     int tile_start[kMaxGroup + 1];
     int count;
 };
-
-// ---------------------------------------------------------------- tcgen05 helpers (inline PTX)
-
-// Shared-memory matrix descriptor of a K-major operand in the 128-byte swizzled
-// layout: rows of 64 fp16 (128 bytes) at a 128-byte pitch, 8-row groups 1024 bytes
-// apart (sbo), the 16-byte chunk c of row r stored at chunk c ^ (r % 8) from a
-// 1024-byte aligned base -- the layout a TMA box with the 128-byte swizzle lands in.
-// A K step of 16 within the 64-k row advances the start address by 32 bytes.
-__device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr)
-{
-    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (1ull << 16) |   // leading offset: unused (1)
-           (static_cast<uint64_t>(1024u >> 4) << 32) | (1ull << 46) |       // sbo = 1024; bits 46..48 = 0b001
-           (2ull << 61);                                                    // swizzle mode: 128 bytes
-}
-
-// Instruction descriptor of kind::f16: fp16 A and B (both K-major), fp32 D, M x N.
-__host__ __device__ constexpr uint32_t idesc_f16_f32(int m, int n)
-{
-    return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
-}
-
-// D (+)= A x B with A in tensor memory (128 lanes = rows, fp16 pairs along columns).
-__device__ __forceinline__ void umma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                            uint32_t accumulate)
-{
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-
-// The mbarrier completes (one arrival) when every earlier tcgen05 operation of this
-// thread has completed.
-__device__ __forceinline__ void umma_commit(uint64_t *bar)
-{
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
-                 : "memory");
-}
-
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-// 16 consecutive 32-bit columns of this thread's TMEM lane from v (warp-wide,
-// .sync.aligned); the stores are complete when tcgen05.wait::st returns.
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16])
-{
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
-            taddr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-        : "memory");
-}
-
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// All threads of every CTA of the cluster (release / acquire: shared-memory writes
-// before it are visible to the cluster's reads after it).
-__device__ __forceinline__ void cluster_sync_all()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// The float at the same shared-memory offset in the cluster's CTA `rank`.
-__device__ __forceinline__ float ld_peer_f32(const float *local, int rank)
-{
-    uint32_t remote;
-    float v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_addr(local)), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote) : "memory");
-    return v;
-}
-
-// 16 consecutive fp32 columns of this thread's TMEM lane (warp-wide, .sync.aligned).
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16])
-{
-    uint32_t r[16];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr)
-        : "memory");
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
 
 // ---------------------------------------------------------------- the kernel
 
