@@ -38,8 +38,8 @@ namespace {
 __device__ uint32_t g_attention_error;
 
 constexpr int kTile = 128;              // keys a tile = rows a stream = TMEM lanes
-constexpr int kMmaWarp = 8, kLoadWarpV = 10;
-constexpr int kThreads = 32 * 11;       // two streams of 4 warps, the product warp, the loading warps of K and of V
+constexpr int kMmaWarp = 8;
+constexpr int kThreads = 32 * 10;       // two streams of 4 warps, the product warp, the loading warp
 constexpr int kTmemCols = 512;
 constexpr int kMaxSlots = 8;
 constexpr int kSmemBytes = 232448 - 2048;   // dynamic shared memory: a CTA's limit but the barriers and statistics
@@ -118,11 +118,76 @@ __device__ __forceinline__ uint32_t pack2(float a, float b)
     }
 }
 
-// The order in which tiles go through the ring of slots, K0 K1 V0 K2 V1 K3 ...: a tile's
-// K is needed one step before its V.
-__device__ __forceinline__ int ring_pos(bool v, int j) { return v ? 2 * j + 2 : (j == 0 ? 0 : 2 * j - 1); }
+// The order in which a job's n tiles go through the ring of slots, K0 K1 V0 K2 V1 ... Vn-1:
+// a tile's K is needed a step before its V.
+__device__ __forceinline__ int k_pos(int j) { return j == 0 ? 0 : 2 * j - 1; }
+__device__ __forceinline__ int v_pos(int j, int n) { return j == n - 1 ? 2 * n - 1 : 2 * j + 2; }
 
-template <typename T, int kD>
+struct Job {
+    int h, i0, nrows;       // key head; rows i0 .. i0 + nrows - 1
+    int slot;               // of the partial results
+    int own_b;              // request whose own keys these are, or -1: the prefix's
+    int64_t key0;           // first key, a multiple of 128
+    int keys, ntiles;       // number of keys, of tiles (0: no key)
+    int own_end;            // own keys: the request's length - key0
+};
+
+// Own keys of a request, cut to the caller's bound.
+__device__ __forceinline__ int own_length(const AttnParams &p, int id)
+{
+    if (id < p.plan.prefix_jobs || id >= p.plan.prefix_jobs + p.plan.own_jobs) return 0;
+    const int b = (id - static_cast<int>(p.plan.prefix_jobs)) / (p.plan.own_splits * p.plan.own_groups * p.g.Hkv);
+    return __ldg(p.g.own_len + b);
+}
+
+// Job `id`; len: own_length of it (loaded ahead).
+__device__ __forceinline__ Job job_of(const AttnParams &p, int id, int len)
+{
+    const AttnArgs &g = p.g;
+    const int G = g.Hq / g.Hkv;
+    Job j;
+    int64_t key1;
+    if (id < p.plan.prefix_jobs) {
+        const int tiles = static_cast<int>((g.prefix_len + kTile - 1) / kTile), rows = g.B * g.T * G;
+        const int pair_jobs = g.Hkv * p.plan.pair_groups * p.plan.pair_splits;
+        const bool lone = id >= pair_jobs;
+        const int splits = lone ? p.plan.lone_splits : p.plan.pair_splits;
+        int k = lone ? id - pair_jobs : id;
+        const int split = k % splits;
+        k /= splits;
+        const int group = lone ? p.plan.pair_groups : k % p.plan.pair_groups;
+        j.h = lone ? k : k / p.plan.pair_groups;
+        j.i0 = group * 2 * kTile;
+        j.nrows = min(rows - j.i0, 2 * kTile);
+        j.key0 = static_cast<int64_t>(tiles) * split / splits * kTile;
+        key1 = min(static_cast<int64_t>(tiles) * (split + 1) / splits * kTile, g.prefix_len);
+        j.slot = p.plan.own_splits + split;
+        j.own_b = -1;
+        j.own_end = 0;
+    } else {
+        int k = id - static_cast<int>(p.plan.prefix_jobs);
+        const int split = k % p.plan.own_splits;
+        k /= p.plan.own_splits;
+        const int group = k % p.plan.own_groups;
+        k /= p.plan.own_groups;
+        j.h = k % g.Hkv;
+        j.own_b = k / g.Hkv;
+        const int per = g.T * G;
+        j.i0 = j.own_b * per + group * 2 * kTile;
+        j.nrows = min(per - group * 2 * kTile, 2 * kTile);
+        const int64_t n = min(static_cast<int64_t>(len), g.max_own);
+        j.key0 = static_cast<int64_t>(split) * p.plan.own_tiles * kTile;
+        key1 = min(j.key0 + static_cast<int64_t>(p.plan.own_tiles) * kTile, n);
+        j.slot = split;
+        j.own_end = static_cast<int>(max(static_cast<int64_t>(0), n - j.key0));
+    }
+    j.keys = static_cast<int>(max(static_cast<int64_t>(0), key1 - j.key0));
+    j.ntiles = (j.keys + kTile - 1) / kTile;
+    return j;
+}
+
+// kWide: the launch has jobs of more than 128 rows (two Q tiles, one slot less).
+template <typename T, int kD, bool kWide>
 __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_constant__ AttnParams p)
 {
     constexpr bool kBf16 = std::is_same_v<T, __nv_bfloat16>;
@@ -131,92 +196,40 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     constexpr int kChunks = kD / 64;               // 64-wide (128-byte) blocks of a row
     constexpr uint32_t kBlock = kTile * 128;       // bytes of one block of a tile
     constexpr uint32_t kSlotBytes = kChunks * kBlock;
-    extern __shared__ __align__(1024) uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t full[kMaxSlots], freed[kMaxSlots], s_full[2], p_full[2], o_done[2], drained;
+    constexpr uint32_t kQBytes = (kWide ? 2 : 1) * kSlotBytes;
+    constexpr int kSlots = std::min(kMaxSlots, static_cast<int>((kSmemBytes - kQBytes) / kSlotBytes));
+    extern __shared__ __align__(1024) uint8_t smem[];
+    // full: a slot's copies have landed; freed: its readers are done (two arrivals: each
+    // stream's, or two by the one stream that reads it); s_full / p_full: S, P of a stream's
+    // step; q_full: a job's Q is in place; o_done: its products are complete; o_free: its
+    // results have been read; merged: stream 1's statistics of a job are there for stream 0
+    __shared__ __align__(8) uint64_t full[kSlots], freed[kSlots], s_full[2], p_full[2], q_full, o_done, o_free, merged, drained;
     __shared__ uint32_t tmem_slot, abort_flag;
     __shared__ float merge_m[kTile], merge_l[kTile];
-    uint8_t *smem = smem_raw;
     volatile uint32_t *abort_word = &abort_flag;
+    uint8_t *ring = smem + kQBytes;
     const AttnArgs &g = p.g;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int G = g.Hq / g.Hkv;
-
-    grid_dependency_wait();
-
-    // ---- the job: key head h, rows i0 .. i0 + nrows - 1, keys [key0, key1), result slot
-    int64_t id = blockIdx.x, i0, key0, key1;
-    int h, nrows, slot, own_b = -1;
-    const int64_t rows_all = static_cast<int64_t>(g.B) * g.T * G;
-    if (id < p.plan.prefix_jobs) {
-        const int64_t tiles = (g.prefix_len + kTile - 1) / kTile, pair_jobs = static_cast<int64_t>(g.Hkv) * p.plan.pair_groups * p.plan.pair_splits;
-        int splits, group, split;
-        if (id < pair_jobs) {
-            splits = p.plan.pair_splits;
-            split = static_cast<int>(id % splits);
-            group = static_cast<int>(id / splits % p.plan.pair_groups);
-            h = static_cast<int>(id / splits / p.plan.pair_groups);
-        } else {
-            splits = p.plan.lone_splits;
-            split = static_cast<int>((id - pair_jobs) % splits);
-            group = p.plan.pair_groups;
-            h = static_cast<int>((id - pair_jobs) / splits);
-        }
-        i0 = static_cast<int64_t>(group) * 2 * kTile;
-        nrows = static_cast<int>(min(rows_all - i0, static_cast<int64_t>(2 * kTile)));
-        key0 = tiles * split / splits * kTile;
-        key1 = min(tiles * (split + 1) / splits * kTile, g.prefix_len);
-        slot = p.plan.own_splits + split;
-    } else {
-        id -= p.plan.prefix_jobs;
-        const int split = static_cast<int>(id % p.plan.own_splits);
-        id /= p.plan.own_splits;
-        const int group = static_cast<int>(id % p.plan.own_groups);
-        id /= p.plan.own_groups;
-        h = static_cast<int>(id % g.Hkv);
-        own_b = static_cast<int>(id / g.Hkv);
-        const int per = g.T * G;
-        i0 = static_cast<int64_t>(own_b) * per + group * 2 * kTile;
-        nrows = min(per - group * 2 * kTile, 2 * kTile);
-        int64_t len = g.own_len[own_b];
-        if (len > g.max_own) {
-            if (tid == 0) atomicOr(&g_attention_error, kErrIndex);
-            len = g.max_own;
-        }
-        key0 = static_cast<int64_t>(split) * p.plan.own_tiles * kTile;
-        key1 = min(key0 + static_cast<int64_t>(p.plan.own_tiles) * kTile, len);
-        slot = split;
-    }
-    const int64_t out_row0 = static_cast<int64_t>(slot) * g.B * g.T * g.Hq;
-    // row i of key head h is query head h G + i % G of token i / G
-    auto q_row = [&](int64_t i) { return i / G * g.Hq + h * G + i % G; };
-    if (key1 <= key0) {   // no key: nothing of these rows in this slot
-        for (int r = tid; r < nrows; r += kThreads) p.lse[out_row0 + q_row(i0 + r)] = -INFINITY;
-        grid_launch_dependents();
-        return;
-    }
-    const bool pair = nrows > kTile;
-    const int ntiles = static_cast<int>((key1 - key0 + kTile - 1) / kTile);
-    // stream s takes tiles first, first + step, ...
-    auto steps_of = [&](int s) { return pair ? ntiles : (ntiles - s + 1) / 2; };
-    const int last_keys = static_cast<int>(key1 - key0 - static_cast<int64_t>(ntiles - 1) * kTile);   // keys of the last tile
-    const uint32_t q_bytes = (pair ? 2u : 1u) * kSlotBytes;
-    uint8_t *ring = smem + q_bytes;
-    const int nslots = min(kMaxSlots, static_cast<int>((kSmemBytes - q_bytes) / kSlotBytes));
+    const int G = g.Hq / g.Hkv, jobs = static_cast<int>(p.plan.prefix_jobs + p.plan.own_jobs), stride = static_cast<int>(gridDim.x);
     auto fail = [&]() { note_wait_timeout(&g_attention_error, abort_word); };
     auto wait_all = [&](uint64_t *bar, uint32_t parity) {
         return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity) ? 1 : 0) != 0;
     };
+    auto full_parity = [](int pos) { return static_cast<uint32_t>(pos / kSlots) & 1u; };
 
     if (tid == 0) {
-        for (int i = 0; i < nslots; ++i) {
+        for (int i = 0; i < kSlots; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&freed[i], 1);
+            mbar_init(&freed[i], 2);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&s_full[s], 1);
             mbar_init(&p_full[s], 4);
-            mbar_init(&o_done[s], 1);
         }
+        mbar_init(&q_full, 8);
+        mbar_init(&o_done, 1);
+        mbar_init(&o_free, 8);
+        mbar_init(&merged, 4);
         mbar_init(&drained, 1);
         abort_flag = 0u;
         fence_barrier_init();
@@ -227,280 +240,327 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    // Q into the K-major swizzled layout, rows past the job's as zeros
-    {
-        const int q_rows = pair ? 2 * kTile : kTile;
-        for (int u = tid; u < q_rows * (kD / 8); u += kThreads) {
-            const int r = u / (kD / 8), c = u % (kD / 8);
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (r < nrows) v = *(reinterpret_cast<const uint4 *>(static_cast<const T *>(g.q) + q_row(i0 + r) * kD) + c);
-            uint8_t *dst = smem + (r / kTile) * kSlotBytes + (c / 8) * kBlock + (r % kTile) * 128 + 16 * ((c % 8) ^ (r % 8));
-            *reinterpret_cast<uint4 *>(dst) = v;
-        }
-        fence_proxy_async_shared();
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
+    grid_dependency_wait();
     grid_launch_dependents();
 
+    int id = static_cast<int>(blockIdx.x);
+    int len = own_length(p, id);
     if (warp < 8) {
         // ------------------------------------------------ softmax of stream s: a row a thread
-        const int s = warp >> 2, r = tid & (kTile - 1), steps = steps_of(s);
-        const int rel = pair ? s * kTile + r : r;               // row within the job
-        const bool live = rel < nrows;
-        const bool warp_live = (pair ? s * kTile : 0) + (r & ~31) < nrows;   // any row of this warp
+        const int s = warp >> 2, r = tid & (kTile - 1);
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         const uint32_t s_col = tmem + lanes + static_cast<uint32_t>(s * kTile);
         const uint32_t o_col = tmem + lanes + 256u + static_cast<uint32_t>(s * kTile);
-        // keys of this row: all of the prefix's, or its request's up to its own token
-        int64_t limit = key1;
-        if (own_b >= 0 && live) {
-            const int t = static_cast<int>((i0 + rel) / G % g.T);
-            limit = min(key1, min(static_cast<int64_t>(g.own_len[own_b]), g.max_own) - g.T + 1 + t);
-        }
-        const int64_t least = own_b >= 0 ? min(key1, min(static_cast<int64_t>(g.own_len[own_b]), g.max_own) - g.T + 1) : key1;
         const float c = g.scale * 1.4426950408889634f;
-        float m = -INFINITY, l = 0.0f;
-        bool ok = true;
-        for (int i = 0; i < steps; ++i) {
-            const int64_t k0 = key0 + static_cast<int64_t>(pair ? i : 2 * i + s) * kTile;
-            if (*abort_word || !wait_all(&s_full[s], static_cast<uint32_t>(i) & 1u)) {
-                fail();
-                ok = false;
-                break;
+        // row i of key head h is query head h G + i % G of token i / G
+        auto q_row = [&](int h, int i) { return static_cast<int64_t>(i / G) * g.Hq + h * G + i % G; };
+        // a job's Q into the K-major swizzled layout (rows past the job's keep what is there:
+        // their S, P and O are never used)
+        auto load_q = [&](const Job &j) {
+            for (int u = tid; u < j.nrows * (kD / 8); u += 256) {
+                const int qr = u / (kD / 8), x = u % (kD / 8);
+                const uint4 v = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(g.q) + q_row(j.h, j.i0 + qr) * kD) + x);
+                *reinterpret_cast<uint4 *>(smem + (qr / kTile) * kSlotBytes + (x / 8) * kBlock + (qr % kTile) * 128 +
+                                           16 * ((x % 8) ^ (qr % 8))) = v;
             }
-            if (warp_live) {
-                tc_fence_after();
-                float v[kTile];
-#pragma unroll
-                for (int j = 0; j < kTile; j += 32) tmem_ld32_async(s_col + j, v + j);
-#pragma unroll
-                for (int j = 0; j < kTile; j += 32) tmem_wait_ld32(v + j);
-                if (least - k0 < kTile) {
-                    const int n = static_cast<int>(max(static_cast<int64_t>(0), min(limit - k0, static_cast<int64_t>(kTile))));
-#pragma unroll
-                    for (int j = 0; j < kTile; ++j)
-                        if (j >= n) v[j] = -INFINITY;
-                }
-                float top[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) top[j] = v[j];
-#pragma unroll
-                for (int j = 4; j < kTile; ++j) top[j & 3] = fmaxf(top[j & 3], v[j]);
-                const float best = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
-                const bool grow = best > m + kSlack;   // (m = -inf: the row's first keys)
-                if (__any_sync(0xffffffffu, grow)) {
-                    const float next = grow ? best : m;
-                    const float fix = grow ? exp2_fast(m - next) : 1.0f;
-                    l *= fix;
-                    m = next;
-                    // the sums so far are complete: S of this step was issued after P V of the last
-                    if (i > 0) {
-#pragma unroll
-                        for (int j = 0; j < kD; j += 16) {
-                            float o[16];
-                            tmem_ld16(o_col + j, o);
-                            uint32_t w[16];
-#pragma unroll
-                            for (int x = 0; x < 16; ++x) w[x] = __float_as_uint(o[x] * fix);
-                            tmem_st16(o_col + j, w);
-                        }
-                    }
-                }
-                const float shift = (m == -INFINITY ? 0.0f : m) - kLift;
-                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int q = 0; q < kTile; q += 32) {
-                    uint32_t w[16];
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const float a = exp2_fast(fmaf(v[q + 2 * j], c, -shift));
-                        const float b = exp2_fast(fmaf(v[q + 2 * j + 1], c, -shift));
-                        sum[j & 3] += a + b;
-                        w[j] = pack2<T>(a, b);
-                    }
-                    tmem_st16(s_col + q / 2, w);
-                }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                tmem_wait_st();
-                tc_fence_before();
-            }
+            fence_proxy_async_shared();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[s]);
-        }
-        // (up to 128 rows: stream 1 hands its part over in the memory that stream 0's products read)
-        if (ok && ((steps > 0 && !wait_all(&o_done[s], 0u)) || (!pair && s == 1 && !wait_all(&o_done[0], 0u)))) {
-            fail();
-            ok = false;
-        }
-        tc_fence_after();
-        // ---- results
-        float *acc_smem = reinterpret_cast<float *>(smem);   // Q and the ring are idle now: [d][128 rows]
-        if (!pair) {   // the two streams hold the same rows: stream 1 hands its part over
-            if (s == 1) {
-                merge_m[r] = m;
-                merge_l[r] = l;
-                if (steps > 0 && warp_live && ok) {
-#pragma unroll
-                    for (int j = 0; j < kD; j += 32) {
-                        float o[32];
-                        tmem_ld32_async(o_col + j, o);
-                        tmem_wait_ld32(o);
-#pragma unroll
-                        for (int x = 0; x < 32; ++x) acc_smem[(j + x) * kTile + r] = o[x];
-                    }
-                }
-            }
-            asm volatile("bar.sync 1, 256;" ::: "memory");
-        }
-        if (ok && warp_live && !(s == 1 && !pair) && !*abort_word) {
-            float w0 = 1.0f, w1 = 0.0f;
-            const bool both = !pair && steps_of(1) > 0;
-            if (both) {
-                const float m1 = merge_m[r], top = fmaxf(m, m1);
-                w0 = m == -INFINITY ? 0.0f : exp2_fast(m - top);
-                w1 = m1 == -INFINITY ? 0.0f : exp2_fast(m1 - top);
-                l = l * w0 + merge_l[r] * w1;
-                m = top;
-            }
-            const float inv = 1.0f / l;
-            const int64_t row = live ? out_row0 + q_row(i0 + rel) : 0;
-            if (live) p.lse[row] = l == 0.0f ? -INFINITY : m - kLift + log2f(l);
-#pragma unroll
-            for (int j = 0; j < kD; j += 32) {
-                float o[32];
-                tmem_ld32_async(o_col + j, o);
-                tmem_wait_ld32(o);
-                if (both) {
-#pragma unroll
-                    for (int x = 0; x < 32; ++x) o[x] = o[x] * w0 + acc_smem[(j + x) * kTile + r] * w1;
-                }
-                if (live && l != 0.0f) {
-#pragma unroll
-                    for (int x = 0; x < 32; x += 4)
-                        *reinterpret_cast<float4 *>(p.part + row * kD + j + x) =
-                            make_float4(o[x] * inv, o[x + 1] * inv, o[x + 2] * inv, o[x + 3] * inv);
-                }
-            }
-        }
-        tc_fence_before();
-    } else if (warp == kMmaWarp) {
-        // ------------------------------------------------ products (lane 0 issues; the warp clears tails)
-        const uint32_t idesc_s = idesc_16bit_f32(kTile, kTile, kBf16, false);
-        const uint32_t idesc_o = idesc_16bit_f32(kTile, kD, kBf16, true);
-        const uint32_t q_addr = smem_addr(smem), ring_addr = smem_addr(ring);
-        const int n0 = steps_of(0);
-        auto tile_of = [&](int s, int i) { return pair ? i : 2 * i + s; };
-        // S of stream s, step i; its K slot is free after the last stream that reads it
-        auto issue_s = [&](int s, int i) {
-            const int j = tile_of(s, i), pos = ring_pos(false, j), at = pos % nslots;
-            if (*abort_word || !wait_all(&full[at], static_cast<uint32_t>(pos / nslots) & 1u)) return false;
-            if (lane == 0) {
-                tc_fence_after();
-                const uint32_t qa = q_addr + (pair ? static_cast<uint32_t>(s) * kSlotBytes : 0u);
-                const uint32_t ka = ring_addr + static_cast<uint32_t>(at) * kSlotBytes;
-#pragma unroll
-                for (int k = 0; k < kD / 16; ++k) {
-                    const uint32_t off = static_cast<uint32_t>(k / 4) * kBlock + 32u * (k % 4);
-                    umma_f16_ss(tmem + static_cast<uint32_t>(s * kTile), smem_desc_sw128(qa + off), smem_desc_sw128(ka + off),
-                                idesc_s, k > 0 ? 1u : 0u);
-                }
-                umma_commit(&s_full[s]);
-                if (!pair || s == 1) umma_commit(&freed[at]);
-            }
-            __syncwarp();
-            return true;
+            if (lane == 0) mbar_arrive(&q_full);
         };
+        int pos0 = 0;            // ring positions before this job's
+        uint32_t step = 0, done = 0, merges = 0;   // this stream's steps, the jobs with keys and those joined, so far
         bool ok = true;
-        for (int s = 0; s < 2 && ok; ++s)
-            if (steps_of(s) > 0) ok = issue_s(s, 0);
-        for (int i = 0; i < n0 && ok; ++i) {
-            for (int s = 0; s < 2 && ok; ++s) {
-                if (i >= steps_of(s)) break;
-                const int j = tile_of(s, i), pos = ring_pos(true, j), at = pos % nslots;
-                if (*abort_word || !wait_all(&full[at], static_cast<uint32_t>(pos / nslots) & 1u)) {
+        Job job = job_of(p, id, len);
+        if (id < jobs && job.ntiles > 0) load_q(job);
+        while (id < jobs && ok) {
+            const int next_id = id + stride, next_len = own_length(p, next_id);
+            if (job.own_b >= 0 && len > g.max_own && tid == 0) atomicOr(&g_attention_error, kErrIndex);
+            const int64_t out_row0 = static_cast<int64_t>(job.slot) * g.B * g.T * g.Hq;
+            if (job.ntiles == 0) {   // no key: nothing of these rows in this slot
+                for (int x = tid; x < job.nrows; x += 256) p.lse[out_row0 + q_row(job.h, job.i0 + x)] = -INFINITY;
+                id = next_id;
+                len = next_len;
+                if (id < jobs) {
+                    job = job_of(p, id, len);
+                    if (job.ntiles > 0) load_q(job);
+                }
+                continue;
+            }
+            const bool pair = kWide && job.nrows > kTile;
+            const int n = job.ntiles, steps = pair ? n : (n - s + 1) / 2;
+            const int rel = pair ? s * kTile + r : r;   // row within the job
+            const bool live = rel < job.nrows;
+            const bool warp_live = (pair ? s * kTile : 0) + (r & ~31) < job.nrows;   // any row of this warp
+            // keys of this row: all of the prefix's, or its request's up to its own token; and the fewest of any row
+            const int limit = job.own_b < 0 ? job.keys : min(job.keys, job.own_end - g.T + 1 + (job.i0 + rel) / G % g.T);
+            const int least = job.own_b < 0 ? job.keys : min(job.keys, job.own_end - g.T + 1);
+            const uint32_t arrivals = pair ? 1u : 2u;
+            float m = -INFINITY, l = 0.0f;
+            for (int i = 0; i < steps; ++i, ++step) {
+                const int t = pair ? i : 2 * i + s;
+                if (*abort_word || !wait_all(&s_full[s], step & 1u)) {
+                    fail();
                     ok = false;
                     break;
                 }
-                if (j == ntiles - 1 && last_keys < kTile && (!pair || s == 0)) {
+                if ((warp & 3) == 0 && lane == 0) {   // S is complete, and P V of the last step
+                    mbar_arrive_n(&freed[(pos0 + k_pos(t)) % kSlots], arrivals);
+                    if (i > 0) mbar_arrive_n(&freed[(pos0 + v_pos(pair ? t - 1 : t - 2, n)) % kSlots], arrivals);
+                }
+                if (warp_live) {
+                    tc_fence_after();
+                    float v[kTile];
+#pragma unroll
+                    for (int j = 0; j < kTile; j += 32) tmem_ld32_async(s_col + j, v + j);
+#pragma unroll
+                    for (int j = 0; j < kTile; j += 32) tmem_wait_ld32(v + j);
+                    if (least - t * kTile < kTile) {
+                        const int x = limit - t * kTile;
+#pragma unroll
+                        for (int j = 0; j < kTile; ++j)
+                            if (j >= x) v[j] = -INFINITY;
+                    }
+                    float top[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) top[j] = v[j];
+#pragma unroll
+                    for (int j = 4; j < kTile; ++j) top[j & 3] = fmaxf(top[j & 3], v[j]);
+                    const float best = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
+                    const bool grow = best > m + kSlack;   // (m = -inf: the row's first keys)
+                    if (__any_sync(0xffffffffu, grow)) {
+                        const float next = grow ? best : m;
+                        const float fix = grow ? exp2_fast(m - next) : 1.0f;
+                        l *= fix;
+                        m = next;
+                        // the sums so far are complete: S of this step was issued after P V of the last
+                        if (i > 0) {
+#pragma unroll
+                            for (int j = 0; j < kD; j += 16) {
+                                float o[16];
+                                tmem_ld16(o_col + j, o);
+                                uint32_t w[16];
+#pragma unroll
+                                for (int x = 0; x < 16; ++x) w[x] = __float_as_uint(o[x] * fix);
+                                tmem_st16(o_col + j, w);
+                            }
+                        }
+                    }
+                    const float shift = (m == -INFINITY ? 0.0f : m) - kLift;
+                    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int q = 0; q < kTile; q += 32) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const float a = exp2_fast(fmaf(v[q + 2 * j], c, -shift));
+                            const float b = exp2_fast(fmaf(v[q + 2 * j + 1], c, -shift));
+                            sum[j & 3] += a + b;
+                            w[j] = pack2<T>(a, b);
+                        }
+                        tmem_st16(s_col + q / 2, w);
+                    }
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    tmem_wait_st();
+                    tc_fence_before();
+                }
+                if (t == n - 1 && job.keys % kTile != 0 && (!pair || s == 0)) {
                     // what lies past the last key may be anything, NaN too: zeros, since 0 x NaN is NaN
-                    for (int u = lane; u < (kTile - last_keys) * 8 * kChunks; u += 32) {
-                        const int row = last_keys + u / (8 * kChunks), x = u % (8 * kChunks);
-                        *reinterpret_cast<uint4 *>(ring + at * kSlotBytes + (x / 8) * kBlock + row * 128 + 16 * (x % 8)) =
+                    const int pos = pos0 + v_pos(t, n), first = job.keys % kTile;
+                    if (*abort_word || !wait_all(&full[pos % kSlots], full_parity(pos))) {
+                        fail();
+                        ok = false;
+                        break;
+                    }
+                    for (int u = r; u < (kTile - first) * 8 * kChunks; u += kTile) {
+                        const int row = first + u / (8 * kChunks), x = u % (8 * kChunks);
+                        *reinterpret_cast<uint4 *>(ring + (pos % kSlots) * kSlotBytes + (x / 8) * kBlock + row * 128 + 16 * (x % 8)) =
                             make_uint4(0, 0, 0, 0);
                     }
                     fence_proxy_async_shared();
-                    __syncwarp();
-                }
-                if (*abort_word || !wait_all(&p_full[s], static_cast<uint32_t>(i) & 1u)) {
-                    ok = false;
-                    break;
-                }
-                if (lane == 0) {
-                    tc_fence_after();
-                    const uint32_t va = ring_addr + static_cast<uint32_t>(at) * kSlotBytes;
-#pragma unroll
-                    for (int k = 0; k < kTile / 16; ++k)
-                        umma_f16_ta(tmem + 256u + static_cast<uint32_t>(s * kTile), tmem + static_cast<uint32_t>(s * kTile) + 8u * k,
-                                    smem_desc_sw128_mn(va + 2048u * k, kBlock), idesc_o, (i > 0 || k > 0) ? 1u : 0u);
-                    if (!pair || s == 1) umma_commit(&freed[at]);
-                    if (i + 1 == steps_of(s)) umma_commit(&o_done[s]);
                 }
                 __syncwarp();
-                if (i + 1 < steps_of(s)) ok = issue_s(s, i + 1);
+                if (lane == 0) mbar_arrive(&p_full[s]);
             }
+            if (ok && (*abort_word || !wait_all(&o_done, done & 1u))) {
+                fail();
+                ok = false;
+            }
+            if (!ok) break;
+            ++done;
+            if (steps > 0 && (warp & 3) == 0 && lane == 0)
+                mbar_arrive_n(&freed[(pos0 + v_pos(pair ? n - 1 : 2 * (steps - 1) + s, n)) % kSlots], arrivals);
+            pos0 += 2 * n;
+            // the next job's Q, so that its first products run beside this job's results
+            id = next_id;
+            len = next_len;
+            Job next = job;
+            if (id < jobs) {
+                next = job_of(p, id, len);
+                if (next.ntiles > 0) load_q(next);
+            }
+            // ---- results; up to 128 rows, the streams hold the same rows: stream 0 takes both parts
+            tc_fence_after();
+            const bool both = !pair && n > 1;
+            if (both) {
+                if (s == 1) {
+                    merge_m[r] = m;
+                    merge_l[r] = l;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&merged);
+                } else if (!wait_all(&merged, merges & 1u)) {
+                    fail();
+                    break;
+                }
+                ++merges;
+            }
+            if (warp_live && (pair || s == 0)) {
+                float w0 = 1.0f, w1 = 0.0f;
+                if (both) {
+                    const float m1 = merge_m[r], top = fmaxf(m, m1);
+                    w0 = m == -INFINITY ? 0.0f : exp2_fast(m - top);
+                    w1 = m1 == -INFINITY ? 0.0f : exp2_fast(m1 - top);
+                    l = l * w0 + merge_l[r] * w1;
+                    m = top;
+                }
+                const float inv = 1.0f / l;
+                const int64_t row = live ? out_row0 + q_row(job.h, job.i0 + rel) : 0;
+                if (live) p.lse[row] = l == 0.0f ? -INFINITY : m - kLift + log2f(l);
+#pragma unroll
+                for (int j = 0; j < kD; j += 16) {
+                    float o[16];
+                    tmem_ld16(o_col + j, o);
+                    if (both) {
+                        float o1[16];
+                        tmem_ld16(o_col + kTile + j, o1);
+#pragma unroll
+                        for (int x = 0; x < 16; ++x) o[x] = o[x] * w0 + o1[x] * w1;
+                    }
+                    if (live && l != 0.0f) {
+#pragma unroll
+                        for (int x = 0; x < 16; x += 4)
+                            *reinterpret_cast<float4 *>(p.part + row * kD + j + x) =
+                                make_float4(o[x] * inv, o[x + 1] * inv, o[x + 2] * inv, o[x + 3] * inv);
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&o_free);
+            job = next;
         }
-        if (!ok) fail();
-        // every product has completed before tensor memory is released: a normal end is
-        // seen by the streams' waits on o_done; after a failure this thread waits itself
-        if (!ok && lane == 0) {
+    } else if (warp == kMmaWarp) {
+        // ------------------------------------------------ products: one thread
+        if (elect_one()) {
+            constexpr uint32_t idesc_s = idesc_16bit_f32(kTile, kTile, kBf16, false);
+            constexpr uint32_t idesc_o = idesc_16bit_f32(kTile, kD, kBf16, true);
+            const uint64_t q_desc = smem_desc_sw128(smem_addr(smem)), k_desc = smem_desc_sw128(smem_addr(ring));
+            const uint64_t v_desc = smem_desc_sw128_mn(smem_addr(ring), kBlock);
+            int pos0 = 0;
+            uint32_t done = 0, step[2] = {0, 0};
+            bool ok = true;
+            for (; id < jobs && ok; id += stride) {
+                const Job job = job_of(p, id, len);
+                len = own_length(p, id + stride);
+                const int n = job.ntiles;
+                if (n == 0) continue;
+                const bool pair = kWide && job.nrows > kTile;
+                auto steps_of = [&](int s) { return pair ? n : (n - s + 1) / 2; };
+                auto wait_full = [&](int pos) { return mbar_wait_bounded(&full[pos % kSlots], full_parity(pos)); };
+                auto issue_s = [&](int s, int t) {
+                    const int pos = pos0 + k_pos(t);
+                    if (!wait_full(pos)) return false;
+                    tc_fence_after();
+                    const uint64_t qd = q_desc + (pair && s == 1 ? kSlotBytes >> 4 : 0u);
+                    const uint64_t kd = k_desc + static_cast<uint32_t>(pos % kSlots) * (kSlotBytes >> 4);
+#pragma unroll
+                    for (int k = 0; k < kD / 16; ++k) {
+                        const uint32_t off = (static_cast<uint32_t>(k / 4) * kBlock + 32u * (k % 4)) >> 4;
+                        umma_f16_ss(tmem + static_cast<uint32_t>(s * kTile), qd + off, kd + off, idesc_s, k > 0 ? 1u : 0u);
+                    }
+                    umma_commit(&s_full[s]);
+                    return true;
+                };
+                ok = !*abort_word && mbar_wait_bounded(&q_full, done & 1u);
+                for (int s = 0; s < 2 && ok; ++s)
+                    if (steps_of(s) > 0) ok = issue_s(s, s == 0 || pair ? 0 : 1);
+                // the last job's results have been read before O is written again
+                if (ok && done > 0) ok = mbar_wait_bounded(&o_free, (done - 1) & 1u);
+                for (int i = 0; i < steps_of(0) && ok; ++i) {
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        if (i >= steps_of(s) || !ok) break;
+                        const int t = pair ? i : 2 * i + s, pos = pos0 + v_pos(t, n);
+                        ok = !*abort_word && wait_full(pos) && mbar_wait_bounded(&p_full[s], step[s]++ & 1u);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t vd = v_desc + static_cast<uint32_t>(pos % kSlots) * (kSlotBytes >> 4);
+#pragma unroll
+                        for (int k = 0; k < kTile / 16; ++k)   // 16 keys: 2048 bytes of V, 8 columns of P
+                            umma_f16_ta(tmem + 256u + static_cast<uint32_t>(s * kTile), tmem + static_cast<uint32_t>(s * kTile) + 8u * k,
+                                        vd + 128u * k, idesc_o, (i > 0 || k > 0) ? 1u : 0u);
+                        if (i + 1 < steps_of(s)) ok = issue_s(s, pair ? t + 1 : t + 2);
+                    }
+                }
+                if (ok) umma_commit(&o_done);
+                ++done;
+                pos0 += 2 * n;
+            }
+            if (!ok) fail();
+            // every product has completed before tensor memory is released
             umma_commit(&drained);
             (void)mbar_wait_bounded(&drained, 0u);
         }
         __syncwarp();
     } else {
-        // ------------------------------------------------ K (warp 9) or V (warp 10): a lane a page of a tile
-        const bool is_v = warp == kLoadWarpV;
-        const CUtensorMap *map = is_v ? &p.v : &p.k;
+        // ------------------------------------------------ K and V: a lane a page of a tile
         const int box = min(g.page, kTile), shift = __ffs(g.page) - 1;
-        const int32_t *table = own_b < 0 ? g.prefix_table : g.own_table + static_cast<int64_t>(own_b) * g.own_pages;
-        // the page of this lane's keys of tile j, outside the cache (read as zeros) where it is no page
-        auto page_of = [&](int j) {
-            const int64_t k = key0 + static_cast<int64_t>(j) * kTile + lane * box;
-            if (j >= ntiles || lane * box >= kTile || k >= key1) return -1;
-            const int pg = table[k >> shift];
-            if (pg >= 0 && pg < g.n_pages) return pg;
-            atomicOr(&g_attention_error, kErrIndex);
-            return static_cast<int>(g.n_pages);
-        };
-        int pg = page_of(0), last = -1;
-        for (int j = 0; j < ntiles && !*abort_word; ++j) {
-            const int pos = ring_pos(is_v, j), at = pos % nslots;
-            if (pos >= nslots && !wait_all(&freed[at], static_cast<uint32_t>(pos / nslots - 1) & 1u)) {
-                fail();
-                break;
+        int pos = 0;
+        bool ok = true;
+        for (; id < jobs && ok; id += stride) {
+            const Job job = job_of(p, id, len);
+            len = own_length(p, id + stride);
+            const int32_t *table = job.own_b < 0 ? g.prefix_table : g.own_table + static_cast<int64_t>(job.own_b) * g.own_pages;
+            // the page of this lane's keys of tile t, outside the cache (read as zeros) where it is no page
+            auto page_of = [&](int t) {
+                if (lane * box >= kTile || t * kTile + lane * box >= job.keys) return -1;
+                const int pg = __ldg(table + ((job.key0 + t * kTile + lane * box) >> shift));
+                if (pg >= 0 && pg < g.n_pages) return pg;
+                atomicOr(&g_attention_error, kErrIndex);
+                return static_cast<int>(g.n_pages);
+            };
+            auto load = [&](const CUtensorMap *map, int t, int pg) {
+                const int at = pos % kSlots;
+                if (*abort_word || (pos >= kSlots && !wait_all(&freed[at], full_parity(pos) ^ 1u))) return false;
+                const int boxes = __popc(__ballot_sync(0xffffffffu, pg >= 0));
+                if (lane == 0) mbar_arrive_expect_tx(&full[at], static_cast<uint32_t>(boxes) * box * 128u * kChunks);
+                __syncwarp();
+                if (pg >= 0) {
+                    const int in_page = static_cast<int>((job.key0 + t * kTile + lane * box) & (g.page - 1));
+                    uint8_t *dst = ring + at * kSlotBytes + lane * box * 128;
+#pragma unroll
+                    for (int x = 0; x < kChunks; ++x) tma_load_4d(dst + x * kBlock, map, 64 * x, in_page, job.h, pg, &full[at]);
+                }
+                ++pos;
+                return true;
+            };
+            int pg = job.ntiles > 0 ? page_of(0) : -1, before = -1;
+            for (int t = 0; t < job.ntiles && ok; ++t) {
+                const int next = t + 1 < job.ntiles ? page_of(t + 1) : -1;
+                ok = load(&p.k, t, pg) && (t == 0 || load(&p.v, t - 1, before));
+                before = pg;
+                pg = next;
             }
-            const int boxes = __popc(__ballot_sync(0xffffffffu, pg >= 0));
-            if (lane == 0) mbar_arrive_expect_tx(&full[at], static_cast<uint32_t>(boxes) * box * 128u * kChunks);
-            __syncwarp();
-            if (pg >= 0) {
-                const int64_t k = key0 + static_cast<int64_t>(j) * kTile + lane * box;
-                uint8_t *dst = ring + at * kSlotBytes + lane * box * 128;
-                for (int c = 0; c < kChunks; ++c)
-                    tma_load_4d(dst + c * kBlock, map, 64 * c, static_cast<int>(k & (g.page - 1)), h, pg, &full[at]);
-            }
-            last = j;
-            pg = page_of(j + 1);
+            if (ok && job.ntiles > 0) ok = load(&p.v, job.ntiles - 1, before);
+            if (!ok) fail();
         }
-        // every copy has landed before the CTA can exit: the slots of the last positions are
-        // not used again (after a failure an earlier one may have been, by the other loading
-        // warp; the wait is bounded)
-        for (int j = max(0, last - nslots); j <= last; ++j) {
-            const int pos = ring_pos(is_v, j);
-            if (last + 1 < ntiles || pos > ring_pos(true, ntiles - 1) - nslots)
-                (void)mbar_wait_bounded(&full[pos % nslots], static_cast<uint32_t>(pos / nslots) & 1u);
+        // Every copy lands before the CTA can exit: the products wait for each of them, unless
+        // something gave up; then this warp waits (bounded) for those it last started.
+        if (*abort_word) {
+            for (int x = max(0, pos - kSlots); x < pos; ++x) (void)mbar_wait_bounded(&full[x % kSlots], full_parity(x));
         }
         __syncwarp();
     }
@@ -530,19 +590,35 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const __grid_consta
     float top = -INFINITY;
     for (int k = lane; k < slots; k += 32) top = fmaxf(top, p.lse[k * rows + row]);
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    constexpr int kPer = kD / 32;
+    constexpr int kPer = kD / 32;   // output elements a lane
+    using Vec = std::conditional_t<kPer == 4, float4, float2>;
     float acc[kPer], sum = 0.0f;
 #pragma unroll
     for (int x = 0; x < kPer; ++x) acc[x] = 0.0f;
-    for (int k = 0; k < slots; ++k) {
-        const float lse = p.lse[k * rows + row];
-        if (lse == -INFINITY) continue;
-        const float w = exp2_fast(lse - top);
-        sum += w;
-        const float *o = p.part + (k * rows + row) * kD + lane * kPer;
+    for (int k0 = 0; k0 < slots; k0 += 32) {
+        const float lse = k0 + lane < slots ? p.lse[(k0 + lane) * rows + row] : -INFINITY;
+        const float mine = lse == -INFINITY ? 0.0f : exp2_fast(lse - top);
+        sum += mine;
+        const int n = min(32, slots - k0);
+        for (int k = 0; k < n; k += 4) {   // four partial rows in flight
+            float w[4];
+            Vec v[4];
 #pragma unroll
-        for (int x = 0; x < kPer; ++x) acc[x] = fmaf(w, o[x], acc[x]);
+            for (int u = 0; u < 4; ++u) {
+                w[u] = __shfl_sync(0xffffffffu, mine, (k + u) & 31);
+                if (k + u >= n) w[u] = 0.0f;
+                v[u] = Vec{};
+                if (w[u] != 0.0f) v[u] = *reinterpret_cast<const Vec *>(p.part + ((k0 + k + u) * rows + row) * kD + lane * kPer);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const float *e = reinterpret_cast<const float *>(&v[u]);
+#pragma unroll
+                for (int x = 0; x < kPer; ++x) acc[x] = fmaf(w[u], e[x], acc[x]);
+            }
+        }
     }
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     const float inv = sum > 0.0f || isnan(sum) ? 1.0f / sum : 0.0f;   // no key at all: zeros
     uint32_t *out = reinterpret_cast<uint32_t *>(static_cast<T *>(g.out) + row * kD + lane * kPer);
 #pragma unroll
@@ -560,8 +636,8 @@ cudaError_t encode_cache_map(CUtensorMap *map, const void *cache, const AttnArgs
                          cache, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <typename T, int kD>
-cudaError_t launch_typed(const AttnParams &p, cudaStream_t s)
+template <typename T, int kD, bool kWide>
+cudaError_t launch_typed(const AttnParams &p, int sm_count, cudaStream_t s)
 {
     const AttnArgs &g = p.g;
     cudaLaunchAttribute attr[1];
@@ -570,11 +646,11 @@ cudaError_t launch_typed(const AttnParams &p, cudaStream_t s)
     cfg.attrs = attr;
     const int64_t jobs = p.plan.prefix_jobs + p.plan.own_jobs;
     if (jobs > 0) {
-        auto kern = attention_kernel<T, kD>;
+        auto kern = attention_kernel<T, kD, kWide>;
         cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(kern), kSmemBytes);
         if (e != cudaSuccess) return e;
         cfg.blockDim = dim3(kThreads);
-        cfg.gridDim = dim3(static_cast<unsigned>(jobs));
+        cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(jobs, sm_count)));
         cfg.dynamicSmemBytes = kSmemBytes;
         cfg.numAttrs = set_launch_overlap_attr(attr);
         if ((e = cudaLaunchKernelEx(&cfg, kern, p)) != cudaSuccess) return e;
@@ -606,7 +682,7 @@ int64_t attn_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int64_t prefi
     return part_bytes(plan, B, T, Hq, D) + static_cast<int64_t>(plan.slots) * B * T * Hq * 4;
 }
 
-cudaError_t launch_attention(const DeviceInfo &, const AttnArgs &g, cudaStream_t s)
+cudaError_t launch_attention(const DeviceInfo &dev, const AttnArgs &g, cudaStream_t s)
 {
     route_hit(kRoutePrefixAttention);
     AttnParams p{};
@@ -620,9 +696,14 @@ cudaError_t launch_attention(const DeviceInfo &, const AttnArgs &g, cudaStream_t
         if (e == cudaSuccess) e = encode_cache_map(&p.v, g.v_cache, g);
         if (e != cudaSuccess) return e;
     }
-    if (g.D == 64)
-        return g.type == QMV_F16 ? launch_typed<__half, 64>(p, s) : launch_typed<__nv_bfloat16, 64>(p, s);
-    return g.type == QMV_F16 ? launch_typed<__half, 128>(p, s) : launch_typed<__nv_bfloat16, 128>(p, s);
+    const bool wide = p.plan.pair_groups > 0 || static_cast<int64_t>(g.T) * (g.Hq / g.Hkv) > kTile;
+    auto launch = [&](auto type) {
+        using T = decltype(type);
+        if (g.D == 64)
+            return wide ? launch_typed<T, 64, true>(p, dev.sm_count, s) : launch_typed<T, 64, false>(p, dev.sm_count, s);
+        return wide ? launch_typed<T, 128, true>(p, dev.sm_count, s) : launch_typed<T, 128, false>(p, dev.sm_count, s);
+    };
+    return g.type == QMV_F16 ? launch(__half()) : launch(__nv_bfloat16());
 }
 
 cudaError_t read_error_word_attention(uint32_t *out, bool clear)

@@ -8,6 +8,19 @@
 
 namespace qmv {
 
+// True in one lane of a converged warp. Unlike a test of the lane number it tells the
+// compiler that a single thread goes on, which tensor-core instructions are issued by.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(one)::"memory");
+    return one != 0;
+}
+
 // Shared-memory matrix descriptor of a K-major operand in the 128-byte swizzled
 // layout: rows of 64 fp16 (128 bytes) at a 128-byte pitch, 8-row groups 1024 bytes
 // apart (sbo), the 16-byte chunk c of row r stored at chunk c ^ (r % 8) from a
