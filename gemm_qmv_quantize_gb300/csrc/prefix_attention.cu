@@ -38,8 +38,12 @@ namespace {
 __device__ uint32_t g_attention_error;
 
 constexpr int kTile = 128;              // keys a tile = rows a stream = TMEM lanes
-constexpr int kMmaWarp = 8;
-constexpr int kThreads = 32 * 10;       // two streams of 4 warps, the product warp, the loading warp
+constexpr int kMmaWarp = 8;             // and 9: a thread each issues a stream's products
+constexpr int kLoadWarp = 10;
+constexpr int kThreads = 32 * 12;       // two streams of 4 warps, the product warps, the loading warp, a spare one
+// Registers a thread: the softmax warpgroups hold a row of S each; 256 x 208 + 128 x 80 of
+// the 384 x 168 that the launch has.
+constexpr int kRegsSoftmax = 208, kRegsOther = 80;
 constexpr int kTmemCols = 512;
 constexpr int kMaxSlots = 8;
 constexpr int kSmemBytes = 232448 - 2048;   // dynamic shared memory: a CTA's limit but the barriers and statistics
@@ -203,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     // stream's, or two by the one stream that reads it); s_full / p_full: S, P of a stream's
     // step; q_full: a job's Q is in place; o_done: its products are complete; o_free: its
     // results have been read; merged: stream 1's statistics of a job are there for stream 0
-    __shared__ __align__(8) uint64_t full[kSlots], freed[kSlots], s_full[2], p_full[2], q_full, o_done, o_free, merged, drained;
+    __shared__ __align__(8) uint64_t full[kSlots], freed[kSlots], s_full[2], p_full[2], q_full, o_done, o_free, merged, drained[2];
     __shared__ uint32_t tmem_slot, abort_flag;
     __shared__ float merge_m[kTile], merge_l[kTile];
     volatile uint32_t *abort_word = &abort_flag;
@@ -216,6 +220,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity) ? 1 : 0) != 0;
     };
     auto full_parity = [](int pos) { return static_cast<uint32_t>(pos / kSlots) & 1u; };
+    // Ring position `pos` has landed. A wait is a parity test, right only if the phase
+    // before is known to be over. Where a stream sees half of the tiles, the slot's copy
+    // before may be the other stream's, and late: it is over once its readers have freed
+    // the slot (and the use before that one was, when the loading warp came this far).
+    auto landed = [&](int pos, bool pair) {
+        const int at = pos % kSlots;
+        if (!pair && pos >= kSlots && !mbar_wait_bounded(&freed[at], full_parity(pos) ^ 1u)) return false;
+        return mbar_wait_bounded(&full[at], full_parity(pos));
+    };
 
     if (tid == 0) {
         for (int i = 0; i < kSlots; ++i) {
@@ -227,10 +240,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             mbar_init(&p_full[s], 4);
         }
         mbar_init(&q_full, 8);
-        mbar_init(&o_done, 1);
+        mbar_init(&o_done, 2);
         mbar_init(&o_free, 8);
         mbar_init(&merged, 4);
-        mbar_init(&drained, 1);
+        mbar_init(&drained[0], 1);
+        mbar_init(&drained[1], 1);
         abort_flag = 0u;
         fence_barrier_init();
     }
@@ -250,6 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     int id = static_cast<int>(blockIdx.x);
     int len = own_length(p, id);
     if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
         // ------------------------------------------------ softmax of stream s: a row a thread
         const int s = warp >> 2, r = tid & (kTile - 1);
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
@@ -258,15 +273,22 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         const float c = g.scale * 1.4426950408889634f;
         // row i of key head h is query head h G + i % G of token i / G
         auto q_row = [&](int h, int i) { return static_cast<int64_t>(i / G) * g.Hq + h * G + i % G; };
-        // a job's Q into the K-major swizzled layout (rows past the job's keep what is there:
-        // their S, P and O are never used)
-        auto load_q = [&](const Job &j) {
-            for (int u = tid; u < j.nrows * (kD / 8); u += 256) {
-                const int qr = u / (kD / 8), x = u % (kD / 8);
-                const uint4 v = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(g.q) + q_row(j.h, j.i0 + qr) * kD) + x);
-                *reinterpret_cast<uint4 *>(smem + (qr / kTile) * kSlotBytes + (x / 8) * kBlock + (qr % kTile) * 128 +
-                                           16 * ((x % 8) ^ (qr % 8))) = v;
-            }
+        // A job's Q into the K-major swizzled layout (rows past the job's keep what is there:
+        // their S, P and O are never used). The first 256 of its 16-byte pieces, all of a
+        // decode step's own-key job, are loaded while the job before runs.
+        auto q_piece = [&](const Job &j, int u) {
+            return __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(g.q) + q_row(j.h, j.i0 + u / (kD / 8)) * kD) + u % (kD / 8));
+        };
+        auto put_q = [&](int u, uint4 v) {
+            const int qr = u / (kD / 8), x = u % (kD / 8);
+            *reinterpret_cast<uint4 *>(smem + (qr / kTile) * kSlotBytes + (x / 8) * kBlock + (qr % kTile) * 128 + 16 * ((x % 8) ^ (qr % 8))) = v;
+        };
+        auto has_q = [&](const Job &j) { return j.ntiles > 0 && tid < j.nrows * (kD / 8); };
+        auto load_q = [&](const Job &j, uint4 first) {
+            const int pieces = j.nrows * (kD / 8);
+            if (tid < pieces) put_q(tid, first);
+#pragma unroll 4
+            for (int u = tid + 256; u < pieces; u += 256) put_q(u, q_piece(j, u));
             fence_proxy_async_shared();
             __syncwarp();
             if (lane == 0) mbar_arrive(&q_full);
@@ -275,19 +297,28 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         uint32_t step = 0, done = 0, merges = 0;   // this stream's steps, the jobs with keys and those joined, so far
         bool ok = true;
         Job job = job_of(p, id, len);
-        if (id < jobs && job.ntiles > 0) load_q(job);
+        uint4 first_q = make_uint4(0, 0, 0, 0);
+        if (has_q(job)) first_q = q_piece(job, tid);
+        if (job.ntiles > 0) load_q(job, first_q);
+        int next_len = own_length(p, id + stride);
         while (id < jobs && ok) {
-            const int next_id = id + stride, next_len = own_length(p, next_id);
+            const int next_id = id + stride;
+            Job next = job;
+            next.ntiles = 0;
+            if (next_id < jobs) {
+                next = job_of(p, next_id, next_len);
+                if (has_q(next)) first_q = q_piece(next, tid);
+            }
+            const int after_len = own_length(p, next_id + stride);
             if (job.own_b >= 0 && len > g.max_own && tid == 0) atomicOr(&g_attention_error, kErrIndex);
             const int64_t out_row0 = static_cast<int64_t>(job.slot) * g.B * g.T * g.Hq;
             if (job.ntiles == 0) {   // no key: nothing of these rows in this slot
                 for (int x = tid; x < job.nrows; x += 256) p.lse[out_row0 + q_row(job.h, job.i0 + x)] = -INFINITY;
+                if (next.ntiles > 0) load_q(next, first_q);
                 id = next_id;
                 len = next_len;
-                if (id < jobs) {
-                    job = job_of(p, id, len);
-                    if (job.ntiles > 0) load_q(job);
-                }
+                next_len = after_len;
+                job = next;
                 continue;
             }
             const bool pair = kWide && job.nrows > kTile;
@@ -367,10 +398,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                     tmem_wait_st();
                     tc_fence_before();
                 }
-                if (t == n - 1 && job.keys % kTile != 0 && (!pair || s == 0)) {
+                if (t == n - 1 && job.keys % kTile != 0) {
                     // what lies past the last key may be anything, NaN too: zeros, since 0 x NaN is NaN
+                    // (each stream that reads the tile writes them before its own product)
                     const int pos = pos0 + v_pos(t, n), first = job.keys % kTile;
-                    if (*abort_word || !wait_all(&full[pos % kSlots], full_parity(pos))) {
+                    if (*abort_word || !__all_sync(0xffffffffu, landed(pos, pair) ? 1 : 0)) {
                         fail();
                         ok = false;
                         break;
@@ -395,13 +427,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                 mbar_arrive_n(&freed[(pos0 + v_pos(pair ? n - 1 : 2 * (steps - 1) + s, n)) % kSlots], arrivals);
             pos0 += 2 * n;
             // the next job's Q, so that its first products run beside this job's results
+            if (next.ntiles > 0) load_q(next, first_q);
             id = next_id;
             len = next_len;
-            Job next = job;
-            if (id < jobs) {
-                next = job_of(p, id, len);
-                if (next.ntiles > 0) load_q(next);
-            }
+            next_len = after_len;
             // ---- results; up to 128 rows, the streams hold the same rows: stream 0 takes both parts
             tc_fence_after();
             const bool both = !pair && n > 1;
@@ -427,40 +456,55 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                     m = top;
                 }
                 const float inv = 1.0f / l;
-                const int64_t row = live ? out_row0 + q_row(job.h, job.i0 + rel) : 0;
-                if (live) p.lse[row] = l == 0.0f ? -INFINITY : m - kLift + log2f(l);
+                float o[kD];
 #pragma unroll
-                for (int j = 0; j < kD; j += 16) {
-                    float o[16];
-                    tmem_ld16(o_col + j, o);
-                    if (both) {
-                        float o1[16];
-                        tmem_ld16(o_col + kTile + j, o1);
+                for (int j = 0; j < kD; j += 32) tmem_ld32_async(o_col + j, o + j);
 #pragma unroll
-                        for (int x = 0; x < 16; ++x) o[x] = o[x] * w0 + o1[x] * w1;
+                for (int j = 0; j < kD; j += 32) tmem_wait_ld32(o + j);
+                if (both) {
+#pragma unroll
+                    for (int j = 0; j < kD; j += 32) {
+                        float o1[32];
+                        tmem_ld32_async(o_col + kTile + j, o1);
+                        tmem_wait_ld32(o1);
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) o[j + x] = o[j + x] * w0 + o1[x] * w1;
                     }
-                    if (live && l != 0.0f) {
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&o_free);   // O may be written again
+                if (live) {
+                    const int64_t row = out_row0 + q_row(job.h, job.i0 + rel);
+                    p.lse[row] = l == 0.0f ? -INFINITY : m - kLift + log2f(l);
+                    if (l != 0.0f) {
 #pragma unroll
-                        for (int x = 0; x < 16; x += 4)
-                            *reinterpret_cast<float4 *>(p.part + row * kD + j + x) =
+                        for (int x = 0; x < kD; x += 4)
+                            *reinterpret_cast<float4 *>(p.part + row * kD + x) =
                                 make_float4(o[x] * inv, o[x + 1] * inv, o[x + 2] * inv, o[x + 3] * inv);
                     }
                 }
+            } else {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&o_free);
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&o_free);
             job = next;
         }
-    } else if (warp == kMmaWarp) {
-        // ------------------------------------------------ products: one thread
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    if (warp < kLoadWarp) {
+        // ------------------------------------------------ products of stream s: one thread, in the
+        // order S(0) PV(0) S(1) PV(1) ...; a thread a stream, since what one waits for must not
+        // hold up the other's products
+        const int s = warp - kMmaWarp;
         if (elect_one()) {
             constexpr uint32_t idesc_s = idesc_16bit_f32(kTile, kTile, kBf16, false);
             constexpr uint32_t idesc_o = idesc_16bit_f32(kTile, kD, kBf16, true);
             const uint64_t q_desc = smem_desc_sw128(smem_addr(smem)), k_desc = smem_desc_sw128(smem_addr(ring));
             const uint64_t v_desc = smem_desc_sw128_mn(smem_addr(ring), kBlock);
+            const uint32_t s_tmem = tmem + static_cast<uint32_t>(s * kTile), o_tmem = s_tmem + 256u;
             int pos0 = 0;
-            uint32_t done = 0, step[2] = {0, 0};
+            uint32_t done = 0, step = 0;
             bool ok = true;
             for (; id < jobs && ok; id += stride) {
                 const Job job = job_of(p, id, len);
@@ -468,42 +512,34 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                 const int n = job.ntiles;
                 if (n == 0) continue;
                 const bool pair = kWide && job.nrows > kTile;
-                auto steps_of = [&](int s) { return pair ? n : (n - s + 1) / 2; };
-                auto wait_full = [&](int pos) { return mbar_wait_bounded(&full[pos % kSlots], full_parity(pos)); };
-                auto issue_s = [&](int s, int t) {
-                    const int pos = pos0 + k_pos(t);
-                    if (!wait_full(pos)) return false;
-                    tc_fence_after();
-                    const uint64_t qd = q_desc + (pair && s == 1 ? kSlotBytes >> 4 : 0u);
+                const int steps = pair ? n : (n - s + 1) / 2;
+                const uint64_t qd = q_desc + (pair && s == 1 ? kSlotBytes >> 4 : 0u);
+                auto issue_s = [&](int i) {
+                    const int pos = pos0 + k_pos(pair ? i : 2 * i + s);
                     const uint64_t kd = k_desc + static_cast<uint32_t>(pos % kSlots) * (kSlotBytes >> 4);
+                    if (!landed(pos, pair)) return false;
+                    tc_fence_after();
 #pragma unroll
                     for (int k = 0; k < kD / 16; ++k) {
                         const uint32_t off = (static_cast<uint32_t>(k / 4) * kBlock + 32u * (k % 4)) >> 4;
-                        umma_f16_ss(tmem + static_cast<uint32_t>(s * kTile), qd + off, kd + off, idesc_s, k > 0 ? 1u : 0u);
+                        umma_f16_ss(s_tmem, qd + off, kd + off, idesc_s, k > 0 ? 1u : 0u);
                     }
                     umma_commit(&s_full[s]);
                     return true;
                 };
-                ok = !*abort_word && mbar_wait_bounded(&q_full, done & 1u);
-                for (int s = 0; s < 2 && ok; ++s)
-                    if (steps_of(s) > 0) ok = issue_s(s, s == 0 || pair ? 0 : 1);
+                ok = !*abort_word && mbar_wait_bounded(&q_full, done & 1u) && (steps == 0 || issue_s(0));
                 // the last job's results have been read before O is written again
                 if (ok && done > 0) ok = mbar_wait_bounded(&o_free, (done - 1) & 1u);
-                for (int i = 0; i < steps_of(0) && ok; ++i) {
+                for (int i = 0; i < steps && ok; ++i, ++step) {
+                    const int pos = pos0 + v_pos(pair ? i : 2 * i + s, n);
+                    const uint64_t vd = v_desc + static_cast<uint32_t>(pos % kSlots) * (kSlotBytes >> 4);
+                    ok = landed(pos, pair) && mbar_wait_bounded(&p_full[s], step & 1u) && !*abort_word;
+                    if (!ok) break;
+                    tc_fence_after();
 #pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        if (i >= steps_of(s) || !ok) break;
-                        const int t = pair ? i : 2 * i + s, pos = pos0 + v_pos(t, n);
-                        ok = !*abort_word && wait_full(pos) && mbar_wait_bounded(&p_full[s], step[s]++ & 1u);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint64_t vd = v_desc + static_cast<uint32_t>(pos % kSlots) * (kSlotBytes >> 4);
-#pragma unroll
-                        for (int k = 0; k < kTile / 16; ++k)   // 16 keys: 2048 bytes of V, 8 columns of P
-                            umma_f16_ta(tmem + 256u + static_cast<uint32_t>(s * kTile), tmem + static_cast<uint32_t>(s * kTile) + 8u * k,
-                                        vd + 128u * k, idesc_o, (i > 0 || k > 0) ? 1u : 0u);
-                        if (i + 1 < steps_of(s)) ok = issue_s(s, pair ? t + 1 : t + 2);
-                    }
+                    for (int k = 0; k < kTile / 16; ++k)   // 16 keys: 2048 bytes of V, 8 columns of P
+                        umma_f16_ta(o_tmem, s_tmem + 8u * k, vd + 128u * k, idesc_o, (i > 0 || k > 0) ? 1u : 0u);
+                    if (i + 1 < steps) ok = issue_s(i + 1);
                 }
                 if (ok) umma_commit(&o_done);
                 ++done;
@@ -511,11 +547,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             }
             if (!ok) fail();
             // every product has completed before tensor memory is released
-            umma_commit(&drained);
-            (void)mbar_wait_bounded(&drained, 0u);
+            umma_commit(&drained[s]);
+            (void)mbar_wait_bounded(&drained[s], 0u);
         }
         __syncwarp();
-    } else {
+    } else if (warp == kLoadWarp) {
         // ------------------------------------------------ K and V: a lane a page of a tile
         const int box = min(g.page, kTile), shift = __ffs(g.page) - 1;
         int pos = 0;
@@ -524,21 +560,21 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             const Job job = job_of(p, id, len);
             len = own_length(p, id + stride);
             const int32_t *table = job.own_b < 0 ? g.prefix_table : g.own_table + static_cast<int64_t>(job.own_b) * g.own_pages;
-            // the page of this lane's keys of tile t, outside the cache (read as zeros) where it is no page
-            auto page_of = [&](int t) {
-                if (lane * box >= kTile || t * kTile + lane * box >= job.keys) return -1;
-                const int pg = __ldg(table + ((job.key0 + t * kTile + lane * box) >> shift));
-                if (pg >= 0 && pg < g.n_pages) return pg;
-                atomicOr(&g_attention_error, kErrIndex);
-                return static_cast<int>(g.n_pages);
-            };
+            // the page of this lane's keys of tile t, loaded a tile ahead and looked at when it is used
+            auto has_keys = [&](int t) { return lane * box < kTile && t < job.ntiles && t * kTile + lane * box < job.keys; };
+            auto page_of = [&](int t) { return has_keys(t) ? __ldg(table + ((job.key0 + t * kTile + lane * box) >> shift)) : 0; };
             auto load = [&](const CUtensorMap *map, int t, int pg) {
                 const int at = pos % kSlots;
                 if (*abort_word || (pos >= kSlots && !wait_all(&freed[at], full_parity(pos) ^ 1u))) return false;
-                const int boxes = __popc(__ballot_sync(0xffffffffu, pg >= 0));
+                const bool mine = has_keys(t);
+                const int boxes = __popc(__ballot_sync(0xffffffffu, mine));
                 if (lane == 0) mbar_arrive_expect_tx(&full[at], static_cast<uint32_t>(boxes) * box * 128u * kChunks);
                 __syncwarp();
-                if (pg >= 0) {
+                if (mine) {
+                    if (pg < 0 || pg >= g.n_pages) {   // no page: read past the cache, zeros
+                        atomicOr(&g_attention_error, kErrIndex);
+                        pg = static_cast<int>(g.n_pages);
+                    }
                     const int in_page = static_cast<int>((job.key0 + t * kTile + lane * box) & (g.page - 1));
                     uint8_t *dst = ring + at * kSlotBytes + lane * box * 128;
 #pragma unroll
@@ -547,9 +583,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                 ++pos;
                 return true;
             };
-            int pg = job.ntiles > 0 ? page_of(0) : -1, before = -1;
+            int pg = page_of(0), before = 0;
             for (int t = 0; t < job.ntiles && ok; ++t) {
-                const int next = t + 1 < job.ntiles ? page_of(t + 1) : -1;
+                const int next = page_of(t + 1);
                 ok = load(&p.k, t, pg) && (t == 0 || load(&p.v, t - 1, before));
                 before = pg;
                 pg = next;
@@ -563,6 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             for (int x = max(0, pos - kSlots); x < pos; ++x) (void)mbar_wait_bounded(&full[x % kSlots], full_parity(x));
         }
         __syncwarp();
+    }
     }
     tc_fence_before();
     __syncthreads();
