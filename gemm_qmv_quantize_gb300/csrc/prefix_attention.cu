@@ -39,14 +39,14 @@ __device__ uint32_t g_attention_error;
 
 constexpr int kTile = 128;              // keys a tile = rows a stream = TMEM lanes
 constexpr int kMmaWarp = 8;             // and 9: a thread each issues a stream's products
-constexpr int kLoadWarp = 10;
-constexpr int kThreads = 32 * 12;       // two streams of 4 warps, the product warps, the loading warp, a spare one
-// Registers a thread: the softmax warpgroups hold a row of S each; 256 x 208 + 128 x 80 of
+constexpr int kLoadWarp = 10;            // and 11: each loads half of every tile
+constexpr int kThreads = 32 * 12;       // two streams of 4 warps, the product warps, the loading warps
+// Registers a thread: the softmax warpgroups hold a row of S each; 256 x 224 + 128 x 56 of
 // the 384 x 168 that the launch has.
-constexpr int kRegsSoftmax = 208, kRegsOther = 80;
+constexpr int kRegsSoftmax = 224, kRegsOther = 56;
 constexpr int kTmemCols = 512;
 constexpr int kMaxSlots = 8;
-constexpr int kSmemBytes = 232448 - 2048;   // dynamic shared memory: a CTA's limit but the barriers and statistics
+constexpr int kSmemBytes = 232448 - 3072;   // dynamic shared memory: a CTA's limit but the barriers and statistics
 constexpr int kSms = 152;
 constexpr float kSlack = 8.0f;          // log2 of the growth of a row's maximum that rescales O
 
@@ -99,8 +99,11 @@ struct AttnParams {
     CUtensorMap k, v;    // {D, page, Hkv, pages}: boxes of 64 d x min(page, 128) keys
     AttnArgs g;
     AttnPlan plan;
-    float *part;         // [slots][B T Hq][D], each divided by its sum
-    float *lse;          // [slots][B T Hq], log2 of the sum of exponentials; -inf: no key
+    // Partial results, each divided by its sum: [slots][Hkv][blocks of 32 rows][D / 4][32][4], so
+    // that the 32 threads of a warp, a row each, store whole lines; lse [slots][Hkv][rows], the
+    // log2 of the sum of exponentials; -inf: no key (and no partial result).
+    float *part, *lse;
+    int row_blocks;
 };
 
 __device__ __forceinline__ float exp2_fast(float x)
@@ -108,6 +111,38 @@ __device__ __forceinline__ float exp2_fast(float x)
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// Two fp32 values side by side, one instruction for both.
+__device__ __forceinline__ uint64_t pair_of(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 both_of(uint64_t v)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 
 template <typename T>
@@ -136,7 +171,17 @@ struct Job {
     int own_end;            // own keys: the request's length - key0
 };
 
-// Own keys of a request, cut to the caller's bound.
+// A bounded wait in few instructions (mbar_wait_bounded reads the clock too): a poll of a
+// phase that is not complete returns after some microseconds, so the bound is about a second.
+__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity)
+{
+#pragma unroll 1
+    for (int i = 0; i < 1 << 18; ++i)
+        if (mbar_try_wait_sleep(bar, parity, 1000000u)) return true;
+    return false;
+}
+
+// The length of job `id`'s request, where it has own keys.
 __device__ __forceinline__ int own_length(const AttnParams &p, int id)
 {
     if (id < p.plan.prefix_jobs || id >= p.plan.prefix_jobs + p.plan.own_jobs) return 0;
@@ -144,7 +189,9 @@ __device__ __forceinline__ int own_length(const AttnParams &p, int id)
     return __ldg(p.g.own_len + b);
 }
 
-// Job `id`; len: own_length of it (loaded ahead).
+// Job `id`; len: own_length of it (loaded ahead). (What runs once a job has one place in
+// the code and is not unrolled: a launch finds little of its code in the caches, since the keys pass
+// through them, and fetches it at about a microsecond a miss.)
 __device__ __forceinline__ Job job_of(const AttnParams &p, int id, int len)
 {
     const AttnArgs &g = p.g;
@@ -190,6 +237,40 @@ __device__ __forceinline__ Job job_of(const AttnParams &p, int id, int len)
     return j;
 }
 
+// Piece u (16 bytes) of the Q of rows i0 ... of key head h: row i is query head h G + i % G
+// of token i / G.
+template <int kD>
+__device__ __forceinline__ uint4 q_piece(const AttnArgs &g, int h, int i0, int u)
+{
+    const int G = g.Hq / g.Hkv, i = i0 + u / (kD / 8);
+    const int64_t row = static_cast<int64_t>(i / G) * g.Hq + h * G + i % G;
+    return __ldg(static_cast<const uint4 *>(g.q) + row * (kD / 8) + u % (kD / 8));
+}
+
+// nrows of Q into the K-major swizzled layout, by 256 threads, their first pieces at hand.
+// (Rows past these keep what is there: their S, P and O are never used.)
+template <int kD>
+__device__ __forceinline__ void store_q(uint8_t *smem, const AttnArgs &g, int h, int i0, int nrows, int tid, uint4 first)
+{
+    const int pieces = nrows * (kD / 8);
+    auto put = [&](int u, uint4 v) {
+        const int r = u / (kD / 8), x = u % (kD / 8);
+        *reinterpret_cast<uint4 *>(smem + (r / kTile) * (kTile * kD * 2) + (x / 8) * (kTile * 128) + (r % kTile) * 128 +
+                                   16 * ((x % 8) ^ (r % 8))) = v;
+    };
+    if (tid < pieces) put(tid, first);
+#pragma unroll 1
+    for (int u = tid + 256; u < pieces; u += 5 * 256) {   // (256 rows: three rounds of five loads)
+        uint4 v[5];
+#pragma unroll
+        for (int x = 0; x < 5; ++x)
+            if (u + 256 * x < pieces) v[x] = q_piece<kD>(g, h, i0, u + 256 * x);
+#pragma unroll
+        for (int x = 0; x < 5; ++x)
+            if (u + 256 * x < pieces) put(u + 256 * x, v[x]);
+    }
+}
+
 // kWide: the launch has jobs of more than 128 rows (two Q tiles, one slot less).
 template <typename T, int kD, bool kWide>
 __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_constant__ AttnParams p)
@@ -206,18 +287,20 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     // full: a slot's copies have landed; freed: its readers are done (two arrivals: each
     // stream's, or two by the one stream that reads it); s_full / p_full: S, P of a stream's
     // step; q_full: a job's Q is in place; o_done: its products are complete; o_free: its
-    // results have been read; merged: stream 1's statistics of a job are there for stream 0
-    __shared__ __align__(8) uint64_t full[kSlots], freed[kSlots], s_full[2], p_full[2], q_full, o_done, o_free, merged, drained[2];
+    // results have been read; merged: the streams' statistics of a job are there for one another;
+    // turn: the other stream's products have been issued
+    __shared__ __align__(8) uint64_t full[kSlots], freed[kSlots], s_full[2], p_full[2], q_full, o_done, o_free, merged, turn[2], drained[2];
     __shared__ uint32_t tmem_slot, abort_flag;
-    __shared__ float merge_m[kTile], merge_l[kTile];
+    __shared__ float merge_m[2][kTile], merge_l[2][kTile];
     volatile uint32_t *abort_word = &abort_flag;
     uint8_t *ring = smem + kQBytes;
     const AttnArgs &g = p.g;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // (the product and loading warps are the CTA's first)
+    const int tid = (threadIdx.x + 256) % kThreads, warp = tid >> 5, lane = tid & 31;
     const int G = g.Hq / g.Hkv, jobs = static_cast<int>(p.plan.prefix_jobs + p.plan.own_jobs), stride = static_cast<int>(gridDim.x);
     auto fail = [&]() { note_wait_timeout(&g_attention_error, abort_word); };
     auto wait_all = [&](uint64_t *bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity) ? 1 : 0) != 0;
+        return __all_sync(0xffffffffu, wait_for(bar, parity) ? 1 : 0) != 0;
     };
     auto full_parity = [](int pos) { return static_cast<uint32_t>(pos / kSlots) & 1u; };
     // Ring position `pos` has landed. A wait is a parity test, right only if the phase
@@ -226,13 +309,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     // the slot (and the use before that one was, when the loading warp came this far).
     auto landed = [&](int pos, bool pair) {
         const int at = pos % kSlots;
-        if (!pair && pos >= kSlots && !mbar_wait_bounded(&freed[at], full_parity(pos) ^ 1u)) return false;
-        return mbar_wait_bounded(&full[at], full_parity(pos));
+        if (!pair && pos >= kSlots && !wait_for(&freed[at], full_parity(pos) ^ 1u)) return false;
+        return wait_for(&full[at], full_parity(pos));
     };
 
     if (tid == 0) {
         for (int i = 0; i < kSlots; ++i) {
-            mbar_init(&full[i], 1);
+            mbar_init(&full[i], 2);
             mbar_init(&freed[i], 2);
         }
         for (int s = 0; s < 2; ++s) {
@@ -242,7 +325,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         mbar_init(&q_full, 8);
         mbar_init(&o_done, 2);
         mbar_init(&o_free, 8);
-        mbar_init(&merged, 4);
+        mbar_init(&merged, 8);
+        mbar_init(&turn[0], 1);
+        mbar_init(&turn[1], 1);
         mbar_init(&drained[0], 1);
         mbar_init(&drained[1], 1);
         abort_flag = 0u;
@@ -271,61 +356,28 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         const uint32_t s_col = tmem + lanes + static_cast<uint32_t>(s * kTile);
         const uint32_t o_col = tmem + lanes + 256u + static_cast<uint32_t>(s * kTile);
         const float c = g.scale * 1.4426950408889634f;
-        // row i of key head h is query head h G + i % G of token i / G
-        auto q_row = [&](int h, int i) { return static_cast<int64_t>(i / G) * g.Hq + h * G + i % G; };
-        // A job's Q into the K-major swizzled layout (rows past the job's keep what is there:
-        // their S, P and O are never used). The first 256 of its 16-byte pieces, all of a
-        // decode step's own-key job, are loaded while the job before runs.
-        auto q_piece = [&](const Job &j, int u) {
-            return __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(g.q) + q_row(j.h, j.i0 + u / (kD / 8)) * kD) + u % (kD / 8));
-        };
-        auto put_q = [&](int u, uint4 v) {
-            const int qr = u / (kD / 8), x = u % (kD / 8);
-            *reinterpret_cast<uint4 *>(smem + (qr / kTile) * kSlotBytes + (x / 8) * kBlock + (qr % kTile) * 128 + 16 * ((x % 8) ^ (qr % 8))) = v;
-        };
+        // The first 256 16-byte pieces of a job's Q, all of a decode step's own-key job, are
+        // loaded while the job before ends.
         auto has_q = [&](const Job &j) { return j.ntiles > 0 && tid < j.nrows * (kD / 8); };
         auto load_q = [&](const Job &j, uint4 first) {
-            const int pieces = j.nrows * (kD / 8);
-            if (tid < pieces) put_q(tid, first);
-#pragma unroll 4
-            for (int u = tid + 256; u < pieces; u += 256) put_q(u, q_piece(j, u));
+            store_q<kD>(smem, g, j.h, j.i0, j.nrows, tid, first);
             fence_proxy_async_shared();
             __syncwarp();
             if (lane == 0) mbar_arrive(&q_full);
         };
         int pos0 = 0;            // ring positions before this job's
         uint32_t step = 0, done = 0, merges = 0;   // this stream's steps, the jobs with keys and those joined, so far
-        bool ok = true;
-        Job job = job_of(p, id, len);
-        uint4 first_q = make_uint4(0, 0, 0, 0);
-        if (has_q(job)) first_q = q_piece(job, tid);
-        if (job.ntiles > 0) load_q(job, first_q);
-        int next_len = own_length(p, id + stride);
-        while (id < jobs && ok) {
-            const int next_id = id + stride;
-            Job next = job;
-            next.ntiles = 0;
-            if (next_id < jobs) {
-                next = job_of(p, next_id, next_len);
-                if (has_q(next)) first_q = q_piece(next, tid);
-            }
-            const int after_len = own_length(p, next_id + stride);
-            if (job.own_b >= 0 && len > g.max_own && tid == 0) atomicOr(&g_attention_error, kErrIndex);
-            const int64_t out_row0 = static_cast<int64_t>(job.slot) * g.B * g.T * g.Hq;
-            if (job.ntiles == 0) {   // no key: nothing of these rows in this slot
-                for (int x = tid; x < job.nrows; x += 256) p.lse[out_row0 + q_row(job.h, job.i0 + x)] = -INFINITY;
-                if (next.ntiles > 0) load_q(next, first_q);
-                id = next_id;
-                len = next_len;
-                next_len = after_len;
-                job = next;
-                continue;
-            }
+        bool ok = true, running = false;
+        Job job{};
+        // A turn: the steps of a job; the next job's Q, so that its first products run beside
+        // this job's results; these.
+        for (;;) {
             const bool pair = kWide && job.nrows > kTile;
-            const int n = job.ntiles, steps = pair ? n : (n - s + 1) / 2;
+            const int n = job.ntiles, steps = !running ? 0 : pair ? n : (n - s + 1) / 2;
             const int rel = pair ? s * kTile + r : r;   // row within the job
             const bool live = rel < job.nrows;
             const bool warp_live = (pair ? s * kTile : 0) + (r & ~31) < job.nrows;   // any row of this warp
+            const int64_t out_row0 = (static_cast<int64_t>(job.slot) * g.Hkv + job.h) * p.row_blocks * 32 + job.i0;
             // keys of this row: all of the prefix's, or its request's up to its own token; and the fewest of any row
             const int limit = job.own_b < 0 ? job.keys : min(job.keys, job.own_end - g.T + 1 + (job.i0 + rel) / G % g.T);
             const int least = job.own_b < 0 ? job.keys : min(job.keys, job.own_end - g.T + 1);
@@ -344,22 +396,33 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                 }
                 if (warp_live) {
                     tc_fence_after();
+                    if (least - t * kTile < kTile) {   // the last tile, or the request's own tokens
+                        const int x = limit - t * kTile;
+#pragma unroll 1
+                        for (int j = 0; j < kTile; j += 16) {
+                            float o[16];
+                            tmem_ld16(s_col + j, o);
+                            uint32_t w[16];
+#pragma unroll
+                            for (int y = 0; y < 16; ++y) w[y] = __float_as_uint(j + y < x ? o[y] : -INFINITY);
+                            tmem_st16(s_col + j, w);
+                        }
+                        tmem_wait_st();
+                    }
                     float v[kTile];
 #pragma unroll
                     for (int j = 0; j < kTile; j += 32) tmem_ld32_async(s_col + j, v + j);
 #pragma unroll
                     for (int j = 0; j < kTile; j += 32) tmem_wait_ld32(v + j);
-                    if (least - t * kTile < kTile) {
-                        const int x = limit - t * kTile;
-#pragma unroll
-                        for (int j = 0; j < kTile; ++j)
-                            if (j >= x) v[j] = -INFINITY;
-                    }
                     float top[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) top[j] = v[j];
 #pragma unroll
-                    for (int j = 4; j < kTile; ++j) top[j & 3] = fmaxf(top[j & 3], v[j]);
+                    for (int j = 4; j < kTile - 4; j += 8)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) top[x] = max3(top[x], v[j + 2 * x], v[j + 2 * x + 1]);
+#pragma unroll
+                    for (int j = kTile - 4; j < kTile; ++j) top[j & 3] = fmaxf(top[j & 3], v[j]);
                     const float best = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
                     const bool grow = best > m + kSlack;   // (m = -inf: the row's first keys)
                     if (__any_sync(0xffffffffu, grow)) {
@@ -369,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                         m = next;
                         // the sums so far are complete: S of this step was issued after P V of the last
                         if (i > 0) {
-#pragma unroll
+#pragma unroll 1
                             for (int j = 0; j < kD; j += 16) {
                                 float o[16];
                                 tmem_ld16(o_col + j, o);
@@ -380,21 +443,23 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                             }
                         }
                     }
-                    const float shift = (m == -INFINITY ? 0.0f : m) - kLift;
-                    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    const float shift = kLift - (m == -INFINITY ? 0.0f : m);
+                    const uint64_t shift2 = pair_of(shift, shift), c2 = pair_of(c, c);
+                    uint64_t sum[2] = {0, 0};
 #pragma unroll
                     for (int q = 0; q < kTile; q += 32) {
                         uint32_t w[16];
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
-                            const float a = exp2_fast(fmaf(v[q + 2 * j], c, -shift));
-                            const float b = exp2_fast(fmaf(v[q + 2 * j + 1], c, -shift));
-                            sum[j & 3] += a + b;
+                            const float2 x = both_of(fma_pair(pair_of(v[q + 2 * j], v[q + 2 * j + 1]), c2, shift2));
+                            const float a = exp2_fast(x.x), b = exp2_fast(x.y);
+                            sum[j & 1] = add_pair(sum[j & 1], pair_of(a, b));
                             w[j] = pack2<T>(a, b);
                         }
                         tmem_st16(s_col + q / 2, w);
                     }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    const float2 sums = both_of(add_pair(sum[0], sum[1]));
+                    l += sums.x + sums.y;
                     tmem_wait_st();
                     tc_fence_before();
                 }
@@ -417,78 +482,87 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[s]);
             }
-            if (ok && (*abort_word || !wait_all(&o_done, done & 1u))) {
-                fail();
-                ok = false;
+            Job next{};
+            uint4 first_q{};
+            if (id < jobs) {   // (while this job's last products run)
+                next = job_of(p, id, len);
+                if (has_q(next)) first_q = q_piece<kD>(g, next.h, next.i0, tid);
+                if (next.own_b >= 0 && len > g.max_own && tid == 0) atomicOr(&g_attention_error, kErrIndex);
             }
-            if (!ok) break;
-            ++done;
-            if (steps > 0 && (warp & 3) == 0 && lane == 0)
-                mbar_arrive_n(&freed[(pos0 + v_pos(pair ? n - 1 : 2 * (steps - 1) + s, n)) % kSlots], arrivals);
-            pos0 += 2 * n;
-            // the next job's Q, so that its first products run beside this job's results
+            if (running) {
+                if (ok && (*abort_word || !wait_all(&o_done, done & 1u))) {
+                    fail();
+                    ok = false;
+                }
+                if (!ok) break;
+                ++done;
+                if (steps > 0 && (warp & 3) == 0 && lane == 0)
+                    mbar_arrive_n(&freed[(pos0 + v_pos(pair ? n - 1 : 2 * (steps - 1) + s, n)) % kSlots], arrivals);
+                pos0 += 2 * n;
+            }
             if (next.ntiles > 0) load_q(next, first_q);
-            id = next_id;
-            len = next_len;
-            next_len = after_len;
-            // ---- results; up to 128 rows, the streams hold the same rows: stream 0 takes both parts
-            tc_fence_after();
-            const bool both = !pair && n > 1;
-            if (both) {
-                if (s == 1) {
-                    merge_m[r] = m;
-                    merge_l[r] = l;
+            if (running) {
+                // ---- results: O / l and the log2 of the sum. Up to 128 rows, both streams hold the
+                // same rows: each joins both parts for half of D.
+                tc_fence_after();
+                float w0 = 1.0f, w1 = 0.0f;
+                if (!pair) {
+                    merge_m[s][r] = m;
+                    merge_l[s][r] = l;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&merged);
-                } else if (!wait_all(&merged, merges & 1u)) {
-                    fail();
-                    break;
-                }
-                ++merges;
-            }
-            if (warp_live && (pair || s == 0)) {
-                float w0 = 1.0f, w1 = 0.0f;
-                if (both) {
-                    const float m1 = merge_m[r], top = fmaxf(m, m1);
-                    w0 = m == -INFINITY ? 0.0f : exp2_fast(m - top);
-                    w1 = m1 == -INFINITY ? 0.0f : exp2_fast(m1 - top);
-                    l = l * w0 + merge_l[r] * w1;
-                    m = top;
-                }
-                const float inv = 1.0f / l;
-                float o[kD];
-#pragma unroll
-                for (int j = 0; j < kD; j += 32) tmem_ld32_async(o_col + j, o + j);
-#pragma unroll
-                for (int j = 0; j < kD; j += 32) tmem_wait_ld32(o + j);
-                if (both) {
-#pragma unroll
-                    for (int j = 0; j < kD; j += 32) {
-                        float o1[32];
-                        tmem_ld32_async(o_col + kTile + j, o1);
-                        tmem_wait_ld32(o1);
-#pragma unroll
-                        for (int x = 0; x < 32; ++x) o[j + x] = o[j + x] * w0 + o1[x] * w1;
+                    if (!wait_all(&merged, merges & 1u)) {
+                        fail();
+                        break;
                     }
+                    ++merges;
+                    const float m0 = merge_m[0][r], m1 = merge_m[1][r];
+                    m = fmaxf(m0, m1);
+                    w0 = m0 == -INFINITY ? 0.0f : exp2_fast(m0 - m);
+                    w1 = m1 == -INFINITY ? 0.0f : exp2_fast(m1 - m);
+                    l = merge_l[0][r] * w0 + merge_l[1][r] * w1;
+                }
+                if (warp_live) {
+                    const bool both = !pair && n > 1;
+                    const int d0 = pair ? 0 : s * (kD / 2), d1 = pair ? kD : d0 + kD / 2;
+                    const float inv = 1.0f / l;
+                    w0 *= inv;
+                    w1 *= inv;
+                    const int64_t row = out_row0 + rel;
+                    float4 *dst = reinterpret_cast<float4 *>(p.part) + (row >> 5) * (8 * kD) + (row & 31);
+                    const uint32_t col = pair ? o_col : tmem + lanes + 256u;
+#pragma unroll 1
+                    for (int j = d0; j < d1; j += 32) {
+                        float o[32], o1[32];
+                        tmem_ld32_async(col + j, o);
+                        if (both) tmem_ld32_async(col + kTile + j, o1);
+                        tmem_wait_ld32(o);
+                        if (both) tmem_wait_ld32(o1);
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) {
+                            o[x] *= w0;
+                            if (both) o[x] = fmaf(o1[x], w1, o[x]);
+                        }
+                        if (live && l != 0.0f) {
+#pragma unroll
+                            for (int x = 0; x < 8; ++x) dst[(j / 4 + x) * 32] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+                        }
+                    }
+                    if (live && (pair || s == 0)) p.lse[row] = l == 0.0f ? -INFINITY : m - kLift + log2f(l);
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&o_free);   // O may be written again
-                if (live) {
-                    const int64_t row = out_row0 + q_row(job.h, job.i0 + rel);
-                    p.lse[row] = l == 0.0f ? -INFINITY : m - kLift + log2f(l);
-                    if (l != 0.0f) {
-#pragma unroll
-                        for (int x = 0; x < kD; x += 4)
-                            *reinterpret_cast<float4 *>(p.part + row * kD + x) =
-                                make_float4(o[x] * inv, o[x + 1] * inv, o[x + 2] * inv, o[x + 3] * inv);
-                    }
-                }
-            } else {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&o_free);
             }
+            if (id >= jobs) break;
             job = next;
+            running = job.ntiles > 0;
+            id += stride;
+            len = own_length(p, id);
+            if (!running) {   // no key: nothing of these rows in this slot
+                float *lse = p.lse + (static_cast<int64_t>(job.slot) * g.Hkv + job.h) * p.row_blocks * 32 + job.i0;
+                for (int x = tid; x < job.nrows; x += 256) lse[x] = -INFINITY;
+            }
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
@@ -504,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             const uint64_t v_desc = smem_desc_sw128_mn(smem_addr(ring), kBlock);
             const uint32_t s_tmem = tmem + static_cast<uint32_t>(s * kTile), o_tmem = s_tmem + 256u;
             int pos0 = 0;
-            uint32_t done = 0, step = 0;
+            uint32_t done = 0, step = 0, turns = 0;
             bool ok = true;
             for (; id < jobs && ok; id += stride) {
                 const Job job = job_of(p, id, len);
@@ -514,32 +588,42 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                 const bool pair = kWide && job.nrows > kTile;
                 const int steps = pair ? n : (n - s + 1) / 2;
                 const uint64_t qd = q_desc + (pair && s == 1 ? kSlotBytes >> 4 : 0u);
-                auto issue_s = [&](int i) {
-                    const int pos = pos0 + k_pos(pair ? i : 2 * i + s);
-                    const uint64_t kd = k_desc + static_cast<uint32_t>(pos % kSlots) * (kSlotBytes >> 4);
-                    if (!landed(pos, pair)) return false;
-                    tc_fence_after();
+                auto k_at = [&](int i) { return pos0 + k_pos(pair ? i : 2 * i + s); };
+                ok = !*abort_word && wait_for(&q_full, done & 1u);
+#pragma unroll 1
+                for (int i = -1; i < steps && ok; ++i) {
+                    ok = i + 1 >= steps || landed(k_at(i + 1), pair);
+                    if (i >= 0 && ok) {
+                        const int pos = pos0 + v_pos(pair ? i : 2 * i + s, n);
+                        const uint64_t vd = v_desc + static_cast<uint32_t>(pos % kSlots) * (kSlotBytes >> 4);
+                        ok = landed(pos, pair) && !*abort_word;
+                        // the last job's results have been read before O is written again
+                        if (ok && i == 0 && done > 0) ok = wait_for(&o_free, (done - 1) & 1u);
+                        // Two streams over the same tiles take turns: their products, mixed, would
+                        // end together, and then their exponentials would run together.
+                        if (ok && pair) {
+                            if (s == 1 || turns > 0) ok = wait_for(&turn[s], (turns + s - 1) & 1u);
+                            ++turns;
+                        }
+                        ok = ok && wait_for(&p_full[s], step & 1u);
+                        ++step;
+                        if (!ok) break;
+                        tc_fence_after();
 #pragma unroll
-                    for (int k = 0; k < kD / 16; ++k) {
-                        const uint32_t off = (static_cast<uint32_t>(k / 4) * kBlock + 32u * (k % 4)) >> 4;
-                        umma_f16_ss(s_tmem, qd + off, kd + off, idesc_s, k > 0 ? 1u : 0u);
+                        for (int k = 0; k < kTile / 16; ++k)   // 16 keys: 2048 bytes of V, 8 columns of P
+                            umma_f16_ta(o_tmem, s_tmem + 8u * k, vd + 128u * k, idesc_o, (i > 0 || k > 0) ? 1u : 0u);
                     }
-                    umma_commit(&s_full[s]);
-                    return true;
-                };
-                ok = !*abort_word && mbar_wait_bounded(&q_full, done & 1u) && (steps == 0 || issue_s(0));
-                // the last job's results have been read before O is written again
-                if (ok && done > 0) ok = mbar_wait_bounded(&o_free, (done - 1) & 1u);
-                for (int i = 0; i < steps && ok; ++i, ++step) {
-                    const int pos = pos0 + v_pos(pair ? i : 2 * i + s, n);
-                    const uint64_t vd = v_desc + static_cast<uint32_t>(pos % kSlots) * (kSlotBytes >> 4);
-                    ok = landed(pos, pair) && mbar_wait_bounded(&p_full[s], step & 1u) && !*abort_word;
-                    if (!ok) break;
-                    tc_fence_after();
+                    if (i + 1 < steps && ok) {
+                        const uint64_t kd = k_desc + static_cast<uint32_t>(k_at(i + 1) % kSlots) * (kSlotBytes >> 4);
+                        tc_fence_after();
 #pragma unroll
-                    for (int k = 0; k < kTile / 16; ++k)   // 16 keys: 2048 bytes of V, 8 columns of P
-                        umma_f16_ta(o_tmem, s_tmem + 8u * k, vd + 128u * k, idesc_o, (i > 0 || k > 0) ? 1u : 0u);
-                    if (i + 1 < steps) ok = issue_s(i + 1);
+                        for (int k = 0; k < kD / 16; ++k) {
+                            const uint32_t off = (static_cast<uint32_t>(k / 4) * kBlock + 32u * (k % 4)) >> 4;
+                            umma_f16_ss(s_tmem, qd + off, kd + off, idesc_s, k > 0 ? 1u : 0u);
+                        }
+                        umma_commit(&s_full[s]);
+                    }
+                    if (i >= 0 && pair) mbar_arrive(&turn[1 - s]);
                 }
                 if (ok) umma_commit(&o_done);
                 ++done;
@@ -548,55 +632,60 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             if (!ok) fail();
             // every product has completed before tensor memory is released
             umma_commit(&drained[s]);
-            (void)mbar_wait_bounded(&drained[s], 0u);
+            (void)wait_for(&drained[s], 0u);
         }
         __syncwarp();
-    } else if (warp == kLoadWarp) {
-        // ------------------------------------------------ K and V: a lane a page of a tile
-        const int box = min(g.page, kTile), shift = __ffs(g.page) - 1;
+    } else {
+        // ------------------------------------------------ K and V: warp 10 loads the first, warp 11
+        // the second 64 elements of each row (64-wide heads: the even and the odd pages); a
+        // warp's copies of a tile took about 500 cycles to issue, as long as a tile may take
+        const int box = min(g.page, kTile), shift = __ffs(g.page) - 1, half = warp - kLoadWarp;
+        constexpr int kFirst = kChunks == 1 ? 1 : 0, kStep = kChunks == 1 ? 2 : 1;   // pages of a warp
         int pos = 0;
         bool ok = true;
         for (; id < jobs && ok; id += stride) {
             const Job job = job_of(p, id, len);
             len = own_length(p, id + stride);
             const int32_t *table = job.own_b < 0 ? g.prefix_table : g.own_table + static_cast<int64_t>(job.own_b) * g.own_pages;
-            // the page of this lane's keys of tile t, loaded a tile ahead and looked at when it is used
-            auto has_keys = [&](int t) { return lane * box < kTile && t < job.ntiles && t * kTile + lane * box < job.keys; };
-            auto page_of = [&](int t) { return has_keys(t) ? __ldg(table + ((job.key0 + t * kTile + lane * box) >> shift)) : 0; };
-            auto load = [&](const CUtensorMap *map, int t, int pg) {
-                const int at = pos % kSlots;
-                if (*abort_word || (pos >= kSlots && !wait_all(&freed[at], full_parity(pos) ^ 1u))) return false;
-                const bool mine = has_keys(t);
-                const int boxes = __popc(__ballot_sync(0xffffffffu, mine));
-                if (lane == 0) mbar_arrive_expect_tx(&full[at], static_cast<uint32_t>(boxes) * box * 128u * kChunks);
-                __syncwarp();
-                if (mine) {
-                    if (pg < 0 || pg >= g.n_pages) {   // no page: read past the cache, zeros
-                        atomicOr(&g_attention_error, kErrIndex);
-                        pg = static_cast<int>(g.n_pages);
-                    }
-                    const int in_page = static_cast<int>((job.key0 + t * kTile + lane * box) & (g.page - 1));
-                    uint8_t *dst = ring + at * kSlotBytes + lane * box * 128;
-#pragma unroll
-                    for (int x = 0; x < kChunks; ++x) tma_load_4d(dst + x * kBlock, map, 64 * x, in_page, job.h, pg, &full[at]);
+            // lane b has the page of a tile's b-th `box` keys, loaded a tile ahead
+            auto pages_of = [&](int t) { return t < job.ntiles ? (min(kTile, job.keys - t * kTile) + box - 1) / box : 0; };
+            auto page_of = [&](int t) { return lane < pages_of(t) ? __ldg(table + ((job.key0 + t * kTile + lane * box) >> shift)) : 0; };
+            int pg = page_of(0), last = 0, before = 0;   // of the next tile of K, the last one and the one before
+#pragma unroll 1
+            for (int q = 0; q < 2 * job.ntiles; ++q, ++pos) {   // K0 K1 V0 K2 V1 ...
+                const bool v = (q > 0 && q % 2 == 0) || q == 2 * job.ntiles - 1;
+                const int t = !v ? (q + 1) / 2 : q % 2 == 0 ? q / 2 - 1 : job.ntiles - 1;
+                if (!v) {
+                    before = last;
+                    last = pg;
+                    pg = page_of(t + 1);
                 }
-                ++pos;
-                return true;
-            };
-            int pg = page_of(0), before = 0;
-            for (int t = 0; t < job.ntiles && ok; ++t) {
-                const int next = page_of(t + 1);
-                ok = load(&p.k, t, pg) && (t == 0 || load(&p.v, t - 1, before));
-                before = pg;
-                pg = next;
+                int mine = v && q % 2 == 0 ? before : last;
+                const int at = pos % kSlots, pages = pages_of(t);
+                if (*abort_word || (pos >= kSlots && !wait_all(&freed[at], full_parity(pos) ^ 1u))) {
+                    ok = false;
+                    break;
+                }
+                if (mine < 0 || mine >= g.n_pages) {   // no page: read past the cache, zeros
+                    atomicOr(&g_attention_error, kErrIndex);
+                    mine = static_cast<int>(g.n_pages);
+                }
+                const int first = kFirst * half, boxes = max((pages - first + kStep - 1) / kStep, 0);
+                if (elect_one()) mbar_arrive_expect_tx(&full[at], static_cast<uint32_t>(boxes) * box * 128u);
+                const int in_page = static_cast<int>((job.key0 + t * kTile) & (g.page - 1));   // (0 but for pages of 256)
+                uint8_t *dst = ring + at * kSlotBytes + (kChunks == 1 ? 0 : half * kBlock);
+#pragma unroll 1
+                for (int b = first; b < pages; b += kStep) {
+                    const int page = __shfl_sync(0xffffffffu, mine, b);
+                    if (elect_one()) tma_load_4d(dst + b * box * 128, v ? &p.v : &p.k, kChunks == 1 ? 0 : 64 * half, in_page, job.h, page, &full[at]);
+                }
             }
-            if (ok && job.ntiles > 0) ok = load(&p.v, job.ntiles - 1, before);
             if (!ok) fail();
         }
         // Every copy lands before the CTA can exit: the products wait for each of them, unless
         // something gave up; then this warp waits (bounded) for those it last started.
         if (*abort_word) {
-            for (int x = max(0, pos - kSlots); x < pos; ++x) (void)mbar_wait_bounded(&full[x % kSlots], full_parity(x));
+            for (int x = max(0, pos - kSlots); x < pos; ++x) (void)wait_for(&full[x % kSlots], full_parity(x));
         }
         __syncwarp();
     }
@@ -609,57 +698,58 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     }
 }
 
-// Joins a row's partial results, one warp a row: weights 2^(lse - max) over their sum.
+// Joins the partial results of 32 rows of a key head, a row a lane and 8 of D a warp:
+// weights 2^(lse - max) over their sum. Four slots are in flight: the 14 of a 64-request
+// batch behind 65536 keys take four rounds of memory latency.
 template <typename T, int kD>
-__global__ void __launch_bounds__(256) attention_join_kernel(const __grid_constant__ AttnParams p)
+__global__ void __launch_bounds__(32 * kD / 8) attention_join_kernel(const __grid_constant__ AttnParams p)
 {
     const AttnArgs &g = p.g;
-    const int lane = threadIdx.x & 31;
-    const int64_t rows = static_cast<int64_t>(g.B) * g.T * g.Hq, row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31, d0 = static_cast<int>(threadIdx.x >> 5) * 8;
+    const int block = static_cast<int>(blockIdx.x) % p.row_blocks, h = static_cast<int>(blockIdx.x) / p.row_blocks;
+    const int G = g.Hq / g.Hkv, i = block * 32 + lane;
     grid_launch_dependents();
     grid_dependency_wait();
-    if (row >= rows) return;
-    // this row's prefix slots: those of its row group
-    const int G = g.Hq / g.Hkv;
-    const int64_t i = row / g.Hq * G + row % G;
-    const bool in_pair = i < static_cast<int64_t>(p.plan.pair_groups) * 2 * kTile;
-    const int slots = p.plan.own_splits + (in_pair ? p.plan.pair_splits : p.plan.lone_splits);
+    if (i >= g.B * g.T * G) return;
+    // these rows' prefix slots: those of their row group
+    const int slots = p.plan.own_splits + (i < p.plan.pair_groups * 2 * kTile ? p.plan.pair_splits : p.plan.lone_splits);
+    const int64_t per_slot = static_cast<int64_t>(g.Hkv) * p.row_blocks * 32;
+    const float *lse = p.lse + static_cast<int64_t>(h) * p.row_blocks * 32 + i;
+    const float4 *part = reinterpret_cast<const float4 *>(p.part) + (static_cast<int64_t>(h) * p.row_blocks + block) * 8 * kD + d0 * 8 + lane;
     float top = -INFINITY;
-    for (int k = lane; k < slots; k += 32) top = fmaxf(top, p.lse[k * rows + row]);
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    constexpr int kPer = kD / 32;   // output elements a lane
-    using Vec = std::conditional_t<kPer == 4, float4, float2>;
-    float acc[kPer], sum = 0.0f;
+#pragma unroll 4
+    for (int k = 0; k < slots; ++k) top = fmaxf(top, lse[k * per_slot]);
+    float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f}, sum = 0.0f;
+    for (int k0 = 0; k0 < slots; k0 += 4) {
+        float w[4];
+        float4 v[4][2];
 #pragma unroll
-    for (int x = 0; x < kPer; ++x) acc[x] = 0.0f;
-    for (int k0 = 0; k0 < slots; k0 += 32) {
-        const float lse = k0 + lane < slots ? p.lse[(k0 + lane) * rows + row] : -INFINITY;
-        const float mine = lse == -INFINITY ? 0.0f : exp2_fast(lse - top);
-        sum += mine;
-        const int n = min(32, slots - k0);
-        for (int k = 0; k < n; k += 4) {   // four partial rows in flight
-            float w[4];
-            Vec v[4];
+        for (int u = 0; u < 4; ++u) {
+            const float mine = k0 + u < slots ? lse[(k0 + u) * per_slot] : -INFINITY;
+            w[u] = mine == -INFINITY ? 0.0f : exp2_fast(mine - top);
+            const bool there = mine != -INFINITY;
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                w[u] = __shfl_sync(0xffffffffu, mine, (k + u) & 31);
-                if (k + u >= n) w[u] = 0.0f;
-                v[u] = Vec{};
-                if (w[u] != 0.0f) v[u] = *reinterpret_cast<const Vec *>(p.part + ((k0 + k + u) * rows + row) * kD + lane * kPer);
-            }
+            for (int x = 0; x < 2; ++x) v[u][x] = there ? part[(k0 + u) * per_slot * (kD / 4) + 32 * x] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const float *e = reinterpret_cast<const float *>(&v[u]);
+        for (int u = 0; u < 4; ++u) {
+            sum += w[u];
 #pragma unroll
-                for (int x = 0; x < kPer; ++x) acc[x] = fmaf(w[u], e[x], acc[x]);
+            for (int x = 0; x < 2; ++x) {
+                acc[4 * x] = fmaf(w[u], v[u][x].x, acc[4 * x]);
+                acc[4 * x + 1] = fmaf(w[u], v[u][x].y, acc[4 * x + 1]);
+                acc[4 * x + 2] = fmaf(w[u], v[u][x].z, acc[4 * x + 2]);
+                acc[4 * x + 3] = fmaf(w[u], v[u][x].w, acc[4 * x + 3]);
             }
         }
     }
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     const float inv = sum > 0.0f || isnan(sum) ? 1.0f / sum : 0.0f;   // no key at all: zeros
-    uint32_t *out = reinterpret_cast<uint32_t *>(static_cast<T *>(g.out) + row * kD + lane * kPer);
-#pragma unroll
-    for (int x = 0; x < kPer; x += 2) out[x / 2] = pack2<T>(acc[x] * inv, acc[x + 1] * inv);
+    uint4 out;
+    out.x = pack2<T>(acc[0] * inv, acc[1] * inv);
+    out.y = pack2<T>(acc[2] * inv, acc[3] * inv);
+    out.z = pack2<T>(acc[4] * inv, acc[5] * inv);
+    out.w = pack2<T>(acc[6] * inv, acc[7] * inv);
+    *reinterpret_cast<uint4 *>(static_cast<T *>(g.out) + (static_cast<int64_t>(i / G) * g.Hq + h * G + i % G) * kD + d0) = out;
 }
 
 cudaError_t encode_cache_map(CUtensorMap *map, const void *cache, const AttnArgs &g)
@@ -692,9 +782,8 @@ cudaError_t launch_typed(const AttnParams &p, int sm_count, cudaStream_t s)
         cfg.numAttrs = set_launch_overlap_attr(attr);
         if ((e = cudaLaunchKernelEx(&cfg, kern, p)) != cudaSuccess) return e;
     }
-    const int64_t rows = static_cast<int64_t>(g.B) * g.T * g.Hq;
-    cfg.blockDim = dim3(256);
-    cfg.gridDim = dim3(static_cast<unsigned>((rows + 7) / 8));
+    cfg.blockDim = dim3(32 * kD / 8);
+    cfg.gridDim = dim3(static_cast<unsigned>(p.row_blocks * g.Hkv));
     cfg.dynamicSmemBytes = 0;
     if (jobs > 0) {   // starts as the last jobs run, and waits for all of them
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -706,17 +795,14 @@ cudaError_t launch_typed(const AttnParams &p, int sm_count, cudaStream_t s)
     return cudaLaunchKernelEx(&cfg, attention_join_kernel<T, kD>, p);
 }
 
-int64_t part_bytes(const AttnPlan &plan, int B, int T, int Hq, int D)
-{
-    return static_cast<int64_t>(plan.slots) * B * T * Hq * D * 4;
-}
+int64_t row_blocks_of(int B, int T, int Hq, int Hkv) { return ceil_div(static_cast<int64_t>(B) * T * (Hq / Hkv), 32); }
 
 }  // namespace
 
 int64_t attn_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int64_t prefix_len, int64_t max_own)
 {
     const AttnPlan plan = plan_attention(B, T, Hq, Hkv, prefix_len, max_own);
-    return part_bytes(plan, B, T, Hq, D) + static_cast<int64_t>(plan.slots) * B * T * Hq * 4;
+    return plan.slots * Hkv * row_blocks_of(B, T, Hq, Hkv) * 32 * (D + 1) * 4;
 }
 
 cudaError_t launch_attention(const DeviceInfo &dev, const AttnArgs &g, cudaStream_t s)
@@ -726,8 +812,9 @@ cudaError_t launch_attention(const DeviceInfo &dev, const AttnArgs &g, cudaStrea
     p.g = g;
     p.plan = plan_attention(g.B, g.T, g.Hq, g.Hkv, g.prefix_len, g.max_own);
     if (p.plan.prefix_jobs + p.plan.own_jobs > 0x7fffffffLL) return cudaErrorInvalidValue;
+    p.row_blocks = static_cast<int>(row_blocks_of(g.B, g.T, g.Hq, g.Hkv));
     p.part = static_cast<float *>(g.workspace);
-    p.lse = reinterpret_cast<float *>(static_cast<uint8_t *>(g.workspace) + part_bytes(p.plan, g.B, g.T, g.Hq, g.D));
+    p.lse = p.part + p.plan.slots * static_cast<int64_t>(g.Hkv) * p.row_blocks * 32 * g.D;
     if (g.n_pages > 0) {
         cudaError_t e = encode_cache_map(&p.k, g.k_cache, g);
         if (e == cudaSuccess) e = encode_cache_map(&p.v, g.v_cache, g);

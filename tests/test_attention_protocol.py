@@ -1,6 +1,6 @@
 """CPU model of the shared-prefix attention kernel's handoffs (prefix_attention.cu).
 
-The kernel's roles -- one loading warp, two threads that issue products, the eight
+The kernel's roles -- two loading warps, two threads that issue products, the eight
 softmax warps -- are run as steps in random order under mbarrier semantics: a barrier
 completes a phase when its arrivals (and a copy's bytes) are in, and a wait on a parity
 passes when the barrier's phase in progress has the other one. Copies land in any order
@@ -61,11 +61,12 @@ class Model:
 
     def __init__(self, jobs, slots, rng, second_wait=True):
         self.jobs, self.ks, self.rng, self.second_wait = jobs, slots, rng, second_wait
-        self.full = [Barrier(1) for _ in range(slots)]
+        self.full = [Barrier(2) for _ in range(slots)]
         self.freed = [Barrier(2) for _ in range(slots)]
         self.s_full, self.p_full = [Barrier(1), Barrier(1)], [Barrier(4), Barrier(4)]
-        self.q_full, self.o_done, self.o_free, self.merged = Barrier(8), Barrier(2), Barrier(8), Barrier(4)
-        self.holds = [None] * slots        # (job, "K" or "V", tile) that has landed in a slot
+        self.q_full, self.o_done, self.o_free, self.merged = Barrier(8), Barrier(2), Barrier(8), Barrier(8)
+        self.turn = [Barrier(1), Barrier(1)]
+        self.holds = [[None, None] for _ in range(slots)]   # (job, "K" or "V", tile) of each half that has landed
         self.flying = []                   # copies that have not landed
         self.queue = [[], []]              # products of each issuing thread, in order
         self.reading = {}                  # what unfinished products read: slot or "q" -> count
@@ -82,7 +83,10 @@ class Model:
             waits.insert(0, (self.freed[at], use - 1))
         return waits
 
-    def loader(self):
+    def has(self, at, what):
+        return self.holds[at] == [what, what]
+
+    def loader(self, half):
         pos = 0
         for j, (n, pair, _) in enumerate(self.jobs):
             order = []
@@ -98,13 +102,13 @@ class Model:
                     yield (self.freed[at], pos // self.ks - 1)
                 if self.reading.get(at):
                     raise Fault("a slot is filled while a product reads it")
-                self.holds[at] = None
+                self.holds[at][half] = None
                 self.full[at].arrive(1, copies=1)
-                self.flying.append((at, (j, what, t)))
+                self.flying.append((at, half, (j, what, t)))
                 pos += 1
 
     def issuer(self, s):
-        pos0 = done = step = 0
+        pos0 = done = step = turns = 0
         for j, (n, pair, _) in enumerate(self.jobs):
             if n == 0:
                 continue
@@ -113,29 +117,37 @@ class Model:
             def s_product(i):
                 t = tiles[i]
                 pos = pos0 + k_pos(t)
-                yield from self.landed_waits(pos, pair)
-                if self.holds[pos % self.ks] != (j, "K", t) or self.q_job != j:
+                if not self.has(pos % self.ks, (j, "K", t)) or self.q_job != j:
                     raise Fault("S reads what is not its tile or its Q")
                 self.use(pos % self.ks, 1), self.use("q", 1)
                 self.queue[s].append(("S", [pos % self.ks, "q"], self.s_full[s]))
 
             yield (self.q_full, done)
             if tiles:
-                yield from s_product(0)
+                yield from self.landed_waits(pos0 + k_pos(tiles[0]), pair)
+                s_product(0)
             if done:
                 yield (self.o_free, done - 1)
             for i, t in enumerate(tiles):
                 pos = pos0 + v_pos(t, n)
+                if i + 1 < len(tiles):
+                    yield from self.landed_waits(pos0 + k_pos(tiles[i + 1]), pair)
                 yield from self.landed_waits(pos, pair)
+                if pair:
+                    if s == 1 or turns > 0:
+                        yield (self.turn[s], turns + s - 1)
+                    turns += 1
                 yield (self.p_full[s], step)
                 step += 1
-                if self.holds[pos % self.ks] != (j, "V", t):
+                if not self.has(pos % self.ks, (j, "V", t)):
                     raise Fault("P V reads what is not its tile")
                 self.o_job[s] = j
                 self.use(pos % self.ks, 1)
                 self.queue[s].append(("PV", [pos % self.ks], None))
                 if i + 1 < len(tiles):
-                    yield from s_product(i + 1)
+                    s_product(i + 1)
+                if pair:
+                    self.turn[1 - s].arrive()
             self.queue[s].append(("end", [], self.o_done))
             done += 1
             pos0 += 2 * n
@@ -166,7 +178,7 @@ class Model:
                 if t == n - 1 and tail:
                     pos = pos0 + v_pos(t, n)
                     yield from self.landed_waits(pos, pair)
-                    if self.holds[pos % self.ks] != (j, "V", t):
+                    if not self.has(pos % self.ks, (j, "V", t)):
                         raise Fault("the tail of another tile is cleared")
                 self.p_full[s].arrive()
             yield (self.o_done, done)
@@ -176,20 +188,17 @@ class Model:
             pos0 += 2 * n
             if x + 1 < len(live):
                 load_q(live[x + 1])
-            if not pair and n > 1:
-                if s == 1:
-                    self.merged.arrive()
-                else:
-                    yield (self.merged, merges)
+            if not pair:
+                self.merged.arrive()
+                yield (self.merged, merges)
                 merges += 1
-            if pair or s == 0:   # this warp reads O (both streams' where they are joined)
-                for k in (s,) if pair or n == 1 else (0, 1):
-                    if self.o_job[k] != j:
-                        raise Fault("O is another job's")
+            for k in (s,) if pair else (0,) if n == 1 else (0, 1):   # whose O this warp reads
+                if self.o_job[k] != j:
+                    raise Fault("O is another job's")
             self.o_free.arrive()
 
     def run(self):
-        roles = {("load",): self.loader(), ("issue", 0): self.issuer(0), ("issue", 1): self.issuer(1)}
+        roles = {("load", 0): self.loader(0), ("load", 1): self.loader(1), ("issue", 0): self.issuer(0), ("issue", 1): self.issuer(1)}
         roles.update({("softmax", s, w): self.softmax(s, w) for s in (0, 1) for w in range(4)})
         waits = {r: None for r in roles}
         speed = {r: self.rng.choice([1, 1, 4, 20]) for r in list(roles) + ["land", "product"]}
@@ -206,8 +215,8 @@ class Model:
                 raise Fault("nothing can go on: " + str(sorted(roles)))
             r = self.rng.choice(ready)
             if r == "land":      # any copy, or mostly the first: one may be very late
-                at, what = self.flying.pop(0 if self.rng.random() < 0.7 else self.rng.randrange(len(self.flying)))
-                self.holds[at] = what
+                at, half, what = self.flying.pop(0 if self.rng.random() < 0.7 else self.rng.randrange(len(self.flying)))
+                self.holds[at][half] = what
                 self.full[at].landed()
             elif r == "product":
                 q = self.rng.choice([q for q in self.queue if q])
