@@ -61,9 +61,9 @@ struct AttnPlan {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// The prefix's jobs fill the SMs once: a pair group's tile costs two products where a
-// lone group's costs one, so ranges are cut to the same cost, of two tiles at least (a
-// tile a stream). Own keys: a range a request where the requests and key heads fill the
+// The prefix's jobs fill the SMs once: ranges are cut to the same cost, of two tiles at
+// least (a tile a stream). A tile costs a pair of streams about 3100 cycles and, where the
+// streams take every other tile, 2000 a tile: 3 to 2. Own keys: a range a request where the requests and key heads fill the
 // SMs, else as many as fill them, of 256 keys at least.
 AttnPlan plan_attention(int B, int T, int Hq, int Hkv, int64_t prefix_len, int64_t max_own)
 {
@@ -73,13 +73,13 @@ AttnPlan plan_attention(int B, int T, int Hq, int Hkv, int64_t prefix_len, int64
         const int64_t row_tiles = ceil_div(rows, kTile);
         p.pair_groups = static_cast<int>(row_tiles / 2);
         p.lone = static_cast<int>(row_tiles % 2);
-        const int64_t cost = Hkv * row_tiles * tiles;   // in products of 128 x 128
-        const int64_t budget = std::max<int64_t>(2, ceil_div(cost, kSms));
+        const int64_t cost = Hkv * (3 * p.pair_groups + 2 * p.lone) * tiles;
+        const int64_t budget = std::max<int64_t>(4, ceil_div(cost, kSms));
         auto splits = [&](int64_t per_tile) {
             return static_cast<int>(std::min<int64_t>({std::max<int64_t>(1, (per_tile * tiles + budget / 2) / budget), tiles, 256}));
         };
-        p.pair_splits = p.pair_groups ? splits(2) : 0;
-        p.lone_splits = p.lone ? splits(1) : 0;
+        p.pair_splits = p.pair_groups ? splits(3) : 0;
+        p.lone_splits = p.lone ? splits(2) : 0;
         p.prefix_jobs = Hkv * (static_cast<int64_t>(p.pair_groups) * p.pair_splits + p.lone_splits);
     }
     const int64_t own_tiles = ceil_div(max_own, kTile);
@@ -240,11 +240,11 @@ __device__ __forceinline__ Job job_of(const AttnParams &p, int id, int len)
 // Piece u (16 bytes) of the Q of rows i0 ... of key head h: row i is query head h G + i % G
 // of token i / G.
 template <int kD>
-__device__ __forceinline__ uint4 q_piece(const AttnArgs &g, int h, int i0, int u)
+__device__ __forceinline__ const uint4 *q_piece(const AttnArgs &g, int h, int i0, int u)
 {
     const int G = g.Hq / g.Hkv, i = i0 + u / (kD / 8);
     const int64_t row = static_cast<int64_t>(i / G) * g.Hq + h * G + i % G;
-    return __ldg(static_cast<const uint4 *>(g.q) + row * (kD / 8) + u % (kD / 8));
+    return static_cast<const uint4 *>(g.q) + row * (kD / 8) + u % (kD / 8);
 }
 
 // nrows of Q into the K-major swizzled layout, by 256 threads, their first pieces at hand.
@@ -253,22 +253,14 @@ template <int kD>
 __device__ __forceinline__ void store_q(uint8_t *smem, const AttnArgs &g, int h, int i0, int nrows, int tid, uint4 first)
 {
     const int pieces = nrows * (kD / 8);
-    auto put = [&](int u, uint4 v) {
+    auto place = [&](int u) {
         const int r = u / (kD / 8), x = u % (kD / 8);
-        *reinterpret_cast<uint4 *>(smem + (r / kTile) * (kTile * kD * 2) + (x / 8) * (kTile * 128) + (r % kTile) * 128 +
-                                   16 * ((x % 8) ^ (r % 8))) = v;
+        return smem + (r / kTile) * (kTile * kD * 2) + (x / 8) * (kTile * 128) + (r % kTile) * 128 + 16 * ((x % 8) ^ (r % 8));
     };
-    if (tid < pieces) put(tid, first);
+    if (tid < pieces) *reinterpret_cast<uint4 *>(place(tid)) = first;
 #pragma unroll 1
-    for (int u = tid + 256; u < pieces; u += 5 * 256) {   // (256 rows: three rounds of five loads)
-        uint4 v[5];
-#pragma unroll
-        for (int x = 0; x < 5; ++x)
-            if (u + 256 * x < pieces) v[x] = q_piece<kD>(g, h, i0, u + 256 * x);
-#pragma unroll
-        for (int x = 0; x < 5; ++x)
-            if (u + 256 * x < pieces) put(u + 256 * x, v[x]);
-    }
+    for (int u = tid + 256; u < pieces; u += 256) cp_async_16(place(u), q_piece<kD>(g, h, i0, u));
+    cp_async_wait_all();
 }
 
 // kWide: the launch has jobs of more than 128 rows (two Q tiles, one slot less).
@@ -486,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             uint4 first_q{};
             if (id < jobs) {   // (while this job's last products run)
                 next = job_of(p, id, len);
-                if (has_q(next)) first_q = q_piece<kD>(g, next.h, next.i0, tid);
+                if (has_q(next)) first_q = __ldg(q_piece<kD>(g, next.h, next.i0, tid));
                 if (next.own_b >= 0 && len > g.max_own && tid == 0) atomicOr(&g_attention_error, kErrIndex);
             }
             if (running) {
@@ -636,56 +628,55 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         }
         __syncwarp();
     } else {
-        // ------------------------------------------------ K and V: warp 10 loads the first, warp 11
-        // the second 64 elements of each row (64-wide heads: the even and the odd pages); a
-        // warp's copies of a tile took about 500 cycles to issue, as long as a tile may take
-        const int box = min(g.page, kTile), shift = __ffs(g.page) - 1, half = warp - kLoadWarp;
-        constexpr int kFirst = kChunks == 1 ? 1 : 0, kStep = kChunks == 1 ? 2 : 1;   // pages of a warp
-        int pos = 0;
-        bool ok = true;
-        for (; id < jobs && ok; id += stride) {
-            const Job job = job_of(p, id, len);
-            len = own_length(p, id + stride);
-            const int32_t *table = job.own_b < 0 ? g.prefix_table : g.own_table + static_cast<int64_t>(job.own_b) * g.own_pages;
-            // lane b has the page of a tile's b-th `box` keys, loaded a tile ahead
-            auto pages_of = [&](int t) { return t < job.ntiles ? (min(kTile, job.keys - t * kTile) + box - 1) / box : 0; };
-            auto page_of = [&](int t) { return lane < pages_of(t) ? __ldg(table + ((job.key0 + t * kTile + lane * box) >> shift)) : 0; };
-            int pg = page_of(0), last = 0, before = 0;   // of the next tile of K, the last one and the one before
+        // ------------------------------------------------ K and V: a thread of warp 10 loads the
+        // first, one of warp 11 the second 64 elements of each row (64-wide heads: the even and
+        // the odd pages). One thread for all took 500 cycles a slot to issue its copies, and a
+        // whole warp, a lane a page, as long.
+        if (elect_one()) {
+            const int box = min(g.page, kTile), shift = __ffs(g.page) - 1, half = warp - kLoadWarp;
+            constexpr int kStep = kChunks == 1 ? 2 : 1, kMost = kTile / 16 / kStep;   // this thread's pages of a tile:
+            const int first = kChunks == 1 ? half : 0;                                // first, first + kStep, ...
+            int pos = 0;
+            bool ok = true;
+            for (; id < jobs && ok; id += stride) {
+                const Job job = job_of(p, id, len);
+                len = own_length(p, id + stride);
+                const int32_t *table = (job.own_b < 0 ? g.prefix_table : g.own_table + static_cast<int64_t>(job.own_b) * g.own_pages) + (job.key0 >> shift);
+                const int in_page = static_cast<int>(job.key0 & (g.page - 1));   // (0 but for pages of 256)
 #pragma unroll 1
-            for (int q = 0; q < 2 * job.ntiles; ++q, ++pos) {   // K0 K1 V0 K2 V1 ...
-                const bool v = (q > 0 && q % 2 == 0) || q == 2 * job.ntiles - 1;
-                const int t = !v ? (q + 1) / 2 : q % 2 == 0 ? q / 2 - 1 : job.ntiles - 1;
-                if (!v) {
-                    before = last;
-                    last = pg;
-                    pg = page_of(t + 1);
+                for (int q = 0; q < 2 * job.ntiles; ++q, ++pos) {   // K0 K1 V0 K2 V1 ...
+                    const bool v = (q > 0 && q % 2 == 0) || q == 2 * job.ntiles - 1;
+                    const int t = !v ? (q + 1) / 2 : q % 2 == 0 ? q / 2 - 1 : job.ntiles - 1;
+                    const int at = pos % kSlots, pages = (min(kTile, job.keys - t * kTile) + box - 1) / box;
+                    // the pages' numbers, all on their way at once
+                    int page[kMost];
+#pragma unroll
+                    for (int x = 0; x < kMost; ++x)
+                        if (first + kStep * x < pages) page[x] = __ldg(table + ((in_page + t * kTile + (first + kStep * x) * box) >> shift));
+                    if (*abort_word || (pos >= kSlots && !wait_for(&freed[at], full_parity(pos) ^ 1u))) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(&full[at], static_cast<uint32_t>(max((pages - first + kStep - 1) / kStep, 0)) * box * 128u);
+                    uint8_t *dst = ring + at * kSlotBytes + (kChunks == 1 ? first * box * 128 : half * kBlock);
+#pragma unroll
+                    for (int x = 0; x < kMost; ++x) {
+                        if (first + kStep * x >= pages) break;
+                        if (page[x] < 0 || page[x] >= g.n_pages) {   // no page: read past the cache, zeros
+                            atomicOr(&g_attention_error, kErrIndex);
+                            page[x] = static_cast<int>(g.n_pages);
+                        }
+                        tma_load_4d(dst + kStep * x * box * 128, v ? &p.v : &p.k, kChunks == 1 ? 0 : 64 * half,
+                                    (in_page + t * kTile) & (g.page - 1), job.h, page[x], &full[at]);
+                    }
                 }
-                int mine = v && q % 2 == 0 ? before : last;
-                const int at = pos % kSlots, pages = pages_of(t);
-                if (*abort_word || (pos >= kSlots && !wait_all(&freed[at], full_parity(pos) ^ 1u))) {
-                    ok = false;
-                    break;
-                }
-                if (mine < 0 || mine >= g.n_pages) {   // no page: read past the cache, zeros
-                    atomicOr(&g_attention_error, kErrIndex);
-                    mine = static_cast<int>(g.n_pages);
-                }
-                const int first = kFirst * half, boxes = max((pages - first + kStep - 1) / kStep, 0);
-                if (elect_one()) mbar_arrive_expect_tx(&full[at], static_cast<uint32_t>(boxes) * box * 128u);
-                const int in_page = static_cast<int>((job.key0 + t * kTile) & (g.page - 1));   // (0 but for pages of 256)
-                uint8_t *dst = ring + at * kSlotBytes + (kChunks == 1 ? 0 : half * kBlock);
-#pragma unroll 1
-                for (int b = first; b < pages; b += kStep) {
-                    const int page = __shfl_sync(0xffffffffu, mine, b);
-                    if (elect_one()) tma_load_4d(dst + b * box * 128, v ? &p.v : &p.k, kChunks == 1 ? 0 : 64 * half, in_page, job.h, page, &full[at]);
-                }
+                if (!ok) fail();
             }
-            if (!ok) fail();
-        }
-        // Every copy lands before the CTA can exit: the products wait for each of them, unless
-        // something gave up; then this warp waits (bounded) for those it last started.
-        if (*abort_word) {
-            for (int x = max(0, pos - kSlots); x < pos; ++x) (void)wait_for(&full[x % kSlots], full_parity(x));
+            // Every copy lands before the CTA can exit: the products wait for each of them, unless
+            // something gave up; then this thread waits (bounded) for those it last started.
+            if (*abort_word) {
+                for (int x = max(0, pos - kSlots); x < pos; ++x) (void)wait_for(&full[x % kSlots], full_parity(x));
+            }
         }
         __syncwarp();
     }
@@ -699,57 +690,71 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
 }
 
 // Joins the partial results of 32 rows of a key head, a row a lane and 8 of D a warp:
-// weights 2^(lse - max) over their sum. Four slots are in flight: the 14 of a 64-request
-// batch behind 65536 keys take four rounds of memory latency.
+// weights 2^(lse - max) over their sum, of up to kJoinSlots slots at a time, computed once
+// for all warps. Bound by latency, so that the loads of eight slots are in flight.
+constexpr int kJoinSlots = 64;
 template <typename T, int kD>
 __global__ void __launch_bounds__(32 * kD / 8) attention_join_kernel(const __grid_constant__ AttnParams p)
 {
+    __shared__ float weight[kJoinSlots][32];
+    constexpr int kWarps = kD / 8;
     const AttnArgs &g = p.g;
-    const int lane = threadIdx.x & 31, d0 = static_cast<int>(threadIdx.x >> 5) * 8;
+    const int lane = threadIdx.x & 31, warp = static_cast<int>(threadIdx.x >> 5);
     const int block = static_cast<int>(blockIdx.x) % p.row_blocks, h = static_cast<int>(blockIdx.x) / p.row_blocks;
     const int G = g.Hq / g.Hkv, i = block * 32 + lane;
-    grid_launch_dependents();
-    grid_dependency_wait();
-    if (i >= g.B * g.T * G) return;
+    const bool live = i < g.B * g.T * G;
     // these rows' prefix slots: those of their row group
-    const int slots = p.plan.own_splits + (i < p.plan.pair_groups * 2 * kTile ? p.plan.pair_splits : p.plan.lone_splits);
+    const int slots = p.plan.own_splits + (block * 32 < p.plan.pair_groups * 2 * kTile ? p.plan.pair_splits : p.plan.lone_splits);
     const int64_t per_slot = static_cast<int64_t>(g.Hkv) * p.row_blocks * 32;
     const float *lse = p.lse + static_cast<int64_t>(h) * p.row_blocks * 32 + i;
-    const float4 *part = reinterpret_cast<const float4 *>(p.part) + (static_cast<int64_t>(h) * p.row_blocks + block) * 8 * kD + d0 * 8 + lane;
-    float top = -INFINITY;
+    const float4 *part = reinterpret_cast<const float4 *>(p.part) + (static_cast<int64_t>(h) * p.row_blocks + block) * 8 * kD + warp * 64 + lane;
+    grid_launch_dependents();
+    grid_dependency_wait();
+    float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f}, sum = 0.0f, top = -INFINITY;
+    for (int k0 = 0; k0 < slots; k0 += kJoinSlots) {
+        const int n = min(kJoinSlots, slots - k0);
+        __syncthreads();
 #pragma unroll 4
-    for (int k = 0; k < slots; ++k) top = fmaxf(top, lse[k * per_slot]);
-    float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f}, sum = 0.0f;
-    for (int k0 = 0; k0 < slots; k0 += 4) {
-        float w[4];
-        float4 v[4][2];
+        for (int k = warp; k < n; k += kWarps) weight[k][lane] = live ? lse[(k0 + k) * per_slot] : -INFINITY;
+        __syncthreads();
+        float best = top;
+        for (int k = 0; k < n; ++k) best = fmaxf(best, weight[k][lane]);
+        const float fix = top == -INFINITY ? 0.0f : exp2_fast(top - best);
+        top = best;
+        sum *= fix;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const float mine = k0 + u < slots ? lse[(k0 + u) * per_slot] : -INFINITY;
-            w[u] = mine == -INFINITY ? 0.0f : exp2_fast(mine - top);
-            const bool there = mine != -INFINITY;
+        for (int x = 0; x < 8; ++x) acc[x] *= fix;
+        for (int k = 0; k < n; k += 8) {
+            float4 v[8][2];
 #pragma unroll
-            for (int x = 0; x < 2; ++x) v[u][x] = there ? part[(k0 + u) * per_slot * (kD / 4) + 32 * x] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        }
+            for (int u = 0; u < 8; ++u)
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            sum += w[u];
+                for (int x = 0; x < 2; ++x)
+                    v[u][x] = k + u < n && live ? part[(k0 + k + u) * per_slot * (kD / 4) + 32 * x] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                acc[4 * x] = fmaf(w[u], v[u][x].x, acc[4 * x]);
-                acc[4 * x + 1] = fmaf(w[u], v[u][x].y, acc[4 * x + 1]);
-                acc[4 * x + 2] = fmaf(w[u], v[u][x].z, acc[4 * x + 2]);
-                acc[4 * x + 3] = fmaf(w[u], v[u][x].w, acc[4 * x + 3]);
+            for (int u = 0; u < 8; ++u) {
+                const float there = k + u < n ? weight[k + u][lane] : -INFINITY;
+                if (there == -INFINITY) continue;   // no key, and nothing written
+                const float w = exp2_fast(there - top);
+                sum += w;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    acc[4 * x] = fmaf(w, v[u][x].x, acc[4 * x]);
+                    acc[4 * x + 1] = fmaf(w, v[u][x].y, acc[4 * x + 1]);
+                    acc[4 * x + 2] = fmaf(w, v[u][x].z, acc[4 * x + 2]);
+                    acc[4 * x + 3] = fmaf(w, v[u][x].w, acc[4 * x + 3]);
+                }
             }
         }
     }
+    if (!live) return;
     const float inv = sum > 0.0f || isnan(sum) ? 1.0f / sum : 0.0f;   // no key at all: zeros
     uint4 out;
     out.x = pack2<T>(acc[0] * inv, acc[1] * inv);
     out.y = pack2<T>(acc[2] * inv, acc[3] * inv);
     out.z = pack2<T>(acc[4] * inv, acc[5] * inv);
     out.w = pack2<T>(acc[6] * inv, acc[7] * inv);
-    *reinterpret_cast<uint4 *>(static_cast<T *>(g.out) + (static_cast<int64_t>(i / G) * g.Hq + h * G + i % G) * kD + d0) = out;
+    *reinterpret_cast<uint4 *>(static_cast<T *>(g.out) + (static_cast<int64_t>(i / G) * g.Hq + h * G + i % G) * kD + warp * 8) = out;
 }
 
 cudaError_t encode_cache_map(CUtensorMap *map, const void *cache, const AttnArgs &g)
