@@ -9,13 +9,22 @@ keeps one of the bytes that the ``_workspace`` function names.
 """
 from __future__ import annotations
 
+import functools
 import math
 
 import torch
 
-from ._binding import QmvError, _check, _need, _stream, lib
+from ._binding import QMV_OK, QmvError, _check, _need, _stream, lib
 
-_TYPE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}   # QMV_F32, QMV_F16, QMV_BF16
+_F32, _F16, _BF16, _I32 = torch.float32, torch.float16, torch.bfloat16, torch.int32
+_TYPE = {_F32: 0, _F16: 1, _BF16: 2}   # QMV_F32, QMV_F16, QMV_BF16
+_16BIT = (_F16, _BF16)
+
+
+@functools.cache
+def _fn(name: str):
+    """The library's function (looked up once: a decode step's calls take microseconds)."""
+    return getattr(lib(), name)
 
 
 def _type(t: torch.Tensor, name: str, allowed) -> int:
@@ -24,18 +33,34 @@ def _type(t: torch.Tensor, name: str, allowed) -> int:
     return _TYPE[t.dtype]
 
 
-def _workspace(buffer, need: int, device, stream):
-    """`buffer`, or a new one of `need` bytes that stays valid for the call's stream."""
+def _is(t, name: str, dtype, shape):
+    """_need, with the checks that pass in a few tenths of a microsecond first."""
+    if not (t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous()):
+        _need(t, name, dtype, shape)
+
+
+def _on(stream) -> int:
+    return torch.cuda.current_stream().cuda_stream if stream is None else _stream(stream)
+
+
+def _workspace(buffer, need, device, stream):
+    """`buffer`, or a new one of need() bytes that stays valid for the call's stream."""
     if buffer is None:
-        buffer = torch.empty((need,), dtype=torch.uint8, device=device)
+        buffer = torch.empty((need(),), dtype=torch.uint8, device=device)
         if stream is not None:
             buffer.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
                                  torch.cuda.ExternalStream(_stream(stream)))
-    else:
+    elif not (buffer.dtype is torch.uint8 and buffer.is_cuda and buffer.is_contiguous()):
         _need(buffer, "workspace", torch.uint8)
-        if buffer.numel() < need:
-            raise ValueError(f"workspace: {buffer.numel()} bytes, the call needs {need}")
     return buffer
+
+
+def _check_with(fn: str, status: int, buffer, need):
+    """_check, naming a workspace that is too small."""
+    if status != QMV_OK:
+        if buffer.numel() < need():
+            raise ValueError(f"workspace: {buffer.numel()} bytes, {fn} needs {need()}")
+        _check(fn, status)
 
 
 def _bytes(fn: str, n: int) -> int:
@@ -46,7 +71,7 @@ def _bytes(fn: str, n: int) -> int:
 
 def qmv_lora_add_workspace(M: int, R: int, K: int) -> int:
     """Bytes of workspace of qmv_lora_add on M rows of K with adapters of rank R."""
-    return _bytes("qmv_lora_add_workspace", lib().qmv_lora_add_workspace(M, R, K))
+    return _bytes("qmv_lora_add_workspace", _fn("qmv_lora_add_workspace")(M, R, K))
 
 
 def qmv_lora_add(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, adapter: torch.Tensor, scale: torch.Tensor,
@@ -58,22 +83,24 @@ def qmv_lora_add(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, adapter: tor
     M, K = x.shape
     L, R, _ = a.shape
     N = base.shape[1]
-    _need(x, "x", x.dtype)
-    xt = _type(x, "x", (torch.float32, torch.float16))
-    wt = _type(a, "a", (torch.float16, torch.bfloat16))
-    _need(a, "a", a.dtype, (L, R, K))
-    _need(b, "b", a.dtype, (L, N, R))
-    _need(adapter, "adapter", torch.int32, (M,))
-    _need(scale, "scale", torch.float32, (L,))
-    _need(base, "base", torch.float32, (M, N))
+    xt, wt = _type(x, "x", (_F32, _F16)), _type(a, "a", _16BIT)
+    _is(x, "x", x.dtype, (M, K))
+    _is(a, "a", a.dtype, (L, R, K))
+    _is(b, "b", a.dtype, (L, N, R))
+    _is(adapter, "adapter", _I32, (M,))
+    _is(scale, "scale", _F32, (L,))
+    _is(base, "base", _F32, (M, N))
     if out is None:
-        out = torch.empty((M, N), dtype=torch.float32, device=base.device)
+        out = torch.empty((M, N), dtype=_F32, device=base.device)
     else:
-        _need(out, "out", torch.float32, (M, N))
-    ws = _workspace(workspace, qmv_lora_add_workspace(M, R, K), x.device, stream)
-    _check("qmv_lora_add", lib().qmv_lora_add(
+        _is(out, "out", _F32, (M, N))
+    need = lambda: qmv_lora_add_workspace(M, R, K)  # noqa: E731
+    ws = _workspace(workspace, need, x.device, stream)
+    status = _fn("qmv_lora_add")(
         x.data_ptr(), xt, a.data_ptr(), b.data_ptr(), wt, adapter.data_ptr(), scale.data_ptr(), base.data_ptr(),
-        out.data_ptr(), ws.data_ptr(), ws.numel(), M, N, K, R, L, _stream(stream)))
+        out.data_ptr(), ws.data_ptr(), ws.numel(), M, N, K, R, L, _on(stream))
+    if status != QMV_OK:
+        _check_with("qmv_lora_add", status, ws, need)
     return out
 
 
@@ -106,28 +133,31 @@ def qmv_rope_append(qkv: torch.Tensor, positions: torch.Tensor, table: torch.Ten
         axis_of_pair = bytes(axis_of_pair)
     if len(axis_of_pair) != pairs:
         raise ValueError(f"axis_of_pair: expected {pairs} entries, got {len(axis_of_pair)}")
-    t = _type(k_cache, "k_cache", (torch.float16, torch.bfloat16))
-    _need(qkv, "qkv", torch.float32)
-    _need(positions, "positions", torch.int32, (axes, M))
-    _need(table, "table", torch.float32, (n_positions, pairs, 2))
-    _need(slots, "slots", torch.int64, (M,))
-    _need(k_cache, "k_cache", k_cache.dtype)
-    _need(v_cache, "v_cache", k_cache.dtype, (pages, page, Hkv, D))
+    dtype = k_cache.dtype
+    t = _type(k_cache, "k_cache", _16BIT)
+    _is(qkv, "qkv", _F32, (M, width))
+    _is(positions, "positions", _I32, (axes, M))
+    _is(table, "table", _F32, (n_positions, pairs, 2))
+    _is(slots, "slots", torch.int64, (M,))
+    _is(k_cache, "k_cache", dtype, (pages, page, Hkv, D))
+    _is(v_cache, "v_cache", dtype, (pages, page, Hkv, D))
     if out is None:
-        out = torch.empty((M, Hq, D), dtype=k_cache.dtype, device=qkv.device)
+        out = torch.empty((M, Hq, D), dtype=dtype, device=qkv.device)
     else:
-        _need(out, "out", k_cache.dtype, (M, Hq, D))
-    _check("qmv_rope_append", lib().qmv_rope_append(
+        _is(out, "out", dtype, (M, Hq, D))
+    status = _fn("qmv_rope_append")(
         qkv.data_ptr(), positions.data_ptr(), table.data_ptr(), axis_of_pair, slots.data_ptr(), out.data_ptr(),
-        k_cache.data_ptr(), v_cache.data_ptr(), t, int(bool(interleaved)), M, Hq, Hkv, D, 2 * pairs, axes,
-        n_positions, pages * page, _stream(stream)))
+        k_cache.data_ptr(), v_cache.data_ptr(), t, 1 if interleaved else 0, M, Hq, Hkv, D, 2 * pairs, axes,
+        n_positions, pages * page, _on(stream))
+    if status != QMV_OK:
+        _check("qmv_rope_append", status)
     return out
 
 
 def qmv_prefix_attention_workspace(B: int, T: int, Hq: int, Hkv: int, D: int, prefix_len: int, max_own: int) -> int:
     """Bytes of workspace of qmv_prefix_attention at these sizes."""
     return _bytes("qmv_prefix_attention_workspace",
-                  lib().qmv_prefix_attention_workspace(B, T, Hq, Hkv, D, prefix_len, max_own))
+                  _fn("qmv_prefix_attention_workspace")(B, T, Hq, Hkv, D, prefix_len, max_own))
 
 
 def qmv_prefix_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, prefix_table: torch.Tensor,
@@ -143,27 +173,30 @@ def qmv_prefix_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     B, T, Hq, D = q.shape
     pages, page, Hkv, _ = k_cache.shape
     own_pages = own_table.shape[1]
-    t = _type(q, "q", (torch.float16, torch.bfloat16))
-    _need(q, "q", q.dtype)
-    _need(k_cache, "k_cache", q.dtype, (pages, page, Hkv, D))
-    _need(v_cache, "v_cache", q.dtype, (pages, page, Hkv, D))
-    _need(prefix_table, "prefix_table", torch.int32)
-    _need(own_table, "own_table", torch.int32, (B, own_pages))
-    _need(own_len, "own_len", torch.int32, (B,))
+    dtype = q.dtype
+    t = _type(q, "q", _16BIT)
+    _is(q, "q", dtype, (B, T, Hq, D))
+    _is(k_cache, "k_cache", dtype, (pages, page, Hkv, D))
+    _is(v_cache, "v_cache", dtype, (pages, page, Hkv, D))
+    _is(prefix_table, "prefix_table", _I32, prefix_table.shape)
+    _is(own_table, "own_table", _I32, (B, own_pages))
+    _is(own_len, "own_len", _I32, (B,))
     if prefix_table.numel() * page < prefix_len:
         raise ValueError(f"prefix_table: {prefix_table.numel()} pages of {page} hold no {prefix_len} keys")
     if max_own is None:
         max_own = own_pages * page
     if out is None:
-        out = torch.empty((B, T, Hq, D), dtype=q.dtype, device=q.device)
+        out = torch.empty((B, T, Hq, D), dtype=dtype, device=q.device)
     else:
-        _need(out, "out", q.dtype, (B, T, Hq, D))
-    need = qmv_prefix_attention_workspace(B, T, Hq, Hkv, D, prefix_len, max_own)
+        _is(out, "out", dtype, (B, T, Hq, D))
+    need = lambda: qmv_prefix_attention_workspace(B, T, Hq, Hkv, D, prefix_len, max_own)  # noqa: E731
     ws = _workspace(workspace, need, q.device, stream)
-    _check("qmv_prefix_attention", lib().qmv_prefix_attention(
+    status = _fn("qmv_prefix_attention")(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), t, pages, page, prefix_table.data_ptr(), prefix_len,
         own_table.data_ptr(), own_pages, own_len.data_ptr(), max_own, 1.0 / math.sqrt(D) if scale is None else scale,
-        out.data_ptr(), ws.data_ptr(), ws.numel(), B, T, Hq, Hkv, D, _stream(stream)))
+        out.data_ptr(), ws.data_ptr(), ws.numel(), B, T, Hq, Hkv, D, _on(stream))
+    if status != QMV_OK:
+        _check_with("qmv_prefix_attention", status, ws, need)
     return out
 
 
@@ -180,34 +213,36 @@ def qmv_penalize_logits(logits: torch.Tensor, tokens: torch.Tensor, prompt_len: 
     set = allowed, with mask_row int32 [M] (negative: none). out may be logits."""
     M, V = logits.shape
     H = tokens.shape[1]
-    _need(logits, "logits", torch.float32)
-    _need(tokens, "tokens", torch.int32, (M, H))
-    _need(prompt_len, "prompt_len", torch.int32, (M,))
-    _need(total_len, "total_len", torch.int32, (M,))
+    _is(logits, "logits", _F32, (M, V))
+    _is(tokens, "tokens", _I32, (M, H))
+    _is(prompt_len, "prompt_len", _I32, (M,))
+    _is(total_len, "total_len", _I32, (M,))
     rows = []
     for name, t in (("repetition", repetition), ("presence", presence), ("frequency", frequency)):
         if t is not None:
-            _need(t, name, torch.float32, (M,))
+            _is(t, name, _F32, (M,))
         rows.append(None if t is None else t.data_ptr())
     n_bias = n_masks = 0
     if (bias_tokens is None) != (bias_values is None):
         raise ValueError("bias_tokens and bias_values come together")
     if bias_tokens is not None:
         n_bias = bias_tokens.shape[1]
-        _need(bias_tokens, "bias_tokens", torch.int32, (M, n_bias))
-        _need(bias_values, "bias_values", torch.float32, (M, n_bias))
+        _is(bias_tokens, "bias_tokens", _I32, (M, n_bias))
+        _is(bias_values, "bias_values", _F32, (M, n_bias))
     if mask is not None:
         n_masks = mask.shape[0]
-        _need(mask, "mask", torch.int32, (n_masks, (V + 31) // 32))
+        _is(mask, "mask", _I32, (n_masks, (V + 31) // 32))
     if mask_row is not None:
-        _need(mask_row, "mask_row", torch.int32, (M,))
+        _is(mask_row, "mask_row", _I32, (M,))
     if out is None:
-        out = torch.empty((M, V), dtype=torch.float32, device=logits.device)
+        out = torch.empty((M, V), dtype=_F32, device=logits.device)
     else:
-        _need(out, "out", torch.float32, (M, V))
-    _check("qmv_penalize_logits", lib().qmv_penalize_logits(
+        _is(out, "out", _F32, (M, V))
+    status = _fn("qmv_penalize_logits")(
         logits.data_ptr(), tokens.data_ptr(), H, prompt_len.data_ptr(), total_len.data_ptr(), *rows,
         None if bias_tokens is None else bias_tokens.data_ptr(), None if bias_values is None else bias_values.data_ptr(),
         n_bias, None if mask is None else mask.data_ptr(), None if mask_row is None else mask_row.data_ptr(), n_masks,
-        out.data_ptr(), M, V, _stream(stream)))
+        out.data_ptr(), M, V, _on(stream))
+    if status != QMV_OK:
+        _check("qmv_penalize_logits", status)
     return out
