@@ -39,8 +39,10 @@ def _is(t, name: str, dtype, shape):
         _need(t, name, dtype, shape)
 
 
-def _on(stream) -> int:
-    return torch.cuda.current_stream().cuda_stream if stream is None else _stream(stream)
+def _on(stream, t: torch.Tensor) -> int:
+    """The handle of `stream`, or of the current one on t's device (without a Stream object
+    for it, which costs as much as a launch)."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else _stream(stream)
 
 
 def _workspace(buffer, need, device, stream):
@@ -98,7 +100,7 @@ def qmv_lora_add(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, adapter: tor
     ws = _workspace(workspace, need, x.device, stream)
     status = _fn("qmv_lora_add")(
         x.data_ptr(), xt, a.data_ptr(), b.data_ptr(), wt, adapter.data_ptr(), scale.data_ptr(), base.data_ptr(),
-        out.data_ptr(), ws.data_ptr(), ws.numel(), M, N, K, R, L, _on(stream))
+        out.data_ptr(), ws.data_ptr(), ws.numel(), M, N, K, R, L, _on(stream, x))
     if status != QMV_OK:
         _check_with("qmv_lora_add", status, ws, need)
     return out
@@ -148,7 +150,7 @@ def qmv_rope_append(qkv: torch.Tensor, positions: torch.Tensor, table: torch.Ten
     status = _fn("qmv_rope_append")(
         qkv.data_ptr(), positions.data_ptr(), table.data_ptr(), axis_of_pair, slots.data_ptr(), out.data_ptr(),
         k_cache.data_ptr(), v_cache.data_ptr(), t, 1 if interleaved else 0, M, Hq, Hkv, D, 2 * pairs, axes,
-        n_positions, pages * page, _on(stream))
+        n_positions, pages * page, _on(stream, qkv))
     if status != QMV_OK:
         _check("qmv_rope_append", status)
     return out
@@ -194,7 +196,7 @@ def qmv_prefix_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     status = _fn("qmv_prefix_attention")(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), t, pages, page, prefix_table.data_ptr(), prefix_len,
         own_table.data_ptr(), own_pages, own_len.data_ptr(), max_own, 1.0 / math.sqrt(D) if scale is None else scale,
-        out.data_ptr(), ws.data_ptr(), ws.numel(), B, T, Hq, Hkv, D, _on(stream))
+        out.data_ptr(), ws.data_ptr(), ws.numel(), B, T, Hq, Hkv, D, _on(stream, q))
     if status != QMV_OK:
         _check_with("qmv_prefix_attention", status, ws, need)
     return out
@@ -242,7 +244,7 @@ def qmv_penalize_logits(logits: torch.Tensor, tokens: torch.Tensor, prompt_len: 
         logits.data_ptr(), tokens.data_ptr(), H, prompt_len.data_ptr(), total_len.data_ptr(), *rows,
         None if bias_tokens is None else bias_tokens.data_ptr(), None if bias_values is None else bias_values.data_ptr(),
         n_bias, None if mask is None else mask.data_ptr(), None if mask_row is None else mask_row.data_ptr(), n_masks,
-        out.data_ptr(), M, V, _on(stream))
+        out.data_ptr(), M, V, _on(stream, logits))
     if status != QMV_OK:
         _check("qmv_penalize_logits", status)
     return out

@@ -131,7 +131,7 @@ qmv_status qmv_penalize_logits(const float *logits, const int32_t *tokens, int m
                                int max_bias, const uint32_t *mask, const int32_t *mask_row, int n_masks, float *y,
                                int M, int V, qmv_stream_t stream)
 {
-    if (M < 0 || M > 65535 || V < 0 || V > (1 << 30) || max_history < 0 || max_bias < 0 || n_masks < 0) return QMV_ERR_SHAPE;
+    if (M < 0 || M > 65535 || V < 0 || V > (1 << 30) || max_history < 0 || max_history > (1 << 29) || max_bias < 0 || n_masks < 0) return QMV_ERR_SHAPE;
     if (mask && !mask_row && n_masks < M) return QMV_ERR_SHAPE;
     if (M == 0 || V == 0) return QMV_OK;
     if (!logits || !y) return QMV_ERR_NULL;

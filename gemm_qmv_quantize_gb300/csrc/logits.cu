@@ -4,11 +4,14 @@
 //   x = in the history at all ? (x > 0 ? x / repetition : x repetition) : x
 //   x = x - (frequency n + presence [n > 0]) + (v's biases);  y = mask bit ? x : -inf
 //
-// A cluster of CTAs shares a row's tokens (or a part of them): each CTA keeps the counts of
-// its own tokens in shared memory and reads a share of the history, counting a token in
-// whichever CTA of the cluster owns it, so that the history is read once a cluster. Counts
-// are whole numbers: their order does not matter. The logits, loaded before the history is
-// counted, pass through registers once; bound by their bytes.
+// A CTA owns a tile of a row's tokens, keeps their counts in shared memory and reads the
+// whole history, which the row's other CTAs find in L2, counting what is in its tile; then
+// its logits, loaded before that, pass through registers once. Counts are whole numbers:
+// the order of the atomics does not matter. Bound by the logits' bytes: a tile is no
+// shorter than the history, so that reading that again costs less than the tile. (Clusters
+// that read the history once and count in each other's shared memory were slower at every
+// size measured: 14 to 23 us against 10 for 8 rows with 16000 tokens of history, 51 to 54
+// against 33 for 96 rows with 3000.)
 #include <algorithm>
 
 #include "decode_ops.h"
@@ -21,161 +24,146 @@ namespace {
 __device__ uint32_t g_logits_error;
 
 constexpr int kThreads = 512;
-constexpr int kAhead = 6;             // float4 of logits a thread loads before the history is counted
-constexpr int kMaxCluster = 8;
-constexpr int kMaxOwned = 48 * 1024;  // tokens of a CTA at most: 192 KB of counts
-constexpr int kSms = 152;
+constexpr int kAhead = 3;             // float4 of logits and int4 of history that a thread loads
+constexpr int kHistoryAhead = 1;      // before it waits for anything
+constexpr int kMinTile = 4096, kMaxTile = 16384;
+constexpr int kSms = 152, kCtasPerSm = 3;
 constexpr uint32_t kSeen = 1u << 31;  // the bit above a token's count: it is in the prompt
-
-__device__ __forceinline__ uint32_t cluster_rank()
-{
-    uint32_t r;
-    asm("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// The shared-memory word at the same place in the cluster's CTA `rank`.
-__device__ __forceinline__ uint32_t peer_addr(const uint32_t *local, int rank)
-{
-    uint32_t remote;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_addr(local)), "r"(rank));
-    return remote;
-}
-__device__ __forceinline__ void count_answered(uint32_t addr)
-{
-    asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], 1;" ::"r"(addr) : "memory");
-}
-__device__ __forceinline__ void mark_seen(uint32_t addr)
-{
-    asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(addr), "r"(kSeen) : "memory");
-}
 
 struct RowTerms {
     float repetition, frequency, presence;
     const uint32_t *mask;   // of this row, or null
 };
 
-__device__ __forceinline__ bool allowed(const RowTerms &t, int v)
+__device__ __forceinline__ bool allowed(const uint32_t *mask, int v)
 {
-    return !t.mask || (__ldg(t.mask + (v >> 5)) >> (v & 31)) & 1u;
+    return !mask || (__ldg(mask + (v >> 5)) >> (v & 31)) & 1u;
 }
 
+// The logit x of a token whose count is not zero.
 __device__ __forceinline__ float penalized(const RowTerms &t, float x, uint32_t count)
 {
-    if (count) {
-        x = x > 0.0f ? x / t.repetition : x * t.repetition;
-        const uint32_t n = count & ~kSeen;
-        if (n) x -= t.frequency * static_cast<float>(n) + t.presence;
-    }
-    return x;
+    x = x > 0.0f ? x / t.repetition : x * t.repetition;
+    const uint32_t n = count & ~kSeen;
+    return n ? x - (t.frequency * static_cast<float>(n) + t.presence) : x;
 }
 
-// owned: tokens a CTA, a multiple of 4; grid (parts * cluster, M), a cluster a part of the
-// row. kVec: the row's logits and outputs may be moved 16 bytes at a time from their first
-// aligned token on.
-template <bool kVec>
-__global__ void __launch_bounds__(kThreads, 2) logits_kernel(const __grid_constant__ LogitsArgs g, int owned, int cluster)
+// Grid (tiles, M). Shared memory: tile + 4 counts, those of the row's 16-byte groups of
+// logits on 16-byte boundaries.
+__global__ void __launch_bounds__(kThreads, 3) logits_kernel(const __grid_constant__ LogitsArgs g, int tile)
 {
-    extern __shared__ __align__(16) uint32_t count[];
-    const int m = blockIdx.y, tid = threadIdx.x;
-    const int rank = cluster > 1 ? static_cast<int>(cluster_rank()) : 0;
-    const int part0 = static_cast<int>(blockIdx.x) / cluster * cluster * owned;   // the cluster's first token
-    const int v0 = min(part0 + rank * owned, g.V), n = min(owned, g.V - v0);
+    extern __shared__ __align__(16) uint32_t counts[];
+    const int m = blockIdx.y, tid = threadIdx.x, v0 = static_cast<int>(blockIdx.x) * tile, n = min(tile, g.V - v0);
     grid_launch_dependents();
     grid_dependency_wait();
     const float *in = g.logits + static_cast<int64_t>(m) * g.V + v0;
     float *out = g.y + static_cast<int64_t>(m) * g.V + v0;
+    const bool vec = ((reinterpret_cast<uintptr_t>(in) ^ reinterpret_cast<uintptr_t>(out)) & 15u) == 0;
     // tokens before the first 16-byte boundary, then groups of 4, then the rest
-    const int head = kVec ? min(n, static_cast<int>((16u - (reinterpret_cast<uintptr_t>(in) & 15u)) & 15u) / 4) : n;
-    const int groups = kVec ? (n - head) / 4 : 0;
+    const int head = vec ? min(n, static_cast<int>((16u - (reinterpret_cast<uintptr_t>(in) & 15u)) & 15u) / 4) : n;
+    const int groups = (n - head) / 4;
+    uint32_t *count = counts + ((4 - head) & 3);   // of token v0
     float4 ahead[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i)
-        if (tid + i * kThreads < groups) ahead[i] = reinterpret_cast<const float4 *>(in + head)[tid + i * kThreads];
-    for (int i = tid; i < owned / 4; i += kThreads) reinterpret_cast<uint4 *>(count)[i] = make_uint4(0, 0, 0, 0);
+        if (tid + i * kThreads < groups) ahead[i] = __ldcs(reinterpret_cast<const float4 *>(in + head) + tid + i * kThreads);
+    const int32_t *tokens = g.tokens + static_cast<int64_t>(m) * g.max_history;
+    const int all_fours = (reinterpret_cast<uintptr_t>(tokens) & 15u) == 0 ? g.max_history / 4 : 0;
+    int4 early[kHistoryAhead];
+#pragma unroll
+    for (int i = 0; i < kHistoryAhead; ++i)
+        if (tid + i * kThreads < all_fours) early[i] = __ldg(reinterpret_cast<const int4 *>(tokens) + tid + i * kThreads);
+    RowTerms t;
+    const int32_t *bias_tokens = g.bias_tokens + static_cast<int64_t>(m) * g.max_bias;
+    const int bias_token = tid < g.max_bias ? __ldg(bias_tokens + tid) : -1;
     int total = g.total_len ? g.total_len[m] : 0;
+    const int prompt = g.prompt_len ? g.prompt_len[m] : 0;
+    const int mr = g.mask ? (g.mask_row ? g.mask_row[m] : m) : -1;
+    t.repetition = g.repetition ? g.repetition[m] : 1.0f;
+    t.frequency = g.frequency ? g.frequency[m] : 0.0f;
+    t.presence = g.presence ? g.presence[m] : 0.0f;
+    for (int i = tid; i < tile / 4 + 1; i += kThreads) reinterpret_cast<uint4 *>(counts)[i] = make_uint4(0, 0, 0, 0);
     if (total > g.max_history) {
         if (tid == 0) atomicOr(&g_logits_error, kErrIndex);
         total = g.max_history;
     }
-    const int prompt = total > 0 ? g.prompt_len[m] : 0;
-    RowTerms t;
-    t.repetition = g.repetition ? g.repetition[m] : 1.0f;
-    t.frequency = g.frequency ? g.frequency[m] : 0.0f;
-    t.presence = g.presence ? g.presence[m] : 0.0f;
-    const int mr = g.mask ? (g.mask_row ? g.mask_row[m] : m) : -1;
     if (mr >= g.n_masks && g.mask && tid == 0) atomicOr(&g_logits_error, kErrIndex);
     t.mask = mr >= 0 && mr < g.n_masks ? g.mask + static_cast<int64_t>(mr) * ((g.V + 31) / 32) : nullptr;
-    if (cluster > 1) {
-        cluster_sync();   // every CTA's counts are zero
-    } else {
-        __syncthreads();
-    }
-    const int32_t *tokens = g.tokens + static_cast<int64_t>(m) * g.max_history;
-    const int span = cluster * owned;
-#pragma unroll 4
-    for (int i = rank * kThreads + tid; i < total; i += cluster * kThreads) {
-        const int v = tokens[i], at = v - part0;
-        if (v >= g.V) {
-            atomicOr(&g_logits_error, kErrIndex);
-        } else if (v >= 0 && at >= 0 && at < span) {
-            const int owner = at / owned;
-            const uint32_t addr = peer_addr(count + (at - owner * owned), owner);
-            if (i >= prompt) {
-                count_answered(addr);
-            } else {
-                mark_seen(addr);
-            }
+    __syncthreads();
+    auto tally = [&](int i, int v) {
+        if (v >= g.V) atomicOr(&g_logits_error, kErrIndex);
+        if (v < v0 || v >= v0 + n) return;
+        if (i >= prompt) {
+            atomicAdd(count + (v - v0), 1u);
+        } else {
+            atomicOr(count + (v - v0), kSeen);
         }
-    }
-    if (cluster > 1) {
-        cluster_sync();   // all of the history is counted, and no CTA counts in another any more
-    } else {
-        __syncthreads();
-    }
+    };
+    auto tally4 = [&](int i, int4 v) {
+        tally(4 * i, v.x);
+        tally(4 * i + 1, v.y);
+        tally(4 * i + 2, v.z);
+        tally(4 * i + 3, v.w);
+    };
+    const int fours = min(all_fours, total / 4);
+#pragma unroll
+    for (int i = 0; i < kHistoryAhead; ++i)
+        if (tid + i * kThreads < fours) tally4(tid + i * kThreads, early[i]);
+#pragma unroll 4
+    for (int i = tid + kHistoryAhead * kThreads; i < fours; i += kThreads) tally4(i, __ldg(reinterpret_cast<const int4 *>(tokens) + i));
+#pragma unroll 4
+    for (int i = 4 * fours + tid; i < total; i += kThreads) tally(i, __ldg(tokens + i));
+    __syncthreads();
     auto one = [&](int i) {
-        const float x = penalized(t, in[i], count[i]);
-        out[i] = allowed(t, v0 + i) ? x : -INFINITY;
+        float x = in[i];
+        if (count[i]) x = penalized(t, x, count[i]);
+        out[i] = allowed(t.mask, v0 + i) ? x : -INFINITY;
     };
     for (int i = tid; i < head; i += kThreads) one(i);
     for (int i = head + 4 * groups + tid; i < n; i += kThreads) one(i);
     auto four = [&](int group, float4 x) {
         const int i = head + 4 * group, v = v0 + i;
-        float e[4] = {x.x, x.y, x.z, x.w};
-        uint32_t bits = 0xfu;
+        const uint4 c = *reinterpret_cast<const uint4 *>(count + i);
+        if (c.x | c.y | c.z | c.w) {
+            const uint32_t cs[4] = {c.x, c.y, c.z, c.w};
+            float e[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (cs[j]) e[j] = penalized(t, e[j], cs[j]);
+            x = make_float4(e[0], e[1], e[2], e[3]);
+        }
         if (t.mask) {
             const uint32_t lo = __ldg(t.mask + (v >> 5)), hi = (v & 31) > 28 ? __ldg(t.mask + (v >> 5) + 1) : 0u;
-            bits = __funnelshift_r(lo, hi, v & 31);
+            const uint32_t bits = __funnelshift_r(lo, hi, v & 31);
+            x.x = bits & 1u ? x.x : -INFINITY;
+            x.y = bits & 2u ? x.y : -INFINITY;
+            x.z = bits & 4u ? x.z : -INFINITY;
+            x.w = bits & 8u ? x.w : -INFINITY;
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            e[j] = penalized(t, e[j], count[i + j]);
-            if (!((bits >> j) & 1u)) e[j] = -INFINITY;
-        }
-        reinterpret_cast<float4 *>(out + head)[group] = make_float4(e[0], e[1], e[2], e[3]);
+        __stcs(reinterpret_cast<float4 *>(out + head) + group, x);
     };
 #pragma unroll
     for (int i = 0; i < kAhead; ++i)
         if (tid + i * kThreads < groups) four(tid + i * kThreads, ahead[i]);
-    for (int i = tid + kAhead * kThreads; i < groups; i += kThreads) four(i, reinterpret_cast<const float4 *>(in + head)[i]);
+#pragma unroll 2
+    for (int i = tid + kAhead * kThreads; i < groups; i += kThreads) four(i, __ldcs(reinterpret_cast<const float4 *>(in + head) + i));
     if (g.max_bias == 0) return;
     // Biases, onto what this CTA has just written: the first entry of a token adds all of
-    // that token's, in their order.
+    // that token's, in their order. (Inside the pass above, each thread that met a token with
+    // a bias searching the list, 8 rows with 100 biases took 13.5 us for 10.7.)
     __syncthreads();
-    const int32_t *bt = g.bias_tokens + static_cast<int64_t>(m) * g.max_bias;
-    const float *bv = g.bias_values + static_cast<int64_t>(m) * g.max_bias;
+    const float *bias_values = g.bias_values + static_cast<int64_t>(m) * g.max_bias;
     for (int j = tid; j < g.max_bias; j += kThreads) {
-        const int v = bt[j];
-        if (v < v0 || v >= v0 + n || !allowed(t, v)) continue;
-        bool first = true;
-        for (int k = 0; k < j && first; ++k) first = bt[k] != v;
-        if (!first) continue;
-        float x = out[v - v0] + bv[j];
+        const int v = j < kThreads ? bias_token : __ldg(bias_tokens + j);
+        if (v < v0 || v >= v0 + n || !allowed(t.mask, v)) continue;
+        bool again = false;
+#pragma unroll 8
+        for (int k = 0; k < j; ++k) again |= __ldg(bias_tokens + k) == v;
+        if (again) continue;
+        float x = out[v - v0] + __ldg(bias_values + j);
+#pragma unroll 8
         for (int k = j + 1; k < g.max_bias; ++k)
-            if (bt[k] == v) x += bv[k];
+            if (__ldg(bias_tokens + k) == v) x += __ldg(bias_values + k);
         out[v - v0] = x;
     }
 }
@@ -185,34 +173,20 @@ __global__ void __launch_bounds__(kThreads, 2) logits_kernel(const __grid_consta
 cudaError_t launch_logits(const LogitsArgs &g, cudaStream_t s)
 {
     route_hit(kRouteLogits);
-    // Up to 8 CTAs a cluster, of 2048 tokens at least; more clusters a row (each reads the
-    // history) where the rows leave SMs idle, or a CTA's counts would not fit.
-    int cluster = kMaxCluster;
-    while (cluster > 1 && g.V < 2048 * cluster) cluster /= 2;
-    const int fill = std::max(1, std::min(2 * kSms / (cluster * g.M), g.V / (2048 * cluster)));
-    const int fit = (g.V + kMaxOwned * cluster - 1) / (kMaxOwned * cluster);
-    const int parts = std::max(fill, fit);
-    const int owned = ((g.V + parts * cluster - 1) / (parts * cluster) + 3) & ~3;
-    const bool vec = ((reinterpret_cast<uintptr_t>(g.logits) ^ reinterpret_cast<uintptr_t>(g.y)) & 15u) == 0;
-    auto kern = vec ? logits_kernel<true> : logits_kernel<false>;
-    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(kern), owned * 4);
+    int tile = kMinTile;
+    while (tile < kMaxTile && static_cast<int64_t>(g.M) * ((g.V + 2 * tile - 1) / (2 * tile)) >= kCtasPerSm * kSms) tile *= 2;
+    const size_t smem = static_cast<size_t>(tile + 4) * 4;
+    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(logits_kernel), static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    cudaLaunchAttribute attr[2];
+    cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kThreads);
-    cfg.gridDim = dim3(static_cast<unsigned>(parts * cluster), static_cast<unsigned>(g.M));
-    cfg.dynamicSmemBytes = static_cast<size_t>(owned) * 4;
+    cfg.gridDim = dim3(static_cast<unsigned>((g.V + tile - 1) / tile), static_cast<unsigned>(g.M));
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = set_launch_overlap_attr(attr);
-    if (cluster > 1) {
-        attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
-        attr[cfg.numAttrs].val.clusterDim.x = static_cast<unsigned>(cluster);
-        attr[cfg.numAttrs].val.clusterDim.y = 1;
-        attr[cfg.numAttrs].val.clusterDim.z = 1;
-        ++cfg.numAttrs;
-    }
-    return cudaLaunchKernelEx(&cfg, kern, g, owned, cluster);
+    return cudaLaunchKernelEx(&cfg, logits_kernel, g, tile);
 }
 
 cudaError_t read_error_word_logits(uint32_t *out, bool clear)

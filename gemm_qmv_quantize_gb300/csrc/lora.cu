@@ -11,7 +11,10 @@
 // The products run on m16n8k8 TF32: 16-bit weights (binary16 or bfloat16) and binary16
 // activations are exact in TF32, fp32 activations and A x go in as two terms whose sum
 // keeps 22 bits, and sums are fp32. Bound by the weights' bytes: one row an adapter leaves
-// 7 of the product's 8 columns empty and still reads memory at its rate.
+// 7 of the product's 8 columns empty and still reads memory at its rate. A lane's share of
+// the operands comes by asynchronous copies into shared memory of its own, several stages
+// ahead: 96 adapters of rank 64 beside 17408 x 5120 take 61 us, 4.8 TB/s (loads into
+// registers: 65 us), the expand launch 47 us of them.
 #include <algorithm>
 #include <type_traits>
 
@@ -28,8 +31,9 @@ namespace {
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kBlockRows = 8;      // rows of a block: the product's columns
 constexpr int kRankTile = 16;      // ranks of a shrink CTA, outputs of an expand step: the product's rows
-constexpr int kMaxRows = 96, kMaxRank = 256;
-constexpr int kSms = 152;
+constexpr int kMaxRows = 96;
+constexpr int kSms = 152, kCtasPerSm = 3;
+constexpr int kStages = 4;         // of 64 k or ranks, in flight for a warp
 
 // D(16x8) += A(16x8, row) B(8x8, col) in TF32. A lane (g = lane / 4, t = lane % 4) holds
 // a0 A[g][t], a1 A[g+8][t], a2 A[g][t+4], a3 A[g+8][t+4]; b0 B[t][g], b1 B[t+4][g];
@@ -114,13 +118,35 @@ __device__ __forceinline__ void list_rows(const LoraArgs &g, int m, int lane, in
     }
 }
 
+// 16 bytes global -> shared, or zeros.
+__device__ __forceinline__ void copy_or_zero(void *dst, const void *src, bool there)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the last n groups of this thread's copies have landed.
+template <int n>
+__device__ __forceinline__ void copies_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
+}
+
+template <typename X>
+constexpr int kXPieces = std::is_same_v<X, float> ? 2 : 1;   // 16-byte pieces of 8 activations
+
+template <typename X>
+constexpr int shrink_smem() { return kWarps * kStages * (4 + 2 * kXPieces<X>) * 512; }
+
 // Partial sums of A x: grid (rows, rank tiles, ranges of K). The CTA of a row's rank-th
-// sharer takes block `rank` of the rows, if there is one; a warp a range of warp_k.
+// sharer takes block `rank` of the rows, if there is one; a warp a range of warp_k, in
+// stages of 64.
 template <typename X, typename W>
 __global__ void __launch_bounds__(kThreads) lora_shrink_kernel(LoraArgs g, int warp_k)
 {
+    extern __shared__ __align__(16) uint8_t ring[];   // [warp][stage][piece][lane] of 16 bytes
     __shared__ float sums[kWarps][kRankTile][kBlockRows];
     __shared__ int rows[kBlockRows];
+    constexpr int kP = kXPieces<X>, kPieces = 4 + 2 * kP;
     const int m = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, t = lane & 3;
     grid_dependency_wait();
     grid_launch_dependents();
@@ -130,36 +156,55 @@ __global__ void __launch_bounds__(kThreads) lora_shrink_kernel(LoraArgs g, int w
     if (warp == 0) list_rows(g, m, lane, s.rank, rows);
     const int r0 = blockIdx.y * kRankTile;
     const int64_t k0 = (static_cast<int64_t>(blockIdx.z) * kWarps + warp) * warp_k, k1 = min(k0 + warp_k, g.K);
-    const W *a0 = static_cast<const W *>(g.a) + (static_cast<int64_t>(s.adapter) * g.R + r0 + gid) * g.K;
+    const W *a = static_cast<const W *>(g.a) + (static_cast<int64_t>(s.adapter) * g.R + r0 + gid) * g.K;
     const bool has0 = r0 + gid < g.R, has1 = r0 + gid + 8 < g.R;
+    const int stages = k1 > k0 ? static_cast<int>((k1 - k0 + 63) / 64) : 0;
+    uint4 *mine = reinterpret_cast<uint4 *>(ring) + (warp * kStages * kPieces) * 32 + lane;
+    auto piece = [&](int st, int i) { return mine + ((st % kStages) * kPieces + i) * 32; };
+    auto load_a = [&](int st) {
+        if (st >= stages) return;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const int64_t k = k0 + 64 * st + 32 * c + 8 * t;
+            const bool in = k < k1;
+            copy_or_zero(piece(st, 2 * c), in && has0 ? a + k : g.a, in && has0);
+            copy_or_zero(piece(st, 2 * c + 1), in && has1 ? a + 8 * g.K + k : g.a, in && has1);
+        }
+    };
+    for (int st = 0; st < kStages - 1; ++st) load_a(st);
     __syncthreads();
     const bool has_x = gid < nrows;
     const X *x = static_cast<const X *>(g.x) + (has_x ? rows[gid] : 0) * g.K;
-    const uint64_t stream = policy_evict_first();
-    float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int64_t kb = k0; kb < k1; kb += 128) {   // four steps' loads in flight
-        uint4 w0[4], w1[4];
-        constexpr int kXLoads = std::is_same_v<X, float> ? 2 : 1;
-        uint4 xv[4][kXLoads];
+    auto load_x = [&](int st) {
+        if (st < stages) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const int64_t k = kb + 32 * c + 8 * t;
-            const bool in = k < k1;
-            w0[c] = in && has0 ? ld_stream_v4(a0 + k, stream) : make_uint4(0, 0, 0, 0);
-            w1[c] = in && has1 ? ld_stream_v4(a0 + 8 * g.K + k, stream) : make_uint4(0, 0, 0, 0);
+            for (int c = 0; c < 2; ++c) {
+                const int64_t k = k0 + 64 * st + 32 * c + 8 * t;
+                const bool in = k < k1 && has_x;
 #pragma unroll
-            for (int i = 0; i < kXLoads; ++i)
-                xv[c][i] = in && has_x ? ld_shared_v4(reinterpret_cast<const uint4 *>(x + k) + i) : make_uint4(0, 0, 0, 0);
+                for (int i = 0; i < kP; ++i)
+                    copy_or_zero(piece(st, 4 + c * kP + i), in ? static_cast<const void *>(x + k + 4 * i) : g.x, in);
+            }
         }
+        copies_commit();
+    };
+    for (int st = 0; st < kStages - 1; ++st) load_x(st);
+    float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int st = 0; st < stages; ++st) {
+        copies_wait<kStages - 2>();
+        load_a(st + kStages - 1);   // (into the stage that this lane read last)
+        load_x(st + kStages - 1);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 2; ++c) {
             float hi[8], lo[8];
-            if constexpr (std::is_same_v<X, float>) {
-                const uint32_t v[8] = {xv[c][0].x, xv[c][0].y, xv[c][0].z, xv[c][0].w, xv[c][1].x, xv[c][1].y, xv[c][1].z, xv[c][1].w};
+            if constexpr (kP == 2) {
+                const uint4 p = *piece(st, 4 + 2 * c), q = *piece(st, 5 + 2 * c);
+                const uint32_t v[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
 #pragma unroll
                 for (int i = 0; i < 8; ++i) split_tf32(__uint_as_float(v[i]), hi[i], lo[i]);
             } else {
-                const uint32_t v[4] = {xv[c][0].x, xv[c][0].y, xv[c][0].z, xv[c][0].w};
+                const uint4 p = *piece(st, 4 + c);
+                const uint32_t v[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float2 f = widen<__half>(v[i]);
@@ -167,7 +212,7 @@ __global__ void __launch_bounds__(kThreads) lora_shrink_kernel(LoraArgs g, int w
                     hi[2 * i + 1] = f.y;
                 }
             }
-            mma_step<W, std::is_same_v<X, float>>(d, w0[c], w1[c], hi, lo);
+            mma_step<W, kP == 2>(d, *piece(st, 2 * c), *piece(st, 2 * c + 1), hi, lo);
         }
     }
     sums[warp][gid][2 * t] = d[0];
@@ -184,13 +229,18 @@ __global__ void __launch_bounds__(kThreads) lora_shrink_kernel(LoraArgs g, int w
     }
 }
 
+// Shared memory of an expand CTA: its warps' stages, then scale A x as two TF32 terms,
+// [2][8 rows][ranks + 4].
+constexpr int kExpandRing = kWarps * kStages * 4 * 512;
+int expand_smem(int R) { return kExpandRing + 2 * kBlockRows * (((R + 63) & ~63) + 4) * 4; }
+
 // y = base + scale B (A x): grid (rows, gridDim.y). The c sharers of an adapter have c x
 // gridDim.y CTAs: those of block b of the rows are the sharers b, b + blocks, ...; their
-// warps take the 16-output steps of N in turn.
+// warps take the 16-output steps of N in turn, in stages of 64 ranks.
 template <typename W>
 __global__ void __launch_bounds__(kThreads) lora_expand_kernel(LoraArgs g, int splits)
 {
-    __shared__ __align__(16) float ax[2][kBlockRows][kMaxRank + 4];   // scale A x as two TF32 terms
+    extern __shared__ __align__(16) uint8_t ring[];
     __shared__ int rows[kBlockRows];
     const int m = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, t = lane & 3;
     grid_launch_dependents();
@@ -205,27 +255,42 @@ __global__ void __launch_bounds__(kThreads) lora_expand_kernel(LoraArgs g, int s
     const int blocks = (s.count + kBlockRows - 1) / kBlockRows, block = s.rank % blocks;
     const int nrows = min(kBlockRows, s.count - block * kBlockRows);
     const int mine = s.rank / blocks, ctas = (s.count - block + blocks - 1) / blocks;
-    const int64_t steps = (g.N + kRankTile - 1) / kRankTile, stride = static_cast<int64_t>(ctas) * gridDim.y * kWarps;
-    int64_t step = (static_cast<int64_t>(mine) * gridDim.y + blockIdx.y) * kWarps + warp;
+    const int64_t all = (g.N + kRankTile - 1) / kRankTile;
+    const int stride = ctas * static_cast<int>(gridDim.y) * kWarps;
+    const int first = (mine * static_cast<int>(gridDim.y) + static_cast<int>(blockIdx.y)) * kWarps + warp;
+    const int steps = first < all ? static_cast<int>((all - first + stride - 1) / stride) : 0;   // of this warp
+    const int per = (g.R + 63) / 64, stages = steps * per;   // stages a step, and of this warp
     const W *b = static_cast<const W *>(g.b) + static_cast<int64_t>(s.adapter) * g.N * g.R;
-    const uint64_t stream = policy_evict_first();
-    // 64 ranks of a step: lane (g, t) holds ranks 32 c + 8 t .. + 7 of outputs g and g + 8
-    uint4 w[2][2];
-    auto load = [&](int64_t st, int r0) {
-        const int64_t n = st * kRankTile + gid;
+    uint4 *own = reinterpret_cast<uint4 *>(ring) + warp * kStages * 4 * 32 + lane;
+    auto piece = [&](int st, int i) { return own + ((st % kStages) * 4 + i) * 32; };
+    // the next stage to load: lane (g, t) has ranks 32 c + 8 t .. + 7 of outputs g and g + 8
+    int next = 0, next_r = 0;
+    int64_t next_n = static_cast<int64_t>(first) * kRankTile + gid;
+    auto load = [&]() {
+        if (next < stages) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            const int r = r0 + 32 * c + 8 * t;
-            w[c][0] = n < g.N && r < g.R ? ld_stream_v4(b + n * g.R + r, stream) : make_uint4(0, 0, 0, 0);
-            w[c][1] = n + 8 < g.N && r < g.R ? ld_stream_v4(b + (n + 8) * g.R + r, stream) : make_uint4(0, 0, 0, 0);
+            for (int c = 0; c < 2; ++c) {
+                const int r = next_r + 32 * c + 8 * t;
+                const bool in0 = next_n < g.N && r < g.R, in1 = next_n + 8 < g.N && r < g.R;
+                copy_or_zero(piece(next, 2 * c), in0 ? b + next_n * g.R + r : b, in0);
+                copy_or_zero(piece(next, 2 * c + 1), in1 ? b + (next_n + 8) * g.R + r : b, in1);
+            }
+        }
+        copies_commit();
+        ++next;
+        next_r += 64;
+        if (next_r >= g.R) {
+            next_r = 0;
+            next_n += static_cast<int64_t>(stride) * kRankTile;
         }
     };
-    if (step < steps) load(step, 0);
+    for (int i = 0; i < kStages - 1; ++i) load();
     if (warp == 0) list_rows(g, m, lane, block, rows);
     __syncthreads();
     grid_dependency_wait();
     const float scale = __ldg(g.scale + s.adapter);
-    const int ranks = (g.R + 63) & ~63;
+    const int ranks = per * 64, pitch = ranks + 4;
+    float *ax = reinterpret_cast<float *>(ring + kExpandRing), *ax_lo = ax + kBlockRows * pitch;
     for (int i = tid; i < kBlockRows * ranks; i += kThreads) {
         const int row = i / ranks, r = i % ranks;
         float sum = 0.0f;
@@ -234,42 +299,48 @@ __global__ void __launch_bounds__(kThreads) lora_expand_kernel(LoraArgs g, int s
 #pragma unroll 4
             for (int k = 0; k < splits; ++k) sum += p[static_cast<int64_t>(k) * g.M * g.R];
         }
-        float hi, lo;
-        split_tf32(sum * scale, hi, lo);
-        ax[0][row][r] = hi;
-        ax[1][row][r] = lo;
+        split_tf32(sum * scale, ax[row * pitch + r], ax_lo[row * pitch + r]);
     }
     __syncthreads();
-    for (; step < steps; step += stride) {
-        // the projection's output for this step: rows 2 t and 2 t + 1, outputs g and g + 8
-        float out[4];
-        int64_t at[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t n = step * kRankTile + gid + (i & 2 ? 8 : 0);
-            const int row = 2 * t + (i & 1);
-            at[i] = row < nrows && n < g.N ? rows[row] * g.N + n : -1;
-            out[i] = at[i] >= 0 ? g.base[at[i]] : 0.0f;
-        }
+    // the projection's output for a step, loaded a step ahead: rows 2 t and 2 t + 1 (the
+    // place of output 0, or -1), outputs g and g + 8
+    const int64_t row0 = 2 * t < nrows ? rows[2 * t] * g.N : -1, row1 = 2 * t + 1 < nrows ? rows[2 * t + 1] * g.N : -1;
+    float before[4];
+    auto load_base = [&](int i) {
+        const int64_t n = (static_cast<int64_t>(first) + static_cast<int64_t>(i) * stride) * kRankTile + gid;
+        before[0] = i < steps && row0 >= 0 && n < g.N ? g.base[row0 + n] : 0.0f;
+        before[1] = i < steps && row1 >= 0 && n < g.N ? g.base[row1 + n] : 0.0f;
+        before[2] = i < steps && row0 >= 0 && n + 8 < g.N ? g.base[row0 + n + 8] : 0.0f;
+        before[3] = i < steps && row1 >= 0 && n + 8 < g.N ? g.base[row1 + n + 8] : 0.0f;
+    };
+    load_base(0);
+    for (int i = 0, st = 0; i < steps; ++i) {
+        const float now[4] = {before[0], before[1], before[2], before[3]};
+        load_base(i + 1);
         float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int r0 = 0; r0 < g.R; r0 += 64) {
-            uint4 now[2][2] = {{w[0][0], w[0][1]}, {w[1][0], w[1][1]}};
-            const bool more = r0 + 64 < g.R;
-            if (more || step + stride < steps) load(more ? step : step + stride, more ? r0 + 64 : 0);
+        for (int r0 = 0; r0 < g.R; r0 += 64, ++st) {
+            copies_wait<kStages - 2>();
+            load();   // (into the stage that this lane read last)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 float hi[8], lo[8];
 #pragma unroll
-                for (int i = 0; i < 8; i += 4) {
-                    *reinterpret_cast<float4 *>(hi + i) = *reinterpret_cast<const float4 *>(&ax[0][gid][r0 + 32 * c + 8 * t + i]);
-                    *reinterpret_cast<float4 *>(lo + i) = *reinterpret_cast<const float4 *>(&ax[1][gid][r0 + 32 * c + 8 * t + i]);
+                for (int j = 0; j < 8; j += 4) {
+                    *reinterpret_cast<float4 *>(hi + j) = *reinterpret_cast<const float4 *>(ax + gid * pitch + r0 + 32 * c + 8 * t + j);
+                    *reinterpret_cast<float4 *>(lo + j) = *reinterpret_cast<const float4 *>(ax_lo + gid * pitch + r0 + 32 * c + 8 * t + j);
                 }
-                mma_step<W, true>(d, now[c][0], now[c][1], hi, lo);
+                mma_step<W, true>(d, *piece(st, 2 * c), *piece(st, 2 * c + 1), hi, lo);
             }
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (at[i] >= 0) g.y[at[i]] = out[i] + d[i];
+        const int64_t n = (static_cast<int64_t>(first) + static_cast<int64_t>(i) * stride) * kRankTile + gid;
+        if (n < g.N) {
+            if (row0 >= 0) g.y[row0 + n] = now[0] + d[0];
+            if (row1 >= 0) g.y[row1 + n] = now[1] + d[1];
+        }
+        if (n + 8 < g.N) {
+            if (row0 >= 0) g.y[row0 + n + 8] = now[2] + d[2];
+            if (row1 >= 0) g.y[row1 + n + 8] = now[3] + d[3];
+        }
     }
 }
 
@@ -293,17 +364,24 @@ cudaError_t launch_both(const LoraArgs &g, cudaStream_t s)
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = {};
     const int splits = static_cast<int>(shrink_splits(g.M, g.R, g.K));
+    const void *shrink = reinterpret_cast<const void *>(lora_shrink_kernel<X, W>);
+    const void *expand = reinterpret_cast<const void *>(lora_expand_kernel<W>);
+    cudaError_t e = ensure_smem_attr(shrink, shrink_smem<X>());
+    if (e == cudaSuccess) e = ensure_smem_attr(expand, expand_smem(g.R));
+    if (e != cudaSuccess) return e;
     cfg.blockDim = dim3(kThreads);
     cfg.gridDim = dim3(static_cast<unsigned>(g.M), static_cast<unsigned>((g.R + kRankTile - 1) / kRankTile), static_cast<unsigned>(splits));
+    cfg.dynamicSmemBytes = static_cast<size_t>(shrink_smem<X>());
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = set_launch_overlap_attr(attr);
-    cudaError_t e = cudaLaunchKernelEx(&cfg, lora_shrink_kernel<X, W>, g, shrink_k(g.M, g.R, g.K));
-    if (e != cudaSuccess) return e;
-    // starts beside the shrink launch, loads its first weights and waits for it; CTAs for
-    // one step a warp, but no more than eight an SM
+    if ((e = cudaLaunchKernelEx(&cfg, lora_shrink_kernel<X, W>, g, shrink_k(g.M, g.R, g.K))) != cudaSuccess) return e;
+    // Starts beside the shrink launch, loads its first weights and waits for it. CTAs for one
+    // step a warp, but no more than the three an SM that fit: eight took 9.1 us for 7.0 (8
+    // rows, 14336 x 4096) and 20 for 15 (96 rows that share one adapter).
     const int64_t tiles = (g.N + kRankTile * kWarps - 1) / (kRankTile * kWarps);
-    cfg.gridDim = dim3(static_cast<unsigned>(g.M), static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(tiles, 8 * kSms / g.M))));
+    cfg.gridDim = dim3(static_cast<unsigned>(g.M), static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(tiles, kCtasPerSm * kSms / g.M))));
+    cfg.dynamicSmemBytes = static_cast<size_t>(expand_smem(g.R));
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.numAttrs = 1;

@@ -350,7 +350,7 @@ QMV_API qmv_status qmv_prefix_attention(const void *q, const void *k_cache, cons
  *   if n > 0: x = x - (frequency[m] * n + presence[m])
  *   x = x + the biases that name v, in their order;  y[m][v] = mask bit v ? x : -inf
  *   logits, y  fp32 [M][V], M = 0..65535, V up to 2^30; y may be logits.
- *   tokens     int32 [M][max_history], the prompt's tokens before the answer's; negative
+ *   tokens     int32 [M][max_history], max_history up to 2^29, the prompt's tokens before the answer's; negative
  *              ones are skipped, those of V or more too (bit 2). total_len above
  *              max_history is cut to it (bit 2). prompt_len, total_len int32 [M].
  *   repetition, presence, frequency fp32 [M], each NULL for none (1, 0, 0).
