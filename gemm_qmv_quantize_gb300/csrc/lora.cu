@@ -10,7 +10,9 @@
 //
 // The products run on m16n8k8 TF32: 16-bit weights (binary16 or bfloat16) and binary16
 // activations are exact in TF32, fp32 activations and A x go in as two terms whose sum
-// keeps 22 bits, and sums are fp32. Bound by the weights' bytes: one row an adapter leaves
+// keeps 22 bits. The tensor core cuts its running sums, so that a stage of 64 has sums of
+// its own (8 products long) that are added in fp32, rounded: chains over all of K were off by
+// 7e-7 of the outputs (5120 long). Bound by the weights' bytes: one row an adapter leaves
 // 7 of the product's 8 columns empty and still reads memory at its rate. A lane's share of
 // the operands comes by asynchronous copies into shared memory of its own, several stages
 // ahead: 96 adapters of rank 64 beside 17408 x 5120 take 61 us, 4.8 TB/s (loads into
@@ -68,16 +70,16 @@ __device__ __forceinline__ float2 widen(uint32_t two)
 
 // One step of 32 k on a 16 x 8 tile: lane (g, t) holds k 8t .. 8t + 7 of rows g and g + 8
 // (w0, w1) and of column g (hi, and lo where `two` terms); the order of k within a product
-// is free, as long as both operands have the same.
+// is free, as long as both operands have the same. The second terms have sums of their own.
 template <typename W, bool kTwo>
-__device__ __forceinline__ void mma_step(float (&d)[4], uint4 w0, uint4 w1, const float (&hi)[8], const float (&lo)[8])
+__device__ __forceinline__ void mma_step(float (&d)[4], float (&e)[4], uint4 w0, uint4 w1, const float (&hi)[8], const float (&lo)[8])
 {
     const uint32_t a[4] = {w0.x, w0.y, w0.z, w0.w}, b[4] = {w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const float2 p = widen<W>(a[j]), q = widen<W>(b[j]);
         mma_tf32(d, p.x, q.x, p.y, q.y, hi[2 * j], hi[2 * j + 1]);
-        if constexpr (kTwo) mma_tf32(d, p.x, q.x, p.y, q.y, lo[2 * j], lo[2 * j + 1]);
+        if constexpr (kTwo) mma_tf32(e, p.x, q.x, p.y, q.y, lo[2 * j], lo[2 * j + 1]);
     }
 }
 
@@ -194,6 +196,7 @@ __global__ void __launch_bounds__(kThreads) lora_shrink_kernel(LoraArgs g, int w
         copies_wait<kStages - 2>();
         load_a(st + kStages - 1);   // (into the stage that this lane read last)
         load_x(st + kStages - 1);
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f}, rest[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
             float hi[8], lo[8];
@@ -212,8 +215,10 @@ __global__ void __launch_bounds__(kThreads) lora_shrink_kernel(LoraArgs g, int w
                     hi[2 * i + 1] = f.y;
                 }
             }
-            mma_step<W, kP == 2>(d, *piece(st, 2 * c), *piece(st, 2 * c + 1), hi, lo);
+            mma_step<W, kP == 2>(sum, rest, *piece(st, 2 * c), *piece(st, 2 * c + 1), hi, lo);
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[i] += sum[i] + rest[i];
     }
     sums[warp][gid][2 * t] = d[0];
     sums[warp][gid][2 * t + 1] = d[1];
@@ -321,6 +326,7 @@ __global__ void __launch_bounds__(kThreads) lora_expand_kernel(LoraArgs g, int s
         for (int r0 = 0; r0 < g.R; r0 += 64, ++st) {
             copies_wait<kStages - 2>();
             load();   // (into the stage that this lane read last)
+            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f}, rest[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 float hi[8], lo[8];
@@ -329,8 +335,10 @@ __global__ void __launch_bounds__(kThreads) lora_expand_kernel(LoraArgs g, int s
                     *reinterpret_cast<float4 *>(hi + j) = *reinterpret_cast<const float4 *>(ax + gid * pitch + r0 + 32 * c + 8 * t + j);
                     *reinterpret_cast<float4 *>(lo + j) = *reinterpret_cast<const float4 *>(ax_lo + gid * pitch + r0 + 32 * c + 8 * t + j);
                 }
-                mma_step<W, true>(d, *piece(st, 2 * c), *piece(st, 2 * c + 1), hi, lo);
+                mma_step<W, true>(sum, rest, *piece(st, 2 * c), *piece(st, 2 * c + 1), hi, lo);
             }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) d[j] += sum[j] + rest[j];
         }
         const int64_t n = (static_cast<int64_t>(first) + static_cast<int64_t>(i) * stride) * kRankTile + gid;
         if (n < g.N) {
@@ -344,7 +352,7 @@ __global__ void __launch_bounds__(kThreads) lora_expand_kernel(LoraArgs g, int s
     }
 }
 
-// K of a shrink warp: 512 (at most 64 products in a chain of sums) where that fills the SMs
+// K of a shrink warp: 512 where that fills the SMs
 // twice, else 128, one round of loads.
 int shrink_k(int M, int R, int64_t K)
 {

@@ -689,25 +689,26 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     }
 }
 
-// Joins the partial results of 32 rows of a key head, a row a lane and 8 of D a warp:
+// Joins the partial results of 32 rows of a key head for 32 of D, a row a lane and 8 of D a
+// warp (a CTA for all of D left most SMs idle: 8 us for 24 requests, for XX):
 // weights 2^(lse - max) over their sum, of up to kJoinSlots slots at a time, computed once
 // for all warps. Bound by latency, so that the loads of eight slots are in flight.
 constexpr int kJoinSlots = 64;
 template <typename T, int kD>
-__global__ void __launch_bounds__(32 * kD / 8) attention_join_kernel(const __grid_constant__ AttnParams p)
+__global__ void __launch_bounds__(128) attention_join_kernel(const __grid_constant__ AttnParams p)
 {
     __shared__ float weight[kJoinSlots][32];
-    constexpr int kWarps = kD / 8;
+    constexpr int kWarps = 4, kParts = kD / 32;
     const AttnArgs &g = p.g;
-    const int lane = threadIdx.x & 31, warp = static_cast<int>(threadIdx.x >> 5);
-    const int block = static_cast<int>(blockIdx.x) % p.row_blocks, h = static_cast<int>(blockIdx.x) / p.row_blocks;
+    const int lane = threadIdx.x & 31, warp = static_cast<int>(threadIdx.x >> 5), d0 = static_cast<int>(blockIdx.x) % kParts * 32 + warp * 8;
+    const int block = static_cast<int>(blockIdx.x) / kParts % p.row_blocks, h = static_cast<int>(blockIdx.x) / kParts / p.row_blocks;
     const int G = g.Hq / g.Hkv, i = block * 32 + lane;
     const bool live = i < g.B * g.T * G;
     // these rows' prefix slots: those of their row group
     const int slots = p.plan.own_splits + (block * 32 < p.plan.pair_groups * 2 * kTile ? p.plan.pair_splits : p.plan.lone_splits);
     const int64_t per_slot = static_cast<int64_t>(g.Hkv) * p.row_blocks * 32;
     const float *lse = p.lse + static_cast<int64_t>(h) * p.row_blocks * 32 + i;
-    const float4 *part = reinterpret_cast<const float4 *>(p.part) + (static_cast<int64_t>(h) * p.row_blocks + block) * 8 * kD + warp * 64 + lane;
+    const float4 *part = reinterpret_cast<const float4 *>(p.part) + (static_cast<int64_t>(h) * p.row_blocks + block) * 8 * kD + d0 * 8 + lane;
     grid_launch_dependents();
     grid_dependency_wait();
     float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f}, sum = 0.0f, top = -INFINITY;
@@ -754,7 +755,7 @@ __global__ void __launch_bounds__(32 * kD / 8) attention_join_kernel(const __gri
     out.y = pack2<T>(acc[2] * inv, acc[3] * inv);
     out.z = pack2<T>(acc[4] * inv, acc[5] * inv);
     out.w = pack2<T>(acc[6] * inv, acc[7] * inv);
-    *reinterpret_cast<uint4 *>(static_cast<T *>(g.out) + (static_cast<int64_t>(i / G) * g.Hq + h * G + i % G) * kD + warp * 8) = out;
+    *reinterpret_cast<uint4 *>(static_cast<T *>(g.out) + (static_cast<int64_t>(i / G) * g.Hq + h * G + i % G) * kD + d0) = out;
 }
 
 cudaError_t encode_cache_map(CUtensorMap *map, const void *cache, const AttnArgs &g)
@@ -787,8 +788,8 @@ cudaError_t launch_typed(const AttnParams &p, int sm_count, cudaStream_t s)
         cfg.numAttrs = set_launch_overlap_attr(attr);
         if ((e = cudaLaunchKernelEx(&cfg, kern, p)) != cudaSuccess) return e;
     }
-    cfg.blockDim = dim3(32 * kD / 8);
-    cfg.gridDim = dim3(static_cast<unsigned>(p.row_blocks * g.Hkv));
+    cfg.blockDim = dim3(128);
+    cfg.gridDim = dim3(static_cast<unsigned>(p.row_blocks * g.Hkv * (kD / 32)));
     cfg.dynamicSmemBytes = 0;
     if (jobs > 0) {   // starts as the last jobs run, and waits for all of them
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
