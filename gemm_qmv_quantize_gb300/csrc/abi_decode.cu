@@ -116,10 +116,7 @@ qmv_status qmv_prefix_attention(const void *q, const void *k_cache, const void *
     const int64_t need = attn_workspace_bytes(B, T, Hq, Hkv, D, prefix_len, max_own);
     if (need > 0 && !workspace) return QMV_ERR_NULL;
     if (workspace_bytes < need) return QMV_ERR_SHAPE;
-    DeviceInfo dev;
-    if (current_device_info(&dev) != cudaSuccess) return QMV_ERR_CUDA;
-    return from_cuda(launch_attention(dev,
-                                      AttnArgs{q, k_cache, v_cache, prefix_table, own_table, own_len, out, workspace,
+    return from_cuda(launch_attention(AttnArgs{q, k_cache, v_cache, prefix_table, own_table, own_len, out, workspace,
                                                n_pages, prefix_len, max_own, scale, type, page, own_pages, B, T, Hq,
                                                Hkv, D},
                                       stream));

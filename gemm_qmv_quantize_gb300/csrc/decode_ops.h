@@ -52,7 +52,7 @@ struct AttnArgs {
     int type, page, own_pages, B, T, Hq, Hkv, D;
 };
 int64_t attn_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int64_t prefix_len, int64_t max_own);
-cudaError_t launch_attention(const DeviceInfo &dev, const AttnArgs &g, cudaStream_t s);
+cudaError_t launch_attention(const AttnArgs &g, cudaStream_t s);
 
 // ---- logits
 struct LogitsArgs {

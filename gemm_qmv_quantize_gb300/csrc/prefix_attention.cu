@@ -48,6 +48,7 @@ constexpr int kTmemCols = 512;
 constexpr int kMaxSlots = 8;
 constexpr int kSmemBytes = 232448 - 3072;   // dynamic shared memory: a CTA's limit but the barriers and statistics
 constexpr int kSms = 152;
+constexpr int kFewRows = 64;            // rows of a request and key head up to which its own keys have a kernel of their own
 constexpr float kSlack = 8.0f;          // log2 of the growth of a row's maximum that rescales O
 
 // Splits of the work, by sizes alone.
@@ -55,42 +56,63 @@ struct AttnPlan {
     int pair_groups, lone;              // row groups of the prefix: of 256 rows, and one of up to 128
     int pair_splits, lone_splits;       // ranges of prefix tiles for each
     int own_groups, own_splits, own_tiles;   // row groups of a request, ranges of own_tiles own tiles
+    int few_row_tiles, few_keys;        // requests of few rows, by the kernel for those: 16-row tiles, keys a range
+    int64_t few_jobs;
     int64_t prefix_jobs, own_jobs;
+    int prefix_ctas, own_ctas;          // CTAs that take the ones, and the others, in turn
     int slots;                          // partial results a row: own_splits, then the prefix's
 };
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// The prefix's jobs fill the SMs once: ranges are cut to the same cost, of two tiles at
-// least (a tile a stream). A tile costs a pair of streams about 3100 cycles and, where the
-// streams take every other tile, 2000 a tile: 3 to 2. Own keys: a range a request where the requests and key heads fill the
-// SMs, else as many as fill them, of 256 keys at least.
+// Costs, in thousands of cycles as measured: a tile 3 for a pair of streams, 2 where the
+// streams take every other tile; a job 8 beside its tiles. The SMs are divided
+// between the prefix and the own keys by their shares of the cost (own lengths are on the
+// device: 0.6 of the bound is taken), so that no CTA starts on the one after the other; the
+// prefix is then cut into a range a CTA, of equal cost and two tiles at least, and own keys
+// into ranges that leave each CTA several, of two tiles at least.
 AttnPlan plan_attention(int B, int T, int Hq, int Hkv, int64_t prefix_len, int64_t max_own)
 {
     AttnPlan p{};
     const int64_t G = Hq / Hkv, rows = static_cast<int64_t>(B) * T * G, tiles = ceil_div(prefix_len, kTile);
+    const int64_t own_tiles = ceil_div(max_own, kTile);
+    int64_t own_cost = 0, prefix_cost = 0;
+    if (own_tiles > 0 && rows > 0 && T * G <= kFewRows) {
+        // ranges of 256 keys at least (four steps a warp), for four CTAs a place on the SMs
+        p.few_row_tiles = static_cast<int>(ceil_div(T * G, 16));
+        const int64_t jobs = static_cast<int64_t>(B) * Hkv * p.few_row_tiles;
+        const int64_t splits = std::max<int64_t>(1, std::min<int64_t>({8 * kSms / jobs, ceil_div(max_own, 256), 256}));
+        p.few_keys = static_cast<int>(ceil_div(ceil_div(max_own, splits), 64) * 64);
+        p.own_splits = static_cast<int>(ceil_div(max_own, p.few_keys));
+        p.few_jobs = jobs * p.own_splits;
+    } else if (own_tiles > 0 && rows > 0) {
+        p.own_groups = static_cast<int>(ceil_div(T * G, 2 * kTile));
+        const int64_t jobs = static_cast<int64_t>(B) * Hkv * p.own_groups;
+        const int64_t most = std::max<int64_t>({2, jobs * own_tiles / (2 * kSms), ceil_div(own_tiles, 256)});
+        const int64_t splits = ceil_div(own_tiles, most);
+        p.own_tiles = static_cast<int>(ceil_div(own_tiles, splits));
+        p.own_splits = static_cast<int>(ceil_div(own_tiles, p.own_tiles));
+        p.own_jobs = jobs * p.own_splits;
+        own_cost = 8 * p.own_jobs + jobs * own_tiles * 6 / 5;
+    }
     if (tiles > 0 && rows > 0) {
         const int64_t row_tiles = ceil_div(rows, kTile);
         p.pair_groups = static_cast<int>(row_tiles / 2);
         p.lone = static_cast<int>(row_tiles % 2);
-        const int64_t cost = Hkv * (3 * p.pair_groups + 2 * p.lone) * tiles;
-        const int64_t budget = std::max<int64_t>(4, ceil_div(cost, kSms));
+        prefix_cost = Hkv * ((3 * p.pair_groups + 2 * p.lone) * tiles + 8 * (p.pair_groups + p.lone));
+        int64_t ctas = own_cost == 0 ? kSms : std::min<int64_t>(std::max<int64_t>({1, kSms * prefix_cost / (prefix_cost + own_cost), kSms - p.own_jobs}), kSms - 1);
+        const int64_t budget = std::max<int64_t>(4, ceil_div(prefix_cost, ctas));
         auto splits = [&](int64_t per_tile) {
             return static_cast<int>(std::min<int64_t>({std::max<int64_t>(1, (per_tile * tiles + budget / 2) / budget), tiles, 256}));
         };
         p.pair_splits = p.pair_groups ? splits(3) : 0;
         p.lone_splits = p.lone ? splits(2) : 0;
         p.prefix_jobs = Hkv * (static_cast<int64_t>(p.pair_groups) * p.pair_splits + p.lone_splits);
+        // a CTA a range, unless whole row groups are several a CTA
+        if (p.pair_splits > 1 || p.lone_splits > 1) ctas = std::max<int64_t>(ctas, p.prefix_jobs);
+        p.prefix_ctas = static_cast<int>(std::min<int64_t>({ctas, p.prefix_jobs, own_cost == 0 ? kSms : kSms - 1}));
     }
-    const int64_t own_tiles = ceil_div(max_own, kTile);
-    if (own_tiles > 0 && rows > 0) {
-        p.own_groups = static_cast<int>(ceil_div(T * G, 2 * kTile));
-        const int64_t jobs = static_cast<int64_t>(B) * Hkv * p.own_groups;
-        const int64_t want = std::max<int64_t>(1, std::min<int64_t>({kSms / jobs, ceil_div(own_tiles, 2), 256}));
-        p.own_tiles = static_cast<int>(ceil_div(own_tiles, want));
-        p.own_splits = static_cast<int>(ceil_div(own_tiles, p.own_tiles));
-        p.own_jobs = jobs * p.own_splits;
-    }
+    p.own_ctas = static_cast<int>(std::min<int64_t>(p.own_jobs, kSms - p.prefix_ctas));
     p.slots = p.own_splits + std::max(p.pair_splits, p.lone_splits);
     return p;
 }
@@ -104,6 +126,7 @@ struct AttnParams {
     // log2 of the sum of exponentials; -inf: no key (and no partial result).
     float *part, *lse;
     int row_blocks;
+    bool chained;        // launched beside the own-key kernel: waits for that at its end
 };
 
 __device__ __forceinline__ float exp2_fast(float x)
@@ -289,7 +312,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     const AttnArgs &g = p.g;
     // (the product and loading warps are the CTA's first)
     const int tid = (threadIdx.x + 256) % kThreads, warp = tid >> 5, lane = tid & 31;
-    const int G = g.Hq / g.Hkv, jobs = static_cast<int>(p.plan.prefix_jobs + p.plan.own_jobs), stride = static_cast<int>(gridDim.x);
+    const int G = g.Hq / g.Hkv, cta = static_cast<int>(blockIdx.x);
+    // this CTA's jobs: id, id + stride, ... below `jobs`
+    const bool on_prefix = cta < p.plan.prefix_ctas;
+    const int jobs = static_cast<int>(p.plan.prefix_jobs + (on_prefix ? 0 : p.plan.own_jobs));
+    const int stride = on_prefix ? p.plan.prefix_ctas : p.plan.own_ctas;
     auto fail = [&]() { note_wait_timeout(&g_attention_error, abort_word); };
     auto wait_all = [&](uint64_t *bar, uint32_t parity) {
         return __all_sync(0xffffffffu, wait_for(bar, parity) ? 1 : 0) != 0;
@@ -335,10 +362,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
-    grid_dependency_wait();
+    if (!p.chained) grid_dependency_wait();   // (chained: the own-key kernel began after the inputs were there)
     grid_launch_dependents();
 
-    int id = static_cast<int>(blockIdx.x);
+    int id = on_prefix ? cta : static_cast<int>(p.plan.prefix_jobs) + cta - p.plan.prefix_ctas;
     int len = own_length(p, id);
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
@@ -681,11 +708,244 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         __syncwarp();
     }
     }
+    if (p.chained) grid_dependency_wait();   // whoever waits for this launch waits for both
     tc_fence_before();
     __syncthreads();
     if (warp == kMmaWarp) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    }
+}
+
+// ---- a request's own keys against its few rows (T G <= 64)
+//
+// A decode step's requests have a handful of rows each and no key in common: bound by the
+// bytes of K and V. A CTA takes 16 rows (m16n8k16 products) and a range of keys; its four
+// warps take 16 keys in turn, each with a ring of asynchronous copies, statistics and output
+// sums of its own, so that nothing waits for anything but memory, and are joined at the end.
+// (As jobs of the kernel above, 128 rows a product and one range at a time an SM, 64
+// requests of up to 1024 keys took 51 us; so XX.)
+constexpr int kFewWarps = 4, kFewStages = 3;
+template <int kD>
+constexpr int few_smem() { return kFewWarps * kFewStages * 2 * 16 * kD * 2; }
+
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+template <typename T>
+__device__ __forceinline__ void mma_16bit(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    if constexpr (std::is_same_v<T, __half>) {
+        mma_16816(d, a[0], a[1], a[2], a[3], b0, b1);
+    } else {
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    }
+}
+
+template <typename T, int kD>
+__global__ void __launch_bounds__(32 * kFewWarps) few_rows_kernel(const __grid_constant__ AttnParams p)
+{
+    constexpr float kLift = std::is_same_v<T, __half> ? 6.0f : 0.0f;   // as above
+    constexpr int kRowBytes = kD * 2, kTileBytes = 16 * kRowBytes, kPieces = kD / 8;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ float stat_m[kFewWarps][16], stat_l[kFewWarps][16];
+    const AttnArgs &g = p.g;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, t = lane & 3;
+    const int G = g.Hq / g.Hkv, per = g.T * G;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    int id = static_cast<int>(blockIdx.x);
+    const int rt = id % p.plan.few_row_tiles;
+    id /= p.plan.few_row_tiles;
+    const int split = id % p.plan.own_splits;
+    id /= p.plan.own_splits;
+    const int h = id % g.Hkv, b = id / g.Hkv;
+    int64_t len = g.own_len[b];
+    if (len > g.max_own) {
+        if (tid == 0) atomicOr(&g_attention_error, kErrIndex);
+        len = g.max_own;
+    }
+    const int i0 = b * per + rt * 16, nrows = min(16, per - rt * 16);
+    const int64_t out_row0 = (static_cast<int64_t>(split) * g.Hkv + h) * p.row_blocks * 32 + i0;
+    const int64_t key0 = static_cast<int64_t>(split) * p.plan.few_keys;
+    const int keys = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(p.plan.few_keys), len - key0)));
+    if (keys == 0) {
+        if (tid < nrows) p.lse[out_row0 + tid] = -INFINITY;
+        return;
+    }
+    // ---- this warp's 16-key tiles warp, warp + 4, ...: page lookup and copies
+    const int ntiles = (keys + 15) / 16, mine = (ntiles - warp + kFewWarps - 1) / kFewWarps;
+    const int32_t *table = g.own_table + static_cast<int64_t>(b) * g.own_pages;
+    const int shift = __ffs(g.page) - 1;
+    uint8_t *ring = smem + warp * kFewStages * 2 * kTileBytes;
+    auto page_of = [&](int x) { return x < mine ? __ldg(table + ((key0 + (warp + kFewWarps * x) * 16) >> shift)) : 0; };
+    auto load = [&](int x, int page) {
+        if (x < mine) {
+            const int k = (warp + kFewWarps * x) * 16;   // first key, from key0
+            const bool there = page >= 0 && page < g.n_pages;   // (elsewhere: zeros)
+            if (!there && lane == 0) atomicOr(&g_attention_error, kErrIndex);
+            const int64_t at = ((static_cast<int64_t>(there ? page : 0) * g.page + ((key0 + k) & (g.page - 1))) * g.Hkv + h) * kD;
+            const T *kc = static_cast<const T *>(g.k_cache) + at, *vc = static_cast<const T *>(g.v_cache) + at;
+            uint8_t *dst = ring + (x % kFewStages) * 2 * kTileBytes;
+#pragma unroll
+            for (int i = 0; i < 16 * kPieces / 32; ++i) {
+                const int key = (i * 32 + lane) / kPieces, c = (i * 32 + lane) % kPieces;
+                const int64_t off = static_cast<int64_t>(key) * g.Hkv * kD + 8 * c;
+                const int n = there && k + key < keys ? 16 : 0;   // past the last key: zeros, whatever is there
+                const uint32_t to = smem_addr(dst) + key * kRowBytes + 16 * (c ^ (key & 7));
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(n ? kc + off : kc), "r"(n) : "memory");
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + kTileBytes), "l"(n ? vc + off : vc), "r"(n) : "memory");
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    int ahead[kFewStages - 1];
+#pragma unroll
+    for (int x = 0; x < kFewStages - 1; ++x) ahead[x] = page_of(x);
+    int page = page_of(kFewStages - 1);
+#pragma unroll
+    for (int x = 0; x < kFewStages - 1; ++x) load(x, ahead[x]);
+    // ---- Q: row gid and gid + 8 of the tile, 16 of D a step
+    uint32_t q[kD / 16][4];
+    {
+        const int ra = i0 + gid, rb = i0 + gid + 8;
+        const bool has_a = gid < nrows, has_b = gid + 8 < nrows;
+        const uint32_t *qa = reinterpret_cast<const uint32_t *>(static_cast<const T *>(g.q) + (static_cast<int64_t>(ra / G) * g.Hq + h * G + ra % G) * kD);
+        const uint32_t *qb = reinterpret_cast<const uint32_t *>(static_cast<const T *>(g.q) + (static_cast<int64_t>(rb / G) * g.Hq + h * G + rb % G) * kD);
+#pragma unroll
+        for (int k = 0; k < kD / 16; ++k) {
+            q[k][0] = has_a ? __ldg(qa + 8 * k + t) : 0u;
+            q[k][1] = has_b ? __ldg(qb + 8 * k + t) : 0u;
+            q[k][2] = has_a ? __ldg(qa + 8 * k + 4 + t) : 0u;
+            q[k][3] = has_b ? __ldg(qb + 8 * k + 4 + t) : 0u;
+        }
+    }
+    // keys, from key0, that rows gid and gid + 8 see: their request's up to their own token
+    const int end = static_cast<int>(len - key0) - g.T + 1;
+    const int limit[2] = {min(keys, end + (rt * 16 + gid) / G), min(keys, end + (rt * 16 + gid + 8) / G)};
+    const float c = g.scale * 1.4426950408889634f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, o[kD / 8][4];
+#pragma unroll
+    for (int d = 0; d < kD / 8; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[d][e] = 0.0f;
+    for (int x = 0; x < mine; ++x) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kFewStages - 2) : "memory");
+        __syncwarp();   // every lane's copies of this tile have landed, and all have read the last one
+        load(x + kFewStages - 1, page);
+        page = page_of(x + kFewStages);
+        const uint32_t kt = smem_addr(ring + (x % kFewStages) * 2 * kTileBytes), vt = kt + kTileBytes;
+        float s[2][4] = {};
+#pragma unroll
+        for (int k = 0; k < kD / 16; ++k) {
+            uint32_t f[4];   // keys 0 .. 7 and 8 .. 15, two halves of 16 of D each
+            const int key = (lane & 7) + 8 * (lane >> 4), piece = 2 * k + ((lane >> 3) & 1);
+            ldmatrix4(f, kt + key * kRowBytes + 16 * (piece ^ (key & 7)));
+            mma_16bit<T>(s[0], q[k], f[0], f[1]);
+            mma_16bit<T>(s[1], q[k], f[2], f[3]);
+        }
+        const int k0 = (warp + kFewWarps * x) * 16 + 2 * t;
+        uint32_t pr[4];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {   // rows gid, gid + 8
+            float e[4] = {s[0][2 * r], s[0][2 * r + 1], s[1][2 * r], s[1][2 * r + 1]};
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+                if (k0 + (y & 1) + 8 * (y >> 1) >= limit[r]) e[y] = -INFINITY;
+            float best = fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3]));
+            best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 1));
+            best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 2)) * c;
+            const bool grow = best > m[r] + kSlack;
+            if (__any_sync(0xffffffffu, grow)) {
+                const float next = grow ? best : m[r], fix = grow ? exp2_fast(m[r] - next) : 1.0f;
+                m[r] = next;
+                l[r] *= fix;
+#pragma unroll
+                for (int d = 0; d < kD / 8; ++d) {
+                    o[d][2 * r] *= fix;
+                    o[d][2 * r + 1] *= fix;
+                }
+            }
+            const float shift = kLift - (m[r] == -INFINITY ? 0.0f : m[r]);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                e[y] = exp2_fast(fmaf(e[y], c, shift));
+                l[r] += e[y];
+            }
+            pr[r] = pack2<T>(e[0], e[1]);       // keys 0 .. 7 of P
+            pr[2 + r] = pack2<T>(e[2], e[3]);   // keys 8 .. 15
+        }
+#pragma unroll
+        for (int d = 0; d < kD / 8; d += 2) {
+            uint32_t f[4];   // 8 of D: keys 0 .. 7, 8 .. 15; the next 8: the same
+            const int key = (lane & 7) + 8 * ((lane >> 3) & 1), piece = d + (lane >> 4);
+            ldmatrix4_trans(f, vt + key * kRowBytes + 16 * (piece ^ (key & 7)));
+            mma_16bit<T>(o[d], pr, f[0], f[1]);
+            mma_16bit<T>(o[d + 1], pr, f[2], f[3]);
+        }
+    }
+    // ---- the warps' parts joined
+    asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+        if (t == 0) {
+            stat_m[warp][gid + 8 * r] = m[r];
+            stat_l[warp][gid + 8 * r] = l[r];
+        }
+    }
+    __syncthreads();
+    constexpr int kPitch = kD + 4;
+    float *part = reinterpret_cast<float *>(ring);   // this warp's ring, [16][kD + 4]
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kFewWarps; ++w) top = fmaxf(top, stat_m[w][gid + 8 * r]);
+#pragma unroll
+        for (int w = 0; w < kFewWarps; ++w) {
+            const float mw = stat_m[w][gid + 8 * r];
+            sum += mw == -INFINITY ? 0.0f : stat_l[w][gid + 8 * r] * exp2_fast(mw - top);
+        }
+        const float fix = m[r] == -INFINITY ? 0.0f : exp2_fast(m[r] - top) / sum;
+#pragma unroll
+        for (int d = 0; d < kD / 8; ++d)
+            *reinterpret_cast<float2 *>(part + (gid + 8 * r) * kPitch + 8 * d + 2 * t) = make_float2(o[d][2 * r] * fix, o[d][2 * r + 1] * fix);
+        if (warp == 0 && t == 0 && gid + 8 * r < nrows) p.lse[out_row0 + gid + 8 * r] = top == -INFINITY ? -INFINITY : top - kLift + log2f(sum);
+    }
+    __syncthreads();
+    constexpr int kRingFloats = kFewStages * 2 * kTileBytes / 4;
+    static_assert(16 * kPitch <= kRingFloats, "a warp's part fits its ring");
+    for (int e = tid; e < 16 * (kD / 4); e += 32 * kFewWarps) {
+        const int r = e % 16, d4 = e / 16;
+        if (r >= nrows) continue;
+        const float *src = reinterpret_cast<const float *>(smem) + r * kPitch + 4 * d4;
+        float4 v = *reinterpret_cast<const float4 *>(src);
+#pragma unroll
+        for (int w = 1; w < kFewWarps; ++w) {
+            const float4 u = *reinterpret_cast<const float4 *>(src + w * kRingFloats);
+            v.x += u.x;
+            v.y += u.y;
+            v.z += u.z;
+            v.w += u.w;
+        }
+        const int64_t row = out_row0 + r;
+        reinterpret_cast<float4 *>(p.part)[(row >> 5) * (8 * kD) + d4 * 32 + (row & 31)] = v;
     }
 }
 
@@ -770,7 +1030,7 @@ cudaError_t encode_cache_map(CUtensorMap *map, const void *cache, const AttnArgs
 }
 
 template <typename T, int kD, bool kWide>
-cudaError_t launch_typed(const AttnParams &p, int sm_count, cudaStream_t s)
+cudaError_t launch_typed(const AttnParams &p, cudaStream_t s)
 {
     const AttnArgs &g = p.g;
     cudaLaunchAttribute attr[1];
@@ -778,26 +1038,35 @@ cudaError_t launch_typed(const AttnParams &p, int sm_count, cudaStream_t s)
     cfg.stream = s;
     cfg.attrs = attr;
     const int64_t jobs = p.plan.prefix_jobs + p.plan.own_jobs;
+    auto beside_the_last = [&]() {   // starts as the last of the launch before run
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.numAttrs = 1;
+    };
+    cfg.numAttrs = set_launch_overlap_attr(attr);
+    if (p.plan.few_jobs > 0) {
+        auto kern = few_rows_kernel<T, kD>;
+        cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(kern), few_smem<kD>());
+        if (e != cudaSuccess) return e;
+        cfg.blockDim = dim3(32 * kFewWarps);
+        cfg.gridDim = dim3(static_cast<unsigned>(p.plan.few_jobs));
+        cfg.dynamicSmemBytes = few_smem<kD>();
+        if ((e = cudaLaunchKernelEx(&cfg, kern, p)) != cudaSuccess) return e;
+        beside_the_last();
+    }
     if (jobs > 0) {
         auto kern = attention_kernel<T, kD, kWide>;
         cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(kern), kSmemBytes);
         if (e != cudaSuccess) return e;
         cfg.blockDim = dim3(kThreads);
-        cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(jobs, sm_count)));
+        cfg.gridDim = dim3(static_cast<unsigned>(p.plan.prefix_ctas + p.plan.own_ctas));
         cfg.dynamicSmemBytes = kSmemBytes;
-        cfg.numAttrs = set_launch_overlap_attr(attr);
         if ((e = cudaLaunchKernelEx(&cfg, kern, p)) != cudaSuccess) return e;
+        beside_the_last();
     }
     cfg.blockDim = dim3(128);
     cfg.gridDim = dim3(static_cast<unsigned>(p.row_blocks * g.Hkv * (kD / 32)));
     cfg.dynamicSmemBytes = 0;
-    if (jobs > 0) {   // starts as the last jobs run, and waits for all of them
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.numAttrs = 1;
-    } else {
-        cfg.numAttrs = set_launch_overlap_attr(attr);
-    }
     return cudaLaunchKernelEx(&cfg, attention_join_kernel<T, kD>, p);
 }
 
@@ -811,13 +1080,14 @@ int64_t attn_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int64_t prefi
     return plan.slots * Hkv * row_blocks_of(B, T, Hq, Hkv) * 32 * (D + 1) * 4;
 }
 
-cudaError_t launch_attention(const DeviceInfo &dev, const AttnArgs &g, cudaStream_t s)
+cudaError_t launch_attention(const AttnArgs &g, cudaStream_t s)
 {
     route_hit(kRoutePrefixAttention);
     AttnParams p{};
     p.g = g;
     p.plan = plan_attention(g.B, g.T, g.Hq, g.Hkv, g.prefix_len, g.max_own);
-    if (p.plan.prefix_jobs + p.plan.own_jobs > 0x7fffffffLL) return cudaErrorInvalidValue;
+    if (p.plan.prefix_jobs + p.plan.own_jobs > 0x7fffffffLL || p.plan.few_jobs > 0x7fffffffLL) return cudaErrorInvalidValue;
+    p.chained = p.plan.few_jobs > 0;
     p.row_blocks = static_cast<int>(row_blocks_of(g.B, g.T, g.Hq, g.Hkv));
     p.part = static_cast<float *>(g.workspace);
     p.lse = p.part + p.plan.slots * static_cast<int64_t>(g.Hkv) * p.row_blocks * 32 * g.D;
@@ -826,12 +1096,12 @@ cudaError_t launch_attention(const DeviceInfo &dev, const AttnArgs &g, cudaStrea
         if (e == cudaSuccess) e = encode_cache_map(&p.v, g.v_cache, g);
         if (e != cudaSuccess) return e;
     }
-    const bool wide = p.plan.pair_groups > 0 || static_cast<int64_t>(g.T) * (g.Hq / g.Hkv) > kTile;
+    const bool wide = p.plan.pair_groups > 0 || (p.plan.own_jobs > 0 && static_cast<int64_t>(g.T) * (g.Hq / g.Hkv) > kTile);
     auto launch = [&](auto type) {
         using T = decltype(type);
         if (g.D == 64)
-            return wide ? launch_typed<T, 64, true>(p, dev.sm_count, s) : launch_typed<T, 64, false>(p, dev.sm_count, s);
-        return wide ? launch_typed<T, 128, true>(p, dev.sm_count, s) : launch_typed<T, 128, false>(p, dev.sm_count, s);
+            return wide ? launch_typed<T, 64, true>(p, s) : launch_typed<T, 64, false>(p, s);
+        return wide ? launch_typed<T, 128, true>(p, s) : launch_typed<T, 128, false>(p, s);
     };
     return g.type == QMV_F16 ? launch(__half()) : launch(__nv_bfloat16());
 }

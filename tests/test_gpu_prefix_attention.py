@@ -75,6 +75,22 @@ def test_more_rows_than_a_tile():
     check(inputs(48, 2, 5, 1, 128, 300, [2 + i for i in range(48)], 32, "f16", seed=2), "f16")
 
 
+@pytest.mark.parametrize("type_,B,T,Hq,Hkv,D,prefix,own_len,page", [
+    ("f16", 2, 10, 8, 1, 128, 200, [10, 333], 16),        # 80 rows of a request and key head
+    ("bf16", 3, 40, 5, 1, 64, 129, [40, 7, 300], 32),     # 200 rows
+    ("bf16", 2, 70, 8, 1, 128, 0, [70, 200], 64),         # 560 rows, no prefix
+    ("f16", 1, 17, 8, 2, 128, 640, [1000], 128),
+    ("f16", 2, 16, 4, 1, 64, 0, [0, 40], 16)])            # 64 rows: the few-rows kernel's most
+def test_many_tokens_of_a_request(type_, B, T, Hq, Hkv, D, prefix, own_len, page):
+    check(inputs(B, T, Hq, Hkv, D, prefix, own_len, page, type_, seed=T), type_)
+
+
+@pytest.mark.parametrize("type_", ["f16", "bf16"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_long_own_keys_in_ranges(type_, D):
+    check(inputs(2, 2, 6, 2, D, 70, [3001, 1500], 16, type_, seed=11), type_)
+
+
 def test_rows_without_a_key_are_zero():
     args = inputs(3, 4, 4, 2, 64, 0, [0, 2, 5], 16)
     got = check(args, "f16")
