@@ -58,6 +58,8 @@ struct AttnPlan {
     int own_groups, own_splits, own_tiles;   // row groups of a request, ranges of own_tiles own tiles
     int few_row_tiles, few_keys;        // requests of few rows, by the kernel for those: 16-row tiles, keys a range
     int64_t few_jobs;
+    int few_prefix_keys;                // the same for the prefix, where all rows together are 16 at most
+    int64_t few_prefix_jobs;
     int64_t prefix_jobs, own_jobs;
     int prefix_ctas, own_ctas;          // CTAs that take the ones, and the others, in turn
     int slots;                          // partial results a row: own_splits, then the prefix's
@@ -95,7 +97,13 @@ AttnPlan plan_attention(int B, int T, int Hq, int Hkv, int64_t prefix_len, int64
         p.own_jobs = jobs * p.own_splits;
         own_cost = 8 * p.own_jobs + jobs * own_tiles * 6 / 5;
     }
-    if (tiles > 0 && rows > 0) {
+    if (tiles > 0 && rows > 0 && rows <= 16) {
+        // (with 32 rows, the prefix read twice: 18 us for 16 with 4096 keys)
+        const int64_t splits = std::max<int64_t>(1, std::min<int64_t>({2 * kSms / Hkv, ceil_div(prefix_len, 128), 256}));
+        p.few_prefix_keys = static_cast<int>(ceil_div(ceil_div(prefix_len, splits), 64) * 64);
+        p.lone_splits = static_cast<int>(ceil_div(prefix_len, p.few_prefix_keys));
+        p.few_prefix_jobs = static_cast<int64_t>(Hkv) * p.lone_splits;
+    } else if (tiles > 0 && rows > 0) {
         const int64_t row_tiles = ceil_div(rows, kTile);
         p.pair_groups = static_cast<int>(row_tiles / 2);
         p.lone = static_cast<int>(row_tiles % 2);
@@ -717,14 +725,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     }
 }
 
-// ---- a request's own keys against its few rows (T G <= 64)
+// ---- few rows: a request's own keys against its rows (T G <= 64), and the prefix where all
+// requests together have 16 at most
 //
-// A decode step's requests have a handful of rows each and no key in common: bound by the
-// bytes of K and V. A CTA takes 16 rows (m16n8k16 products) and a range of keys; its four
+// A decode step's requests have a handful of rows each and no own key in common: bound by
+// the bytes of K and V. A CTA takes 16 rows (m16n8k16 products) and a range of keys; its four
 // warps take 16 keys in turn, each with a ring of asynchronous copies, statistics and output
 // sums of its own, so that nothing waits for anything but memory, and are joined at the end.
 // (As jobs of the kernel above, 128 rows a product and one range at a time an SM, 64
-// requests of up to 1024 keys took 51 us; so XX.)
+// requests of up to 1024 keys took 48 to 65 us; so 38.)
 constexpr int kFewWarps = 4, kFewStages = 3;
 template <int kD>
 constexpr int few_smem() { return kFewWarps * kFewStages * 2 * 16 * kD * 2; }
@@ -768,28 +777,33 @@ __global__ void __launch_bounds__(32 * kFewWarps) few_rows_kernel(const __grid_c
     const int G = g.Hq / g.Hkv, per = g.T * G;
     grid_dependency_wait();
     grid_launch_dependents();
-    int id = static_cast<int>(blockIdx.x);
-    const int rt = id % p.plan.few_row_tiles;
-    id /= p.plan.few_row_tiles;
-    const int split = id % p.plan.own_splits;
-    id /= p.plan.own_splits;
-    const int h = id % g.Hkv, b = id / g.Hkv;
-    int64_t len = g.own_len[b];
-    if (len > g.max_own) {
+    // the job: 16 rows of key head h, a range of a request's own keys or of the prefix
+    const bool on_prefix = blockIdx.x >= static_cast<unsigned>(p.plan.few_jobs);
+    int id = static_cast<int>(blockIdx.x) - (on_prefix ? static_cast<int>(p.plan.few_jobs) : 0);
+    const int tiles = on_prefix ? 1 : p.plan.few_row_tiles;
+    const int splits = on_prefix ? p.plan.lone_splits : p.plan.own_splits, most = on_prefix ? p.plan.few_prefix_keys : p.plan.few_keys;
+    const int rt = id % tiles;
+    id /= tiles;
+    const int split = id % splits;
+    id /= splits;
+    const int h = id % g.Hkv, b = id / g.Hkv;   // (b: 0 on the prefix)
+    int64_t len = on_prefix ? g.prefix_len : g.own_len[b];
+    if (!on_prefix && len > g.max_own) {
         if (tid == 0) atomicOr(&g_attention_error, kErrIndex);
         len = g.max_own;
     }
-    const int i0 = b * per + rt * 16, nrows = min(16, per - rt * 16);
-    const int64_t out_row0 = (static_cast<int64_t>(split) * g.Hkv + h) * p.row_blocks * 32 + i0;
-    const int64_t key0 = static_cast<int64_t>(split) * p.plan.few_keys;
-    const int keys = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(p.plan.few_keys), len - key0)));
+    const int rows = on_prefix ? g.B * per : per, i0 = b * per + rt * 16, nrows = min(16, rows - rt * 16);
+    const int slot = (on_prefix ? p.plan.own_splits : 0) + split;
+    const int64_t out_row0 = (static_cast<int64_t>(slot) * g.Hkv + h) * p.row_blocks * 32 + i0;
+    const int64_t key0 = static_cast<int64_t>(split) * most;
+    const int keys = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(most), len - key0)));
     if (keys == 0) {
         if (tid < nrows) p.lse[out_row0 + tid] = -INFINITY;
         return;
     }
     // ---- this warp's 16-key tiles warp, warp + 4, ...: page lookup and copies
     const int ntiles = (keys + 15) / 16, mine = (ntiles - warp + kFewWarps - 1) / kFewWarps;
-    const int32_t *table = g.own_table + static_cast<int64_t>(b) * g.own_pages;
+    const int32_t *table = on_prefix ? g.prefix_table : g.own_table + static_cast<int64_t>(b) * g.own_pages;
     const int shift = __ffs(g.page) - 1;
     uint8_t *ring = smem + warp * kFewStages * 2 * kTileBytes;
     auto page_of = [&](int x) { return x < mine ? __ldg(table + ((key0 + (warp + kFewWarps * x) * 16) >> shift)) : 0; };
@@ -834,9 +848,11 @@ __global__ void __launch_bounds__(32 * kFewWarps) few_rows_kernel(const __grid_c
             q[k][3] = has_b ? __ldg(qb + 8 * k + 4 + t) : 0u;
         }
     }
-    // keys, from key0, that rows gid and gid + 8 see: their request's up to their own token
+    // keys, from key0, that rows gid and gid + 8 see: the prefix's, or their request's up to
+    // their own token
     const int end = static_cast<int>(len - key0) - g.T + 1;
-    const int limit[2] = {min(keys, end + (rt * 16 + gid) / G), min(keys, end + (rt * 16 + gid + 8) / G)};
+    const int limit[2] = {on_prefix ? keys : min(keys, end + (rt * 16 + gid) / G),
+                          on_prefix ? keys : min(keys, end + (rt * 16 + gid + 8) / G)};
     const float c = g.scale * 1.4426950408889634f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, o[kD / 8][4];
 #pragma unroll
@@ -950,7 +966,7 @@ __global__ void __launch_bounds__(32 * kFewWarps) few_rows_kernel(const __grid_c
 }
 
 // Joins the partial results of 32 rows of a key head for 32 of D, a row a lane and 8 of D a
-// warp (a CTA for all of D left most SMs idle: 8 us for 24 requests, for XX):
+// warp (a CTA for all of D left most SMs idle: 8 us for 24 requests, now 5):
 // weights 2^(lse - max) over their sum, of up to kJoinSlots slots at a time, computed once
 // for all warps. Bound by latency, so that the loads of eight slots are in flight.
 constexpr int kJoinSlots = 64;
@@ -1044,12 +1060,12 @@ cudaError_t launch_typed(const AttnParams &p, cudaStream_t s)
         cfg.numAttrs = 1;
     };
     cfg.numAttrs = set_launch_overlap_attr(attr);
-    if (p.plan.few_jobs > 0) {
+    if (p.plan.few_jobs + p.plan.few_prefix_jobs > 0) {
         auto kern = few_rows_kernel<T, kD>;
         cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(kern), few_smem<kD>());
         if (e != cudaSuccess) return e;
         cfg.blockDim = dim3(32 * kFewWarps);
-        cfg.gridDim = dim3(static_cast<unsigned>(p.plan.few_jobs));
+        cfg.gridDim = dim3(static_cast<unsigned>(p.plan.few_jobs + p.plan.few_prefix_jobs));
         cfg.dynamicSmemBytes = few_smem<kD>();
         if ((e = cudaLaunchKernelEx(&cfg, kern, p)) != cudaSuccess) return e;
         beside_the_last();
@@ -1086,8 +1102,8 @@ cudaError_t launch_attention(const AttnArgs &g, cudaStream_t s)
     AttnParams p{};
     p.g = g;
     p.plan = plan_attention(g.B, g.T, g.Hq, g.Hkv, g.prefix_len, g.max_own);
-    if (p.plan.prefix_jobs + p.plan.own_jobs > 0x7fffffffLL || p.plan.few_jobs > 0x7fffffffLL) return cudaErrorInvalidValue;
-    p.chained = p.plan.few_jobs > 0;
+    if (p.plan.prefix_jobs + p.plan.own_jobs > 0x7fffffffLL || p.plan.few_jobs + p.plan.few_prefix_jobs > 0x7fffffffLL) return cudaErrorInvalidValue;
+    p.chained = p.plan.few_jobs + p.plan.few_prefix_jobs > 0;
     p.row_blocks = static_cast<int>(row_blocks_of(g.B, g.T, g.Hq, g.Hkv));
     p.part = static_cast<float *>(g.workspace);
     p.lse = p.part + p.plan.slots * static_cast<int64_t>(g.Hkv) * p.row_blocks * 32 * g.D;

@@ -1,0 +1,81 @@
+"""The decode step's operators together, as gemm_qmv_quantize_gb300/decode_step.py runs
+them: each call's output against its definition in 64 bits on the inputs that the calls
+before it made, over several steps. Tolerances as in the operators' own tests."""
+import math
+
+import pytest
+import torch
+
+import decode_ref
+import oracle
+
+pytestmark = pytest.mark.gpu
+
+
+def test_steps_against_definitions():
+    import gemm_qmv_quantize_gb300 as q
+    from gemm_qmv_quantize_gb300.decode_step import DecodeStep
+    q.error_flags(clear=True)
+    hidden, Hq, Hkv, D, V, B, prefix = 256, 8, 2, 64, 1003, 5, 130
+    net = DecodeStep(B, prefix, 24, hidden=hidden, Hq=Hq, Hkv=Hkv, D=D, vocab=V, adapters=3, rank=8, page=16, seed=3)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    for step in range(20):
+        x = torch.randn((B, hidden), generator=g, device="cuda").half()
+        tokens, total = net.tokens.clone(), net.own_len.clone()
+        r = net.step(x)
+
+        def projected(name, inp, got):
+            codes, scales, gs = net.w[name]
+            y, bound = oracle.nvfp4_w4a16(codes.cpu().numpy(), scales.cpu().numpy(), gs, inp.cpu().numpy())
+            y, bound = torch.from_numpy(y).cuda(), torch.from_numpy(bound).cuda()
+            if name in net.a:
+                y, more = decode_ref.lora(inp, net.a[name], net.b[name], net.adapter, net.scale, y)
+                bound = bound + more
+            assert bool(((got.double() - y).abs() <= 1e-3 * bound + 1e-6).all()), (step, name)
+
+        projected("qkv", x, r["qkv"])
+        position = (net.own_len - 1 + prefix)[None]
+        qr, kr, vr = decode_ref.rope(r["qkv"], position, net.table, [0] * (D // 2), Hkv, D, False)
+        u = 2.0 ** -11
+        near = lambda a, b: bool(((a.double() - b).abs() <= u * b.abs() + 2.0 ** -20 * float(r["qkv"].abs().max()) + 2.0 ** -25).all())  # noqa: E731
+        assert near(r["q"], qr)
+        for b in range(B):
+            page, at = int(net.own_table[b, (int(net.own_len[b]) - 1) // 16]), (int(net.own_len[b]) - 1) % 16
+            assert near(net.k_cache[page, at], kr[b]) and near(net.v_cache[page, at], vr[b])
+        o, bound = decode_ref.attention(r["q"].view(B, 1, Hq, D), net.k_cache, net.v_cache, net.prefix_table, prefix,
+                                        net.own_table, net.own_len, 1 / math.sqrt(D))
+        got = r["o"].view(B, 1, Hq, D).double()
+        assert bool(((got - o).abs() <= u * o.abs() + (u + 2e-3) * bound + 2.0 ** -24).all()), step
+        projected("o", r["o"], r["hidden"])
+        projected("head", r["hidden"].half(), r["raw"])
+        y = decode_ref.logits(r["raw"], tokens, net.prompt_len, total, net.repetition, net.presence, net.frequency, None,
+                              None, net.mask, net.mask_row)
+        logits = r["logits"].double().cpu()
+        fine = torch.isfinite(y)
+        assert torch.equal(logits[~fine], y[~fine])
+        big = 2 * r["raw"].double().abs().cpu() + 30.0
+        assert bool(((logits - y).abs()[fine] <= 2.0 ** -22 * big[fine]).all())
+        assert torch.equal(net.tokens.gather(1, total.long()[:, None])[:, 0].long().cpu(), logits.argmax(1))
+    assert int(net.own_len[0]) == 20
+    assert q.error_flags(clear=True) == 0
+
+
+def test_step_in_a_cuda_graph_gives_the_same():
+    """A step's calls, captured once and replayed."""
+    import gemm_qmv_quantize_gb300 as q
+    from gemm_qmv_quantize_gb300.decode_step import DecodeStep
+    net = DecodeStep(4, 200, 32, hidden=256, Hq=8, Hkv=2, D=64, vocab=1003, adapters=3, rank=8, page=16, seed=5)
+    x = torch.randn((4, 256), device="cuda").half()
+    q_ = torch.randn((4, 1, 8, 64), device="cuda").half()
+    own = torch.full((4,), 9, dtype=torch.int32, device="cuda")
+    run = lambda: (net.project("qkv", x), q.qmv_prefix_attention(  # noqa: E731
+        q_, net.k_cache, net.v_cache, net.prefix_table, 200, net.own_table, own, max_own=32, workspace=net.workspace))
+    plain = run()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = run()
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(plain, captured):
+        assert torch.equal(a, b)

@@ -85,6 +85,13 @@ def test_many_tokens_of_a_request(type_, B, T, Hq, Hkv, D, prefix, own_len, page
     check(inputs(B, T, Hq, Hkv, D, prefix, own_len, page, type_, seed=T), type_)
 
 
+@pytest.mark.parametrize("type_,B,T,Hq,Hkv,D,prefix,own_len,page", [
+    ("f16", 2, 1, 8, 2, 128, 5001, [0, 30], 16), ("bf16", 1, 2, 8, 1, 64, 3333, [40], 64),
+    ("bf16", 16, 1, 2, 2, 128, 1025, [i for i in range(16)], 256), ("f16", 3, 1, 7, 1, 64, 200, [0, 0, 0], 32)])
+def test_few_rows_behind_a_prefix(type_, B, T, Hq, Hkv, D, prefix, own_len, page):
+    check(inputs(B, T, Hq, Hkv, D, prefix, own_len, page, type_, seed=prefix), type_)
+
+
 @pytest.mark.parametrize("type_", ["f16", "bf16"])
 @pytest.mark.parametrize("D", [64, 128])
 def test_long_own_keys_in_ranges(type_, D):
