@@ -198,6 +198,7 @@ struct Job {
     int slot;               // of the partial results
     int own_b;              // request whose own keys these are, or -1: the prefix's
     int64_t key0;           // first key, a multiple of 128
+    int step;               // tile t holds the keys key0 + 128 step t ...
     int keys, ntiles;       // number of keys, of tiles (0: no key)
     int own_end;            // own keys: the request's length - key0
 };
@@ -228,7 +229,6 @@ __device__ __forceinline__ Job job_of(const AttnParams &p, int id, int len)
     const AttnArgs &g = p.g;
     const int G = g.Hq / g.Hkv;
     Job j;
-    int64_t key1;
     if (id < p.plan.prefix_jobs) {
         const int tiles = static_cast<int>((g.prefix_len + kTile - 1) / kTile), rows = g.B * g.T * G;
         const int pair_jobs = g.Hkv * p.plan.pair_groups * p.plan.pair_splits;
@@ -241,8 +241,14 @@ __device__ __forceinline__ Job job_of(const AttnParams &p, int id, int len)
         j.h = lone ? k : k / p.plan.pair_groups;
         j.i0 = group * 2 * kTile;
         j.nrows = min(rows - j.i0, 2 * kTile);
-        j.key0 = static_cast<int64_t>(tiles) * split / splits * kTile;
-        key1 = min(static_cast<int64_t>(tiles) * (split + 1) / splits * kTile, g.prefix_len);
+        // Every splits-th tile, not a run of them: all row groups of a key head then pass over
+        // the prefix side by side and find one another's tiles in L2 (runs: 447 MB read from
+        // memory for 268 MB of keys, 64 requests behind 65536).
+        j.key0 = static_cast<int64_t>(split) * kTile;
+        j.step = splits;
+        j.ntiles = (tiles - split + splits - 1) / splits;
+        j.keys = (j.ntiles - 1) * kTile +
+                 static_cast<int>(min(static_cast<int64_t>(kTile), g.prefix_len - (j.key0 + static_cast<int64_t>(j.ntiles - 1) * splits * kTile)));
         j.slot = p.plan.own_splits + split;
         j.own_b = -1;
         j.own_end = 0;
@@ -259,12 +265,13 @@ __device__ __forceinline__ Job job_of(const AttnParams &p, int id, int len)
         j.nrows = min(per - group * 2 * kTile, 2 * kTile);
         const int64_t n = min(static_cast<int64_t>(len), g.max_own);
         j.key0 = static_cast<int64_t>(split) * p.plan.own_tiles * kTile;
-        key1 = min(j.key0 + static_cast<int64_t>(p.plan.own_tiles) * kTile, n);
+        const int64_t key1 = min(j.key0 + static_cast<int64_t>(p.plan.own_tiles) * kTile, n);
+        j.step = 1;
+        j.keys = static_cast<int>(max(static_cast<int64_t>(0), key1 - j.key0));
+        j.ntiles = (j.keys + kTile - 1) / kTile;
         j.slot = split;
         j.own_end = static_cast<int>(max(static_cast<int64_t>(0), n - j.key0));
     }
-    j.keys = static_cast<int>(max(static_cast<int64_t>(0), key1 - j.key0));
-    j.ntiles = (j.keys + kTile - 1) / kTile;
     return j;
 }
 
@@ -308,11 +315,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     constexpr int kSlots = std::min(kMaxSlots, static_cast<int>((kSmemBytes - kQBytes) / kSlotBytes));
     extern __shared__ __align__(1024) uint8_t smem[];
     // full: a slot's copies have landed; freed: its readers are done (two arrivals: each
-    // stream's, or two by the one stream that reads it); s_full / p_full: S, P of a stream's
-    // step; q_full: a job's Q is in place; o_done: its products are complete; o_free: its
+    // stream's, or two by the one stream that reads it); s_full / p_half / p_full: S, P for the
+    // first 64 keys, all of P of a stream's step; q_full: a job's Q is in place; o_done: its products are complete; o_free: its
     // results have been read; merged: the streams' statistics of a job are there for one another;
     // turn: the other stream's products have been issued
-    __shared__ __align__(8) uint64_t full[kSlots], freed[kSlots], s_full[2], p_full[2], q_full, o_done, o_free, merged, turn[2], drained[2];
+    __shared__ __align__(8) uint64_t full[kSlots], freed[kSlots], s_full[2], p_half[2], p_full[2], q_full, o_done, o_free, merged, turn[2], drained[2];
     __shared__ uint32_t tmem_slot, abort_flag;
     __shared__ float merge_m[2][kTile], merge_l[2][kTile];
     volatile uint32_t *abort_word = &abort_flag;
@@ -347,6 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&s_full[s], 1);
+            mbar_init(&p_half[s], 4);
             mbar_init(&p_full[s], 4);
         }
         mbar_init(&q_full, 8);
@@ -421,6 +429,22 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                     mbar_arrive_n(&freed[(pos0 + k_pos(t)) % kSlots], arrivals);
                     if (i > 0) mbar_arrive_n(&freed[(pos0 + v_pos(pair ? t - 1 : t - 2, n)) % kSlots], arrivals);
                 }
+                if (t == n - 1 && job.keys % kTile != 0) {
+                    // what lies past the last key may be anything, NaN too: zeros, since 0 x NaN is NaN
+                    // (each stream that reads the tile writes them before its own product)
+                    const int pos = pos0 + v_pos(t, n), first = job.keys % kTile;
+                    if (*abort_word || !__all_sync(0xffffffffu, landed(pos, pair) ? 1 : 0)) {
+                        fail();
+                        ok = false;
+                        break;
+                    }
+                    for (int u = r; u < (kTile - first) * 8 * kChunks; u += kTile) {
+                        const int row = first + u / (8 * kChunks), x = u % (8 * kChunks);
+                        *reinterpret_cast<uint4 *>(ring + (pos % kSlots) * kSlotBytes + (x / 8) * kBlock + row * 128 + 16 * (x % 8)) =
+                            make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_shared();
+                }
                 if (warp_live) {
                     tc_fence_after();
                     if (least - t * kTile < kTile) {   // the last tile, or the request's own tokens
@@ -484,27 +508,20 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                             w[j] = pack2<T>(a, b);
                         }
                         tmem_st16(s_col + q / 2, w);
+                        if (q == kTile / 2 - 32) {   // the products with the first 64 keys may begin
+                            tmem_wait_st();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&p_half[s]);
+                        }
                     }
                     const float2 sums = both_of(add_pair(sum[0], sum[1]));
                     l += sums.x + sums.y;
                     tmem_wait_st();
                     tc_fence_before();
-                }
-                if (t == n - 1 && job.keys % kTile != 0) {
-                    // what lies past the last key may be anything, NaN too: zeros, since 0 x NaN is NaN
-                    // (each stream that reads the tile writes them before its own product)
-                    const int pos = pos0 + v_pos(t, n), first = job.keys % kTile;
-                    if (*abort_word || !__all_sync(0xffffffffu, landed(pos, pair) ? 1 : 0)) {
-                        fail();
-                        ok = false;
-                        break;
-                    }
-                    for (int u = r; u < (kTile - first) * 8 * kChunks; u += kTile) {
-                        const int row = first + u / (8 * kChunks), x = u % (8 * kChunks);
-                        *reinterpret_cast<uint4 *>(ring + (pos % kSlots) * kSlotBytes + (x / 8) * kBlock + row * 128 + 16 * (x % 8)) =
-                            make_uint4(0, 0, 0, 0);
-                    }
-                    fence_proxy_async_shared();
+                } else {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&p_half[s]);
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[s]);
@@ -626,9 +643,17 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                         ok = landed(pos, pair) && !*abort_word;
                         // the last job's results have been read before O is written again
                         if (ok && i == 0 && done > 0) ok = wait_for(&o_free, (done - 1) & 1u);
+                        ok = ok && wait_for(&p_half[s], step & 1u);
+                        if (!ok) break;
+                        tc_fence_after();
+                        auto issue_pv = [&](int k) {   // 16 keys: 2048 bytes of V, 8 columns of P
+                            umma_f16_ta(o_tmem, s_tmem + 8u * k, vd + 128u * k, idesc_o, (i > 0 || k > 0) ? 1u : 0u);
+                        };
+#pragma unroll
+                        for (int k = 0; k < kTile / 32; ++k) issue_pv(k);
                         // Two streams over the same tiles take turns: their products, mixed, would
                         // end together, and then their exponentials would run together.
-                        if (ok && pair) {
+                        if (pair) {
                             if (s == 1 || turns > 0) ok = wait_for(&turn[s], (turns + s - 1) & 1u);
                             ++turns;
                         }
@@ -637,8 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                         if (!ok) break;
                         tc_fence_after();
 #pragma unroll
-                        for (int k = 0; k < kTile / 16; ++k)   // 16 keys: 2048 bytes of V, 8 columns of P
-                            umma_f16_ta(o_tmem, s_tmem + 8u * k, vd + 128u * k, idesc_o, (i > 0 || k > 0) ? 1u : 0u);
+                        for (int k = kTile / 32; k < kTile / 16; ++k) issue_pv(k);
                     }
                     if (i + 1 < steps && ok) {
                         const uint64_t kd = k_desc + static_cast<uint32_t>(k_at(i + 1) % kSlots) * (kSlotBytes >> 4);
@@ -687,7 +711,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                     int page[kMost];
 #pragma unroll
                     for (int x = 0; x < kMost; ++x)
-                        if (first + kStep * x < pages) page[x] = __ldg(table + ((in_page + t * kTile + (first + kStep * x) * box) >> shift));
+                        if (first + kStep * x < pages) page[x] = __ldg(table + ((in_page + t * job.step * kTile + (first + kStep * x) * box) >> shift));
                     if (*abort_word || (pos >= kSlots && !wait_for(&freed[at], full_parity(pos) ^ 1u))) {
                         ok = false;
                         break;
@@ -702,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                             page[x] = static_cast<int>(g.n_pages);
                         }
                         tma_load_4d(dst + kStep * x * box * 128, v ? &p.v : &p.k, kChunks == 1 ? 0 : 64 * half,
-                                    (in_page + t * kTile) & (g.page - 1), job.h, page[x], &full[at]);
+                                    (in_page + t * job.step * kTile) & (g.page - 1), job.h, page[x], &full[at]);
                     }
                 }
                 if (!ok) fail();
@@ -965,18 +989,17 @@ __global__ void __launch_bounds__(32 * kFewWarps) few_rows_kernel(const __grid_c
     }
 }
 
-// Joins the partial results of 32 rows of a key head for 32 of D, a row a lane and 8 of D a
-// warp (a CTA for all of D left most SMs idle: 8 us for 24 requests, now 5):
-// weights 2^(lse - max) over their sum, of up to kJoinSlots slots at a time, computed once
-// for all warps. Bound by latency, so that the loads of eight slots are in flight.
-constexpr int kJoinSlots = 64;
+// Joins the partial results of 32 rows of a key head for 8 of D, a row a lane: weights
+// 2^(lse - max) over their sum. Bound by latency: the four warps take every fourth slot, so
+// that about all loads are under way at once, statistics and results alike, and are joined
+// in shared memory. (A warp for all slots of 8 of D: 24 requests behind 8191 keys took 30 us in all, so 26.)
 template <typename T, int kD>
 __global__ void __launch_bounds__(128) attention_join_kernel(const __grid_constant__ AttnParams p)
 {
-    __shared__ float weight[kJoinSlots][32];
-    constexpr int kWarps = 4, kParts = kD / 32;
+    constexpr int kWarps = 4, kAhead = 6, kParts = kD / 8;
+    __shared__ float tops[kWarps][32], sums[kWarps][32], accs[kWarps][8][32];
     const AttnArgs &g = p.g;
-    const int lane = threadIdx.x & 31, warp = static_cast<int>(threadIdx.x >> 5), d0 = static_cast<int>(blockIdx.x) % kParts * 32 + warp * 8;
+    const int lane = threadIdx.x & 31, warp = static_cast<int>(threadIdx.x >> 5), d0 = static_cast<int>(blockIdx.x) % kParts * 8;
     const int block = static_cast<int>(blockIdx.x) / kParts % p.row_blocks, h = static_cast<int>(blockIdx.x) / kParts / p.row_blocks;
     const int G = g.Hq / g.Hkv, i = block * 32 + lane;
     const bool live = i < g.B * g.T * G;
@@ -988,43 +1011,60 @@ __global__ void __launch_bounds__(128) attention_join_kernel(const __grid_consta
     grid_launch_dependents();
     grid_dependency_wait();
     float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f}, sum = 0.0f, top = -INFINITY;
-    for (int k0 = 0; k0 < slots; k0 += kJoinSlots) {
-        const int n = min(kJoinSlots, slots - k0);
-        __syncthreads();
-#pragma unroll 4
-        for (int k = warp; k < n; k += kWarps) weight[k][lane] = live ? lse[(k0 + k) * per_slot] : -INFINITY;
-        __syncthreads();
+    for (int k0 = warp; k0 < slots; k0 += kWarps * kAhead) {
+        float e[kAhead];
+        float4 v[kAhead][2];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int k = k0 + u * kWarps;
+            const bool in = k < slots && live;
+            e[u] = in ? lse[k * per_slot] : -INFINITY;
+#pragma unroll
+            for (int x = 0; x < 2; ++x)   // (where lse is -inf nothing was written: looked at no further)
+                v[u][x] = in ? part[k * per_slot * (kD / 4) + 32 * x] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
         float best = top;
-        for (int k = 0; k < n; ++k) best = fmaxf(best, weight[k][lane]);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) best = fmaxf(best, e[u]);
         const float fix = top == -INFINITY ? 0.0f : exp2_fast(top - best);
         top = best;
         sum *= fix;
 #pragma unroll
         for (int x = 0; x < 8; ++x) acc[x] *= fix;
-        for (int k = 0; k < n; k += 8) {
-            float4 v[8][2];
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
+        for (int u = 0; u < kAhead; ++u) {
+            if (e[u] == -INFINITY) continue;
+            const float w = exp2_fast(e[u] - top);
+            sum += w;
 #pragma unroll
-                for (int x = 0; x < 2; ++x)
-                    v[u][x] = k + u < n && live ? part[(k0 + k + u) * per_slot * (kD / 4) + 32 * x] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const float there = k + u < n ? weight[k + u][lane] : -INFINITY;
-                if (there == -INFINITY) continue;   // no key, and nothing written
-                const float w = exp2_fast(there - top);
-                sum += w;
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    acc[4 * x] = fmaf(w, v[u][x].x, acc[4 * x]);
-                    acc[4 * x + 1] = fmaf(w, v[u][x].y, acc[4 * x + 1]);
-                    acc[4 * x + 2] = fmaf(w, v[u][x].z, acc[4 * x + 2]);
-                    acc[4 * x + 3] = fmaf(w, v[u][x].w, acc[4 * x + 3]);
-                }
+            for (int x = 0; x < 2; ++x) {
+                acc[4 * x] = fmaf(w, v[u][x].x, acc[4 * x]);
+                acc[4 * x + 1] = fmaf(w, v[u][x].y, acc[4 * x + 1]);
+                acc[4 * x + 2] = fmaf(w, v[u][x].z, acc[4 * x + 2]);
+                acc[4 * x + 3] = fmaf(w, v[u][x].w, acc[4 * x + 3]);
             }
         }
     }
-    if (!live) return;
+    tops[warp][lane] = top;
+    sums[warp][lane] = sum;
+#pragma unroll
+    for (int x = 0; x < 8; ++x) accs[warp][x][lane] = acc[x];
+    __syncthreads();
+    if (warp > 0 || !live) return;
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) top = fmaxf(top, tops[w][lane]);
+    const float own = tops[0][lane], mine = own == -INFINITY ? 0.0f : exp2_fast(own - top);
+    sum *= mine;
+#pragma unroll
+    for (int x = 0; x < 8; ++x) acc[x] *= mine;
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) {
+        if (tops[w][lane] == -INFINITY && sums[w][lane] == 0.0f) continue;
+        const float f = exp2_fast(tops[w][lane] - top);
+        sum = fmaf(f, sums[w][lane], sum);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) acc[x] = fmaf(f, accs[w][x][lane], acc[x]);
+    }
     const float inv = sum > 0.0f || isnan(sum) ? 1.0f / sum : 0.0f;   // no key at all: zeros
     uint4 out;
     out.x = pack2<T>(acc[0] * inv, acc[1] * inv);
@@ -1081,7 +1121,7 @@ cudaError_t launch_typed(const AttnParams &p, cudaStream_t s)
         beside_the_last();
     }
     cfg.blockDim = dim3(128);
-    cfg.gridDim = dim3(static_cast<unsigned>(p.row_blocks * g.Hkv * (kD / 32)));
+    cfg.gridDim = dim3(static_cast<unsigned>(p.row_blocks * g.Hkv * (kD / 8)));
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, attention_join_kernel<T, kD>, p);
 }
@@ -1107,7 +1147,7 @@ cudaError_t launch_attention(const AttnArgs &g, cudaStream_t s)
     p.row_blocks = static_cast<int>(row_blocks_of(g.B, g.T, g.Hq, g.Hkv));
     p.part = static_cast<float *>(g.workspace);
     p.lse = p.part + p.plan.slots * static_cast<int64_t>(g.Hkv) * p.row_blocks * 32 * g.D;
-    if (g.n_pages > 0) {
+    if (p.plan.prefix_jobs + p.plan.own_jobs > 0) {
         cudaError_t e = encode_cache_map(&p.k, g.k_cache, g);
         if (e == cudaSuccess) e = encode_cache_map(&p.v, g.v_cache, g);
         if (e != cudaSuccess) return e;

@@ -63,7 +63,7 @@ class Model:
         self.jobs, self.ks, self.rng, self.second_wait = jobs, slots, rng, second_wait
         self.full = [Barrier(2) for _ in range(slots)]
         self.freed = [Barrier(2) for _ in range(slots)]
-        self.s_full, self.p_full = [Barrier(1), Barrier(1)], [Barrier(4), Barrier(4)]
+        self.s_full, self.p_half, self.p_full = [Barrier(1), Barrier(1)], [Barrier(4), Barrier(4)], [Barrier(4), Barrier(4)]
         self.q_full, self.o_done, self.o_free, self.merged = Barrier(8), Barrier(2), Barrier(8), Barrier(8)
         self.turn = [Barrier(1), Barrier(1)]
         self.holds = [[None, None] for _ in range(slots)]   # (job, "K" or "V", tile) of each half that has landed
@@ -71,6 +71,7 @@ class Model:
         self.queue = [[], []]              # products of each issuing thread, in order
         self.reading = {}                  # what unfinished products read: slot or "q" -> count
         self.q_job, self.o_job = None, [None, None]
+        self.clears = {}                   # (stream, warp) -> the last tile whose tail it cleared
 
     def use(self, what, n):
         self.reading[what] = self.reading.get(what, 0) + n
@@ -85,6 +86,13 @@ class Model:
 
     def has(self, at, what):
         return self.holds[at] == [what, what]
+
+    def cleared(self, j, t, pos):
+        """Have all warps of a stream that reads this tile cleared its tail, if it has one?"""
+        n, pair, tail = self.jobs[j]
+        if t < n - 1 or not tail:
+            return True
+        return any(all(self.clears.get((s, w)) == (j, t) for w in range(4)) for s in (0, 1))
 
     def loader(self, half):
         pos = 0
@@ -126,22 +134,25 @@ class Model:
             if tiles:
                 yield from self.landed_waits(pos0 + k_pos(tiles[0]), pair)
                 s_product(0)
-            if done:
-                yield (self.o_free, done - 1)
             for i, t in enumerate(tiles):
                 pos = pos0 + v_pos(t, n)
                 if i + 1 < len(tiles):
                     yield from self.landed_waits(pos0 + k_pos(tiles[i + 1]), pair)
                 yield from self.landed_waits(pos, pair)
+                if i == 0 and done:
+                    yield (self.o_free, done - 1)
+                yield (self.p_half[s], step)
+                if not self.has(pos % self.ks, (j, "V", t)) or not self.cleared(j, t, pos):
+                    raise Fault("P V reads what is not its tile, or what lies past its keys")
+                self.o_job[s] = j
+                self.use(pos % self.ks, 1)
+                self.queue[s].append(("PV", [pos % self.ks], None))
                 if pair:
                     if s == 1 or turns > 0:
                         yield (self.turn[s], turns + s - 1)
                     turns += 1
                 yield (self.p_full[s], step)
                 step += 1
-                if not self.has(pos % self.ks, (j, "V", t)):
-                    raise Fault("P V reads what is not its tile")
-                self.o_job[s] = j
                 self.use(pos % self.ks, 1)
                 self.queue[s].append(("PV", [pos % self.ks], None))
                 if i + 1 < len(tiles):
@@ -180,6 +191,10 @@ class Model:
                     yield from self.landed_waits(pos, pair)
                     if not self.has(pos % self.ks, (j, "V", t)):
                         raise Fault("the tail of another tile is cleared")
+                    self.clears[s, w] = (j, t)
+                    yield None
+                self.p_half[s].arrive()
+                yield None
                 self.p_full[s].arrive()
             yield (self.o_done, done)
             done += 1
