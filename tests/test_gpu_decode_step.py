@@ -79,3 +79,25 @@ def test_step_in_a_cuda_graph_gives_the_same():
     torch.cuda.synchronize()
     for a, b in zip(plain, captured):
         assert torch.equal(a, b)
+
+
+def test_steps_with_overlapping_launches_give_the_same():
+    """Programmatic overlap between the calls of a step: every launch waits for what it reads."""
+    import gemm_qmv_quantize_gb300 as q
+    from gemm_qmv_quantize_gb300.decode_step import DecodeStep
+    results = []
+    for overlap in (False, True):
+        net = DecodeStep(6, 700, 32, hidden=512, Hq=8, Hkv=2, D=64, vocab=4001, adapters=3, rank=16, page=16, seed=9)
+        g = torch.Generator(device="cuda").manual_seed(2)
+        xs = [torch.randn((6, 512), generator=g, device="cuda").half() for _ in range(12)]
+        torch.cuda.synchronize()
+        try:
+            q.set_launch_overlap(overlap)
+            out = [net.step(x) for x in xs]
+            torch.cuda.synchronize()
+        finally:
+            q.set_launch_overlap(False)
+        results.append(out)
+    for a, b in zip(*results):
+        for name in a:
+            assert torch.equal(a[name], b[name]), name
