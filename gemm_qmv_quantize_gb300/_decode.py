@@ -39,6 +39,12 @@ def _is(t, name: str, dtype, shape):
         _need(t, name, dtype, shape)
 
 
+def _held(t, name: str, dtype):
+    """_is for a tensor whose own shape the call goes by."""
+    if not (t.dtype is dtype and t.is_cuda and t.is_contiguous()):
+        _need(t, name, dtype)
+
+
 def _on(stream, t: torch.Tensor) -> int:
     """The handle of `stream`, or of the current one on t's device (without a Stream object
     for it, which costs as much as a launch)."""
@@ -86,7 +92,7 @@ def qmv_lora_add(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, adapter: tor
     L, R, _ = a.shape
     N = base.shape[1]
     xt, wt = _type(x, "x", (_F32, _F16)), _type(a, "a", _16BIT)
-    _is(x, "x", x.dtype, (M, K))
+    _held(x, "x", x.dtype)
     _is(a, "a", a.dtype, (L, R, K))
     _is(b, "b", a.dtype, (L, N, R))
     _is(adapter, "adapter", _I32, (M,))
@@ -137,12 +143,12 @@ def qmv_rope_append(qkv: torch.Tensor, positions: torch.Tensor, table: torch.Ten
         raise ValueError(f"axis_of_pair: expected {pairs} entries, got {len(axis_of_pair)}")
     dtype = k_cache.dtype
     t = _type(k_cache, "k_cache", _16BIT)
-    _is(qkv, "qkv", _F32, (M, width))
+    _held(qkv, "qkv", _F32)
     _is(positions, "positions", _I32, (axes, M))
     _is(table, "table", _F32, (n_positions, pairs, 2))
     _is(slots, "slots", torch.int64, (M,))
-    _is(k_cache, "k_cache", dtype, (pages, page, Hkv, D))
-    _is(v_cache, "v_cache", dtype, (pages, page, Hkv, D))
+    _held(k_cache, "k_cache", dtype)
+    _is(v_cache, "v_cache", dtype, k_cache.shape)
     if out is None:
         out = torch.empty((M, Hq, D), dtype=dtype, device=qkv.device)
     else:
@@ -177,10 +183,10 @@ def qmv_prefix_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     own_pages = own_table.shape[1]
     dtype = q.dtype
     t = _type(q, "q", _16BIT)
-    _is(q, "q", dtype, (B, T, Hq, D))
+    _held(q, "q", dtype)
     _is(k_cache, "k_cache", dtype, (pages, page, Hkv, D))
-    _is(v_cache, "v_cache", dtype, (pages, page, Hkv, D))
-    _is(prefix_table, "prefix_table", _I32, prefix_table.shape)
+    _is(v_cache, "v_cache", dtype, k_cache.shape)
+    _held(prefix_table, "prefix_table", _I32)
     _is(own_table, "own_table", _I32, (B, own_pages))
     _is(own_len, "own_len", _I32, (B,))
     if prefix_table.numel() * page < prefix_len:
@@ -190,7 +196,7 @@ def qmv_prefix_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     if out is None:
         out = torch.empty((B, T, Hq, D), dtype=dtype, device=q.device)
     else:
-        _is(out, "out", dtype, (B, T, Hq, D))
+        _is(out, "out", dtype, q.shape)
     need = lambda: qmv_prefix_attention_workspace(B, T, Hq, Hkv, D, prefix_len, max_own)  # noqa: E731
     ws = _workspace(workspace, need, q.device, stream)
     status = _fn("qmv_prefix_attention")(
@@ -215,7 +221,7 @@ def qmv_penalize_logits(logits: torch.Tensor, tokens: torch.Tensor, prompt_len: 
     set = allowed, with mask_row int32 [M] (negative: none). out may be logits."""
     M, V = logits.shape
     H = tokens.shape[1]
-    _is(logits, "logits", _F32, (M, V))
+    _held(logits, "logits", _F32)
     _is(tokens, "tokens", _I32, (M, H))
     _is(prompt_len, "prompt_len", _I32, (M,))
     _is(total_len, "total_len", _I32, (M,))

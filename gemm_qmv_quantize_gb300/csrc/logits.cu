@@ -7,8 +7,8 @@
 // A CTA owns a tile of a row's tokens, keeps their counts in shared memory and reads the
 // whole history, which the row's other CTAs find in L2, counting what is in its tile; then
 // its logits, loaded before that, pass through registers once. Counts are whole numbers:
-// the order of the atomics does not matter. Bound by the logits' bytes: a tile is no
-// shorter than the history, so that reading that again costs less than the tile. (Clusters
+// the order of the atomics does not matter. Bound by the logits' bytes, and by the latencies
+// of history, logits and biases one after the other, which a wave of CTAs has. (Clusters
 // that read the history once and count in each other's shared memory were slower at every
 // size measured: 14 to 23 us against 10 for 8 rows with 16000 tokens of history, 51 to 54
 // against 33 for 96 rows with 3000.)
@@ -26,7 +26,7 @@ __device__ uint32_t g_logits_error;
 constexpr int kThreads = 512;
 constexpr int kAhead = 3;             // float4 of logits and int4 of history that a thread loads
 constexpr int kHistoryAhead = 1;      // before it waits for anything
-constexpr int kMinTile = 4096, kMaxTile = 16384;
+constexpr int kMinTile = 2048, kMaxTile = 16384;
 constexpr int kSms = 152, kCtasPerSm = 3;
 constexpr uint32_t kSeen = 1u << 31;  // the bit above a token's count: it is in the prompt
 
@@ -150,7 +150,8 @@ __global__ void __launch_bounds__(kThreads, 3) logits_kernel(const __grid_consta
     if (g.max_bias == 0) return;
     // Biases, onto what this CTA has just written: the first entry of a token adds all of
     // that token's, in their order. (Inside the pass above, each thread that met a token with
-    // a bias searching the list, 8 rows with 100 biases took 13.5 us for 10.7.)
+    // a bias searching the list, 8 rows with 100 biases took 13.5 us for 10.7; each such token
+    // finished by the thread that marks it first, before the pass, 11.8.)
     __syncthreads();
     const float *bias_values = g.bias_values + static_cast<int64_t>(m) * g.max_bias;
     for (int j = tid; j < g.max_bias; j += kThreads) {
@@ -168,13 +169,23 @@ __global__ void __launch_bounds__(kThreads, 3) logits_kernel(const __grid_consta
     }
 }
 
+// The largest tile up to 16384 that leaves a wave of CTAs, three an SM (96 rows of 151936:
+// 33 us, 36 with 8192, 44 with 4096); 4096 for fewer rows, and 2048 where that leaves SMs
+// without a CTA (1 row: 5.0 us for 5.6).
+int tile_of(int M, int V)
+{
+    auto ctas = [&](int tile) { return static_cast<int64_t>(M) * ((V + tile - 1) / tile); };
+    int tile = ctas(2 * kMinTile) < kSms ? kMinTile : 2 * kMinTile;
+    while (tile > kMinTile && tile < kMaxTile && ctas(2 * tile) >= kCtasPerSm * kSms) tile *= 2;
+    return tile;
+}
+
 }  // namespace
 
 cudaError_t launch_logits(const LogitsArgs &g, cudaStream_t s)
 {
     route_hit(kRouteLogits);
-    int tile = kMinTile;
-    while (tile < kMaxTile && static_cast<int64_t>(g.M) * ((g.V + 2 * tile - 1) / (2 * tile)) >= kCtasPerSm * kSms) tile *= 2;
+    const int tile = tile_of(g.M, g.V);
     const size_t smem = static_cast<size_t>(tile + 4) * 4;
     cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(logits_kernel), static_cast<int>(smem));
     if (e != cudaSuccess) return e;

@@ -73,6 +73,13 @@ def test_many_repeats_of_one_token():
     check(args)
 
 
+def test_long_bias_lists_with_repeats():
+    args = inputs(2, 3000, 60, 1700, 1, seed=9)      # more entries than a CTA has threads, each token several
+    args["bias_tokens"] = args["bias_tokens"].remainder(400)
+    check(args)
+    check(args, out=args["logits"])
+
+
 def test_special_values():
     args = inputs(3, 300, 50, 10, 2, seed=3)
     args["logits"][0, :40] = -math.inf
