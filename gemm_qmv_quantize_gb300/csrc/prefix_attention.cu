@@ -4,10 +4,11 @@
 //
 // The rows of all requests that read one key head meet the same prefix keys, so they are
 // the rows of one matrix product: B T G rows (G = query heads a key head) x 128 keys a
-// step on the 5th-generation tensor cores, the prefix read once for up to 256 of them.
-// A request's own keys are the same product with its T G rows. Both are "jobs" of one
-// kernel: a key head, up to 256 consecutive rows i = (b T + t) G + g, and a range of
-// 128-key tiles; a row's jobs leave partial results that a second kernel joins.
+// step on the 5th-generation tensor cores, the prefix read once for up to 256 of them. A
+// "job" is a key head, up to 256 consecutive rows i = (b T + t) G + g, and a share of the
+// 128-key tiles. A request's own keys against more than 64 rows are jobs of the same kernel;
+// for up to 64 rows, and for a prefix that at most 16 rows see, few_rows_kernel further down
+// has products of 16 rows. What a row's jobs leave is joined by a last kernel.
 //
 // A job (one CTA; TMEM columns: S0, S1, O0, O1 of 128 each):
 //   S = Q K^T into tensor memory (fp32); 128 threads, a row each, take the running
@@ -19,6 +20,11 @@
 //   row's maximum has grown by more, which is rare, and P stays far below the 16-bit
 //   types' range. Statistics and sums are fp32; P is rounded to the inputs' type, the
 //   operand that the product takes.
+//
+// 51 requests of 5 query heads a key head (255 rows) behind 65536 keys take 69 us, 990
+// TFLOP/s; 25 of them (125 rows, bound by the keys' bytes) 55 us, 4.9 TB/s. A stream's
+// products, softmax and P V follow one another, about 3000 cycles a tile; its exponentials
+// and the handing over, not the tensor cores (50 % busy), bound the first.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
