@@ -9,6 +9,7 @@ inputs (|q . k| sums below 60 after scaling), which moves a probability by as mu
 (u |o|, 2^-24 below binary16's normal range).
 """
 import math
+import random
 
 import pytest
 import torch
@@ -68,6 +69,25 @@ def test_sizes_types_pages(B, T, Hq, Hkv, D, prefix, own_len, page, type_):
 @pytest.mark.parametrize("prefix", [2000, 4096 + 63])
 def test_long_prefix_split_over_the_device(prefix):
     check(inputs(6, 1, 8, 2, 128, prefix, [9, 600, 0, 1, 129, 255], 64, "bf16", seed=1), "bf16")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("B,T,Hq,Hkv,prefix,own_len", [
+    (20, 1, 8, 2, 1500, [3 * i for i in range(20)]), (2, 20, 8, 2, 515, [300, 20]), (9, 4, 9, 1, 1100, [4 + 60 * i for i in range(9)])])
+def test_pages_longer_than_a_tile(B, T, Hq, Hkv, D, prefix, own_len):
+    check(inputs(B, T, Hq, Hkv, D, prefix, own_len, 256, "bf16", seed=B), "bf16")
+
+
+@pytest.mark.parametrize("seed", range(20))
+def test_drawn_sizes(seed):
+    rng = random.Random(seed)
+    Hkv, G, D, T = rng.choice([1, 2, 3]), rng.randint(1, 9), rng.choice([64, 128]), rng.choice([1, 1, 2, 4, 11])
+    B = rng.choice([1, 2, 7, 30, 70])
+    most = rng.choice([0, 1, 40, 300]) if B > 7 else rng.choice([1, 200, 1500])
+    own_len = [rng.randint(0, most) for _ in range(B)]
+    prefix = rng.choice([0, 1, 63, 128, 129, 400, 2200])
+    type_ = rng.choice(["f16", "bf16"])
+    check(inputs(B, T, Hkv * G, Hkv, D, prefix, own_len, rng.choice([16, 32, 64, 128, 256]), type_, seed=seed), type_)
 
 
 def test_more_rows_than_a_tile():
