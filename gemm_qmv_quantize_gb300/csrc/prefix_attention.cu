@@ -52,7 +52,7 @@ constexpr int kThreads = 32 * 12;       // two streams of 4 warps, the product w
 constexpr int kRegsSoftmax = 224, kRegsOther = 56;
 constexpr int kTmemCols = 512;
 constexpr int kMaxSlots = 8;
-constexpr int kSmemBytes = 232448 - 3072;   // dynamic shared memory: a CTA's limit but the barriers and statistics
+constexpr int kSmemBytes = 224 * 1024;   // dynamic shared memory: a CTA's 227 KB but the barriers and statistics
 constexpr int kSms = 152;
 constexpr int kFewRows = 64;            // rows of a request and key head up to which its own keys have a kernel of their own
 constexpr float kSlack = 8.0f;          // log2 of the growth of a row's maximum that rescales O
