@@ -960,19 +960,21 @@ __global__ void __launch_bounds__(32 * kFewWarps) few_rows_kernel(const __grid_c
     float *part = reinterpret_cast<float *>(ring);   // this warp's ring, [16][kD + 4]
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
+        // A warp without a key for this row has the sum 0 beside m = -inf. A sum of NaN stands
+        // beside -inf too where all its scores are NaN (no maximum is above -inf then): it goes on.
         float top = -INFINITY, sum = 0.0f;
 #pragma unroll
         for (int w = 0; w < kFewWarps; ++w) top = fmaxf(top, stat_m[w][gid + 8 * r]);
 #pragma unroll
         for (int w = 0; w < kFewWarps; ++w) {
-            const float mw = stat_m[w][gid + 8 * r];
-            sum += mw == -INFINITY ? 0.0f : stat_l[w][gid + 8 * r] * exp2_fast(mw - top);
+            const float lw = stat_l[w][gid + 8 * r];
+            sum += lw == 0.0f ? 0.0f : lw * exp2_fast(stat_m[w][gid + 8 * r] - top);
         }
-        const float fix = m[r] == -INFINITY ? 0.0f : exp2_fast(m[r] - top) / sum;
+        const float fix = l[r] == 0.0f ? 0.0f : exp2_fast(m[r] - top) / sum;
 #pragma unroll
         for (int d = 0; d < kD / 8; ++d)
             *reinterpret_cast<float2 *>(part + (gid + 8 * r) * kPitch + 8 * d + 2 * t) = make_float2(o[d][2 * r] * fix, o[d][2 * r + 1] * fix);
-        if (warp == 0 && t == 0 && gid + 8 * r < nrows) p.lse[out_row0 + gid + 8 * r] = top == -INFINITY ? -INFINITY : top - kLift + log2f(sum);
+        if (warp == 0 && t == 0 && gid + 8 * r < nrows) p.lse[out_row0 + gid + 8 * r] = sum == 0.0f ? -INFINITY : top - kLift + log2f(sum);
     }
     __syncthreads();
     constexpr int kRingFloats = kFewStages * 2 * kTileBytes / 4;

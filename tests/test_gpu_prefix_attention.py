@@ -222,3 +222,49 @@ def test_refusals():
         q.qmv_prefix_attention(**{**args, "q": args["q"].bfloat16()})
     with pytest.raises(TypeError):
         q.qmv_prefix_attention(**{**args, "own_len": args["own_len"].long()})
+
+
+def check_special(args, type_, **kw):
+    """check, where inputs that are used hold infinities and NaN: those of the result are the definition's."""
+    import gemm_qmv_quantize_gb300 as q
+    D = args["q"].shape[3]
+    ref, bound = decode_ref.attention(**args, scale=1 / math.sqrt(D))
+    got = q.qmv_prefix_attention(**args, **kw).double()
+    u = TYPES[type_][1]
+    fine = torch.isfinite(ref)
+    assert torch.equal(torch.isnan(got), torch.isnan(ref))
+    assert torch.equal(got[torch.isinf(ref)], ref[torch.isinf(ref)])
+    assert bool(((got - ref).abs() <= u * ref.abs() + (u + 2e-3) * bound + 2.0 ** -24)[fine].all())
+    return got
+
+
+def own_place(args, b, key):
+    """(page, offset) of an own key of request b."""
+    page = args["k_cache"].shape[1]
+    return int(args["own_table"][b, key // page]), key % page
+
+
+# prefix and own keys through the 16-row kernel; without a prefix; own keys alone there; the
+# prefix as one stream pair and as several; own keys of many rows as tcgen05 jobs, 128 rows and more
+EACH_KERNEL = [(2, 1, 8, 2, 64, 300, [5, 40], 16), (3, 2, 12, 2, 128, 0, [9, 2, 300], 32), (20, 1, 8, 2, 128, 700, [1 + 9 * i for i in range(20)], 64),
+               (70, 2, 4, 2, 64, 1500, [2 + i for i in range(70)], 16), (2, 20, 8, 2, 128, 260, [20, 300], 16),
+               (2, 70, 4, 1, 64, 129, [70, 333], 32)]
+
+
+@pytest.mark.parametrize("type_", ["f16", "bf16"])
+@pytest.mark.parametrize("B,T,Hq,Hkv,D,prefix,own_len,page", EACH_KERNEL)
+def test_nan_query_row_is_nan(type_, B, T, Hq, Hkv, D, prefix, own_len, page):
+    args = inputs(B, T, Hq, Hkv, D, prefix, own_len, page, type_, seed=31)
+    args["q"][1, T - 1, 2, 7] = math.nan
+    got = check_special(args, type_)
+    assert bool(torch.isnan(got[1, T - 1, 2]).all()) and int(torch.isnan(got).sum()) == D
+
+
+@pytest.mark.parametrize("type_", ["f16", "bf16"])
+@pytest.mark.parametrize("B,T,Hq,Hkv,D,prefix,own_len,page", EACH_KERNEL)
+def test_nan_key_that_is_used_gives_nan(type_, B, T, Hq, Hkv, D, prefix, own_len, page):
+    """The first own key of request 1, all that its first rows have there."""
+    args = inputs(B, T, Hq, Hkv, D, prefix, [T if b == 1 else n for b, n in enumerate(own_len)], page, type_, seed=32)
+    args["k_cache"][(*own_place(args, 1, 0), 1 % Hkv)] = math.nan
+    got = check_special(args, type_)
+    assert int(torch.isnan(got).sum()) == T * (Hq // Hkv) * D
