@@ -997,6 +997,75 @@ __global__ void __launch_bounds__(32 * kFewWarps) few_rows_kernel(const __grid_c
     }
 }
 
+template <typename T>
+__device__ __forceinline__ float2 widen2(uint32_t two)
+{
+    if constexpr (std::is_same_v<T, __half>) {
+        return __half22float2(*reinterpret_cast<const __half2 *>(&two));
+    } else {
+        return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&two));
+    }
+}
+
+// Columns d0 .. d0 + 7 of row i once more, where they did not come out finite. In the products
+// above a key that the row does not see (a later token of its request) has P = 0, which an
+// infinity or NaN among that key's values turns into NaN. Here the row's own keys are gone
+// through one by one, only those that it sees, beside the prefix's partial results: what is
+// still not finite is the formula's. (Looking through those values before each product
+// instead cost 3 to 5 % of the calls with several tokens a request.)
+template <typename T, int kD>
+__device__ __forceinline__ void row_again(const AttnParams &p, int h, int i, int d0, int64_t per_slot, int slots, const float *lse,
+                                          const float4 *part, float (&acc)[8], float &sum)
+{
+    const AttnArgs &g = p.g;
+    const int G = g.Hq / g.Hkv, b = i / G / g.T, shift = __ffs(g.page) - 1;
+    const int64_t seen = min(static_cast<int64_t>(__ldg(g.own_len + b)), g.max_own) - g.T + 1 + i / G % g.T;
+    const float c = g.scale * 1.4426950408889634f;
+    const int64_t q_row = (static_cast<int64_t>(i / G) * g.Hq + h * G + i % G) * kD;
+    float top = -INFINITY;
+    sum = 0.0f;
+#pragma unroll
+    for (int x = 0; x < 8; ++x) acc[x] = 0.0f;
+    // eight values v with the logarithm e of their weight
+    auto add = [&](float e, const float *v) {
+        if (e == -INFINITY) return;
+        const float next = fmaxf(top, e), fix = top == -INFINITY ? 1.0f : exp2_fast(top - next), w = exp2_fast(e - next);
+        top = next;
+        sum = fmaf(sum, fix, w);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) acc[x] = fmaf(w, v[x], acc[x] * fix);
+    };
+#pragma unroll 1
+    for (int k = p.plan.own_splits; k < slots; ++k) {
+        const float4 lo = part[k * per_slot * (kD / 4)], hi = part[k * per_slot * (kD / 4) + 32];
+        const float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        add(lse[k * per_slot], v);
+    }
+#pragma unroll 1
+    for (int64_t key = 0; key < seen; ++key) {
+        const int page = __ldg(g.own_table + static_cast<int64_t>(b) * g.own_pages + (key >> shift));
+        float s = 0.0f, v[8] = {};   // (what a page outside the cache reads as)
+        if (page >= 0 && page < g.n_pages) {
+            const int64_t at = ((static_cast<int64_t>(page) * g.page + (key & (g.page - 1))) * g.Hkv + h) * kD;
+            const uint32_t *k2 = reinterpret_cast<const uint32_t *>(static_cast<const T *>(g.k_cache) + at);
+            const uint32_t *v2 = reinterpret_cast<const uint32_t *>(static_cast<const T *>(g.v_cache) + at + d0);
+            const uint32_t *q2 = reinterpret_cast<const uint32_t *>(static_cast<const T *>(g.q) + q_row);
+#pragma unroll 4
+            for (int d = 0; d < kD / 2; ++d) {
+                const float2 a = widen2<T>(__ldg(q2 + d)), e = widen2<T>(__ldg(k2 + d));
+                s = fmaf(a.x, e.x, fmaf(a.y, e.y, s));
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const float2 e = widen2<T>(__ldg(v2 + x));
+                v[2 * x] = e.x;
+                v[2 * x + 1] = e.y;
+            }
+        }
+        add(s * c, v);
+    }
+}
+
 // Joins the partial results of 32 rows of a key head for 8 of D, a row a lane: weights
 // 2^(lse - max) over their sum. Bound by latency: the four warps take every fourth slot, so
 // that about all loads are under way at once, statistics and results alike, and are joined
@@ -1072,6 +1141,12 @@ __global__ void __launch_bounds__(128) attention_join_kernel(const __grid_consta
         sum = fmaf(f, sums[w][lane], sum);
 #pragma unroll
         for (int x = 0; x < 8; ++x) acc[x] = fmaf(f, accs[w][x][lane], acc[x]);
+    }
+    if (g.T > 1 && p.plan.own_splits > 0) {
+        bool finite = true;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) finite &= isfinite(acc[x]);
+        if (!finite) row_again<T, kD>(p, h, i, d0, per_slot, slots, lse, part, acc, sum);
     }
     const float inv = sum > 0.0f || isnan(sum) ? 1.0f / sum : 0.0f;   // no key at all: zeros
     uint4 out;

@@ -330,7 +330,7 @@ QMV_API qmv_status qmv_rope_append(const float *qkv, const int32_t *positions, c
  *            caller knows, itself at most own_pages * page; a longer one is cut to
  *            max_own and sets bit 2). A page outside the cache reads as zeros (bit 2).
  *            Whatever lies in the cache past a request's length or the prefix's is not
- *            used, NaN included.
+ *            used, NaN included, and no row is touched by tokens after its own.
  *   scale    finite and positive.
  *   Workspace: qmv_prefix_attention_workspace(...) bytes (negative: QMV_ERR_SHAPE).
  */

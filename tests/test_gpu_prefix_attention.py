@@ -268,3 +268,18 @@ def test_nan_key_that_is_used_gives_nan(type_, B, T, Hq, Hkv, D, prefix, own_len
     args["k_cache"][(*own_place(args, 1, 0), 1 % Hkv)] = math.nan
     got = check_special(args, type_)
     assert int(torch.isnan(got).sum()) == T * (Hq // Hkv) * D
+
+
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+@pytest.mark.parametrize("type_", ["f16", "bf16"])
+@pytest.mark.parametrize("B,T,Hq,Hkv,D,prefix,own_len,page", [c for c in EACH_KERNEL if c[1] > 1] + [
+    (1, 5, 4, 2, 128, 0, [5], 16), (3, 3, 6, 2, 64, 40, [1, 2, 19], 32), (1, 200, 1, 1, 64, 0, [290], 64)])
+def test_a_later_tokens_value_does_not_reach_earlier_rows(type_, value, B, T, Hq, Hkv, D, prefix, own_len, page):
+    """Values of the last tokens of a request, which its earlier tokens do not see, are NaN or infinite."""
+    args = inputs(B, T, Hq, Hkv, D, prefix, own_len, page, type_, seed=33)
+    b, n = B - 1, own_len[B - 1]
+    args["v_cache"][(*own_place(args, b, n - 1), 0, 3)] = value
+    args["v_cache"][(*own_place(args, b, n - 2), Hkv - 1, D - 1)] = -value
+    got = check_special(args, type_)
+    assert bool(torch.isfinite(got[:, :T - 2]).all()) and bool(torch.isfinite(got[:b]).all())
+    assert not bool(torch.isfinite(got[b, T - 1, 0, 3])) and not bool(torch.isfinite(got[b, T - 1, Hq - 1, D - 1]))
