@@ -1148,7 +1148,11 @@ __global__ void __launch_bounds__(128) attention_join_kernel(const __grid_consta
         for (int x = 0; x < 8; ++x) finite &= isfinite(acc[x]);
         if (!finite) row_again<T, kD>(p, h, i, d0, per_slot, slots, lse, part, acc, sum);
     }
-    const float inv = sum > 0.0f || isnan(sum) ? 1.0f / sum : 0.0f;   // no key at all: zeros
+    float inv = 1.0f / sum;   // (all scores -inf: 0 / 0, as the formula has it)
+    if (sum == 0.0f && g.prefix_len == 0) {   // no key at all: zeros
+        const int64_t own = g.max_own > 0 ? min(static_cast<int64_t>(g.own_len[i / G / g.T]), g.max_own) : 0;
+        if (own - g.T + 1 + i / G % g.T <= 0) inv = 0.0f;
+    }
     uint4 out;
     out.x = pack2<T>(acc[0] * inv, acc[1] * inv);
     out.y = pack2<T>(acc[2] * inv, acc[3] * inv);

@@ -320,7 +320,8 @@ QMV_API qmv_status qmv_rope_append(const float *qkv, const int32_t *positions, c
  *   out[b][t][h] = sum_j p_j V_j,  p = softmax_j(scale * q[b][t][h] . K_j)
  * over the keys j of the prefix and the first own_len[b] - T + 1 + t own ones; head h
  * reads key head h / (Hq / Hkv). The T tokens are the last of own_len[b], so their keys
- * are in the cache before the call. A row without any key gives zeros.
+ * are in the cache before the call. A row without any key gives zeros (one whose scores
+ * are all -inf, NaN).
  *   q, out   [B][T][Hq][D], D = 64 or 128, Hkv dividing Hq.
  *   k_cache, v_cache [n_pages][page][Hkv][D], page a power of two, 16..256. All of the
  *            type `type` (QMV_F16 or QMV_BF16), 16-byte aligned.

@@ -283,3 +283,17 @@ def test_a_later_tokens_value_does_not_reach_earlier_rows(type_, value, B, T, Hq
     got = check_special(args, type_)
     assert bool(torch.isfinite(got[:, :T - 2]).all()) and bool(torch.isfinite(got[:b]).all())
     assert not bool(torch.isfinite(got[b, T - 1, 0, 3])) and not bool(torch.isfinite(got[b, T - 1, Hq - 1, D - 1]))
+
+
+@pytest.mark.parametrize("type_", ["f16", "bf16"])
+@pytest.mark.parametrize("B,T,Hq,Hkv,D,prefix,own_len,page", EACH_KERNEL)
+def test_scores_that_are_all_minus_infinity(type_, B, T, Hq, Hkv, D, prefix, own_len, page):
+    """0 / 0, not the zeros of a row without a key; beside finite scores they count for nothing."""
+    args = inputs(B, T, Hq, Hkv, D, prefix, own_len, page, type_, seed=34)
+    args["q"][..., 0] = 1.0
+    for table, n in [(args["prefix_table"], prefix)] + [(args["own_table"][b], own_len[b]) for b in range(0, B, 2)]:
+        for j in range(0, n, page):
+            args["k_cache"][int(table[j // page]), :min(page, n - j), 0, 0] = -math.inf
+    got = check_special(args, type_)
+    G, last = Hq // Hkv, T - 1
+    assert bool(torch.isnan(got[0, last, :G]).all()) and bool(torch.isfinite(got[1, last]).all())
