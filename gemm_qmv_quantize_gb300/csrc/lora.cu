@@ -352,12 +352,12 @@ __global__ void __launch_bounds__(kThreads) lora_expand_kernel(LoraArgs g, int s
     }
 }
 
-// K of a shrink warp: 512 where that fills the SMs
-// twice, else 128, one round of loads.
+// K of a shrink warp: 512 where that fills the SMs twice, else 128, one round of loads.
+constexpr int kShortRange = 128, kLongRange = 512;
 int shrink_k(int M, int R, int64_t K)
 {
-    const int64_t ctas = static_cast<int64_t>(M) * ((R + kRankTile - 1) / kRankTile) * ((K + 512 * kWarps - 1) / (512 * kWarps));
-    return ctas >= 2 * kSms ? 512 : 128;
+    const int64_t ctas = static_cast<int64_t>(M) * ((R + kRankTile - 1) / kRankTile) * ((K + kLongRange * kWarps - 1) / (kLongRange * kWarps));
+    return ctas >= 2 * kSms ? kLongRange : kShortRange;
 }
 
 int64_t shrink_splits(int M, int R, int64_t K)
@@ -398,7 +398,13 @@ cudaError_t launch_both(const LoraArgs &g, cudaStream_t s)
 
 }  // namespace
 
-int64_t lora_workspace_bytes(int M, int R, int64_t K) { return shrink_splits(M, R, K) * M * R * 4; }
+// As for the shortest ranges at every size: a caller keeps the workspace of its largest batch,
+// and a smaller one has the more of them.
+int64_t lora_workspace_bytes(int M, int R, int64_t K)
+{
+    const int64_t per = kShortRange * kWarps;
+    return (K + per - 1) / per * M * R * 4;
+}
 
 cudaError_t launch_lora(const LoraArgs &g, cudaStream_t s)
 {

@@ -1217,10 +1217,21 @@ int64_t row_blocks_of(int B, int T, int Hq, int Hkv) { return ceil_div(static_ca
 
 }  // namespace
 
+// Bytes for any plan of at most these sizes: a caller keeps the workspace of its largest
+// batch. (A plan's own need is not monotone, since fewer rows are split into more ranges.) In
+// blocks of 32 rows of a key head, of which there are n: the prefix is cut into at most a
+// range a tile, 256 ranges, and in all n + 8 blocks x 152 SMs (plan_attention gives a pair of
+// streams, 8 blocks, 152 times its share of the cost, rounded); own keys into a range of 256
+// keys at least, 256 ranges, and n + 8 x 152, or above 64 rows a request, of 8 blocks a job,
+// n + 8 x 3/2 x 304.
 int64_t attn_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int64_t prefix_len, int64_t max_own)
 {
-    const AttnPlan plan = plan_attention(B, T, Hq, Hkv, prefix_len, max_own);
-    return plan.slots * Hkv * row_blocks_of(B, T, Hq, Hkv) * 32 * (D + 1) * 4;
+    const int64_t n = Hkv * row_blocks_of(B, T, Hq, Hkv), most = 256;
+    const int64_t prefix = std::min(n * std::min(ceil_div(prefix_len, kTile), most), n + 8 * kSms);
+    const int64_t own = std::min(n * std::min(ceil_div(max_own, 2 * kTile), most),
+                                 n + 8 * kSms * (static_cast<int64_t>(T) * (Hq / Hkv) > kFewRows ? 3 : 1));
+    const int64_t planned = n * plan_attention(B, T, Hq, Hkv, prefix_len, max_own).slots;
+    return std::max(prefix + own, planned) * 32 * (D + 1) * 4;
 }
 
 cudaError_t launch_attention(const AttnArgs &g, cudaStream_t s)

@@ -261,8 +261,9 @@ QMV_API int qmv_get_launch_overlap(void);
  * 16-bit tensors are IEEE binary16 or bfloat16, named by a type argument. Sums,
  * softmax statistics and products are fp32; an output is rounded once. A workspace is
  * device memory of the caller, 16-byte aligned, of at least the bytes that the call's
- * _workspace function names; its contents need no initialisation and hold nothing
- * between calls. Calls in flight at the same time need workspaces of their own.
+ * _workspace function names, which for more rows, requests, tokens or keys is never less
+ * (the workspace of a program's largest batch serves all of its calls); its contents need
+ * no initialisation and hold nothing between calls. Calls in flight at the same time need workspaces of their own.
  * Indices that the kernels read from device memory are checked against their arrays:
  * one outside sets bit 2 of qmv_error_flags and is handled as each call says, never
  * followed.

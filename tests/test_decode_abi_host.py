@@ -1,6 +1,7 @@
 """Argument validation of the decode-step operators, without a GPU: refusals and empty
 calls answer before any CUDA call. Only pointer values are passed, never followed."""
 import ctypes
+import random
 
 import pytest
 
@@ -107,3 +108,31 @@ def test_penalize_logits(lib, changes, status):
 def test_workspaces_are_64_bit(lib):
     assert lib.qmv_lora_add_workspace.restype is ctypes.c_int64
     assert lib.qmv_prefix_attention_workspace.restype is ctypes.c_int64
+
+
+def test_lora_add_workspace_of_the_largest_serves_all(lib):
+    need = lib.qmv_lora_add_workspace
+    assert need(96, 64, 4096) >= need(75, 64, 4096) and need(96, 16, 16384) >= need(96, 16, 12288)
+    rng = random.Random(1)
+    for _ in range(5000):
+        M, R, K = rng.randint(1, 96), 8 * rng.randint(1, 32), 8 * rng.randint(1, 3000)
+        most = need(M, R, K)
+        assert most >= need(rng.randint(0, M), R, K) and most >= need(M, 8 * rng.randint(1, R // 8), K)
+        assert most >= need(M, R, 8 * rng.randint(0, K // 8))
+
+
+def test_prefix_attention_workspace_of_the_largest_serves_all(lib):
+    need = lib.qmv_prefix_attention_workspace
+    assert need(64, 1, 40, 8, 128, 65536, 1024) >= need(45, 1, 40, 8, 128, 65536, 1024)
+    rng = random.Random(2)
+    any_of = lambda n: int(n ** rng.random())  # noqa: E731
+    for _ in range(20000):
+        Hkv = rng.choice([1, 2, 4, 8, 16])
+        heads = (Hkv * rng.randint(1, 10), Hkv, rng.choice([64, 128]))
+        B, T, prefix, own = any_of(400), rng.choice([1, 1, 2, 5, 8, 30, 96, 700]), any_of(200000) - 1, any_of(60000) - 1
+        most = need(B, T, *heads, prefix, own)
+        if most < 0:      # more rows than a call takes
+            continue
+        b, t, p, o = rng.randint(0, B), rng.randint(1, T), rng.randint(0, prefix), rng.randint(0, own)
+        for fewer in ((b, T, prefix, own), (B, t, prefix, own), (B, T, p, own), (B, T, prefix, o), (b, t, p, o)):
+            assert most >= need(fewer[0], fewer[1], *heads, *fewer[2:])

@@ -128,3 +128,10 @@ def test_refusals():
         q.qmv_lora_add(**inputs(2, 32, 64, 12, 2))         # rank not a multiple of 8
     with pytest.raises(q.QmvError):
         q.qmv_lora_add(**inputs(97, 32, 64, 8, 2))         # more rows than a projection takes
+
+
+def test_one_workspace_for_a_shrinking_batch():
+    import gemm_qmv_quantize_gb300 as q
+    ws = torch.empty((q.qmv_lora_add_workspace(96, 64, 4096),), dtype=torch.uint8, device="cuda")
+    for M in (96, 75, 20, 1):
+        check(inputs(M, 130, 4096, 64, 5, seed=M), workspace=ws)
