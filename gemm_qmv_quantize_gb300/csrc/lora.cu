@@ -49,7 +49,7 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], float a0, float a1, floa
           "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)));
 }
 
-// v as two TF32 terms: the first cut, the second rounded.
+// v as two TF32 terms: the first cut, the second rounded (NaN beside an infinity).
 __device__ __forceinline__ void split_tf32(float v, float &hi, float &lo)
 {
     hi = __uint_as_float(__float_as_uint(v) & 0xffffe000u);
@@ -57,6 +57,10 @@ __device__ __forceinline__ void split_tf32(float v, float &hi, float &lo)
     asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(v - hi));
     lo = __uint_as_float(r);
 }
+
+// Sums of first and of second terms. An infinity among the operands shows in the first
+// terms' sum, and in the second's only as NaN (inf - inf, or 0 x inf).
+__device__ __forceinline__ float both_terms(float first, float second) { return isfinite(first) ? first + second : first; }
 
 template <typename W>
 __device__ __forceinline__ float2 widen(uint32_t two)
@@ -218,7 +222,7 @@ __global__ void __launch_bounds__(kThreads) lora_shrink_kernel(LoraArgs g, int w
             mma_step<W, kP == 2>(sum, rest, *piece(st, 2 * c), *piece(st, 2 * c + 1), hi, lo);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) d[i] += sum[i] + rest[i];
+        for (int i = 0; i < 4; ++i) d[i] += kP == 2 ? both_terms(sum[i], rest[i]) : sum[i];
     }
     sums[warp][gid][2 * t] = d[0];
     sums[warp][gid][2 * t + 1] = d[1];
@@ -338,7 +342,7 @@ __global__ void __launch_bounds__(kThreads) lora_expand_kernel(LoraArgs g, int s
                 mma_step<W, true>(sum, rest, *piece(st, 2 * c), *piece(st, 2 * c + 1), hi, lo);
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) d[j] += sum[j] + rest[j];
+            for (int j = 0; j < 4; ++j) d[j] += both_terms(sum[j], rest[j]);
         }
         const int64_t n = (static_cast<int64_t>(first) + static_cast<int64_t>(i) * stride) * kRankTile + gid;
         if (n < g.N) {

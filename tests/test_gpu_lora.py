@@ -135,3 +135,29 @@ def test_one_workspace_for_a_shrinking_batch():
     ws = torch.empty((q.qmv_lora_add_workspace(96, 64, 4096),), dtype=torch.uint8, device="cuda")
     for M in (96, 75, 20, 1):
         check(inputs(M, 130, 4096, 64, 5, seed=M), workspace=ws)
+
+
+@pytest.mark.parametrize("w", ["f16", "bf16"])
+@pytest.mark.parametrize("x", ["f32", "f16"])
+def test_infinite_activations(x, w):
+    import gemm_qmv_quantize_gb300 as q
+    args = inputs(3, 200, 256, 16, 2, x, w, seed=10, adapter=[0, 1, 0])
+    args["a"], args["b"] = (t.abs().clamp(min=1e-3) for t in (args["a"], args["b"]))   # no 0 x inf, no inf - inf
+    args["x"][1, 5] = -float("inf")
+    y, _ = decode_ref.lora(**args)
+    got = q.qmv_lora_add(**args).double()
+    assert bool(torch.isneginf(got[1]).all()) and bool(torch.isneginf(y[1]).all())
+    assert bool(torch.isfinite(got[::2]).all())
+
+
+def test_products_beyond_fp32_and_infinite_weights():
+    import gemm_qmv_quantize_gb300 as q
+    args = inputs(3, 64, 256, 16, 2, "f32", "f16", seed=11, adapter=[0, 1, 0])
+    args["x"], args["b"] = torch.zeros_like(args["x"]), args["b"].abs().clamp(min=1e-3)
+    args["x"][0, 0], args["x"][1, 0] = 3e38, 2.0
+    args["a"][:, :, 0] = 60000.0
+    args["b"][1, 7, 3] = float("inf")
+    got = q.qmv_lora_add(**args)
+    assert bool(torch.isposinf(got[0]).all())              # A x is past fp32's range
+    assert bool(torch.isposinf(got[1, 7])) and int(torch.isfinite(got[1]).sum()) == 63
+    assert torch.equal(got[2], args["base"][2])
