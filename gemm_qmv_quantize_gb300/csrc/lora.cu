@@ -356,12 +356,15 @@ __global__ void __launch_bounds__(kThreads) lora_expand_kernel(LoraArgs g, int s
     }
 }
 
-// K of a shrink warp: 512 where that fills the SMs twice, else 128, one round of loads.
+// K of a shrink warp: 512 where that fills the SMs twice, else 128, one round of loads; more
+// where a grid has no room for as many ranges (K above 2^28).
 constexpr int kShortRange = 128, kLongRange = 512;
 int shrink_k(int M, int R, int64_t K)
 {
     const int64_t ctas = static_cast<int64_t>(M) * ((R + kRankTile - 1) / kRankTile) * ((K + kLongRange * kWarps - 1) / (kLongRange * kWarps));
-    return ctas >= 2 * kSms ? kLongRange : kShortRange;
+    int range = ctas >= 2 * kSms ? kLongRange : kShortRange;
+    while (K > static_cast<int64_t>(range) * kWarps * 65535) range *= 2;
+    return range;
 }
 
 int64_t shrink_splits(int M, int R, int64_t K)

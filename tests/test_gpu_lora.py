@@ -161,3 +161,15 @@ def test_products_beyond_fp32_and_infinite_weights():
     assert bool(torch.isposinf(got[0]).all())              # A x is past fp32's range
     assert bool(torch.isposinf(got[1, 7])) and int(torch.isfinite(got[1]).sum()) == 63
     assert torch.equal(got[2], args["base"][2])
+
+
+def test_sums_longer_than_a_grid_has_ranges():
+    import gemm_qmv_quantize_gb300 as q
+    K = (1 << 28) + (1 << 15)
+    x = torch.zeros((1, K), dtype=torch.float16, device="cuda")
+    x[0, ::1 << 20] = 1.0
+    x[0, -1] = 1.0
+    one = lambda *s, dtype=torch.float16: torch.ones(s, dtype=dtype, device="cuda")  # noqa: E731
+    y = q.qmv_lora_add(x, one(1, 8, K), one(1, 5, 8), torch.zeros((1,), dtype=torch.int32, device="cuda"),
+                       one(1, dtype=torch.float32), torch.zeros((1, 5), device="cuda"))
+    assert y.tolist() == [[8.0 * 258] * 5]
