@@ -4,8 +4,9 @@ shared prefix, and penalties, biases and masks on logits.
 
 As in ``_binding``: tensors are checked for type, shape and contiguity, pointers and
 sizes go to the C entry point of the same name, and all arithmetic runs in the library.
-A workspace that is not given is allocated for the call; a program that repeats calls
-keeps one of the bytes that the ``_workspace`` function names.
+An output or a workspace that is not given is allocated for the call, from the memory of
+its stream; a program that repeats calls keeps a workspace of the bytes that the
+``_workspace`` function names for its largest batch.
 """
 from __future__ import annotations
 
@@ -51,13 +52,22 @@ def _on(stream, t: torch.Tensor) -> int:
     return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else _stream(stream)
 
 
+def _empty(shape, dtype, device, stream):
+    """A new tensor for a call on `stream`, from the memory of that stream: a block that the
+    current one has freed may still be in use by its queued work, which `stream` does not
+    wait for."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _workspace(buffer, need, device, stream):
-    """`buffer`, or a new one of need() bytes that stays valid for the call's stream."""
+    """`buffer`, or a new one of need() bytes for a call on `stream`."""
     if buffer is None:
-        buffer = torch.empty((need(),), dtype=torch.uint8, device=device)
-        if stream is not None:
-            buffer.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
-                                 torch.cuda.ExternalStream(_stream(stream)))
+        buffer = _empty((need(),), torch.uint8, device, stream)
     elif not (buffer.dtype is torch.uint8 and buffer.is_cuda and buffer.is_contiguous()):
         _need(buffer, "workspace", torch.uint8)
     return buffer
@@ -99,7 +109,7 @@ def qmv_lora_add(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, adapter: tor
     _is(scale, "scale", _F32, (L,))
     _is(base, "base", _F32, (M, N))
     if out is None:
-        out = torch.empty((M, N), dtype=_F32, device=base.device)
+        out = _empty((M, N), _F32, base.device, stream)
     else:
         _is(out, "out", _F32, (M, N))
     need = lambda: qmv_lora_add_workspace(M, R, K)  # noqa: E731
@@ -150,7 +160,7 @@ def qmv_rope_append(qkv: torch.Tensor, positions: torch.Tensor, table: torch.Ten
     _held(k_cache, "k_cache", dtype)
     _is(v_cache, "v_cache", dtype, k_cache.shape)
     if out is None:
-        out = torch.empty((M, Hq, D), dtype=dtype, device=qkv.device)
+        out = _empty((M, Hq, D), dtype, qkv.device, stream)
     else:
         _is(out, "out", dtype, (M, Hq, D))
     status = _fn("qmv_rope_append")(
@@ -194,7 +204,7 @@ def qmv_prefix_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     if max_own is None:
         max_own = own_pages * page
     if out is None:
-        out = torch.empty((B, T, Hq, D), dtype=dtype, device=q.device)
+        out = _empty((B, T, Hq, D), dtype, q.device, stream)
     else:
         _is(out, "out", dtype, q.shape)
     need = lambda: qmv_prefix_attention_workspace(B, T, Hq, Hkv, D, prefix_len, max_own)  # noqa: E731
@@ -243,7 +253,7 @@ def qmv_penalize_logits(logits: torch.Tensor, tokens: torch.Tensor, prompt_len: 
     if mask_row is not None:
         _is(mask_row, "mask_row", _I32, (M,))
     if out is None:
-        out = torch.empty((M, V), dtype=_F32, device=logits.device)
+        out = _empty((M, V), _F32, logits.device, stream)
     else:
         _is(out, "out", _F32, (M, V))
     status = _fn("qmv_penalize_logits")(

@@ -101,3 +101,53 @@ def test_steps_with_overlapping_launches_give_the_same():
     for a, b in zip(*results):
         for name in a:
             assert torch.equal(a[name], b[name]), name
+
+
+def calls_without_buffers():
+    """Each operator without an output or a workspace: (call, bytes of its output, of its workspace)."""
+    import gemm_qmv_quantize_gb300 as q
+    rand = lambda *s, dtype=torch.float32: torch.randn(s, device="cuda").to(dtype)  # noqa: E731
+    ints = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    half, M, N, K = torch.float16, 64, 1 << 16, 512
+    x, a, b, base = rand(M, K, dtype=half), rand(2, 32, K, dtype=half), rand(2, N, 32, dtype=half), rand(M, N)
+    scale, adapter = rand(2), torch.arange(M, dtype=torch.int32, device="cuda") % 2
+    qkv, table = rand(2048, 24 * 128), q.qmv_rope_table(64, 128, device="cuda")
+    k, v = rand(200, 16, 4, 128, dtype=half), rand(200, 16, 4, 128, dtype=half)
+    slots, positions = torch.arange(2048, device="cuda"), torch.zeros((1, 2048), dtype=torch.int32, device="cuda")
+    qa, pages = rand(2, 200, 32, 128, dtype=half), torch.arange(200, dtype=torch.int32, device="cuda")
+    own_table, own_len = pages[:26].reshape(2, 13).contiguous(), ints(200, 208)
+    x2, tokens, one = rand(40, 100000), ints(*[1] * 40).reshape(40, 1), ints(*[1] * 40)
+    return [
+        (lambda s: q.qmv_lora_add(x, a, b, adapter, scale, base, stream=s), M * N * 4, q.qmv_lora_add_workspace(M, 32, K)),
+        (lambda s: q.qmv_rope_append(qkv, positions, table, bytes(64), slots, k, v, stream=s), 2048 * 16 * 128 * 2, None),
+        (lambda s: q.qmv_prefix_attention(qa, k, v, pages, 3000, own_table, own_len, stream=s), 2 * 200 * 32 * 128 * 2,
+         q.qmv_prefix_attention_workspace(2, 200, 32, 4, 128, 3000, 208)),
+        (lambda s: q.qmv_penalize_logits(x2, tokens, one, one, stream=s), 40 * 100000 * 4, None)]
+
+
+def raw(s):
+    return s.cuda_stream
+
+
+@pytest.mark.parametrize("handle", [lambda s: s, raw], ids=["stream", "handle"])
+@pytest.mark.parametrize("which", range(4))
+def test_buffers_of_a_call_are_its_streams_own(which, handle):
+    """Blocks that the current stream has freed, which its queued work may still use, are
+    neither written nor handed out by a call on another stream."""
+    call, *sizes = calls_without_buffers()[which]
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    plain = call(None)
+    torch.cuda.synchronize()
+    freed = [torch.full((n,), 7, dtype=torch.uint8, device="cuda") for n in sizes if n]
+    places = [t.data_ptr() for t in freed]
+    torch.cuda.synchronize()
+    del freed
+    out = call(handle(s))
+    s.synchronize()
+    assert out.data_ptr() not in places
+    again = [torch.empty((n,), dtype=torch.uint8, device="cuda") for n in sizes if n]
+    assert [t.data_ptr() for t in again] == places
+    for t in again:
+        assert bool((t == 7).all())
+    assert torch.equal(out, plain)
