@@ -2,7 +2,7 @@
 low-rank adapters, rotary positions with the append to a paged cache, attention over a
 shared prefix, and penalties, biases and masks on logits.
 
-As in ``_binding``: tensors are checked for type, shape and contiguity, pointers and
+As in ``_binding``: tensors are checked for type, shape, contiguity and device, pointers and
 sizes go to the C entry point of the same name, and all arithmetic runs in the library.
 An output or a workspace that is not given is allocated for the call, from the memory of
 its stream; a program that repeats calls keeps a workspace of the bytes that the
@@ -20,6 +20,7 @@ from ._binding import QMV_OK, QmvError, _check, _need, _stream, lib
 _F32, _F16, _BF16, _I32 = torch.float32, torch.float16, torch.bfloat16, torch.int32
 _TYPE = {_F32: 0, _F16: 1, _BF16: 2}   # QMV_F32, QMV_F16, QMV_BF16
 _16BIT = (_F16, _BF16)
+_current_device = torch._C._cuda_getDevice
 
 
 @functools.cache
@@ -34,22 +35,36 @@ def _type(t: torch.Tensor, name: str, allowed) -> int:
     return _TYPE[t.dtype]
 
 
-def _is(t, name: str, dtype, shape):
-    """_need, with the checks that pass in a few tenths of a microsecond first."""
-    if not (t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous()):
+def _is(t, name: str, dtype, shape, device: int):
+    """_need, with the checks that pass in a few tenths of a microsecond first; and t is on
+    the device of the call's other tensors (by number)."""
+    if not (t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous()):
         _need(t, name, dtype, shape)
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the call's first tensor on cuda:{device}")
 
 
-def _held(t, name: str, dtype):
+def _held(t, name: str, dtype, device: int):
     """_is for a tensor whose own shape the call goes by."""
+    if not (t.dtype is dtype and t.get_device() == device and t.is_contiguous()):
+        _need(t, name, dtype)
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the call's first tensor on cuda:{device}")
+
+
+def _first(t, name: str, dtype) -> int:
+    """_held for a call's first tensor: its device, which is the current one, where the
+    library launches."""
     if not (t.dtype is dtype and t.is_cuda and t.is_contiguous()):
         _need(t, name, dtype)
+    device = t.get_device()
+    if device != _current_device():
+        raise ValueError(f"{name} is on cuda:{device}, the current device is cuda:{_current_device()}")
+    return device
 
 
-def _on(stream, t: torch.Tensor) -> int:
-    """The handle of `stream`, or of the current one on t's device (without a Stream object
-    for it, which costs as much as a launch)."""
-    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else _stream(stream)
+def _on(stream, device: int) -> int:
+    """The handle of `stream`, or of the device's current one (without a Stream object for it,
+    which costs as much as a launch)."""
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
 
 
 def _empty(shape, dtype, device, stream):
@@ -64,12 +79,11 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _workspace(buffer, need, device, stream):
+def _workspace(buffer, need, device: int, stream):
     """`buffer`, or a new one of need() bytes for a call on `stream`."""
     if buffer is None:
-        buffer = _empty((need(),), torch.uint8, device, stream)
-    elif not (buffer.dtype is torch.uint8 and buffer.is_cuda and buffer.is_contiguous()):
-        _need(buffer, "workspace", torch.uint8)
+        return _empty((need(),), torch.uint8, torch.device("cuda", device), stream)
+    _held(buffer, "workspace", torch.uint8, device)
     return buffer
 
 
@@ -102,21 +116,21 @@ def qmv_lora_add(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, adapter: tor
     L, R, _ = a.shape
     N = base.shape[1]
     xt, wt = _type(x, "x", (_F32, _F16)), _type(a, "a", _16BIT)
-    _held(x, "x", x.dtype)
-    _is(a, "a", a.dtype, (L, R, K))
-    _is(b, "b", a.dtype, (L, N, R))
-    _is(adapter, "adapter", _I32, (M,))
-    _is(scale, "scale", _F32, (L,))
-    _is(base, "base", _F32, (M, N))
+    dev = _first(x, "x", x.dtype)
+    _is(a, "a", a.dtype, (L, R, K), dev)
+    _is(b, "b", a.dtype, (L, N, R), dev)
+    _is(adapter, "adapter", _I32, (M,), dev)
+    _is(scale, "scale", _F32, (L,), dev)
+    _is(base, "base", _F32, (M, N), dev)
     if out is None:
         out = _empty((M, N), _F32, base.device, stream)
     else:
-        _is(out, "out", _F32, (M, N))
+        _is(out, "out", _F32, (M, N), dev)
     need = lambda: qmv_lora_add_workspace(M, R, K)  # noqa: E731
-    ws = _workspace(workspace, need, x.device, stream)
+    ws = _workspace(workspace, need, dev, stream)
     status = _fn("qmv_lora_add")(
         x.data_ptr(), xt, a.data_ptr(), b.data_ptr(), wt, adapter.data_ptr(), scale.data_ptr(), base.data_ptr(),
-        out.data_ptr(), ws.data_ptr(), ws.numel(), M, N, K, R, L, _on(stream, x))
+        out.data_ptr(), ws.data_ptr(), ws.numel(), M, N, K, R, L, _on(stream, dev))
     if status != QMV_OK:
         _check_with("qmv_lora_add", status, ws, need)
     return out
@@ -153,20 +167,20 @@ def qmv_rope_append(qkv: torch.Tensor, positions: torch.Tensor, table: torch.Ten
         raise ValueError(f"axis_of_pair: expected {pairs} entries, got {len(axis_of_pair)}")
     dtype = k_cache.dtype
     t = _type(k_cache, "k_cache", _16BIT)
-    _held(qkv, "qkv", _F32)
-    _is(positions, "positions", _I32, (axes, M))
-    _is(table, "table", _F32, (n_positions, pairs, 2))
-    _is(slots, "slots", torch.int64, (M,))
-    _held(k_cache, "k_cache", dtype)
-    _is(v_cache, "v_cache", dtype, k_cache.shape)
+    dev = _first(qkv, "qkv", _F32)
+    _is(positions, "positions", _I32, (axes, M), dev)
+    _is(table, "table", _F32, (n_positions, pairs, 2), dev)
+    _is(slots, "slots", torch.int64, (M,), dev)
+    _held(k_cache, "k_cache", dtype, dev)
+    _is(v_cache, "v_cache", dtype, k_cache.shape, dev)
     if out is None:
         out = _empty((M, Hq, D), dtype, qkv.device, stream)
     else:
-        _is(out, "out", dtype, (M, Hq, D))
+        _is(out, "out", dtype, (M, Hq, D), dev)
     status = _fn("qmv_rope_append")(
         qkv.data_ptr(), positions.data_ptr(), table.data_ptr(), axis_of_pair, slots.data_ptr(), out.data_ptr(),
         k_cache.data_ptr(), v_cache.data_ptr(), t, 1 if interleaved else 0, M, Hq, Hkv, D, 2 * pairs, axes,
-        n_positions, pages * page, _on(stream, qkv))
+        n_positions, pages * page, _on(stream, dev))
     if status != QMV_OK:
         _check("qmv_rope_append", status)
     return out
@@ -193,12 +207,12 @@ def qmv_prefix_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     own_pages = own_table.shape[1]
     dtype = q.dtype
     t = _type(q, "q", _16BIT)
-    _held(q, "q", dtype)
-    _is(k_cache, "k_cache", dtype, (pages, page, Hkv, D))
-    _is(v_cache, "v_cache", dtype, k_cache.shape)
-    _held(prefix_table, "prefix_table", _I32)
-    _is(own_table, "own_table", _I32, (B, own_pages))
-    _is(own_len, "own_len", _I32, (B,))
+    dev = _first(q, "q", dtype)
+    _is(k_cache, "k_cache", dtype, (pages, page, Hkv, D), dev)
+    _is(v_cache, "v_cache", dtype, k_cache.shape, dev)
+    _held(prefix_table, "prefix_table", _I32, dev)
+    _is(own_table, "own_table", _I32, (B, own_pages), dev)
+    _is(own_len, "own_len", _I32, (B,), dev)
     if prefix_table.numel() * page < prefix_len:
         raise ValueError(f"prefix_table: {prefix_table.numel()} pages of {page} hold no {prefix_len} keys")
     if max_own is None:
@@ -206,13 +220,13 @@ def qmv_prefix_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     if out is None:
         out = _empty((B, T, Hq, D), dtype, q.device, stream)
     else:
-        _is(out, "out", dtype, q.shape)
+        _is(out, "out", dtype, q.shape, dev)
     need = lambda: qmv_prefix_attention_workspace(B, T, Hq, Hkv, D, prefix_len, max_own)  # noqa: E731
-    ws = _workspace(workspace, need, q.device, stream)
+    ws = _workspace(workspace, need, dev, stream)
     status = _fn("qmv_prefix_attention")(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), t, pages, page, prefix_table.data_ptr(), prefix_len,
         own_table.data_ptr(), own_pages, own_len.data_ptr(), max_own, 1.0 / math.sqrt(D) if scale is None else scale,
-        out.data_ptr(), ws.data_ptr(), ws.numel(), B, T, Hq, Hkv, D, _on(stream, q))
+        out.data_ptr(), ws.data_ptr(), ws.numel(), B, T, Hq, Hkv, D, _on(stream, dev))
     if status != QMV_OK:
         _check_with("qmv_prefix_attention", status, ws, need)
     return out
@@ -231,36 +245,36 @@ def qmv_penalize_logits(logits: torch.Tensor, tokens: torch.Tensor, prompt_len: 
     set = allowed, with mask_row int32 [M] (negative: none). out may be logits."""
     M, V = logits.shape
     H = tokens.shape[1]
-    _held(logits, "logits", _F32)
-    _is(tokens, "tokens", _I32, (M, H))
-    _is(prompt_len, "prompt_len", _I32, (M,))
-    _is(total_len, "total_len", _I32, (M,))
+    dev = _first(logits, "logits", _F32)
+    _is(tokens, "tokens", _I32, (M, H), dev)
+    _is(prompt_len, "prompt_len", _I32, (M,), dev)
+    _is(total_len, "total_len", _I32, (M,), dev)
     rows = []
     for name, t in (("repetition", repetition), ("presence", presence), ("frequency", frequency)):
         if t is not None:
-            _is(t, name, _F32, (M,))
+            _is(t, name, _F32, (M,), dev)
         rows.append(None if t is None else t.data_ptr())
     n_bias = n_masks = 0
     if (bias_tokens is None) != (bias_values is None):
         raise ValueError("bias_tokens and bias_values come together")
     if bias_tokens is not None:
         n_bias = bias_tokens.shape[1]
-        _is(bias_tokens, "bias_tokens", _I32, (M, n_bias))
-        _is(bias_values, "bias_values", _F32, (M, n_bias))
+        _is(bias_tokens, "bias_tokens", _I32, (M, n_bias), dev)
+        _is(bias_values, "bias_values", _F32, (M, n_bias), dev)
     if mask is not None:
         n_masks = mask.shape[0]
-        _is(mask, "mask", _I32, (n_masks, (V + 31) // 32))
+        _is(mask, "mask", _I32, (n_masks, (V + 31) // 32), dev)
     if mask_row is not None:
-        _is(mask_row, "mask_row", _I32, (M,))
+        _is(mask_row, "mask_row", _I32, (M,), dev)
     if out is None:
         out = _empty((M, V), _F32, logits.device, stream)
     else:
-        _is(out, "out", _F32, (M, V))
+        _is(out, "out", _F32, (M, V), dev)
     status = _fn("qmv_penalize_logits")(
         logits.data_ptr(), tokens.data_ptr(), H, prompt_len.data_ptr(), total_len.data_ptr(), *rows,
         None if bias_tokens is None else bias_tokens.data_ptr(), None if bias_values is None else bias_values.data_ptr(),
         n_bias, None if mask is None else mask.data_ptr(), None if mask_row is None else mask_row.data_ptr(), n_masks,
-        out.data_ptr(), M, V, _on(stream, logits))
+        out.data_ptr(), M, V, _on(stream, dev))
     if status != QMV_OK:
         _check("qmv_penalize_logits", status)
     return out
