@@ -28,11 +28,14 @@ from . import (qgemm_nvfp4_w4a16, qmv_lora_add, qmv_lora_add_workspace, qmv_pena
 
 class DecodeStep:
     """Weights, cache and workspaces of the step. The cache's first pages hold the prompt
-    (written by one qmv_rope_append over its tokens), then each request has pages of its own."""
+    (written by one qmv_rope_append over its tokens), then each request has pages of its own,
+    for max_own tokens: as many steps can be taken. (A step replayed from a CUDA graph is not
+    counted here; one too many takes the last token's place and sets bit 2 of error_flags.)"""
 
     def __init__(self, batch: int, prefix_len: int, max_own: int, hidden: int = 5120, Hq: int = 40, Hkv: int = 8,
                  D: int = 128, vocab: int = 151936, adapters: int = 8, rank: int = 16, page: int = 64, seed: int = 0,
                  device="cuda"):
+        self.taken = 0   # steps
         self.B, self.prefix_len, self.max_own, self.Hq, self.Hkv, self.D, self.page = batch, prefix_len, max_own, Hq, Hkv, D, page
         g = torch.Generator(device=device).manual_seed(seed)
         normal = lambda *s: torch.randn(s, generator=g, device=device)  # noqa: E731
@@ -76,7 +79,10 @@ class DecodeStep:
     def step(self, x: torch.Tensor, timed=lambda name, f: f()) -> dict:
         """x fp16 [batch, hidden]: the state of each request's newest token. Returns what
         each call made; the logits under "logits". timed(name, call) runs each call."""
-        at = self.own_len.long()
+        if self.taken >= self.max_own:
+            raise ValueError(f"{self.taken} steps taken: the requests have room for {self.max_own} tokens of their own")
+        self.taken += 1
+        at = self.own_len.clamp(max=self.max_own - 1).long()
         own_slot = self.own_table.gather(1, (at // self.page)[:, None])[:, 0].long() * self.page + at % self.page
         position = (self.own_len + self.prefix_len)[None].contiguous()
         qkv = timed("qkv projection + adapters", lambda: self.project("qkv", x))
@@ -102,6 +108,8 @@ def main():
     p.add_argument("--max-own", type=int, default=512)
     p.add_argument("--steps", type=int, default=20)
     args = p.parse_args()
+    if not 3 < args.steps <= args.max_own:
+        p.error(f"--steps: more than the 3 of the warm-up and at most --max-own ({args.max_own})")
     net = DecodeStep(args.batch, args.prefix, args.max_own)
     x = torch.randn((args.batch, 5120), device="cuda").half()
     times = {}

@@ -151,3 +151,22 @@ def test_buffers_of_a_call_are_its_streams_own(which, handle):
     for t in again:
         assert bool((t == 7).all())
     assert torch.equal(out, plain)
+
+
+def test_more_replays_than_there_is_room_for_are_flagged():
+    """The last token's place is taken again: nothing is written or read out of range."""
+    import gemm_qmv_quantize_gb300 as q
+    from gemm_qmv_quantize_gb300.decode_step import DecodeStep
+    net = DecodeStep(3, 40, 5, hidden=256, Hq=8, Hkv=2, D=64, vocab=1003, adapters=3, rank=8, page=16, seed=13)
+    x = torch.randn((3, 256), device="cuda").half()
+    net.step(x)
+    torch.cuda.synchronize()
+    q.error_flags(clear=True)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        net.step(x)
+    for _ in range(4):
+        graph.replay()
+    assert q.error_flags(clear=True) == 0
+    graph.replay()
+    assert q.error_flags(clear=True) == 2
