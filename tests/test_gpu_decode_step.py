@@ -170,3 +170,26 @@ def test_more_replays_than_there_is_room_for_are_flagged():
     assert q.error_flags(clear=True) == 0
     graph.replay()
     assert q.error_flags(clear=True) == 2
+
+
+def test_whole_step_in_a_cuda_graph_gives_the_same():
+    """step(), captured once and replayed: every operator and the projections between them."""
+    import gemm_qmv_quantize_gb300 as q
+    from gemm_qmv_quantize_gb300.decode_step import DecodeStep
+    q.error_flags(clear=True)
+    plain, net = (DecodeStep(6, 300, 16, hidden=256, Hq=8, Hkv=2, D=64, vocab=1003, adapters=3, rank=8, page=16, seed=12)
+                  for _ in range(2))
+    x = torch.randn((6, 256), generator=torch.Generator(device="cuda").manual_seed(3), device="cuda").half()
+    expected = [plain.step(x) for _ in range(8)]
+    first = net.step(x)
+    assert all(torch.equal(expected[0][n], first[n]) for n in first)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = net.step(x)
+    for step in range(1, 8):
+        graph.replay()
+        for name in captured:
+            assert torch.equal(captured[name], expected[step][name]), (step, name)
+    assert torch.equal(net.tokens, plain.tokens) and torch.equal(net.own_len, plain.own_len)
+    assert q.error_flags(clear=True) == 0
