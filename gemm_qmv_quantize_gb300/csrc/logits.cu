@@ -156,6 +156,7 @@ __global__ void __launch_bounds__(kThreads, 3) logits_kernel(const __grid_consta
     const float *bias_values = g.bias_values + static_cast<int64_t>(m) * g.max_bias;
     for (int j = tid; j < g.max_bias; j += kThreads) {
         const int v = j < kThreads ? bias_token : __ldg(bias_tokens + j);
+        if (v >= g.V && blockIdx.x == 0) atomicOr(&g_logits_error, kErrIndex);
         if (v < v0 || v >= v0 + n || !allowed(t.mask, v)) continue;
         bool again = false;
 #pragma unroll 8

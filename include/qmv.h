@@ -357,7 +357,7 @@ QMV_API qmv_status qmv_prefix_attention(const void *q, const void *k_cache, cons
  *              max_history is cut to it (bit 2). prompt_len, total_len int32 [M].
  *   repetition, presence, frequency fp32 [M], each NULL for none (1, 0, 0).
  *   bias_tokens int32, bias_values fp32 [M][max_bias]; negative tokens are unused
- *              entries. max_bias 0: none.
+ *              entries, those of V or more too (bit 2). max_bias 0: none.
  *   mask       uint32 [n_masks][ceil(V / 32)], bit v % 32 of word v / 32 set = allowed;
  *              NULL for none. mask_row int32 [M]: the row's mask, negative for none, one
  *              of n_masks or more counts as none (bit 2); NULL: row m has mask m.

@@ -136,3 +136,17 @@ def test_refusals():
         q.qmv_penalize_logits(**{**args, "tokens": args["tokens"].T})
     with pytest.raises(q.QmvError):
         q.qmv_penalize_logits(**{**args, "mask": args["mask"][:1].contiguous(), "mask_row": None})   # a mask a row
+
+
+@pytest.mark.parametrize("at", [0, 511, 512, 699])
+def test_bias_tokens_outside_are_flagged_and_not_followed(at):
+    import gemm_qmv_quantize_gb300 as q
+    q.error_flags(clear=True)
+    args = inputs(2, 9000, 50, 700, 2, seed=8)
+    args["bias_tokens"][1, at] = 8999
+    check(args)
+    assert q.error_flags(clear=True) == 0
+    for token in (9000, 2 ** 31 - 1):
+        args["bias_tokens"][1, at] = token
+        check(args)
+        assert q.error_flags(clear=True) == 2
