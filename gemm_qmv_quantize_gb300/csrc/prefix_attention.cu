@@ -73,6 +73,12 @@ struct AttnPlan {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// Keys of each of `splits` ranges, whole blocks of 64, within 31 bits.
+int range_of(int64_t keys, int64_t splits)
+{
+    return static_cast<int>(std::min<int64_t>(ceil_div(ceil_div(keys, splits), 64) * 64, 0x7fffffc0));
+}
+
 // Costs, in thousands of cycles as measured: a tile 3 for a pair of streams, 2 where the
 // streams take every other tile; a job 8 beside its tiles. The SMs are divided
 // between the prefix and the own keys by their shares of the cost (own lengths are on the
@@ -90,7 +96,7 @@ AttnPlan plan_attention(int B, int T, int Hq, int Hkv, int64_t prefix_len, int64
         p.few_row_tiles = static_cast<int>(ceil_div(T * G, 16));
         const int64_t jobs = static_cast<int64_t>(B) * Hkv * p.few_row_tiles;
         const int64_t splits = std::max<int64_t>(1, std::min<int64_t>({8 * kSms / jobs, ceil_div(max_own, 256), 256}));
-        p.few_keys = static_cast<int>(ceil_div(ceil_div(max_own, splits), 64) * 64);
+        p.few_keys = range_of(max_own, splits);
         p.own_splits = static_cast<int>(ceil_div(max_own, p.few_keys));
         p.few_jobs = jobs * p.own_splits;
     } else if (own_tiles > 0 && rows > 0) {
@@ -106,7 +112,7 @@ AttnPlan plan_attention(int B, int T, int Hq, int Hkv, int64_t prefix_len, int64
     if (tiles > 0 && rows > 0 && rows <= 16) {
         // (with 32 rows, the prefix read twice: 18 us for 16 with 4096 keys)
         const int64_t splits = std::max<int64_t>(1, std::min<int64_t>({2 * kSms / Hkv, ceil_div(prefix_len, 128), 256}));
-        p.few_prefix_keys = static_cast<int>(ceil_div(ceil_div(prefix_len, splits), 64) * 64);
+        p.few_prefix_keys = range_of(prefix_len, splits);
         p.lone_splits = static_cast<int>(ceil_div(prefix_len, p.few_prefix_keys));
         p.few_prefix_jobs = static_cast<int64_t>(Hkv) * p.lone_splits;
     } else if (tiles > 0 && rows > 0) {

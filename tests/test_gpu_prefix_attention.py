@@ -297,3 +297,13 @@ def test_scores_that_are_all_minus_infinity(type_, B, T, Hq, Hkv, D, prefix, own
     got = check_special(args, type_)
     G, last = Hq // Hkv, T - 1
     assert bool(torch.isnan(got[0, last, :G]).all()) and bool(torch.isfinite(got[1, last]).all())
+
+
+def test_bounds_of_nearly_31_bits():
+    """A table of 2^31 keys a request, of which a few are there, by a call of enough requests
+    for one range each."""
+    args = inputs(80, 1, 8, 8, 64, 20, [i % 7 for i in range(80)], 256, seed=12, own_pages=1)
+    wide = torch.full((80, 1 << 23), 2 ** 31 - 1, dtype=torch.int32, device="cuda")
+    wide[:, :1] = args["own_table"]
+    for most in (2 ** 31 - 1, 2 ** 31 - 64, 2 ** 31 - 65):
+        check({**args, "own_table": wide}, "f16", max_own=most)
