@@ -34,7 +34,8 @@ constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kBlockRows = 8;      // rows of a block: the product's columns
 constexpr int kRankTile = 16;      // ranks of a shrink CTA, outputs of an expand step: the product's rows
 constexpr int kMaxRows = 96;
-constexpr int kSms = 152, kCtasPerSm = 3;
+constexpr int kSms = 152;
+constexpr int kSmShared = 228 * 1024, kCtaShared = 1024;   // shared memory of an SM; what a CTA takes beside its own
 constexpr int kStages = 4;         // of 64 k or ranks, in flight for a warp
 
 // D(16x8) += A(16x8, row) B(8x8, col) in TF32. A lane (g = lane / 4, t = lane % 4) holds
@@ -392,10 +393,12 @@ cudaError_t launch_both(const LoraArgs &g, cudaStream_t s)
     cfg.numAttrs = set_launch_overlap_attr(attr);
     if ((e = cudaLaunchKernelEx(&cfg, lora_shrink_kernel<X, W>, g, shrink_k(g.M, g.R, g.K))) != cudaSuccess) return e;
     // Starts beside the shrink launch, loads its first weights and waits for it. CTAs for one
-    // step a warp, but no more than the three an SM that fit: eight took 9.1 us for 7.0 (8
-    // rows, 14336 x 4096) and 20 for 15 (96 rows that share one adapter).
+    // step a warp, but no more than fit an SM: eight took 9.1 us for 7.0 (8 rows, 14336 x 4096)
+    // and 20 for 15 (96 rows that share one adapter). By shared memory three fit, two above rank
+    // 128, where a grid for three took 212 us for 196 (96 adapters of rank 256, 17408 x 5120).
+    const int fit = kSms * std::min(3, kSmShared / (expand_smem(g.R) + kCtaShared));
     const int64_t tiles = (g.N + kRankTile * kWarps - 1) / (kRankTile * kWarps);
-    cfg.gridDim = dim3(static_cast<unsigned>(g.M), static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(tiles, kCtasPerSm * kSms / g.M))));
+    cfg.gridDim = dim3(static_cast<unsigned>(g.M), static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(tiles, fit / g.M))));
     cfg.dynamicSmemBytes = static_cast<size_t>(expand_smem(g.R));
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;

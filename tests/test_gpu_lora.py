@@ -173,3 +173,9 @@ def test_sums_longer_than_a_grid_has_ranges():
     y = q.qmv_lora_add(x, one(1, 8, K), one(1, 5, 8), torch.zeros((1,), dtype=torch.int32, device="cuda"),
                        one(1, dtype=torch.float32), torch.zeros((1, 5), device="cuda"))
     assert y.tolist() == [[8.0 * 258] * 5]
+
+
+@pytest.mark.parametrize("R", [128, 136, 256])
+def test_full_batch_of_high_ranks(R):
+    """Grids of three and of two CTAs an SM."""
+    check(inputs(96, 1500, 512, R, 96, "f16", "bf16", seed=R, adapter=[(7 * i) % 96 for i in range(96)]))
