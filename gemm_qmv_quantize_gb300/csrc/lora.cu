@@ -50,10 +50,11 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], float a0, float a1, floa
           "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)));
 }
 
-// v as two TF32 terms: the first cut, the second rounded (NaN beside an infinity).
+// v as two TF32 terms: the first cut (NaN as NaN: its payload may lie in what is cut), the
+// second rounded (NaN beside an infinity).
 __device__ __forceinline__ void split_tf32(float v, float &hi, float &lo)
 {
-    hi = __uint_as_float(__float_as_uint(v) & 0xffffe000u);
+    hi = v == v ? __uint_as_float(__float_as_uint(v) & 0xffffe000u) : v + v;
     uint32_t r;
     asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(v - hi));
     lo = __uint_as_float(r);

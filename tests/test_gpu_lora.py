@@ -179,3 +179,12 @@ def test_sums_longer_than_a_grid_has_ranges():
 def test_full_batch_of_high_ranks(R):
     """Grids of three and of two CTAs an SM."""
     check(inputs(96, 1500, 512, R, 96, "f16", "bf16", seed=R, adapter=[(7 * i) % 96 for i in range(96)]))
+
+
+@pytest.mark.parametrize("bits", [0x7f800001, 0x7fc00000, -1])
+def test_nan_of_any_payload_stays_nan(bits):
+    import gemm_qmv_quantize_gb300 as q
+    args = inputs(3, 50, 256, 8, 2, "f32", "f16", seed=12, adapter=[0, 1, 0])
+    args["x"].view(torch.int32)[1, 9] = bits
+    got = q.qmv_lora_add(**args)
+    assert bool(torch.isnan(got[1]).all()) and bool(torch.isfinite(got[::2]).all())
