@@ -15,8 +15,9 @@
 // 7e-7 of the outputs (5120 long). Bound by the weights' bytes: one row an adapter leaves
 // 7 of the product's 8 columns empty and still reads memory at its rate. A lane's share of
 // the operands comes by asynchronous copies into shared memory of its own, several stages
-// ahead: 96 adapters of rank 64 beside 17408 x 5120 take 61 us, 4.8 TB/s (loads into
-// registers: 65 us), the expand launch 47 us of them.
+// ahead: 96 adapters of rank 64 beside 17408 x 5120 take 62 us, 4.7 TB/s (loads into
+// registers: 65 us). The expand launch alone, 50 us for 227 MB, is short of issue slots
+// (61 % used) as much as of bandwidth: weights are widened by hand and meet two terms each.
 #include <algorithm>
 #include <type_traits>
 

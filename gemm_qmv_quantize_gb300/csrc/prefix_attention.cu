@@ -21,10 +21,10 @@
 //   types' range. Statistics and sums are fp32; P is rounded to the inputs' type, the
 //   operand that the product takes.
 //
-// 51 requests of 5 query heads a key head (255 rows) behind 65536 keys take 69 us, 990
-// TFLOP/s; 25 of them (125 rows, bound by the keys' bytes) 55 us, 4.9 TB/s. A stream's
+// 51 requests of 5 query heads a key head (255 rows) behind 65536 keys take 70 us, 984
+// TFLOP/s; 25 of them (125 rows, bound by the keys' bytes) 56 us, 4.8 TB/s. A stream's
 // products, softmax and P V follow one another, about 3000 cycles a tile; its exponentials
-// and the handing over, not the tensor cores (50 % busy), bound the first.
+// and the handing over, not the tensor cores (56 % busy), bound the first.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -769,7 +769,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
 // warps take 16 keys in turn, each with a ring of asynchronous copies, statistics and output
 // sums of its own, so that nothing waits for anything but memory, and are joined at the end.
 // (As jobs of the kernel above, 128 rows a product and one range at a time an SM, 64
-// requests of up to 1024 keys took 48 to 65 us; so 38.)
+// requests of up to 1024 keys took 48 to 65 us; so 40.)
 constexpr int kFewWarps = 4, kFewStages = 3;
 template <int kD>
 constexpr int few_smem() { return kFewWarps * kFewStages * 2 * 16 * kD * 2; }

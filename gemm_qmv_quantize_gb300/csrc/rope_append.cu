@@ -35,7 +35,7 @@ __device__ __forceinline__ uint32_t pack2(float a, float b)
 // A CTA takes 256 units of 8 elements of one token's heads, a thread a unit: 4 pairs of the
 // rotated part, or 8 elements that are copied. The token's angles go to shared memory once
 // for the CTA, while the units' elements are on their way. Bound by the bytes: 4001 tokens of
-// 40 + 8 + 8 heads of 128 take 36 us, 4.9 TB/s (each thread loading its angles from the
+// 40 + 8 + 8 heads of 128 take 33 us, 5.3 TB/s (each thread loading its angles from the
 // table: 53 us; four units a thread: 40).
 template <typename T, bool kInterleaved>
 __global__ void __launch_bounds__(kThreads) rope_append_kernel(const __grid_constant__ RopeArgs g)

@@ -258,15 +258,19 @@ QMV_API int qmv_get_launch_overlap(void);
  * projection's rows, rotary positions with the append to a paged cache, attention
  * over a shared prefix, and penalties, biases and masks on the logits.
  *
- * 16-bit tensors are IEEE binary16 or bfloat16, named by a type argument. Sums,
- * softmax statistics and products are fp32; an output is rounded once. A workspace is
- * device memory of the caller, 16-byte aligned, of at least the bytes that the call's
- * _workspace function names, which for more rows, requests, tokens or keys is never less
- * (the workspace of a program's largest batch serves all of its calls); its contents need
- * no initialisation and hold nothing between calls. Calls in flight at the same time need workspaces of their own.
+ * 16-bit tensors are IEEE binary16 or bfloat16, named by a type argument. Sums and
+ * softmax statistics are fp32 and an output is rounded once. Two operands of products
+ * hold fewer bits: the attention's probabilities are rounded to the inputs' 16-bit type
+ * before they meet the values, and the adapters' fp32 activations and A x keep 22 bits.
+ * NaN and infinities among what a result is made of show in it; those elsewhere do not.
+ * A workspace is device memory of the caller, 16-byte aligned, of at least the bytes that
+ * the call's _workspace function names, which for more rows, requests, tokens or keys is
+ * never less (the workspace of a program's largest batch serves all of its calls); its
+ * contents need no initialisation and hold nothing between calls. Calls in flight at the
+ * same time need workspaces of their own.
  * Indices that the kernels read from device memory are checked against their arrays:
- * one outside sets bit 2 of qmv_error_flags and is handled as each call says, never
- * followed.
+ * one outside sets bit 2 of qmv_error_flags (the value 2) and is handled as each call
+ * says, never followed.
  * ------------------------------------------------------------------------- */
 #define QMV_F32  0
 #define QMV_F16  1
@@ -330,7 +334,7 @@ QMV_API qmv_status qmv_rope_append(const float *qkv, const int32_t *positions, c
  *            once for all rows; prefix_len 0 is allowed.
  *   own_table int32 [B][own_pages], own_len int32 [B] (at most max_own, a bound the
  *            caller knows, itself at most own_pages * page; a longer one is cut to
- *            max_own and sets bit 2). A page outside the cache reads as zeros (bit 2).
+ *            max_own and sets bit 2; max_own 0: not read). A page outside the cache reads as zeros (bit 2).
  *            Whatever lies in the cache past a request's length or the prefix's is not
  *            used, NaN included, and no row is touched by tokens after its own.
  *   scale    finite and positive.
@@ -357,7 +361,10 @@ QMV_API qmv_status qmv_prefix_attention(const void *q, const void *k_cache, cons
  *              max_history is cut to it (bit 2). prompt_len, total_len int32 [M].
  *   repetition, presence, frequency fp32 [M], each NULL for none (1, 0, 0).
  *   bias_tokens int32, bias_values fp32 [M][max_bias]; negative tokens are unused
- *              entries, those of V or more too (bit 2). max_bias 0: none.
+ *              entries, those of V or more too (bit 2). max_bias 0: none. A row's list is
+ *              searched for repeats: the cost grows with its square (8 rows of 151936: 12 us
+ *              with 300 entries, 52 with 1000, 790 with 4096; what names most of the
+ *              vocabulary is a sum of its own before the call).
  *   mask       uint32 [n_masks][ceil(V / 32)], bit v % 32 of word v / 32 set = allowed;
  *              NULL for none. mask_row int32 [M]: the row's mask, negative for none, one
  *              of n_masks or more counts as none (bit 2); NULL: row m has mask m.
