@@ -1015,9 +1015,10 @@ __device__ __forceinline__ float2 widen2(uint32_t two)
 
 // Columns d0 .. d0 + 7 of row i once more, where they did not come out finite. In the products
 // above a key that the row does not see (a later token of its request) has P = 0, which an
-// infinity or NaN among that key's values turns into NaN. Here the row's own keys are gone
-// through one by one, only those that it sees, beside the prefix's partial results: what is
-// still not finite is the formula's. (Looking through those values before each product
+// infinity or NaN among that key's values turns into NaN. If there is one, the row's own keys
+// are gone through one by one, only those that it sees, beside the prefix's partial results:
+// what is still not finite is the formula's. Bound by latency, 2 us a key, for such rows alone.
+// (Looking through those values before each product
 // instead cost 3 to 5 % of the calls with several tokens a request.)
 template <typename T, int kD>
 __device__ __forceinline__ void row_again(const AttnParams &p, int h, int i, int d0, int64_t per_slot, int slots, const float *lse,
@@ -1025,7 +1026,33 @@ __device__ __forceinline__ void row_again(const AttnParams &p, int h, int i, int
 {
     const AttnArgs &g = p.g;
     const int G = g.Hq / g.Hkv, b = i / G / g.T, shift = __ffs(g.page) - 1;
-    const int64_t seen = min(static_cast<int64_t>(__ldg(g.own_len + b)), g.max_own) - g.T + 1 + i / G % g.T;
+    const int64_t own = min(static_cast<int64_t>(__ldg(g.own_len + b)), g.max_own), seen = own - g.T + 1 + i / G % g.T;
+    // where an own key's row of the caches begins, or -1: its page is outside
+    auto place = [&](int64_t key) -> int64_t {
+        const int page = __ldg(g.own_table + static_cast<int64_t>(b) * g.own_pages + (key >> shift));
+        return page < 0 || page >= g.n_pages ? -1 : ((static_cast<int64_t>(page) * g.page + (key & (g.page - 1))) * g.Hkv + h) * kD;
+    };
+    auto load_v = [&](int64_t at, float (&v)[8]) {
+        const uint4 eight = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(g.v_cache) + at + d0));
+        const uint32_t twos[4] = {eight.x, eight.y, eight.z, eight.w};
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const float2 e = widen2<T>(twos[x]);
+            v[2 * x] = e.x;
+            v[2 * x + 1] = e.y;
+        }
+    };
+    bool hidden = false;
+#pragma unroll 1
+    for (int64_t key = max(static_cast<int64_t>(0), seen); key < own && !hidden; ++key) {
+        const int64_t at = place(key);
+        if (at < 0) continue;
+        float v[8];
+        load_v(at, v);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) hidden |= !isfinite(v[x]);
+    }
+    if (!hidden) return;   // what is not finite is the formula's own
     const float c = g.scale * 1.4426950408889634f;
     const int64_t q_row = (static_cast<int64_t>(i / G) * g.Hq + h * G + i % G) * kD;
     float top = -INFINITY;
@@ -1049,23 +1076,21 @@ __device__ __forceinline__ void row_again(const AttnParams &p, int h, int i, int
     }
 #pragma unroll 1
     for (int64_t key = 0; key < seen; ++key) {
-        const int page = __ldg(g.own_table + static_cast<int64_t>(b) * g.own_pages + (key >> shift));
         float s = 0.0f, v[8] = {};   // (what a page outside the cache reads as)
-        if (page >= 0 && page < g.n_pages) {
-            const int64_t at = ((static_cast<int64_t>(page) * g.page + (key & (g.page - 1))) * g.Hkv + h) * kD;
-            const uint32_t *k2 = reinterpret_cast<const uint32_t *>(static_cast<const T *>(g.k_cache) + at);
-            const uint32_t *v2 = reinterpret_cast<const uint32_t *>(static_cast<const T *>(g.v_cache) + at + d0);
-            const uint32_t *q2 = reinterpret_cast<const uint32_t *>(static_cast<const T *>(g.q) + q_row);
+        const int64_t at = place(key);
+        if (at >= 0) {
+            const uint4 *k8 = reinterpret_cast<const uint4 *>(static_cast<const T *>(g.k_cache) + at);
+            const uint4 *q8 = reinterpret_cast<const uint4 *>(static_cast<const T *>(g.q) + q_row);
+            load_v(at, v);
 #pragma unroll 4
-            for (int d = 0; d < kD / 2; ++d) {
-                const float2 a = widen2<T>(__ldg(q2 + d)), e = widen2<T>(__ldg(k2 + d));
-                s = fmaf(a.x, e.x, fmaf(a.y, e.y, s));
-            }
+            for (int d = 0; d < kD / 8; ++d) {
+                const uint4 a = __ldg(q8 + d), e = __ldg(k8 + d);
+                const uint32_t as[4] = {a.x, a.y, a.z, a.w}, es[4] = {e.x, e.y, e.z, e.w};
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const float2 e = widen2<T>(__ldg(v2 + x));
-                v[2 * x] = e.x;
-                v[2 * x + 1] = e.y;
+                for (int x = 0; x < 4; ++x) {
+                    const float2 u = widen2<T>(as[x]), y = widen2<T>(es[x]);
+                    s = fmaf(u.x, y.x, fmaf(u.y, y.y, s));
+                }
             }
         }
         add(s * c, v);
