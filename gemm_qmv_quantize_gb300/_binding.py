@@ -55,6 +55,11 @@ SIGNATURES = {
     "qmv_prefix_attention": (_i32, [_vp, _vp, _vp, _i32, _i64, _i32, _vp, _i64, _vp, _i32, _vp, _i64, _f32, _vp, _vp,
                                     _i64] + [_i32] * 5 + [_vp]),
     "qmv_penalize_logits": (_i32, [_vp, _vp, _i32] + [_vp] * 7 + [_i32, _vp, _vp, _i32, _vp, _i32, _i32, _vp]),
+    "qmv_norm_rope_append": (_i32, [_vp, _vp, _vp, ctypes.c_char_p, _vp, _vp, _vp, _f32, _vp, _vp, _vp] + [_i32] * 9 + [_i64, _vp]),
+    "qmv_rope_append_e4m3": (_i32, [_vp, _vp, _vp, ctypes.c_char_p, _vp, _vp, _vp, _f32] + [_vp] * 5 + [_i32] * 9 + [_i64, _vp]),
+    "qmv_paged_attention_e4m3_workspace": (_i64, [_i32] * 5 + [_i64]),
+    "qmv_paged_attention_e4m3": (_i32, [_vp] * 5 + [_i32, _i64, _i32, _vp, _i32, _vp, _i64, _f32, _vp, _vp, _i64] + [_i32] * 5 + [_vp]),
+    "qmv_sample": (_i32, [_vp] * 8 + [_i32, _i32, _vp]),
     "qmv_set_launch_overlap": (None, [_i32]),
     "qmv_get_launch_overlap": (_i32, []),
     "qmv_route_count": (_i32, []),

@@ -1,6 +1,7 @@
 """Binding of the operators beside the matmuls in a batched decode step (include/qmv.h):
-low-rank adapters, rotary positions with the append to a paged cache, attention over a
-shared prefix, and penalties, biases and masks on logits.
+low-rank adapters, rotary positions (with norms of q and k) and the append to a paged cache
+of 16 or 8 bits, attention over a shared prefix or over a cache of 8 bits, penalties, biases
+and masks on logits, and sampling.
 
 As in ``_binding``: tensors are checked for type, shape, contiguity and device, pointers and
 sizes go to the C entry point of the same name, and all arithmetic runs in the library.
@@ -20,6 +21,7 @@ from ._binding import QMV_OK, QmvError, _check, _need, _stream, lib
 _F32, _F16, _BF16, _I32 = torch.float32, torch.float16, torch.bfloat16, torch.int32
 _TYPE = {_F32: 0, _F16: 1, _BF16: 2}   # QMV_F32, QMV_F16, QMV_BF16
 _16BIT = (_F16, _BF16)
+_E4M3 = torch.float8_e4m3fn
 _current_device = torch._C._cuda_getDevice
 
 
@@ -186,6 +188,134 @@ def qmv_rope_append(qkv: torch.Tensor, positions: torch.Tensor, table: torch.Ten
     return out
 
 
+def _rope_args(qkv, positions, table, axis_of_pair, slots, k_cache, v_cache, q_norm, k_norm, cache_type):
+    """What both appends with norms check and pass on: (device, Hq, axis_of_pair)."""
+    pages, page, Hkv, D = k_cache.shape
+    M, width = qkv.shape
+    n_positions, pairs, _ = table.shape
+    heads, odd = divmod(width, D)
+    if odd or heads <= 2 * Hkv:
+        raise ValueError(f"qkv: rows of {width} are not q heads and 2 x {Hkv} heads of {D}")
+    if not isinstance(axis_of_pair, bytes):
+        axis_of_pair = bytes(axis_of_pair)
+    if len(axis_of_pair) != pairs:
+        raise ValueError(f"axis_of_pair: expected {pairs} entries, got {len(axis_of_pair)}")
+    dev = _first(qkv, "qkv", _F32)
+    _is(positions, "positions", _I32, (positions.shape[0], M), dev)
+    _is(table, "table", _F32, (n_positions, pairs, 2), dev)
+    _is(slots, "slots", torch.int64, (M,), dev)
+    _held(k_cache, "k_cache", cache_type, dev)
+    _is(v_cache, "v_cache", cache_type, k_cache.shape, dev)
+    if q_norm is not None:
+        _is(q_norm, "q_norm", _F32, (D,), dev)
+    if k_norm is not None:
+        _is(k_norm, "k_norm", _F32, (D,), dev)
+    return dev, heads - 2 * Hkv, axis_of_pair
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def qmv_norm_rope_append(qkv: torch.Tensor, positions: torch.Tensor, table: torch.Tensor, axis_of_pair,
+                         slots: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                         q_norm: torch.Tensor | None, k_norm: torch.Tensor | None, eps: float = 1e-6,
+                         interleaved: bool = False, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """qmv_rope_append with an RMS norm of each q and k head before it is turned, weights
+    q_norm and k_norm fp32 [D] (None: no norm)."""
+    pages, page, Hkv, D = k_cache.shape
+    M, dtype = qkv.shape[0], k_cache.dtype
+    t = _type(k_cache, "k_cache", _16BIT)
+    dev, Hq, axis_of_pair = _rope_args(qkv, positions, table, axis_of_pair, slots, k_cache, v_cache, q_norm, k_norm, dtype)
+    if out is None:
+        out = _empty((M, Hq, D), dtype, qkv.device, stream)
+    else:
+        _is(out, "out", dtype, (M, Hq, D), dev)
+    status = _fn("qmv_norm_rope_append")(
+        qkv.data_ptr(), positions.data_ptr(), table.data_ptr(), axis_of_pair, slots.data_ptr(), _ptr(q_norm), _ptr(k_norm),
+        eps, out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), t, 1 if interleaved else 0, M, Hq, Hkv, D,
+        2 * len(axis_of_pair), positions.shape[0], table.shape[0], pages * page, _on(stream, dev))
+    if status != QMV_OK:
+        _check("qmv_norm_rope_append", status)
+    return out
+
+
+def qmv_rope_append_e4m3(qkv: torch.Tensor, positions: torch.Tensor, table: torch.Tensor, axis_of_pair,
+                         slots: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
+                         v_scale: torch.Tensor, q_norm: torch.Tensor | None = None, k_norm: torch.Tensor | None = None,
+                         eps: float = 1e-6, interleaved: bool = False, dtype: torch.dtype = torch.float16,
+                         out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The same into a cache of 8-bit codes: k_cache, v_cache float8_e4m3fn [pages, page, Hkv, D]
+    with scales k_scale, v_scale fp32 [pages, page / 16, Hkv] of blocks of 16 slots, which
+    grow with what is appended (rows of one block follow one another, in the slots' order).
+    Returns q [M, Hq, D], fp16 or bf16 (dtype, or out's)."""
+    pages, page, Hkv, D = k_cache.shape
+    M = qkv.shape[0]
+    dev, Hq, axis_of_pair = _rope_args(qkv, positions, table, axis_of_pair, slots, k_cache, v_cache, q_norm, k_norm, _E4M3)
+    _is(k_scale, "k_scale", _F32, (pages, page // 16, Hkv), dev)
+    _is(v_scale, "v_scale", _F32, (pages, page // 16, Hkv), dev)
+    if page % 16 != 0:
+        raise ValueError(f"k_cache: pages of {page} are not whole blocks of 16")
+    if out is None:
+        if dtype not in _16BIT:
+            raise TypeError(f"dtype: expected {_F16} or {_BF16}, got {dtype}")
+        out = _empty((M, Hq, D), dtype, qkv.device, stream)
+    else:
+        _type(out, "out", _16BIT)
+        _is(out, "out", out.dtype, (M, Hq, D), dev)
+    status = _fn("qmv_rope_append_e4m3")(
+        qkv.data_ptr(), positions.data_ptr(), table.data_ptr(), axis_of_pair, slots.data_ptr(), _ptr(q_norm), _ptr(k_norm),
+        eps, out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+        _TYPE[out.dtype], 1 if interleaved else 0, M, Hq, Hkv, D, 2 * len(axis_of_pair), positions.shape[0],
+        table.shape[0], pages * page, _on(stream, dev))
+    if status != QMV_OK:
+        _check("qmv_rope_append_e4m3", status)
+    return out
+
+
+def qmv_paged_attention_e4m3_workspace(B: int, T: int, Hq: int, Hkv: int, D: int, max_len: int) -> int:
+    """Bytes of workspace of qmv_paged_attention_e4m3 at these sizes."""
+    return _bytes("qmv_paged_attention_e4m3_workspace",
+                  _fn("qmv_paged_attention_e4m3_workspace")(B, T, Hq, Hkv, D, max_len))
+
+
+def qmv_paged_attention_e4m3(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
+                             v_scale: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, scale: float | None = None,
+                             max_len: int | None = None, out: torch.Tensor | None = None,
+                             workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Attention of q [B, T, Hq, D], the last T of each request's lens[b] tokens (int32 [B]),
+    over the pages table[b] (int32 [B, n]) of a cache of codes as qmv_rope_append_e4m3 fills
+    it. scale: 1 / sqrt(D) unless given. max_len: a bound of lens that the caller knows (the
+    table's width unless given; the work is split by it)."""
+    B, T, Hq, D = q.shape
+    pages, page, Hkv, _ = k_cache.shape
+    width = table.shape[1]
+    dtype = q.dtype
+    t = _type(q, "q", _16BIT)
+    dev = _first(q, "q", dtype)
+    _is(k_cache, "k_cache", _E4M3, (pages, page, Hkv, D), dev)
+    _is(v_cache, "v_cache", _E4M3, k_cache.shape, dev)
+    _is(k_scale, "k_scale", _F32, (pages, page // 16, Hkv), dev)
+    _is(v_scale, "v_scale", _F32, k_scale.shape, dev)
+    _is(table, "table", _I32, (B, width), dev)
+    _is(lens, "lens", _I32, (B,), dev)
+    if max_len is None:
+        max_len = width * page
+    if out is None:
+        out = _empty((B, T, Hq, D), dtype, q.device, stream)
+    else:
+        _is(out, "out", dtype, q.shape, dev)
+    need = lambda: qmv_paged_attention_e4m3_workspace(B, T, Hq, Hkv, D, max_len)  # noqa: E731
+    ws = _workspace(workspace, need, dev, stream)
+    status = _fn("qmv_paged_attention_e4m3")(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), t, pages, page,
+        table.data_ptr(), width, lens.data_ptr(), max_len, 1.0 / math.sqrt(D) if scale is None else scale, out.data_ptr(),
+        ws.data_ptr(), ws.numel(), B, T, Hq, Hkv, D, _on(stream, dev))
+    if status != QMV_OK:
+        _check_with("qmv_paged_attention_e4m3", status, ws, need)
+    return out
+
+
 def qmv_prefix_attention_workspace(B: int, T: int, Hq: int, Hkv: int, D: int, prefix_len: int, max_own: int) -> int:
     """Bytes of workspace of qmv_prefix_attention at these sizes."""
     return _bytes("qmv_prefix_attention_workspace",
@@ -277,4 +407,29 @@ def qmv_penalize_logits(logits: torch.Tensor, tokens: torch.Tensor, prompt_len: 
         out.data_ptr(), M, V, _on(stream, dev))
     if status != QMV_OK:
         _check("qmv_penalize_logits", status)
+    return out
+
+
+def qmv_sample(logits: torch.Tensor, u: torch.Tensor, temperature: torch.Tensor | None = None,
+               top_k: torch.Tensor | None = None, top_p: torch.Tensor | None = None, min_p: torch.Tensor | None = None,
+               out: torch.Tensor | None = None, prob: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """A token int32 for each row of logits fp32 [M, V], drawn by the random numbers u fp32 [M],
+    0 <= u < 1, among those that top_k int32, top_p and min_p fp32 [M] keep (None: all), at
+    temperature fp32 [M] (None: 1; 0: the largest logit). prob fp32 [M], where given, gets the
+    token's probability among those kept. A row without a logit above -inf gives -1."""
+    M, V = logits.shape
+    dev = _first(logits, "logits", _F32)
+    _is(u, "u", _F32, (M,), dev)
+    for name, t, dtype in (("temperature", temperature, _F32), ("top_k", top_k, _I32), ("top_p", top_p, _F32),
+                           ("min_p", min_p, _F32), ("prob", prob, _F32)):
+        if t is not None:
+            _is(t, name, dtype, (M,), dev)
+    if out is None:
+        out = _empty((M,), _I32, logits.device, stream)
+    else:
+        _is(out, "out", _I32, (M,), dev)
+    status = _fn("qmv_sample")(logits.data_ptr(), u.data_ptr(), _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p),
+                               out.data_ptr(), _ptr(prob), M, V, _on(stream, dev))
+    if status != QMV_OK:
+        _check("qmv_sample", status)
     return out

@@ -21,6 +21,7 @@ constexpr const char *kRouteNames[kRouteCount] = {
     "fp8_mma_m16n8k16", "fp8_generic", "zero_fill", "q4_0_mma_m16n8k32", "q4_0_mma_fused_quantize",
     "q4_k_stream_dp4a", "q4_k_stream_fused_quantize", "q4_k_mma_m16n8k32", "q4_k_mma_fused_quantize",
     "nvfp4_tcgen05", "fp8_tcgen05", "lora_add", "rope_append", "prefix_attention", "penalize_logits",
+    "norm_rope_append", "rope_append_e4m3", "paged_attention_e4m3", "sample",
 };
 
 constexpr int kMaxDevices = 64;
@@ -530,16 +531,18 @@ qmv_status qmv_error_flags(uint32_t *flags, int clear)
     if (read_error_word_umma(&w5, clear != 0) != cudaSuccess) return QMV_ERR_CUDA;
     if (read_error_word_wq(&w2, clear != 0) != cudaSuccess) return QMV_ERR_CUDA;
     if (read_error_word_q4_0_mma(&w3, clear != 0) != cudaSuccess) return QMV_ERR_CUDA;
-    uint32_t d[3] = {0, 0, 0};
+    uint32_t d[5] = {0, 0, 0, 0, 0};
     if (read_error_word_rope(&d[0], clear != 0) != cudaSuccess) return QMV_ERR_CUDA;
     if (read_error_word_attention(&d[1], clear != 0) != cudaSuccess) return QMV_ERR_CUDA;
     if (read_error_word_logits(&d[2], clear != 0) != cudaSuccess) return QMV_ERR_CUDA;
+    if (read_error_word_norm_rope(&d[3], clear != 0) != cudaSuccess) return QMV_ERR_CUDA;
+    if (read_error_word_paged(&d[4], clear != 0) != cudaSuccess) return QMV_ERR_CUDA;
     if (cudaMemcpyFromSymbol(&w4, g_abi_error, sizeof(uint32_t)) != cudaSuccess) return QMV_ERR_CUDA;
     if (clear) {
         const uint32_t zero = 0;
         if (cudaMemcpyToSymbol(g_abi_error, &zero, sizeof(uint32_t)) != cudaSuccess) return QMV_ERR_CUDA;
     }
-    *flags = w | w2 | w3 | w4 | w5 | d[0] | d[1] | d[2];
+    *flags = w | w2 | w3 | w4 | w5 | d[0] | d[1] | d[2] | d[3] | d[4];
     return QMV_OK;
 }
 

@@ -31,6 +31,39 @@ bool attention_shape_ok(int B, int T, int Hq, int Hkv, int D, int64_t prefix_len
            static_cast<int64_t>(B) * T <= kMaxDim && static_cast<int64_t>(B) * T * Hq <= kMaxDim / 128;
 }
 
+// Of both appends with norms; codes: heads that the attention over them takes.
+qmv_status norm_rope_shape(int type, int M, int Hq, int Hkv, int D, int rot, int axes, int n_positions, int64_t n_slots,
+                           float eps, bool codes)
+{
+    if (!is_16bit(type) || M < 0 || Hq < 1 || Hkv < 1 || Hq > 65536 || Hkv > 65536) return QMV_ERR_SHAPE;
+    if (D < 8 || D > 2 * kMaxRopePairs || D % 8 != 0 || rot < 0 || rot > D || rot % 8 != 0) return QMV_ERR_SHAPE;
+    if (codes && ((D != 64 && D != 128) || n_slots % 16 != 0)) return QMV_ERR_SHAPE;
+    if (axes < 1 || axes > kMaxRopeAxes || n_positions < (rot > 0 ? 1 : 0) || n_slots < 0) return QMV_ERR_SHAPE;
+    if (!(eps >= 0.0f) || std::isinf(eps)) return QMV_ERR_SHAPE;
+    return QMV_OK;
+}
+
+qmv_status run_norm_rope(NormRopeArgs g, const uint8_t *axis_of_pair, int axes, qmv_stream_t stream)
+{
+    if (!g.qkv || !g.q || !g.slots || !g.k_cache || !g.v_cache) return QMV_ERR_NULL;
+    if (g.rot > 0 && (!g.positions || !g.table || !axis_of_pair)) return QMV_ERR_NULL;
+    if (misaligned(g.qkv, 16) || misaligned(g.q, 16) || misaligned(g.k_cache, 16) || misaligned(g.v_cache, 16) ||
+        misaligned(g.table, 16) || misaligned(g.positions, 4) || misaligned(g.slots, 8) || misaligned(g.q_norm, 4) ||
+        misaligned(g.k_norm, 4) || misaligned(g.k_scale, 4) || misaligned(g.v_scale, 4))
+        return QMV_ERR_ALIGN;
+    for (int i = 0; i < g.rot / 2; ++i) {
+        if (axis_of_pair[i] >= axes) return QMV_ERR_SHAPE;
+        g.axis_of_pair[i] = axis_of_pair[i];
+    }
+    return from_cuda(launch_norm_rope(g, stream));
+}
+
+bool paged_shape_ok(int B, int T, int Hq, int Hkv, int D, int64_t max_len)
+{
+    return B >= 0 && B <= 65535 && T >= 1 && Hq >= 1 && Hkv >= 1 && Hkv <= 65535 && Hq % Hkv == 0 && (D == 64 || D == 128) &&
+           max_len >= 0 && max_len <= (1 << 30) && static_cast<int64_t>(T) * Hq <= (1 << 30);
+}
+
 }  // namespace
 
 extern "C" {
@@ -85,6 +118,78 @@ qmv_status qmv_rope_append(const float *qkv, const int32_t *positions, const flo
         g.axis_of_pair[i] = axis_of_pair[i];
     }
     return from_cuda(launch_rope(g, stream));
+}
+
+qmv_status qmv_norm_rope_append(const float *qkv, const int32_t *positions, const float *table,
+                                const uint8_t *axis_of_pair, const int64_t *slots, const float *q_norm,
+                                const float *k_norm, float eps, void *q, void *k_cache, void *v_cache, int type,
+                                int interleaved, int M, int Hq, int Hkv, int D, int rot, int axes, int n_positions,
+                                int64_t n_slots, qmv_stream_t stream)
+{
+    const qmv_status st = norm_rope_shape(type, M, Hq, Hkv, D, rot, axes, n_positions, n_slots, eps, false);
+    if (st != QMV_OK || M == 0) return st;
+    return run_norm_rope(NormRopeArgs{qkv, positions, table, slots, q_norm, k_norm, q, k_cache, v_cache, nullptr, nullptr,
+                                      n_slots, eps, type, M, Hq, Hkv, D, rot, n_positions, interleaved != 0, {}},
+                         axis_of_pair, axes, stream);
+}
+
+qmv_status qmv_rope_append_e4m3(const float *qkv, const int32_t *positions, const float *table,
+                                const uint8_t *axis_of_pair, const int64_t *slots, const float *q_norm,
+                                const float *k_norm, float eps, void *q, void *k_cache, void *v_cache, float *k_scale,
+                                float *v_scale, int type, int interleaved, int M, int Hq, int Hkv, int D, int rot,
+                                int axes, int n_positions, int64_t n_slots, qmv_stream_t stream)
+{
+    const qmv_status st = norm_rope_shape(type, M, Hq, Hkv, D, rot, axes, n_positions, n_slots, eps, true);
+    if (st != QMV_OK || M == 0) return st;
+    if (!k_scale || !v_scale) return QMV_ERR_NULL;
+    return run_norm_rope(NormRopeArgs{qkv, positions, table, slots, q_norm, k_norm, q, k_cache, v_cache, k_scale, v_scale,
+                                      n_slots, eps, type, M, Hq, Hkv, D, rot, n_positions, interleaved != 0, {}},
+                         axis_of_pair, axes, stream);
+}
+
+int64_t qmv_paged_attention_e4m3_workspace(int B, int T, int Hq, int Hkv, int D, int64_t max_len)
+{
+    return paged_shape_ok(B, T, Hq, Hkv, D, max_len) ? paged_workspace_bytes(B, T, Hq, Hkv, D, max_len) : QMV_ERR_SHAPE;
+}
+
+qmv_status qmv_paged_attention_e4m3(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
+                                    const float *v_scale, int type, int64_t n_pages, int page, const int32_t *table,
+                                    int table_pages, const int32_t *lens, int64_t max_len, float scale, void *out,
+                                    void *workspace, int64_t workspace_bytes, int B, int T, int Hq, int Hkv, int D,
+                                    qmv_stream_t stream)
+{
+    if (!is_16bit(type) || !paged_shape_ok(B, T, Hq, Hkv, D, max_len)) return QMV_ERR_SHAPE;
+    if (page < 16 || page > 256 || (page & (page - 1)) != 0 || n_pages < 0 || n_pages > kMaxDim || table_pages < 0)
+        return QMV_ERR_SHAPE;
+    if (max_len > static_cast<int64_t>(table_pages) * page) return QMV_ERR_SHAPE;
+    if (n_pages == 0 && max_len > 0) return QMV_ERR_SHAPE;
+    if (!(scale > 0.0f) || std::isinf(scale)) return QMV_ERR_SHAPE;
+    if (B == 0) return QMV_OK;
+    if (!q || !out || !lens) return QMV_ERR_NULL;
+    if (max_len > 0 && (!k_cache || !v_cache || !k_scale || !v_scale || !table)) return QMV_ERR_NULL;
+    if (misaligned(q, 16) || misaligned(k_cache, 16) || misaligned(v_cache, 16) || misaligned(out, 16) ||
+        misaligned(k_scale, 4) || misaligned(v_scale, 4) || misaligned(table, 4) || misaligned(lens, 4) ||
+        misaligned(workspace, 16))
+        return QMV_ERR_ALIGN;
+    const int64_t need = paged_workspace_bytes(B, T, Hq, Hkv, D, max_len);
+    if (need > 0 && !workspace) return QMV_ERR_NULL;
+    if (workspace_bytes < need) return QMV_ERR_SHAPE;
+    return from_cuda(launch_paged_e4m3(PagedArgs{q, k_cache, v_cache, k_scale, v_scale, table, lens, out, workspace, n_pages,
+                                                 max_len, scale, type, page, table_pages, B, T, Hq, Hkv, D},
+                                       stream));
+}
+
+qmv_status qmv_sample(const float *logits, const float *u, const float *temperature, const int32_t *top_k,
+                      const float *top_p, const float *min_p, int32_t *token, float *prob, int M, int V,
+                      qmv_stream_t stream)
+{
+    if (M < 0 || M > 65535 || V < 1 || V > sample_max_vocabulary()) return QMV_ERR_SHAPE;
+    if (M == 0) return QMV_OK;
+    if (!logits || !u || !token) return QMV_ERR_NULL;
+    if (misaligned(logits, 4) || misaligned(u, 4) || misaligned(temperature, 4) || misaligned(top_k, 4) ||
+        misaligned(top_p, 4) || misaligned(min_p, 4) || misaligned(token, 4) || misaligned(prob, 4))
+        return QMV_ERR_ALIGN;
+    return from_cuda(launch_sample(SampleArgs{logits, u, temperature, top_k, top_p, min_p, token, prob, M, V}, stream));
 }
 
 int64_t qmv_prefix_attention_workspace(int B, int T, int Hq, int Hkv, int D, int64_t prefix_len, int64_t max_own)

@@ -1,6 +1,6 @@
 // decode_ops.h -- host-side interface between the C ABI layer (abi_decode.cu) and the
 // kernels of the operators that stand beside the matmuls in a decode step: adapters,
-// rotary positions with the cache append, shared-prefix attention, logits. Not
+// rotary positions with the cache append, attention, logits, sampling. Not
 // installed; not part of the ABI.
 #pragma once
 
@@ -42,6 +42,35 @@ struct RopeArgs {
 };
 cudaError_t launch_rope(const RopeArgs &g, cudaStream_t s);
 
+// ---- the same with norms of q's and k's heads, into a cache of 16 bits or (k_scale) of codes
+struct NormRopeArgs {
+    const float *qkv;           // [M][(Hq + 2 Hkv) D]
+    const int32_t *positions;   // [axes][M]
+    const float *table;         // [n_positions][rot / 2][2]
+    const int64_t *slots;       // [M]
+    const float *q_norm, *k_norm;   // [D], may be null
+    void *q, *k_cache, *v_cache;
+    float *k_scale, *v_scale;   // [n_slots / 16][Hkv], or null
+    int64_t n_slots;
+    float eps;
+    int type, M, Hq, Hkv, D, rot, n_positions, interleaved;
+    uint8_t axis_of_pair[kMaxRopePairs];
+};
+cudaError_t launch_norm_rope(const NormRopeArgs &g, cudaStream_t s);
+
+// ---- attention over a cache of codes
+struct PagedArgs {
+    const void *q, *k, *v;
+    const float *ks, *vs;
+    const int32_t *table, *lens;
+    void *out, *workspace;
+    int64_t n_pages, max_len;
+    float scale;
+    int type, page, table_pages, B, T, Hq, Hkv, D;
+};
+int64_t paged_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int64_t max_len);
+cudaError_t launch_paged_e4m3(const PagedArgs &g, cudaStream_t s);
+
 // ---- attention over a shared prefix
 struct AttnArgs {
     const void *q, *k_cache, *v_cache;
@@ -68,9 +97,23 @@ struct LogitsArgs {
 };
 cudaError_t launch_logits(const LogitsArgs &g, cudaStream_t s);
 
+// ---- sampling
+struct SampleArgs {
+    const float *logits, *u, *temperature;
+    const int32_t *top_k;          // may be null, as the next two
+    const float *top_p, *min_p;
+    int32_t *token;
+    float *prob;                   // may be null
+    int M, V;
+};
+int sample_max_vocabulary();
+cudaError_t launch_sample(const SampleArgs &g, cudaStream_t s);
+
 // Device error words of the operators that follow indices held in device memory.
 cudaError_t read_error_word_rope(uint32_t *out, bool clear);
 cudaError_t read_error_word_attention(uint32_t *out, bool clear);
 cudaError_t read_error_word_logits(uint32_t *out, bool clear);
+cudaError_t read_error_word_norm_rope(uint32_t *out, bool clear);
+cudaError_t read_error_word_paged(uint32_t *out, bool clear);
 
 }  // namespace qmv

@@ -31,6 +31,10 @@ enum Route : int {
     kRouteRopeAppend,     // rotary positions and the append to a paged cache
     kRoutePrefixAttention,  // attention over a shared prefix and the requests' own tokens
     kRouteLogits,         // penalties, biases and masks on logits
+    kRouteNormRope,       // norms and rotary positions, append to a 16-bit cache
+    kRouteRopeE4m3,       // the same into a cache of E4M3 codes
+    kRoutePagedE4m3,      // attention over a cache of E4M3 codes
+    kRouteSample,         // draws from filtered distributions
     kRouteCount
 };
 

@@ -3,11 +3,10 @@
 //   (a, b) -> (a c - b s, b c + a s),  (c, s) = table[position on the pair's axis][pair]
 // computed in fp32 from the projection's fp32 output and rounded once, to the 16-bit type
 // of q and the cache.
-#include <type_traits>
-
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "decode_device.cuh"
 #include "decode_ops.h"
 #include "qmv.h"
 #include "qmv_device.cuh"
@@ -18,19 +17,6 @@ namespace {
 __device__ uint32_t g_rope_error;
 
 constexpr int kThreads = 256;
-
-// Two values rounded to the 16-bit type, a in the low half.
-template <typename T>
-__device__ __forceinline__ uint32_t pack2(float a, float b)
-{
-    if constexpr (std::is_same_v<T, __half>) {
-        const __half2 h = __floats2half2_rn(a, b);
-        return *reinterpret_cast<const uint32_t *>(&h);
-    } else {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-        return *reinterpret_cast<const uint32_t *>(&h);
-    }
-}
 
 // A CTA takes 256 units of 8 elements of one token's heads, a thread a unit: 4 pairs of the
 // rotated part, or 8 elements that are copied. The token's angles go to shared memory once

@@ -255,8 +255,9 @@ QMV_API int qmv_get_launch_overlap(void);
 
 /* ---------------------------------------------------------------------------
  * Operators of a batched decode step, beside the matmuls: the adapters of a
- * projection's rows, rotary positions with the append to a paged cache, attention
- * over a shared prefix, and penalties, biases and masks on the logits.
+ * projection's rows, rotary positions (with norms of q and k) and the append to a paged
+ * cache of 16 or 8 bits, attention over a shared prefix or over a cache of 8 bits,
+ * penalties, biases and masks on the logits, and sampling.
  *
  * 16-bit tensors are IEEE binary16 or bfloat16, named by a type argument. Sums and
  * softmax statistics are fp32 and an output is rounded once. Two operands of products
@@ -375,6 +376,99 @@ QMV_API qmv_status qmv_penalize_logits(const float *logits, const int32_t *token
                                        const float *bias_values, int max_bias, const uint32_t *mask,
                                        const int32_t *mask_row, int n_masks, float *y, int M, int V,
                                        qmv_stream_t stream);
+
+/*
+ * qmv_rope_append with an RMS norm of each q and k head before it is turned:
+ *   x[i] = x[i] / sqrt(sum_j x[j]^2 / D + eps) * q_norm[i]   (k_norm for k heads; v has none)
+ * in fp32, squares included (a head with elements of 1e19 or more overflows them).
+ *   q_norm, k_norm  fp32 [D], each NULL for no norm; eps 0 or more and finite.
+ *   All else as in qmv_rope_append.
+ */
+QMV_API qmv_status qmv_norm_rope_append(const float *qkv, const int32_t *positions, const float *table,
+                                        const uint8_t *axis_of_pair, const int64_t *slots, const float *q_norm,
+                                        const float *k_norm, float eps, void *q, void *k_cache, void *v_cache, int type,
+                                        int interleaved, int M, int Hq, int Hkv, int D, int rot, int axes,
+                                        int n_positions, int64_t n_slots, qmv_stream_t stream);
+
+/*
+ * The same into a cache held in 8 bits: E4M3 codes with a scale for each block of 16
+ * consecutive slots (16 b .. 16 b + 15) and head, value = code * scale.
+ *   k_cache, v_cache uint8 [n_slots][Hkv][D], D = 64 or 128; k_scale, v_scale fp32
+ *            [n_slots / 16][Hkv]; n_slots a multiple of 16. q is of type `type`, all
+ *            arguments but the caches as in qmv_norm_rope_append.
+ *   A block's slots are filled in order. A token at a block's first slot starts it: what
+ *   was there is forgotten. One at a later slot keeps the tokens before it in the block (the
+ *   codes of the tokens after it are left as they are, and mean nothing from then on: they
+ *   may have been written for another scale).
+ *   scale    the least power of two, 2^-64 at least, of which no finite element of the
+ *            call's new tokens in the block is above 448 times, nor less than the scale
+ *            that kept tokens have. Where it grows, their codes are multiplied by the old
+ *            scale over the new one and rounded again: exact for codes that stay at 2^-6
+ *            or above, within 2^-10 new scales for the others.
+ *   code     value / scale rounded to the nearest, ties to even. There are no infinities:
+ *            they become NaN, as NaN does.
+ *   Rows of a call with slots of one block follow one another, in the slots' order and
+ *   without gaps. Different blocks come in any order.
+ */
+QMV_API qmv_status qmv_rope_append_e4m3(const float *qkv, const int32_t *positions, const float *table,
+                                        const uint8_t *axis_of_pair, const int64_t *slots, const float *q_norm,
+                                        const float *k_norm, float eps, void *q, void *k_cache, void *v_cache,
+                                        float *k_scale, float *v_scale, int type, int interleaved, int M, int Hq, int Hkv,
+                                        int D, int rot, int axes, int n_positions, int64_t n_slots, qmv_stream_t stream);
+
+/*
+ * Attention of T tokens of each of B requests over a paged cache of such codes. The T
+ * tokens are the last of lens[b], so their keys are in the cache before the call:
+ *   out[b][t][h] = sum_j p_j V_j,  p = softmax_j(scale * q[b][t][h] . K_j)
+ * over the first lens[b] - T + 1 + t keys j, K = code * k_scale and V = code * v_scale; head
+ * h reads key head h / (Hq / Hkv). A row without any key gives zeros (one whose scores
+ * are all -inf, NaN).
+ *   q, out   [B][T][Hq][D], QMV_F16 or QMV_BF16 (type); B up to 65535, D = 64 or 128, Hkv
+ *            dividing Hq.
+ *   k_cache, v_cache uint8 [n_pages][page][Hkv][D], page a power of two, 16..256, 16-byte
+ *            aligned; k_scale, v_scale fp32 [n_pages][page / 16][Hkv], finite and not negative.
+ *   table    int32 [B][table_pages]; lens int32 [B] (at most max_len, a bound the caller
+ *            knows, itself at most table_pages * page and 2^30; a longer one is cut to
+ *            max_len and sets bit 2). A page outside the cache reads as zeros (bit 2).
+ *            Whatever lies in the cache past a request's length is not used, NaN included, and no
+ *            row is touched by tokens after its own.
+ *   scale    finite and positive.
+ *   q is held in binary16: of a bfloat16 row, scaled by a power of two, elements smaller
+ *   than 2^-28 of the row's largest lose bits. The terms of the sum over V are rounded to binary16, relative to the
+ *   largest of the row.
+ *   Workspace: qmv_paged_attention_e4m3_workspace(...) bytes (negative: QMV_ERR_SHAPE).
+ */
+QMV_API int64_t qmv_paged_attention_e4m3_workspace(int B, int T, int Hq, int Hkv, int D, int64_t max_len);
+QMV_API qmv_status qmv_paged_attention_e4m3(const void *q, const void *k_cache, const void *v_cache,
+                                            const float *k_scale, const float *v_scale, int type, int64_t n_pages,
+                                            int page, const int32_t *table, int table_pages, const int32_t *lens,
+                                            int64_t max_len, float scale, void *out, void *workspace,
+                                            int64_t workspace_bytes, int B, int T, int Hq, int Hkv, int D,
+                                            qmv_stream_t stream);
+
+/*
+ * A token for each row of logits, drawn with the random number u[m] of 0 <= u < 1:
+ *   w_v = exp((logits[m][v] - max) / temperature[m]); tokens in order: the larger logit
+ *   first, equal logits by index (-0 equals 0)
+ *   kept: the first top_k[m] tokens; of these, those before which the sum of w is below
+ *         top_p[m] times the sum over these; of those, the ones with w_v >= min_p[m]; and
+ *         always the first token
+ *   token[m] = the first v, by index, for which the kept w_0 + .. + w_v exceed u[m] times
+ *   the kept sum;  prob[m] = w_v over the kept sum.
+ * Sums are whole numbers of 2^-44 of the largest weight, each weight within 2^-32 of its
+ * value and those below 2^-44 zero.
+ *   logits   fp32 [M][V], M = 0..65535, V = 1..524288. NaN counts as -inf; a row without
+ *            a logit above -inf gives token -1 and prob 0; +inf weighs 1, all else beside it 0.
+ *   u        fp32 [M]; below 0 or NaN counts as 0, 1 or more as just below 1.
+ *   temperature fp32 [M], NULL for 1; one that is not above 0 takes the first token.
+ *   top_k int32 [M], top_p, min_p fp32 [M], each NULL for none; top_k of 0 or less or above
+ *            V, top_p of 1 or more, min_p of 0 or less, and NaN are none; top_p of 0 or
+ *            less and min_p above 1 keep the first token alone.
+ *   token    int32 [M]; prob fp32 [M] or NULL.
+ */
+QMV_API qmv_status qmv_sample(const float *logits, const float *u, const float *temperature, const int32_t *top_k,
+                              const float *top_p, const float *min_p, int32_t *token, float *prob, int M, int V,
+                              qmv_stream_t stream);
 
 /* ---------------------------------------------------------------------------
  * Introspection (tests and benchmarks)
