@@ -68,7 +68,7 @@ struct PagedArgs {
     float scale;
     int type, page, table_pages, B, T, Hq, Hkv, D;
 };
-int64_t paged_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int64_t max_len);
+int64_t paged_workspace_bytes();
 cudaError_t launch_paged_e4m3(const PagedArgs &g, cudaStream_t s);
 
 // ---- attention over a shared prefix

@@ -423,8 +423,8 @@ QMV_API qmv_status qmv_rope_append_e4m3(const float *qkv, const int32_t *positio
  * over the first lens[b] - T + 1 + t keys j, K = code * k_scale and V = code * v_scale; head
  * h reads key head h / (Hq / Hkv). A row without any key gives zeros (one whose scores
  * are all -inf, NaN).
- *   q, out   [B][T][Hq][D], QMV_F16 or QMV_BF16 (type); B up to 65535, D = 64 or 128, Hkv
- *            dividing Hq.
+ *   q, out   [B][T][Hq][D], QMV_F16 or QMV_BF16 (type); B up to 65535, T Hq up to 2^20,
+ *            D = 64 or 128, Hkv dividing Hq.
  *   k_cache, v_cache uint8 [n_pages][page][Hkv][D], page a power of two, 16..256, 16-byte
  *            aligned; k_scale, v_scale fp32 [n_pages][page / 16][Hkv], finite and not negative.
  *   table    int32 [B][table_pages]; lens int32 [B] (at most max_len, a bound the caller
