@@ -61,7 +61,8 @@ qmv_status run_norm_rope(NormRopeArgs g, const uint8_t *axis_of_pair, int axes, 
 bool paged_shape_ok(int B, int T, int Hq, int Hkv, int D, int64_t max_len)
 {
     return B >= 0 && B <= 65535 && T >= 1 && Hq >= 1 && Hkv >= 1 && Hkv <= 65535 && Hq % Hkv == 0 && (D == 64 || D == 128) &&
-           max_len >= 0 && max_len <= (1 << 30) && static_cast<int64_t>(T) * Hq <= (1 << 20);
+           max_len >= 0 && max_len <= (1 << 30) && static_cast<int64_t>(T) * Hq <= (1 << 20) &&
+           static_cast<int64_t>(B) * T * Hq <= kMaxDim;
 }
 
 }  // namespace
@@ -149,7 +150,7 @@ qmv_status qmv_rope_append_e4m3(const float *qkv, const int32_t *positions, cons
 
 int64_t qmv_paged_attention_e4m3_workspace(int B, int T, int Hq, int Hkv, int D, int64_t max_len)
 {
-    return paged_shape_ok(B, T, Hq, Hkv, D, max_len) ? paged_workspace_bytes() : QMV_ERR_SHAPE;
+    return paged_shape_ok(B, T, Hq, Hkv, D, max_len) ? paged_workspace_bytes(B, T * (Hq / Hkv)) : QMV_ERR_SHAPE;
 }
 
 qmv_status qmv_paged_attention_e4m3(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
@@ -171,7 +172,7 @@ qmv_status qmv_paged_attention_e4m3(const void *q, const void *k_cache, const vo
         misaligned(k_scale, 4) || misaligned(v_scale, 4) || misaligned(table, 4) || misaligned(lens, 4) ||
         misaligned(workspace, 16))
         return QMV_ERR_ALIGN;
-    const int64_t need = paged_workspace_bytes();
+    const int64_t need = paged_workspace_bytes(B, T * (Hq / Hkv));
     if (need > 0 && !workspace) return QMV_ERR_NULL;
     if (workspace_bytes < need) return QMV_ERR_SHAPE;
     return from_cuda(launch_paged_e4m3(PagedArgs{q, k_cache, v_cache, k_scale, v_scale, table, lens, out, workspace, n_pages,

@@ -68,7 +68,7 @@ struct PagedArgs {
     float scale;
     int type, page, table_pages, B, T, Hq, Hkv, D;
 };
-int64_t paged_workspace_bytes();
+int64_t paged_workspace_bytes(int B, int rows);
 cudaError_t launch_paged_e4m3(const PagedArgs &g, cudaStream_t s);
 
 // ---- attention over a shared prefix

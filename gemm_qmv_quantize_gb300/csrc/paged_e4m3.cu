@@ -8,9 +8,8 @@
 //   S^T = K Q^T (16 keys x 8 rows a product),   O^T += V^T P^T (16 dimensions x 8 rows).
 // So a product's rows are full however few query rows there are, and a block has one scale.
 // Which key or dimension a row or column of a product stands for is free: it is chosen so
-// that every lane's operands are whole 16-byte pieces of the cache's rows, which the lane
-// copies to shared memory and reads back itself; nothing is shared between lanes, and codes
-// become binary16, exactly, on their way into the product. P^T is S^T transposed in registers.
+// that every lane's operands are whole 16-byte pieces of the cache's rows, and codes become
+// binary16, exactly, on their way from shared memory into the product. P^T is S^T transposed in registers.
 //
 // Numerics: q is held in binary16 (bfloat16 rows are scaled by a power of two that brings
 // their largest element to 2^14 or more: elements 2^-28 of it and less lose bits); S, the softmax's
@@ -36,33 +35,35 @@ namespace {
 __device__ uint32_t g_paged_error;
 
 constexpr int kBlock = kScaleTokens;    // keys a step of a warp
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int64_t kWorkspaceBytes = 2 * 152 * 4352 * 4;   // two parts for each of the most runs, whatever the sizes
+constexpr int kMostWarps = 8;           // of a CTA, a key head each
+constexpr int64_t kFewBytes = 22ll << 20, kMostBytes = 44ll << 20;   // of the workspace's slots
+constexpr int kSms = 152;
+constexpr int kLeastBlocks = 2;         // of a run, where there are few
 constexpr int kBatch = 32;              // blocks whose page and scales a warp looks up at a time, a lane a block
 constexpr float kSlack = 8.0f;
 constexpr float kLowest = -3.402823466e38f;   // a maximum of no scores: the difference to it is never NaN
+constexpr float kLeastLog = -100.0f;          // log2 of the least scale, and of 0
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D>
-struct Ring {   // a stage: 16-byte pieces, [piece][lane]
-    static constexpr int kKPieces = 2 * D / 64;
+struct Ring {
     static constexpr int kBytes = 32 * kBlock * D / 16;   // keys and values of a block: 2 * 16 * D
 };
 
-// Stages of a warp's ring, and CTAs an SM, by the registers that NT row tiles of O take.
+// Warps an SM, by the registers that NT row tiles of O take, and stages of a warp's ring, by the
+// shared memory that is left beside q's operands.
 template <int D, int NT>
 struct Shape {
-    static constexpr int kCtas = NT * D <= 256 ? 2 : 1;
-    static constexpr int kStages = (128 / D) * (kCtas == 2 ? 3 : 6);
+    static constexpr int kWarpsSm = NT * D <= 128 ? 16 : 8;
+    static constexpr int kQueries = NT == 1 ? 0 : NT * D * 16;   // bytes a warp
+    static constexpr int kFit = (216 * 1024 / kWarpsSm - kQueries) / (32 * D), kStages = kFit < 3 ? 3 : kFit > 6 ? 6 : kFit;
+    static constexpr int kOwn = kStages * 32 * D + kQueries;     // a warp's shared memory
+    static constexpr int kMostWarpsOfRuns = 152 * kWarpsSm;
 };
 
 __device__ __forceinline__ void cp_async_16_zfill(uint32_t dst, const void *src, bool there)
 {
     asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async_8_zfill(uint32_t dst, const void *src, bool there)
-{
-    asm volatile("cp.async.ca.shared.global.L2::128B [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(there ? 8 : 0) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -90,6 +91,14 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v)
     return r;
 }
 
+// Four E4M3 codes as two pairs of binary16, exactly, the lowest byte first.
+__device__ __forceinline__ void decode4(uint32_t codes, uint32_t &lo, uint32_t &hi)
+{
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(codes));
+}
+
 __device__ __forceinline__ float exp2_fast(float x)
 {
     float y;
@@ -107,7 +116,8 @@ __device__ __forceinline__ uint32_t half2_bits(float a, float b)
 template <int D, int NT>
 struct Part {
     float o[NT][D / 16][4];        // O^T: [0], [1] dimension d of columns 0 and 1; [2], [3] of d + 1
-    float l[NT][2], m[NT][2], mv[NT][2];
+    float l[NT][2], m[NT][2];
+    uint32_t nan;                  // of a lane, not 0: there are NaN values that some rows do not see
 };
 
 // Where a request's keys lie.
@@ -142,101 +152,118 @@ __device__ __forceinline__ Found find(const Place &p, int block, bool any)
     return f;
 }
 
+// A block to a stage: 16 rows of keys, then 16 of values, D bytes each. Whole rows by
+// neighbouring lanes; 16-byte piece c of row r lies at piece c ^ (r % 8) of it (D = 128) or c ^ (r / 2 % 4)
+// (D = 64), so that the lanes that read together, below, meet all banks.
+template <int D>
+__device__ __forceinline__ uint32_t piece_at(int row, int c)
+{
+    return static_cast<uint32_t>(row * D + ((D == 128 ? c ^ (row & 7) : c ^ (row >> 1 & 3)) * 16));
+}
 template <int D>
 __device__ __forceinline__ void copy_block(const Place &p, int64_t block, uint32_t stage, int lane)
 {
-    const int gid = lane / 4, t = lane % 4;
+    constexpr int kPieces = D / 16, kRows = 32 / kPieces;   // pieces of a row, rows at a time
     const bool there = block >= 0;
-    const int64_t first = (there ? block : 0) * kBlock * p.token;
+    const int64_t at = (there ? block : 0) * kBlock * p.token + lane / kPieces * p.token + lane % kPieces * 16;
 #pragma unroll
-    for (int i = 0; i < Ring<D>::kKPieces; ++i) {   // piece i: key gid + 8 (i % 2), 16 of dimensions 64 (i / 2) ..
-        const uint8_t *src = p.k + first + (gid + 8 * (i % 2)) * p.token + 64 * (i / 2) + 16 * t;
-        cp_async_16_zfill(stage + (i * 32 + lane) * 16, src, there);
-    }
-    const uint32_t values = stage + Ring<D>::kKPieces * 512;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {                   // piece i: key 2 t + i % 2 + 8 (i / 2), D / 8 dimensions from gid D / 8 on
-        const uint8_t *src = p.v + first + (2 * t + i % 2 + 8 * (i / 2)) * p.token + gid * (D / 8);
-        if constexpr (D == 128) {
-            cp_async_16_zfill(values + (i * 32 + lane) * 16, src, there);
-        } else {
-            cp_async_8_zfill(values + (i * 32 + lane) * 8, src, there);
-        }
+    for (int i = 0; i < 16 / kRows; ++i) {
+        const uint32_t to = stage + piece_at<D>(lane / kPieces + i * kRows, lane % kPieces);
+        cp_async_16_zfill(to, p.k + at + i * kRows * p.token, there);
+        cp_async_16_zfill(to + 16 * D, p.v + at + i * kRows * p.token, there);
     }
 }
 
-__device__ __forceinline__ bool has_nan(uint32_t codes)
-{
-    return ((codes & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-}
+// The top bit of each byte that is a NaN code.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t codes) { return ((codes & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
 
-// Values that are NaN, in a block that not every row sees whole: 0 x NaN is NaN, so in the
-// product they are cleared, and only the rows that see their keys get the NaN, here.
-template <int D, int NT>
-__device__ __forceinline__ void add_nan(Part<D, NT> &r, uint32_t (&v)[4][D / 32], const int (&seen)[NT][2], int key0, int lane)
-{
-    for (int t = 0; t < 4; ++t) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int key = key0 + 2 * t + i % 2 + 8 * (i / 2);
-#pragma unroll
-            for (int w = 0; w < D / 32; ++w) {
-                const uint32_t word = __shfl_sync(0xffffffffu, v[i][w], (lane & ~3) + t);
-#pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    if ((word >> (8 * b) & 0x7fu) != 0x7fu) continue;
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        if (key < seen[n][0]) r.o[n][2 * w + b / 2][2 * (b % 2)] = NAN;
-                        if (key < seen[n][1]) r.o[n][2 * w + b / 2][2 * (b % 2) + 1] = NAN;
-                    }
-                }
-            }
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-#pragma unroll
-        for (int w = 0; w < D / 32; ++w) {
-            const uint32_t nan = ((v[i][w] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;   // a byte's top bit: it is NaN
-            v[i][w] &= ~((nan >> 7) * 0xffu);
-        }
-    }
-}
-
-// One block of 16 keys into the warp's part. q: columns' rows as the B operand of S^T.
+// S^T of a block of 16 keys. q: columns' rows as the B operand.
 template <int D, int NT, typename Q>
-__device__ __forceinline__ void add_block(Part<D, NT> &r, const Q &q, const float (&c)[NT][2],
-                                          const int (&seen)[NT][2], uint32_t stage, int lane, int key0, int len, float ks,
-                                          float lv, bool masked)
+__device__ __forceinline__ void scores(float (&s)[NT][4], const Q &q, uint32_t stage, int lane)
 {
-    const int gid = lane / 4, t = lane % 4;
-    float s[NT][4];
+    float odd[NT][4] = {};   // two chains of products
 #pragma unroll
     for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) {
-        const uint4 lo = lds128(stage + (2 * i * 32 + lane) * 16), hi = lds128(stage + ((2 * i + 1) * 32 + lane) * 16);
+        // keys gid and gid + 8, 16 dimensions from 16 (D / 64 t + i) on
+        const uint4 lo = lds128(stage + piece_at<D>(lane / 4, D / 64 * (lane % 4) + i)), hi = lds128(stage + piece_at<D>(lane / 4 + 8, D / 64 * (lane % 4) + i));
         const uint32_t low[4] = {lo.x, lo.y, lo.z, lo.w}, high[4] = {hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const uint32_t a0 = e4m3x2_to_f16x2(low[j] & 0xffffu), a2 = e4m3x2_to_f16x2(low[j] >> 16);
-            const uint32_t a1 = e4m3x2_to_f16x2(high[j] & 0xffffu), a3 = e4m3x2_to_f16x2(high[j] >> 16);
+            uint32_t a0, a1, a2, a3;
+            decode4(low[j], a0, a2);
+            decode4(high[j], a1, a3);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 const uint2 b = q.at(n, 4 * i + j);
-                mma_16816(s[n], a0, a1, a2, a3, b.x, b.y);
+                mma_16816(j & 1 ? odd[n] : s[n], a0, a1, a2, a3, b.x, b.y);
             }
         }
     }
-    bool grow = false;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
+        for (int e = 0; e < 4; ++e) s[n][e] += odd[n][e];
+    }
+}
+
+// What S is multiplied by: never 0, which a score of -inf (a key that is not seen) would turn into
+// NaN; the least normal number makes 0 of any finite one.
+__device__ __forceinline__ float factor(float c, float ks) { return fmaxf(c * ks, 1.17549435e-38f); }
+
+// The block's share of the sums, from its S^T. lv: log2 of its values' scale.
+template <int D, int NT>
+__device__ __forceinline__ void add_block(Part<D, NT> &r, float (&s)[NT][4], const float (&c)[NT][2], const int (&seen)[NT][2],
+                                          uint32_t stage, int lane, int key0, int len, int first_seen, float ks, float lv)
+{
+    const int gid = lane / 4, t = lane % 4;
+    const bool zero = lv <= kLeastLog, masked = key0 + kBlock > first_seen || zero;   // some rows do not see all of it, or its values are 0
+    uint32_t v[4][D / 32];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {   // value of key 2 t + i % 2 + 8 (i / 2), dimensions gid D / 8 on
+        const int row = 2 * t + i % 2 + 8 * (i / 2);
+        if constexpr (D == 128) {
+            const uint4 x = lds128(stage + 16 * D + piece_at<D>(row, gid));
+            v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
+        } else {
+            const uint2 x = lds64(stage + 16 * D + piece_at<D>(row, gid / 2) + gid % 2 * 8);
+            v[i][0] = x.x, v[i][1] = x.y;
+        }
+    }
+    if (masked) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (key0 + gid + (e >> 1) * 8 >= seen[n][e & 1]) s[n][e] = -INFINITY;   // (c is positive)
+        }
+        // Values behind the last token are cleared, whatever lies there. Of keys that not every
+        // row sees, NaN is cleared (0 x NaN is NaN), and the rows that see it get it when they are
+        // written.
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int key = key0 + 2 * t + i % 2 + 8 * (i / 2);
+            const uint32_t keep = key < len && !zero ? ~0u : 0u;
+#pragma unroll
+            for (int w = 0; w < D / 32; ++w) {
+                v[i][w] &= keep;
+                const uint32_t nan = key >= first_seen ? nan_bytes(v[i][w]) : 0u;
+                v[i][w] &= ~((nan >> 7) * 0xffu);
+                r.nan |= nan;
+            }
+        }
+    }
+    // u = z + log2 sv - m of the numerator's terms; the denominator's are u - log2 sv
+    float u[NT][4];
+    bool grow = false;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const float ck[2] = {factor(c[n][0], ks), factor(c[n][1], ks)}, off[2] = {lv - r.m[n][0], lv - r.m[n][1]};
+#pragma unroll
         for (int e = 0; e < 4; ++e) {
-            s[n][e] *= c[n][e & 1] * ks;
-            if (masked && key0 + gid + (e >> 1) * 8 >= seen[n][e & 1]) s[n][e] = -INFINITY;
-            grow |= s[n][e] > r.m[n][e & 1] + kSlack || s[n][e] + lv > r.mv[n][e & 1] + kSlack;
+            u[n][e] = fmaf(s[n][e], ck[e & 1], off[e & 1]);
+            grow |= u[n][e] > kSlack;
         }
     }
     if (__any_sync(0xffffffffu, grow)) {
@@ -244,14 +271,15 @@ __device__ __forceinline__ void add_block(Part<D, NT> &r, const Q &q, const floa
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
+                const float ck = factor(c[n][e], ks);
                 float top = fmaxf(s[n][e], s[n][e + 2]);
 #pragma unroll
                 for (int o = 4; o < 32; o *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                const float m = fmaxf(r.m[n][e], top), mv = fmaxf(r.mv[n][e], top + lv);
-                r.l[n][e] *= exp2_fast(r.m[n][e] - m);
-                const float by = exp2_fast(r.mv[n][e] - mv);
+                const float m = fmaxf(r.m[n][e], fmaf(top, ck, lv)), by = exp2_fast(r.m[n][e] - m);
                 r.m[n][e] = m;
-                r.mv[n][e] = mv;
+                r.l[n][e] *= by;
+                u[n][e] = fmaf(s[n][e], ck, lv - m);
+                u[n][e + 2] = fmaf(s[n][e + 2], ck, lv - m);
 #pragma unroll
                 for (int j = 0; j < D / 16; ++j) {
                     r.o[n][j][e] *= by;
@@ -263,49 +291,21 @@ __device__ __forceinline__ void add_block(Part<D, NT> &r, const Q &q, const floa
     uint32_t p[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        float w[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            r.l[n][e & 1] += exp2_fast(s[n][e] - r.m[n][e & 1]);
-            w[e] = exp2_fast(s[n][e] + lv - r.mv[n][e & 1]);
-        }
-        p[n][0] = transpose8x8(half2_bits(w[0], w[1]));
-        p[n][1] = transpose8x8(half2_bits(w[2], w[3]));
-    }
-    const uint32_t values = stage + Ring<D>::kKPieces * 512;
-    uint32_t v[4][D / 32];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if constexpr (D == 128) {
-            const uint4 x = lds128(values + (i * 32 + lane) * 16);
-            v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
-        } else {
-            const uint2 x = lds64(values + (i * 32 + lane) * 8);
-            v[i][0] = x.x, v[i][1] = x.y;
-        }
-        if (masked && key0 + 2 * t + i % 2 + 8 * (i / 2) >= len) {   // behind the last token: whatever lies there
-#pragma unroll
-            for (int w = 0; w < D / 32; ++w) v[i][w] = 0;
-        }
-    }
-    if (masked) {
-        bool nan = false;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-#pragma unroll
-            for (int w = 0; w < D / 32; ++w) nan |= has_nan(v[i][w]);
-        }
-        if (__any_sync(0xffffffffu, nan)) add_nan<D, NT>(r, v, seen, key0, lane);
+        for (int e = 0; e < 4; ++e) r.l[n][e & 1] += exp2_fast(u[n][e] - lv);
+        p[n][0] = transpose8x8(half2_bits(exp2_fast(u[n][0]), exp2_fast(u[n][1])));
+        p[n][1] = transpose8x8(half2_bits(exp2_fast(u[n][2]), exp2_fast(u[n][3])));
     }
 #pragma unroll
     for (int w = 0; w < D / 32; ++w) {
         // dimensions gid D / 8 + 4 w + 0, 1 (tile 2 w) and + 2, 3 (tile 2 w + 1), two keys a register
         const uint32_t lo01 = __byte_perm(v[0][w], v[1][w], 0x5140), lo23 = __byte_perm(v[0][w], v[1][w], 0x7362);
         const uint32_t hi01 = __byte_perm(v[2][w], v[3][w], 0x5140), hi23 = __byte_perm(v[2][w], v[3][w], 0x7362);
-        const uint32_t a0 = e4m3x2_to_f16x2(lo01 & 0xffffu), a1 = e4m3x2_to_f16x2(lo01 >> 16);
-        const uint32_t a2 = e4m3x2_to_f16x2(hi01 & 0xffffu), a3 = e4m3x2_to_f16x2(hi01 >> 16);
-        const uint32_t b0 = e4m3x2_to_f16x2(lo23 & 0xffffu), b1 = e4m3x2_to_f16x2(lo23 >> 16);
-        const uint32_t b2 = e4m3x2_to_f16x2(hi23 & 0xffffu), b3 = e4m3x2_to_f16x2(hi23 >> 16);
+        uint32_t a0, a1, a2, a3, b0, b1, b2, b3;
+        decode4(lo01, a0, a1);
+        decode4(hi01, a2, a3);
+        decode4(lo23, b0, b1);
+        decode4(hi23, b2, b3);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             mma_16816(r.o[n][2 * w], a0, a1, a2, a3, p[n][0], p[n][1]);
@@ -314,8 +314,8 @@ __device__ __forceinline__ void add_block(Part<D, NT> &r, const Q &q, const floa
     }
 }
 
-// A warp's way through the blocks first, first + kWarps, ... (count of them): pages and scales
-// are looked up a batch ahead, copies run kStages - 1 blocks ahead.
+// A warp's way through `count` blocks from `first` on: pages and scales are looked up a batch
+// ahead, copies run kStages - 1 blocks ahead.
 template <int D, int NT>
 struct Walk {
     static constexpr int kStages = Shape<D, NT>::kStages;
@@ -328,112 +328,84 @@ struct Walk {
     __device__ __forceinline__ Found batch(int n) const   // blocks 32 n .. of the warp's
     {
         const int i = n * kBatch + lane;
-        return find(p, first + i * kWarps, i < count);
+        return find(p, first + i, i < count);
     }
     __device__ __forceinline__ Walk(const Place &place, uint32_t ring_at, int lane_, int first_, int count_)
         : p(place), ring(ring_at), lane(lane_), first(first_), count(count_)
     {
         ahead = batch(0);
         if (count > kBatch) next = batch(1);
-#pragma unroll
-        for (int i = 0; i < kStages - 1; ++i) issue();
     }
-    __device__ __forceinline__ void issue()
+    __device__ __forceinline__ void issue(uint32_t stage)
     {
         if (issued < count) {
             if (issued % kBatch == 0 && issued > 0) {
                 ahead = next;
                 if ((issued / kBatch + 1) * kBatch < count) next = batch(issued / kBatch + 1);
             }
-            const int64_t block = __shfl_sync(0xffffffffu, ahead.block, issued % kBatch);
-            copy_block<D>(p, block, ring + (issued % kStages) * Ring<D>::kBytes, lane);
+            copy_block<D>(p, __shfl_sync(0xffffffffu, ahead.block, issued % kBatch), stage, lane);
         }
         ++issued;
         cp_async_commit();
     }
+    // Block j's softmax and values beside block j + 1's scores, whose instructions do not wait for
+    // one another. (One loop, so that its code, which each launch fetches anew, is there once.)
     template <typename Q>
     __device__ __forceinline__ void add(Part<D, NT> &r, const Q &q, const float (&c)[NT][2], const int (&seen)[NT][2])
     {
-        for (int j = 0; j < count; ++j) {
-            cp_async_wait<kStages - 2>();
-            if (j % kBatch == 0) {   // copies are less than a batch ahead
+        constexpr uint32_t kBytes = Ring<D>::kBytes, kEnd = kStages * kBytes;
+        uint32_t to = 0, now = 0;   // stages of the block that is copied next, and of block j
+        float s[NT][4];
+#pragma unroll 1
+        for (int j = 1 - kStages; j < count; ++j) {
+            const uint32_t then = now + kBytes == kEnd || j < 0 ? 0 : now + kBytes;
+            if (j >= -1) cp_async_wait<kStages - 3>();
+            __syncwarp();   // all lanes' copies have landed, and all have read the stage that is copied to next
+            if (j >= 0 && j % kBatch == 0) {   // copies are less than a batch ahead
                 ks32 = ahead.ks;
-                lv32 = log2f(ahead.vs);
+                lv32 = fmaxf(log2f(ahead.vs), kLeastLog);
             }
-            issue();
-            const float ks = __shfl_sync(0xffffffffu, ks32, j % kBatch), lv = __shfl_sync(0xffffffffu, lv32, j % kBatch);
-            const int key0 = (first + j * kWarps) * kBlock;
-            add_block<D, NT>(r, q, c, seen, ring + (j % kStages) * Ring<D>::kBytes, lane, key0, p.len, ks, lv,
-                             key0 + kBlock > p.first_seen);
+            issue(ring + to);
+            to = to + kBytes == kEnd ? 0 : to + kBytes;
+            float next_s[NT][4] = {};
+            if (j >= -1 && j + 1 < count) scores<D, NT>(next_s, q, ring + then, lane);
+            if (j >= 0) {
+                const float ks = __shfl_sync(0xffffffffu, ks32, j % kBatch), lv = __shfl_sync(0xffffffffu, lv32, j % kBatch);
+                add_block<D, NT>(r, s, c, seen, ring + now, lane, (first + j) * kBlock, p.len, p.first_seen, ks, lv);
+                now = then;
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[n][e] = next_s[n][e];
+            }
         }
         cp_async_wait<0>();
     }
 };
 
+// A part outside registers: 8 NT rows of D floats of O, then l, m and whether there are NaN
+// values that not every row sees.
 template <int D, int NT>
-__device__ __forceinline__ void merge(Part<D, NT> &r, const float *other, int lane)
-{
-    int at = 0;
-    auto get = [&]() { return other[32 * at++ + lane]; };
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        float mine[2], theirs[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const float l = get(), m1 = get(), mv1 = get();
-            const float m = fmaxf(r.m[n][e], m1), mv = fmaxf(r.mv[n][e], mv1);
-            r.l[n][e] = r.l[n][e] * exp2_fast(r.m[n][e] - m) + l * exp2_fast(m1 - m);
-            mine[e] = exp2_fast(r.mv[n][e] - mv);
-            theirs[e] = exp2_fast(mv1 - mv);
-            r.m[n][e] = m;
-            r.mv[n][e] = mv;
-        }
-#pragma unroll
-        for (int j = 0; j < D / 16; ++j) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) r.o[n][j][e] = r.o[n][j][e] * mine[e & 1] + get() * theirs[e & 1];
-        }
-    }
-}
+constexpr int slot_floats() { return 8 * NT * (D + 4); }
 
-template <int D, int NT>
-__device__ __forceinline__ void put(const Part<D, NT> &r, float *to, int lane)
-{
-    int at = 0;
-    auto set = [&](float v) { to[32 * at++ + lane] = v; };
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            set(r.l[n][e]);
-            set(r.m[n][e]);
-            set(r.mv[n][e]);
-        }
-#pragma unroll
-        for (int j = 0; j < D / 16; ++j) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) set(r.o[n][j][e]);
-        }
-    }
-}
-
-template <int D, int NT>
-constexpr int part_floats() { return 32 * NT * (6 + D / 4); }
-
-// The work is cut into units, a block of an item each, an item being a request, a key head and a group of
-// 8 NT query rows, in that order. A CTA takes a run of units; a run's piece of an item that
-// is not all of it leaves a part in the workspace.
+// The work is cut into units: a block of an item, an item being a request, a group of up to 8
+// key heads and a group of 8 NT query rows, in that order. A CTA takes a run of units, its
+// warps a key head each, so that the rows of a block, which lie side by side for all heads,
+// are read together (reads alone: 7.0 TB/s; one head at a time by all warps of a CTA 6.2). All runs
+// are of equal length, whatever the requests' lengths. What a run has of an item that is not
+// all of it is a part, which paged_join_kernel joins with the others'.
 struct Cut {
-    int b, item;          // item of the request: key head * groups + group
+    int b, item;          // item of the request: head group * row groups + row group
     int64_t at;           // units before it in its item (blocks)
     int64_t left;         // units of the run
     int64_t from, units;  // where the run starts; all units
 };
 
-// Where run c of `ctas` starts: shares of equal length, the first ones longer by one.
-__device__ __forceinline__ int64_t start_of(int64_t units, int c, int ctas)
+// a / b of numbers that are not negative: most fit 32 bits, where it takes a tenth of the time.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)
 {
-    return units / ctas * c + min(static_cast<int64_t>(c), units % ctas);
+    return (a | b) >> 32 ? a / b : static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));
 }
 
 __device__ __forceinline__ int blocks_of(const PagedArgs &g, int b)
@@ -451,7 +423,6 @@ __device__ __forceinline__ int64_t scan_before(int64_t v, int64_t *sums, int64_t
         const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
         if (lane >= o) upto += x;
     }
-    __syncthreads();
     if (lane == 31) sums[warp] = upto;
     __syncthreads();
     int64_t before = upto - v;
@@ -460,21 +431,26 @@ __device__ __forceinline__ int64_t scan_before(int64_t v, int64_t *sums, int64_t
         if (i < warp) before += sums[i];
         all += sums[i];
     }
+    __syncthreads();
     return before;
 }
 
-// The c-th run. items: of a request.
-__device__ __forceinline__ Cut cut_of(const PagedArgs &g, int c, int ctas, int items, int64_t *sums, Cut *shared)
+// The c-th run. items: of a request. starts: where not null, gets the units (of one item) before
+// each request, and of all.
+__device__ __forceinline__ Cut cut_of(const PagedArgs &g, int c, int ctas, int items, int64_t *sums, Cut *shared, int64_t *starts)
 {
     const int tid = threadIdx.x, step = static_cast<int>(blockDim.x);
     int64_t total = 0, all, mine = 0, before = 0;
     for (int b0 = 0; b0 < g.B; b0 += step) {
         mine = b0 + tid < g.B ? blocks_of(g, b0 + tid) : 0;
         before = scan_before(mine, sums, all);
+        if (starts && b0 + tid < g.B) starts[b0 + tid] = total + before;
         total += all;
     }
-    const int64_t units = total * items, from = start_of(units, c, ctas), to = start_of(units, c + 1, ctas);
-    if (tid == 0) *shared = Cut{0, 0, 0, 0, from, units};
+    if (starts && tid == 0) starts[g.B] = total;
+    const int64_t units = total * items, q = quotient(units, ctas), rest = units - q * ctas;
+    const int64_t from = q * c + min(static_cast<int64_t>(c), rest), to = from + q + (c < rest ? 1 : 0);
+    if (tid == 0 && from == to) *shared = Cut{0, 0, 0, 0, from, units};   // an empty run; else one thread finds its start
     if (g.B > step) total = 0;
     for (int b0 = 0; b0 < g.B; b0 += step) {
         int64_t base = 0;
@@ -483,53 +459,55 @@ __device__ __forceinline__ Cut cut_of(const PagedArgs &g, int c, int ctas, int i
             before = scan_before(mine, sums, all);
             base = total;
             total += all;
-        } else {
-            __syncthreads();
         }
         const int64_t start = (base + before) * items;
         if (start <= from && from < start + mine * items && from < to)
-            *shared = Cut{b0 + tid, static_cast<int>((from - start) / mine), (from - start) % mine, to - from, from, units};
+{
+            const int64_t item = quotient(from - start, mine);
+            *shared = Cut{b0 + tid, static_cast<int>(item), from - start - item * mine, to - from, from, units};
+        }
     }
     __syncthreads();
     return *shared;
 }
 
+// q's operands of a warp: in registers, or, where they are too many, in its shared memory
+// behind the ring, each lane its own.
 template <int D, int NT>
-struct Staged {                                // in shared memory, behind the rings
-    uint2 q[NT][D / 16][32];                   // B operands of S^T
-    float back[8 * NT];                        // what q's rows were divided by
-    int64_t sums[kWarps];
-    Cut cut;
-};
-
-template <int NT, int D>
-struct QRegs {
-    uint2 v[NT][D / 16];
-    __device__ __forceinline__ uint2 at(int n, int k) const { return v[n][k]; }
-};
-struct QShared {
+struct Queries {
     uint32_t base;   // of this lane
-    int ks;
-    __device__ __forceinline__ uint2 at(int n, int k) const { return lds64(base + (n * ks + k) * 256); }
+    __device__ __forceinline__ uint2 at(int n, int k) const { return lds64(base + (n * (D / 16) + k) * 256); }
+    __device__ __forceinline__ void set(int n, int k, uint2 v) { asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(base + (n * (D / 16) + k) * 256), "r"(v.x), "r"(v.y) : "memory"); }
+};
+template <int D>
+struct Queries<D, 1> {
+    uint32_t base;
+    uint2 v[D / 16];
+    __device__ __forceinline__ uint2 at(int, int k) const { return v[k]; }
+    __device__ __forceinline__ void set(int, int k, uint2 x) { v[k] = x; }
 };
 
-// Row tile n of the item's q, as B operands: lane (gid, t) has row gid.
-template <int D, int NT>
-__device__ __forceinline__ void stage_q(const PagedArgs &g, Staged<D, NT> &s, int n, const uint16_t *q, bool live, int lane)
+// Row tile n of the item's q, as B operands: lane (gid, t) has row gid, D / 4 elements from t D / 4 on.
+template <int D>
+__device__ __forceinline__ void fetch_q(uint32_t (&words)[D / 8], const uint16_t *q, bool live, int t)
 {
-    const int gid = lane / 4, t = lane % 4;
-    uint32_t words[D / 8];
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) {
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
             uint4 x = make_uint4(0, 0, 0, 0);
-            if (live) x = *(reinterpret_cast<const uint4 *>(q + 64 * i + 16 * t) + w);
+            if (live) x = *(reinterpret_cast<const uint4 *>(q + D / 4 * t + 16 * i) + w);
             words[8 * i + 4 * w] = x.x, words[8 * i + 4 * w + 1] = x.y, words[8 * i + 4 * w + 2] = x.z, words[8 * i + 4 * w + 3] = x.w;
         }
     }
+}
+
+// As binary16. Returns what the row was divided by.
+template <int D, int NT>
+__device__ __forceinline__ float set_q(Queries<D, NT> &s, int n, uint32_t (&words)[D / 8], int type)
+{
     float back = 1.0f;
-    if (g.type == QMV_BF16) {
+    if (type == QMV_BF16) {
         uint32_t largest = 0;   // of the finite elements, as the upper half of an fp32's bits
 #pragma unroll
         for (int w = 0; w < D / 8; ++w) {
@@ -546,109 +524,136 @@ __device__ __forceinline__ void stage_q(const PagedArgs &g, Staged<D, NT> &s, in
             words[w] = half2_bits(__uint_as_float(words[w] << 16) * by, __uint_as_float(words[w] & 0xffff0000u) * by);
     }
 #pragma unroll
-    for (int k = 0; k < D / 16; ++k) s.q[n][k][lane] = make_uint2(words[2 * k], words[2 * k + 1]);
-    if (t == 0) s.back[8 * n + gid] = back;
+    for (int k = 0; k < D / 16; ++k) s.set(n, k, make_uint2(words[2 * k], words[2 * k + 1]));
+    return back;
 }
 
-// A part in the workspace: 8 NT rows of D floats, then of (l, m, m', 0).
-template <int D, int NT>
-constexpr int slot_floats() { return 8 * NT * (D + 4); }
+// Four outputs of a row whose request has NaN among the values of keys that earlier rows do not
+// see: NaN where the row sees one.
+__device__ __noinline__ float4 with_nan(const PagedArgs &g, int b, int h, int len, int token, int d, int D, float4 o)
+{
+    const int per_page = 31 - __clz(g.page);
+    for (int key = max(0, len - g.T + 1); key < len - g.T + 1 + token; ++key) {
+        const int page = g.table[static_cast<int64_t>(b) * g.table_pages + (key >> per_page)];
+        if (page < 0 || page >= g.n_pages) continue;
+        const int64_t place = (static_cast<int64_t>(page) << per_page) + (key & (g.page - 1));
+        const uint32_t nan = nan_bytes(*reinterpret_cast<const uint32_t *>(static_cast<const uint8_t *>(g.v) + (place * g.Hkv + h) * D + d));
+        o = make_float4(nan & 0x80u ? NAN : o.x, nan & 0x8000u ? NAN : o.y, nan & 0x800000u ? NAN : o.z, nan & 0x80000000u ? NAN : o.w);
+    }
+    return o;
+}
 
-// direct: CTA i has item i % items of request i / items, whole. Otherwise: the i-th run.
+// What a thread joins of a row's parts: four dimensions, and the statistics. First the maxima
+// of all parts, then the sums.
+struct Joined {
+    float l = 0.0f, m = kLowest, nan = 0.0f;
+    float4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+    __device__ __forceinline__ void top(float4 st)
+    {
+        m = fmaxf(m, st.y);
+        nan = fmaxf(nan, st.z);
+    }
+    __device__ __forceinline__ void add(float4 st, float4 x)
+    {
+        const float by = exp2_fast(st.y - m);
+        l += st.x * by;
+        o = make_float4(o.x + x.x * by, o.y + x.y * by, o.z + x.z * by, o.w + x.w * by);
+    }
+    // The output of row `row` of the request's key head, from dimension d on.
+    __device__ __forceinline__ void write(const PagedArgs &g, int b, int h, int len, int row, int G, int d, int D)
+    {
+        const bool none = len - g.T + 1 + row / G <= 0;
+        const float by = 1.0f / l;
+        float4 y = none ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : make_float4(o.x * by, o.y * by, o.z * by, o.w * by);
+        if (nan != 0.0f && !none) y = with_nan(g, b, h, len, row / G, d, D, y);
+        const int64_t at = (static_cast<int64_t>(b) * g.T + row / G) * g.Hq + static_cast<int64_t>(h) * G + row % G;
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(g.out) + at * D + d) =
+            g.type == QMV_F16 ? make_uint2(pack2<__half>(y.x, y.y), pack2<__half>(y.z, y.w)) : make_uint2(pack2<__nv_bfloat16>(y.x, y.y), pack2<__nv_bfloat16>(y.z, y.w));
+    }
+};
+
+// The workspace: two slots for each warp of a run, [run][first or last][warp]; then the units
+// before each request, and of all.
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas) paged_kernel(const __grid_constant__ PagedArgs g, int groups, bool direct)
+__device__ __forceinline__ float *slot_of(const PagedArgs &g, int run, bool first, int warps, int warp)
+{
+    return static_cast<float *>(g.workspace) + ((2 * static_cast<int64_t>(run) + (first ? 0 : 1)) * warps + warp) * slot_floats<D, NT>();
+}
+template <int D, int NT>
+__device__ __forceinline__ int64_t *starts_of(const PagedArgs &g)
+{
+    return reinterpret_cast<int64_t *>(static_cast<float *>(g.workspace) + 2ll * Shape<D, NT>::kMostWarpsOfRuns * slot_floats<D, NT>());
+}
+
+// A run a CTA. row_groups: groups of 8 NT query rows.
+template <int D, int NT>
+__global__ void __launch_bounds__(32 * kMostWarps, Shape<D, NT>::kWarpsSm / kMostWarps) paged_kernel(const __grid_constant__ PagedArgs g, int row_groups)
 {
     extern __shared__ __align__(128) uint8_t smem[];
-    constexpr int kRings = kWarps * Shape<D, NT>::kStages * Ring<D>::kBytes;
-    Staged<D, NT> &staged = *reinterpret_cast<Staged<D, NT> *>(smem + kRings);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, gid = lane / 4, t = lane % 4;
-    const int G = g.Hq / g.Hkv, rows = g.T * G, items = g.Hkv * groups;
+    __shared__ int64_t sums[kMostWarps];
+    __shared__ Cut shared_cut;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, warps = blockDim.x / 32, gid = lane / 4, t = lane % 4;
+    const int G = g.Hq / g.Hkv, rows = g.T * G, items = (g.Hkv + warps - 1) / warps * row_groups;
+    const uint32_t my_ring = smem_addr(smem) + warp * Shape<D, NT>::kOwn;
     grid_launch_dependents();
     grid_dependency_wait();
-    Cut cut;
-    if (direct) {
-        cut.b = static_cast<int>(blockIdx.x) / items;
-        cut.item = static_cast<int>(blockIdx.x) % items;
-        cut.at = 0;
-        cut.left = 1;
-    } else {
-        cut = cut_of(g, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), items, staged.sums, &staged.cut);
-        // rows of requests without keys are no units
-        for (int b = static_cast<int>(blockIdx.x); b < g.B; b += static_cast<int>(gridDim.x)) {
-            if (g.lens[b] > g.max_len && threadIdx.x == 0) atomicOr(&g_paged_error, kErrIndex);
-            if (blocks_of(g, b) > 0) continue;
-            uint4 *out = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(g.out) + static_cast<int64_t>(b) * g.T * g.Hq * D);
-            for (int64_t i = threadIdx.x; i < static_cast<int64_t>(g.T) * g.Hq * D / 8; i += kThreads) out[i] = make_uint4(0, 0, 0, 0);
-        }
+    Cut cut = cut_of(g, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), items, sums, &shared_cut,
+                     blockIdx.x == 0 ? starts_of<D, NT>(g) : nullptr);
+    // rows of requests without keys are no units
+    for (int i = static_cast<int>(blockIdx.x); i < g.B; i += static_cast<int>(gridDim.x)) {
+        if (g.lens[i] > g.max_len && threadIdx.x == 0) atomicOr(&g_paged_error, kErrIndex);
+        if (blocks_of(g, i) > 0) continue;
+        uint4 *out = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(g.out) + static_cast<int64_t>(i) * g.T * g.Hq * D);
+        for (int64_t j = threadIdx.x; j < static_cast<int64_t>(g.T) * g.Hq * D / 8; j += blockDim.x) out[j] = make_uint4(0, 0, 0, 0);
     }
-    bool first_piece = true;
-    while (cut.left > 0) {
-        const int b = cut.b, h = cut.item / groups, row0 = cut.item % groups * 8 * NT;
-        if (direct && g.lens[b] > g.max_len && threadIdx.x == 0) atomicOr(&g_paged_error, kErrIndex);
+    Part<D, NT> part{};
+    Queries<D, NT> q;
+    q.base = my_ring + Shape<D, NT>::kStages * Ring<D>::kBytes + lane * 8;
+    for (bool first = true; cut.left > 0; first = false) {
+        const int b = cut.b, h = cut.item / row_groups * warps + warp, row0 = cut.item % row_groups * 8 * NT;
         const int len = static_cast<int>(min(static_cast<int64_t>(max(g.lens[b], 0)), g.max_len));
-        const int blocks = (len + kBlock - 1) / kBlock;
-        const int block0 = static_cast<int>(cut.at);
-        const int block1 = direct ? blocks : static_cast<int>(min(static_cast<int64_t>(blocks), cut.at + cut.left));
-        Place p;
-        p.token = static_cast<int64_t>(g.Hkv) * D;
-        p.k = static_cast<const uint8_t *>(g.k) + h * D;
-        p.v = static_cast<const uint8_t *>(g.v) + h * D;
-        p.ks = g.ks + h;
-        p.vs = g.vs + h;
-        p.table = g.table + static_cast<int64_t>(b) * g.table_pages;
-        p.pages = g.n_pages;
-        p.page_shift = 31 - __clz(g.page);
-        p.Hkv = g.Hkv;
-        p.len = len;
-        p.first_seen = len - g.T + 1;
-        const int first = block0 + warp;
-        Walk<D, NT> walk(p, smem_addr(smem) + warp * Shape<D, NT>::kStages * Ring<D>::kBytes, lane, first,
-                         first < block1 ? (block1 - first + kWarps - 1) / kWarps : 0);
-        auto row_at = [&](int r) { return ((static_cast<int64_t>(b) * g.T + r / G) * g.Hq + static_cast<int64_t>(h) * G + r % G) * D; };
-        for (int n = warp; n < NT; n += kWarps) {
-            const int row = row0 + 8 * n + gid;
-            stage_q<D, NT>(g, staged, n, static_cast<const uint16_t *>(g.q) + (row < rows ? row_at(row) : 0), row < rows, lane);
-        }
-        __syncthreads();
-        float c[NT][2];
-        int seen[NT][2];
+        const int blocks = (len + kBlock - 1) / kBlock, at = static_cast<int>(cut.at);
+        const int count = static_cast<int>(min(static_cast<int64_t>(blocks - at), cut.left));
+        if (h < g.Hkv) {
+            Place p;
+            p.token = static_cast<int64_t>(g.Hkv) * D;
+            p.k = static_cast<const uint8_t *>(g.k) + h * D;
+            p.v = static_cast<const uint8_t *>(g.v) + h * D;
+            p.ks = g.ks + h;
+            p.vs = g.vs + h;
+            p.table = g.table + static_cast<int64_t>(b) * g.table_pages;
+            p.pages = g.n_pages;
+            p.page_shift = 31 - __clz(g.page);
+            p.Hkv = g.Hkv;
+            p.len = len;
+            p.first_seen = len - g.T + 1;
+            auto row_at = [&](int r) { return ((static_cast<int64_t>(b) * g.T + r / G) * g.Hq + static_cast<int64_t>(h) * G + r % G) * D; };
+            uint32_t words[D / 8];   // the first row tile's, on their way while the pages are looked up
+            fetch_q<D>(words, static_cast<const uint16_t *>(g.q) + (row0 + gid < rows ? row_at(row0 + gid) : 0), row0 + gid < rows, t);
+            Walk<D, NT> walk(p, my_ring, lane, at, count);
+            float c[NT][2];
+            int seen[NT][2];
+            part.nan = 0;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
+            for (int n = 0; n < NT; ++n) {
+                const float back = set_q<D, NT>(q, n, words, g.type);
+                const int next = row0 + 8 * (n + 1) + gid;
+                if (n + 1 < NT) fetch_q<D>(words, static_cast<const uint16_t *>(g.q) + (next < rows ? row_at(next) : 0), next < rows, t);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int r = row0 + 8 * n + 2 * t + e;
-                c[n][e] = g.scale * kLog2e * staged.back[8 * n + 2 * t + e];
-                seen[n][e] = r < rows ? p.first_seen + r / G : 0;
+                for (int e = 0; e < 2; ++e) {
+                    const int r = row0 + 8 * n + 2 * t + e;
+                    c[n][e] = g.scale * kLog2e * __shfl_sync(0xffffffffu, back, (2 * t + e) * 4);
+                    seen[n][e] = r < rows ? p.first_seen + r / G : 0;
+                    part.l[n][e] = 0.0f;
+                    part.m[n][e] = kLowest;
+                }
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j) part.o[n][j][0] = part.o[n][j][1] = part.o[n][j][2] = part.o[n][j][3] = 0.0f;
             }
-        }
-        Part<D, NT> part;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) part.l[n][e] = 0.0f, part.m[n][e] = part.mv[n][e] = kLowest;
-#pragma unroll
-            for (int j = 0; j < D / 16; ++j) part.o[n][j][0] = part.o[n][j][1] = part.o[n][j][2] = part.o[n][j][3] = 0.0f;
-        }
-        if constexpr (NT == 1) {
-            QRegs<NT, D> q;
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) q.v[0][k] = staged.q[0][k][lane];
             walk.add(part, q, c, seen);
-        } else {
-            walk.add(part, QShared{smem_addr(&staged.q[0][0][lane]), D / 16}, c, seen);
-        }
-        // the warps' parts, half of them into the other half at a time, over the rings
-        float *parts = reinterpret_cast<float *>(smem);
-#pragma unroll
-        for (int half = kWarps / 2; half > 0; half /= 2) {
-            __syncthreads();
-            if (warp >= half && warp < 2 * half) put(part, parts + (warp - half) * part_floats<D, NT>(), lane);
-            __syncthreads();
-            if (warp < half) merge(part, parts + warp * part_floats<D, NT>(), lane);
-        }
-        const bool whole = block0 == 0 && block1 == blocks;
-        if (warp == 0) {
-            float *slot = static_cast<float *>(g.workspace) + (2 * static_cast<int64_t>(blockIdx.x) + (first_piece ? 0 : 1)) * slot_floats<D, NT>();
+            // the output, or a part
+            const bool whole = count == blocks, nan = __any_sync(0xffffffffu, part.nan != 0);
+            float *slot = slot_of<D, NT>(g, static_cast<int>(blockIdx.x), first, warps, warp);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -656,137 +661,124 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas) paged_kernel(co
                     float l = part.l[n][e];
 #pragma unroll
                     for (int o = 4; o < 32; o *= 2) l += __shfl_xor_sync(0xffffffffu, l, o);
-                    const int row = row0 + 8 * n + 2 * t + e;
+                    const int r = 8 * n + 2 * t + e, row = row0 + r;
                     if (row >= rows) continue;
-                    if (!whole) {
-                        float4 *to = reinterpret_cast<float4 *>(slot + (8 * n + 2 * t + e) * D + gid * (D / 8));
+                    float by = 1.0f;
+                    if (whole) by = 1.0f / l;
+                    float4 y[D / 32];
 #pragma unroll
-                        for (int j = 0; j < D / 32; ++j)
-                            to[j] = make_float4(part.o[n][2 * j][e], part.o[n][2 * j][e + 2], part.o[n][2 * j + 1][e], part.o[n][2 * j + 1][e + 2]);
-                        if (gid == 0)
-                            reinterpret_cast<float4 *>(slot + 8 * NT * D)[8 * n + 2 * t + e] = make_float4(l, part.m[n][e], part.mv[n][e], 0.0f);
+                    for (int j = 0; j < D / 32; ++j)
+                        y[j] = make_float4(part.o[n][2 * j][e] * by, part.o[n][2 * j][e + 2] * by, part.o[n][2 * j + 1][e] * by,
+                                           part.o[n][2 * j + 1][e + 2] * by);
+                    if (!whole) {
+#pragma unroll
+                        for (int j = 0; j < D / 32; ++j) reinterpret_cast<float4 *>(slot + r * (D + 4) + gid * (D / 8))[j] = y[j];
+                        if (gid == 0) *reinterpret_cast<float4 *>(slot + r * (D + 4) + D) = make_float4(l, part.m[n][e], nan ? 1.0f : 0.0f, 0.0f);
                         continue;
                     }
-                    const float by = exp2f(part.mv[n][e] - part.m[n][e]) / l;
-                    const bool none = seen[n][e] <= 0;
-                    uint16_t *out = static_cast<uint16_t *>(g.out) + row_at(row) + gid * (D / 8);
-                    uint32_t words[D / 16];
 #pragma unroll
-                    for (int j = 0; j < D / 16; ++j) {
-                        const float a = none ? 0.0f : part.o[n][j][e] * by, z = none ? 0.0f : part.o[n][j][e + 2] * by;
-                        words[j] = g.type == QMV_F16 ? pack2<__half>(a, z) : pack2<__nv_bfloat16>(a, z);
+                    for (int j = 0; j < D / 32; ++j) {
+                        if (seen[n][e] <= 0) y[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        if (nan && seen[n][e] > 0) y[j] = with_nan(g, b, h, len, row / G, gid * (D / 8) + 4 * j, D, y[j]);
+                        reinterpret_cast<uint2 *>(static_cast<uint16_t *>(g.out) + row_at(row) + gid * (D / 8))[j] =
+                            g.type == QMV_F16 ? make_uint2(pack2<__half>(y[j].x, y[j].y), pack2<__half>(y[j].z, y[j].w))
+                                              : make_uint2(pack2<__nv_bfloat16>(y[j].x, y[j].y), pack2<__nv_bfloat16>(y[j].z, y[j].w));
                     }
-#pragma unroll
-                    for (int j = 0; j < D / 64; ++j)
-                        reinterpret_cast<uint4 *>(out)[j] = make_uint4(words[4 * j], words[4 * j + 1], words[4 * j + 2], words[4 * j + 3]);
                 }
             }
         }
-        if (direct) return;
-        first_piece = false;
-        cut.left -= block1 - block0;
+        cut.left -= count;
         cut.at = 0;
-        if (++cut.item == items) {
+        if (++cut.item == items && cut.left > 0) {
             cut.item = 0;
             do {
                 ++cut.b;
-            } while (cut.left > 0 && cut.b < g.B && blocks_of(g, cut.b) == 0);
+            } while (blocks_of(g, cut.b) == 0);   // ends: there are units left
         }
-        if (cut.left > 0) __syncthreads();   // the parts have been read
     }
 }
 
-// The rows of items of which more than one run has a part. Grid (runs - 1, rows): CTA (i, r) has
-// row r of the item that the cut between runs i and i + 1 goes through, unless an earlier cut
-// goes through it too.
+// The items of which runs have parts. Grid (B * Hkv * row_groups, rows / rows of a CTA): `share`
+// warps a row, each every share-th part.
 template <int D, int NT>
-__global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__ PagedArgs g, int groups, int ctas)
+__global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ PagedArgs g, int row_groups, int warps, int ctas, int share)
 {
-    constexpr int kWarpsJoin = 4, kD4 = D / 4;
-    __shared__ int64_t sums[kWarpsJoin];
-    __shared__ Cut found;
-    __shared__ float4 sum_o[kWarpsJoin][kD4];
-    __shared__ float sum_l[kWarpsJoin], sum_m[kWarpsJoin], sum_mv[kWarpsJoin];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, c = static_cast<int>(blockIdx.x) + 1, r = blockIdx.y;
-    const int G = g.Hq / g.Hkv, rows = g.T * G, items = g.Hkv * groups;
+    constexpr int kD4 = D / 4;
+    __shared__ float4 sum_o[8][kD4], sum_l[8];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, G = g.Hq / g.Hkv, rows = g.T * G;
+    const int row_group = static_cast<int>(blockIdx.x) % row_groups, of_b = static_cast<int>(blockIdx.x) / row_groups;
+    const int h = of_b % g.Hkv, b = of_b / g.Hkv, item = h / warps * row_groups + row_group;
+    const int items = (g.Hkv + warps - 1) / warps * row_groups;
     grid_launch_dependents();
     grid_dependency_wait();   // in every CTA: this launch ends after the one before it
-    const Cut cut = cut_of(g, c, ctas, items, sums, &found);
-    if (cut.left == 0 || cut.at == 0) return;
-    const int row = cut.item % groups * 8 * NT + r, h = cut.item / groups;
-    const int64_t item0 = cut.from - cut.at, item1 = item0 + blocks_of(g, cut.b), last = start_of(cut.units, c - 1, ctas);
-    if (row >= rows || last > item0) return;
-    // piece 0: of run c - 1, its first if it starts with the item; piece i: the first of run c - 1 + i
-    float l = 0.0f, m = kLowest, mv = kLowest;
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    auto take = [&](float l1, float m1, float mv1, float4 x) {
-        const float mn = fmaxf(m, m1), mvn = fmaxf(mv, mv1), a = exp2_fast(mv - mvn), z = exp2_fast(mv1 - mvn);
-        l = l * exp2_fast(m - mn) + l1 * exp2_fast(m1 - mn);
-        o = make_float4(o.x * a + x.x * z, o.y * a + x.y * z, o.z * a + x.z * z, o.w * a + x.w * z);
-        m = mn;
-        mv = mvn;
+    const int64_t *starts = starts_of<D, NT>(g);
+    const int64_t before = starts[b], blocks = starts[b + 1] - before, units = starts[g.B] * items;
+    if (blocks == 0) return;
+    const int64_t item0 = before * items + blocks * item, item1 = item0 + blocks;
+    // the runs that have units of the item
+    const int64_t q = quotient(units, ctas), long_ones = units - q * ctas;
+    auto run_of = [&](int64_t unit) {
+        return static_cast<int>(unit < long_ones * (q + 1) ? quotient(unit, q + 1) : long_ones + quotient(unit - long_ones * (q + 1), q));
     };
+    const int run0 = run_of(item0), parts = run_of(item1 - 1) - run0 + 1;
+    if (parts == 1) return;   // one run has all of it
+    const int r = (static_cast<int>(blockIdx.y) * 8 + warp) / share, row = row_group * 8 * NT + r, mine = warp % share;
+    const bool live = r < 8 * NT && row < rows;
+    const bool at_start = q * run0 + min(static_cast<int64_t>(run0), long_ones) == item0;   // the first run starts with the item
+    Joined x;
+    if (live) {
+        auto row_of = [&](int i) { return slot_of<D, NT>(g, run0 + i, i > 0 || at_start, warps, h % warps) + r * (D + 4); };
 #pragma unroll 4
-    for (int i = warp; c - 1 + i < ctas; i += kWarpsJoin) {
-        const int run = c - 1 + i;
-        if (i > 0 && start_of(cut.units, run, ctas) >= item1) break;
-        if (i > 0 && start_of(cut.units, run + 1, ctas) == start_of(cut.units, run, ctas)) continue;   // an empty run
-        const float *slot = static_cast<const float *>(g.workspace) + (2 * static_cast<int64_t>(run) + (i == 0 && last < item0 ? 1 : 0)) * slot_floats<D, NT>();
-        const float4 st = reinterpret_cast<const float4 *>(slot + 8 * NT * D)[r];
-        const float4 x = lane < kD4 ? reinterpret_cast<const float4 *>(slot + r * D)[lane] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        take(st.x, st.y, st.z, x);
+        for (int i = mine; i < parts; i += share) x.top(*reinterpret_cast<const float4 *>(row_of(i) + D));
+#pragma unroll 4
+        for (int i = mine; i < parts; i += share)
+            x.add(*reinterpret_cast<const float4 *>(row_of(i) + D), lane < kD4 ? reinterpret_cast<const float4 *>(row_of(i))[lane] : x.o);
+        if (lane < kD4) sum_o[warp][lane] = x.o;
+        if (lane == 0) sum_l[warp] = make_float4(x.l, x.m, x.nan, 0.0f);
     }
-    if (lane < kD4) sum_o[warp][lane] = o;
-    if (lane == 0) sum_l[warp] = l, sum_m[warp] = m, sum_mv[warp] = mv;
     __syncthreads();
-    if (warp > 0 || lane >= kD4) return;
-#pragma unroll
-    for (int w = 1; w < kWarpsJoin; ++w) take(sum_l[w], sum_m[w], sum_mv[w], sum_o[w][lane]);
-    const int seen = static_cast<int>(min(static_cast<int64_t>(g.lens[cut.b]), g.max_len)) - g.T + 1 + row / G;
-    const float by = seen <= 0 ? 0.0f : exp2f(mv - m) / l;
-    if (seen <= 0) o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    o = make_float4(o.x * by, o.y * by, o.z * by, o.w * by);
-    uint16_t *out = static_cast<uint16_t *>(g.out) + ((static_cast<int64_t>(cut.b) * g.T + row / G) * g.Hq + static_cast<int64_t>(h) * G + row % G) * D;
-    reinterpret_cast<uint2 *>(out)[lane] = g.type == QMV_F16 ? make_uint2(pack2<__half>(o.x, o.y), pack2<__half>(o.z, o.w))
-                                                             : make_uint2(pack2<__nv_bfloat16>(o.x, o.y), pack2<__nv_bfloat16>(o.z, o.w));
+    if (!live || mine > 0 || lane >= kD4) return;
+    Joined all;
+    for (int w = 0; w < share; ++w) all.top(sum_l[warp + w]);
+    for (int w = 0; w < share; ++w) all.add(sum_l[warp + w], sum_o[warp + w][lane]);
+    all.write(g, b, h, static_cast<int>(min(static_cast<int64_t>(g.lens[b]), g.max_len)), row, G, 4 * lane, D);
 }
 
-constexpr int kSms = 152;
-constexpr int kDirectBlocks = 64;   // of a request, up to which an item is one CTA's
-
 template <int D, int NT>
-cudaError_t launch_typed(const PagedArgs &g, int groups, cudaStream_t s)
+cudaError_t launch_typed(const PagedArgs &g, int row_groups, cudaStream_t s)
 {
     using S = Shape<D, NT>;
-    const int64_t items = static_cast<int64_t>(g.Hkv) * groups, blocks = (g.max_len + kBlock - 1) / kBlock;
-    constexpr int kSmem = kWarps * S::kStages * Ring<D>::kBytes + static_cast<int>(sizeof(Staged<D, NT>));
-    static_assert(kWarps / 2 * part_floats<D, NT>() * 4 <= kWarps * S::kStages * Ring<D>::kBytes, "the parts fit the rings");
-    static_assert(2 * kSms * S::kCtas * slot_floats<D, NT>() * 4 <= kWorkspaceBytes, "the workspace has every run's parts");
-    const bool direct = blocks <= kDirectBlocks && items * g.B <= 0x7fffffff;
-    const int64_t most = kSms * S::kCtas;
-    const int ctas = static_cast<int>(direct ? items * g.B : std::max<int64_t>(1, std::min(most, items * g.B * blocks / kWarps)));
-    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(paged_kernel<D, NT>), kSmem);
+    static_assert(S::kWarpsSm * S::kOwn <= 224 * 1024, "the warps' memory fits an SM");
+    static_assert(2ll * S::kMostWarpsOfRuns * slot_floats<D, NT>() * 4 <= (NT == 1 ? kFewBytes : kMostBytes), "the workspace has every run's parts");
+    const int head_groups = (g.Hkv + kMostWarps - 1) / kMostWarps, warps = (g.Hkv + head_groups - 1) / head_groups;
+    const int64_t items = static_cast<int64_t>(head_groups) * row_groups, blocks = (g.max_len + kBlock - 1) / kBlock;
+    const int ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kSms * (S::kWarpsSm / warps), items * g.B * blocks / kLeastBlocks)));
+    const int smem = warps * S::kOwn;
+    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(paged_kernel<D, NT>), smem);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(static_cast<unsigned>(32 * warps));
     cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-    cfg.dynamicSmemBytes = kSmem;
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = set_launch_overlap_attr(attr);
-    e = cudaLaunchKernelEx(&cfg, paged_kernel<D, NT>, g, groups, direct);
-    if (e != cudaSuccess || direct || ctas == 1) return e;
+    e = cudaLaunchKernelEx(&cfg, paged_kernel<D, NT>, g, row_groups);
+    if (e != cudaSuccess || ctas == 1) return e;
     // the join starts while the runs still go on, and waits for their end on the device
+    const int rows = std::min(8 * NT, g.T * (g.Hq / g.Hkv));
+    int share = 1;
+    while (share < 8 && share * 4 * g.B * items < ctas) share *= 2;   // about four parts a warp
     cudaLaunchConfig_t join = {};
-    join.blockDim = dim3(128);
-    join.gridDim = dim3(static_cast<unsigned>(ctas - 1), static_cast<unsigned>(std::min(8 * NT, g.T * (g.Hq / g.Hkv))));
+    join.blockDim = dim3(256);
+    join.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(g.B) * g.Hkv * row_groups), static_cast<unsigned>((rows * share + 7) / 8));
     join.stream = s;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     join.attrs = attr;
     join.numAttrs = 1;
-    return cudaLaunchKernelEx(&join, paged_join_kernel<D, NT>, g, groups, ctas);
+    return cudaLaunchKernelEx(&join, paged_join_kernel<D, NT>, g, row_groups, warps, ctas, share);
 }
 
 // Groups of up to 8 NT rows, all of nearly the same number.
@@ -805,7 +797,11 @@ cudaError_t launch_rows(const PagedArgs &g, cudaStream_t s)
 
 }  // namespace
 
-int64_t paged_workspace_bytes() { return kWorkspaceBytes; }
+// By the query rows of a key head alone: as many parts as the SMs hold warps, of 8 rows or of more.
+int64_t paged_workspace_bytes(int B, int rows)
+{
+    return (rows <= 8 ? kFewBytes : kMostBytes) + 8 * (static_cast<int64_t>(B) + 1);
+}
 
 cudaError_t launch_paged_e4m3(const PagedArgs &g, cudaStream_t s)
 {

@@ -424,9 +424,10 @@ QMV_API qmv_status qmv_rope_append_e4m3(const float *qkv, const int32_t *positio
  * h reads key head h / (Hq / Hkv). A row without any key gives zeros (one whose scores
  * are all -inf, NaN).
  *   q, out   [B][T][Hq][D], QMV_F16 or QMV_BF16 (type); B up to 65535, T Hq up to 2^20,
- *            D = 64 or 128, Hkv dividing Hq.
+ *            B T Hq up to 2^31 - 1, D = 64 or 128, Hkv dividing Hq.
  *   k_cache, v_cache uint8 [n_pages][page][Hkv][D], page a power of two, 16..256, 16-byte
- *            aligned; k_scale, v_scale fp32 [n_pages][page / 16][Hkv], finite and not negative.
+ *            aligned; k_scale, v_scale fp32 [n_pages][page / 16][Hkv]: 0 or, for values to
+ *            count in full, 2^-100 .. 2^90.
  *   table    int32 [B][table_pages]; lens int32 [B] (at most max_len, a bound the caller
  *            knows, itself at most table_pages * page and 2^30; a longer one is cut to
  *            max_len and sets bit 2). A page outside the cache reads as zeros (bit 2).

@@ -37,16 +37,18 @@ def run(args, **kw):
 
 def check(args, type_="f16", scale=None, **kw):
     got = run(args, scale=scale, **kw)
+    near(got, args, type_, args["q"].shape[-1] ** -0.5 if scale is None else scale)
+    return got
+
+
+def near(got, args, type_, scale):
     u = TYPES[type_][1]
-    D = args["q"].shape[-1]
-    o, bound, floor = cache8_ref.attention(args["q"], *(args[n] for n in ("k_cache", "v_cache", "k_scale", "v_scale", "table", "lens")),
-                                           1 / math.sqrt(D) if scale is None else scale)
+    o, bound, floor = cache8_ref.attention(args["q"], *(args[n] for n in ("k_cache", "v_cache", "k_scale", "v_scale", "table", "lens")), scale)
     fine = torch.isfinite(o)
     assert torch.equal(torch.isnan(got), torch.isnan(o))
     err = (got.double() - o).abs()
     tol = u * o.abs() + (2.0 ** -11 + 2.0 ** -13) * bound + 2.0 ** -25 * floor + 2.0 ** -24
     assert bool((err[fine] <= tol[fine]).all()), float((err / tol)[fine].max())
-    return got
 
 
 @pytest.mark.parametrize("type_", ["f16", "bf16"])
@@ -189,7 +191,10 @@ def test_indices_outside_are_flagged_and_not_followed():
         zeros = {**args, "k_cache": args["k_cache"].clone(), "v_cache": args["v_cache"].clone()}
         for n in ("k_cache", "v_cache"):
             zeros[n].view(torch.uint8)[zero] = 0
-        assert torch.equal(got, run(zeros, max_len=90))
+        # Zeros as the definition has them. Not the same bits as a page of zero codes: what the terms of a
+        # row's sum are rounded relative to is its largest weight times scale, and a page outside has no
+        # scale, so either result is within the tolerance of the value, and of the other within twice that.
+        near(got, zeros, "f16", 64 ** -0.5)
 
 
 def test_offsets_past_32_bits():
