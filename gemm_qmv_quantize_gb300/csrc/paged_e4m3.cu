@@ -38,6 +38,7 @@ constexpr int kBlock = kScaleTokens;    // keys a step of a warp
 constexpr int kMostWarps = 8;           // of a CTA, a key head each
 constexpr int64_t kFewBytes = 22ll << 20, kMostBytes = 44ll << 20;   // of the workspace's slots
 constexpr int kSms = 152;
+constexpr int kStartUnits = 8;          // what starting on an item costs, in blocks of a warp's
 constexpr int kLeastBlocks = 2;         // of a run, where there are few
 constexpr int kBatch = 32;              // blocks whose page and scales a warp looks up at a time, a lane a block
 constexpr float kSlack = 8.0f;
@@ -54,7 +55,7 @@ struct Ring {
 // shared memory that is left beside q's operands.
 template <int D, int NT>
 struct Shape {
-    static constexpr int kWarpsSm = NT * D <= 128 ? 16 : 8;
+    static constexpr int kWarpsSm = D == 128 ? 8 : 16;
     static constexpr int kQueries = NT == 1 ? 0 : NT * D * 16;   // bytes a warp
     static constexpr int kFit = (216 * 1024 / kWarpsSm - kQueries) / (32 * D), kStages = kFit < 3 ? 3 : kFit > 6 ? 6 : kFit;
     static constexpr int kOwn = kStages * 32 * D + kQueries;     // a warp's shared memory
@@ -389,15 +390,17 @@ struct Walk {
 template <int D, int NT>
 constexpr int slot_floats() { return 8 * NT * (D + 4); }
 
-// The work is cut into units: a block of an item, an item being a request, a group of up to 8
-// key heads and a group of 8 NT query rows, in that order. A CTA takes a run of units, its
-// warps a key head each, so that the rows of a block, which lie side by side for all heads,
-// are read together (reads alone: 7.0 TB/s; one head at a time by all warps of a CTA 6.2). All runs
-// are of equal length, whatever the requests' lengths. What a run has of an item that is not
-// all of it is a part, which paged_join_kernel joins with the others'.
+// A block is gone through once for each pair of a key head and a group of 8 NT of its query rows, by a
+// warp each. The work is cut into units: a block of an item, an item being a request and up to 8 of its
+// pairs, in that order. A CTA takes a run of units, its warps a pair each, so that the rows
+// of a block, which lie side by side for all heads, are read together (reads alone: 7.0 TB/s;
+// one head at a time by all warps of a CTA 6.2). All runs are of equal length, whatever the requests'
+// lengths; so that a run with more items does not end later, an item counts kStartUnits more,
+// before its blocks. What a run has of an item that is not all of it is a part (an empty one, where
+// it has none of the blocks), which paged_join_kernel joins with the others'.
 struct Cut {
-    int b, item;          // item of the request: head group * row groups + row group
-    int64_t at;           // units before it in its item (blocks)
+    int b, item;          // item of the request
+    int64_t at;           // units before it in its item
     int64_t left;         // units of the run
     int64_t from, units;  // where the run starts; all units
 };
@@ -408,9 +411,13 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)
     return (a | b) >> 32 ? a / b : static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));
 }
 
-__device__ __forceinline__ int blocks_of(const PagedArgs &g, int b)
+__device__ __forceinline__ int len_of(const PagedArgs &g, int b) { return static_cast<int>(min(static_cast<int64_t>(max(g.lens[b], 0)), g.max_len)); }
+
+// Units of an item of a request.
+__device__ __forceinline__ int units_of(const PagedArgs &g, int b)
 {
-    return (static_cast<int>(min(static_cast<int64_t>(max(g.lens[b], 0)), g.max_len)) + kBlock - 1) / kBlock;
+    const int len = len_of(g, b);
+    return len > 0 ? (len + kBlock - 1) / kBlock + kStartUnits : 0;
 }
 
 // Sum over a CTA's threads before this one, and of all.
@@ -442,7 +449,7 @@ __device__ __forceinline__ Cut cut_of(const PagedArgs &g, int c, int ctas, int i
     const int tid = threadIdx.x, step = static_cast<int>(blockDim.x);
     int64_t total = 0, all, mine = 0, before = 0;
     for (int b0 = 0; b0 < g.B; b0 += step) {
-        mine = b0 + tid < g.B ? blocks_of(g, b0 + tid) : 0;
+        mine = b0 + tid < g.B ? units_of(g, b0 + tid) : 0;
         before = scan_before(mine, sums, all);
         if (starts && b0 + tid < g.B) starts[b0 + tid] = total + before;
         total += all;
@@ -455,7 +462,7 @@ __device__ __forceinline__ Cut cut_of(const PagedArgs &g, int c, int ctas, int i
     for (int b0 = 0; b0 < g.B; b0 += step) {
         int64_t base = 0;
         if (g.B > step) {
-            mine = b0 + tid < g.B ? blocks_of(g, b0 + tid) : 0;
+            mine = b0 + tid < g.B ? units_of(g, b0 + tid) : 0;
             before = scan_before(mine, sums, all);
             base = total;
             total += all;
@@ -543,34 +550,17 @@ __device__ __noinline__ float4 with_nan(const PagedArgs &g, int b, int h, int le
     return o;
 }
 
-// What a thread joins of a row's parts: four dimensions, and the statistics. First the maxima
-// of all parts, then the sums.
-struct Joined {
-    float l = 0.0f, m = kLowest, nan = 0.0f;
-    float4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-    __device__ __forceinline__ void top(float4 st)
-    {
-        m = fmaxf(m, st.y);
-        nan = fmaxf(nan, st.z);
-    }
-    __device__ __forceinline__ void add(float4 st, float4 x)
-    {
-        const float by = exp2_fast(st.y - m);
-        l += st.x * by;
-        o = make_float4(o.x + x.x * by, o.y + x.y * by, o.z + x.z * by, o.w + x.w * by);
-    }
-    // The output of row `row` of the request's key head, from dimension d on.
-    __device__ __forceinline__ void write(const PagedArgs &g, int b, int h, int len, int row, int G, int d, int D)
-    {
-        const bool none = len - g.T + 1 + row / G <= 0;
-        const float by = 1.0f / l;
-        float4 y = none ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : make_float4(o.x * by, o.y * by, o.z * by, o.w * by);
-        if (nan != 0.0f && !none) y = with_nan(g, b, h, len, row / G, d, D, y);
-        const int64_t at = (static_cast<int64_t>(b) * g.T + row / G) * g.Hq + static_cast<int64_t>(h) * G + row % G;
-        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(g.out) + at * D + d) =
-            g.type == QMV_F16 ? make_uint2(pack2<__half>(y.x, y.y), pack2<__half>(y.z, y.w)) : make_uint2(pack2<__nv_bfloat16>(y.x, y.y), pack2<__nv_bfloat16>(y.z, y.w));
-    }
-};
+// Four outputs of row `row` of a key head, from their sums over V and the denominator l.
+__device__ __forceinline__ void write_row(const PagedArgs &g, int b, int h, int len, int row, int G, int d, int D, float l, bool nan, float4 o)
+{
+    const bool none = len - g.T + 1 + row / G <= 0;
+    const float by = 1.0f / l;
+    float4 y = none ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : make_float4(o.x * by, o.y * by, o.z * by, o.w * by);
+    if (nan && !none) y = with_nan(g, b, h, len, row / G, d, D, y);
+    const int64_t at = (static_cast<int64_t>(b) * g.T + row / G) * g.Hq + static_cast<int64_t>(h) * G + row % G;
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(g.out) + at * D + d) =
+        g.type == QMV_F16 ? make_uint2(pack2<__half>(y.x, y.y), pack2<__half>(y.z, y.w)) : make_uint2(pack2<__nv_bfloat16>(y.x, y.y), pack2<__nv_bfloat16>(y.z, y.w));
+}
 
 // The workspace: two slots for each warp of a run, [run][first or last][warp]; then the units
 // before each request, and of all.
@@ -593,7 +583,7 @@ __global__ void __launch_bounds__(32 * kMostWarps, Shape<D, NT>::kWarpsSm / kMos
     __shared__ int64_t sums[kMostWarps];
     __shared__ Cut shared_cut;
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, warps = blockDim.x / 32, gid = lane / 4, t = lane % 4;
-    const int G = g.Hq / g.Hkv, rows = g.T * G, items = (g.Hkv + warps - 1) / warps * row_groups;
+    const int G = g.Hq / g.Hkv, rows = g.T * G, pairs = g.Hkv * row_groups, items = (pairs + warps - 1) / warps;
     const uint32_t my_ring = smem_addr(smem) + warp * Shape<D, NT>::kOwn;
     grid_launch_dependents();
     grid_dependency_wait();
@@ -602,7 +592,7 @@ __global__ void __launch_bounds__(32 * kMostWarps, Shape<D, NT>::kWarpsSm / kMos
     // rows of requests without keys are no units
     for (int i = static_cast<int>(blockIdx.x); i < g.B; i += static_cast<int>(gridDim.x)) {
         if (g.lens[i] > g.max_len && threadIdx.x == 0) atomicOr(&g_paged_error, kErrIndex);
-        if (blocks_of(g, i) > 0) continue;
+        if (len_of(g, i) > 0) continue;
         uint4 *out = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(g.out) + static_cast<int64_t>(i) * g.T * g.Hq * D);
         for (int64_t j = threadIdx.x; j < static_cast<int64_t>(g.T) * g.Hq * D / 8; j += blockDim.x) out[j] = make_uint4(0, 0, 0, 0);
     }
@@ -610,11 +600,10 @@ __global__ void __launch_bounds__(32 * kMostWarps, Shape<D, NT>::kWarpsSm / kMos
     Queries<D, NT> q;
     q.base = my_ring + Shape<D, NT>::kStages * Ring<D>::kBytes + lane * 8;
     for (bool first = true; cut.left > 0; first = false) {
-        const int b = cut.b, h = cut.item / row_groups * warps + warp, row0 = cut.item % row_groups * 8 * NT;
-        const int len = static_cast<int>(min(static_cast<int64_t>(max(g.lens[b], 0)), g.max_len));
-        const int blocks = (len + kBlock - 1) / kBlock, at = static_cast<int>(cut.at);
-        const int count = static_cast<int>(min(static_cast<int64_t>(blocks - at), cut.left));
-        if (h < g.Hkv) {
+        const int b = cut.b, pair = cut.item * warps + warp, h = pair / row_groups, row0 = pair % row_groups * 8 * NT;
+        const int len = len_of(g, b), units = units_of(g, b), taken = static_cast<int>(min(units - cut.at, cut.left));
+        const int at = max(static_cast<int>(cut.at) - kStartUnits, 0), count = max(static_cast<int>(cut.at) + taken - kStartUnits, 0) - at;
+        if (pair < pairs) {
             Place p;
             p.token = static_cast<int64_t>(g.Hkv) * D;
             p.k = static_cast<const uint8_t *>(g.k) + h * D;
@@ -652,7 +641,7 @@ __global__ void __launch_bounds__(32 * kMostWarps, Shape<D, NT>::kWarpsSm / kMos
             }
             walk.add(part, q, c, seen);
             // the output, or a part
-            const bool whole = count == blocks, nan = __any_sync(0xffffffffu, part.nan != 0);
+            const bool whole = taken == units, nan = __any_sync(0xffffffffu, part.nan != 0);
             float *slot = slot_of<D, NT>(g, static_cast<int>(blockIdx.x), first, warps, warp);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -661,87 +650,124 @@ __global__ void __launch_bounds__(32 * kMostWarps, Shape<D, NT>::kWarpsSm / kMos
                     float l = part.l[n][e];
 #pragma unroll
                     for (int o = 4; o < 32; o *= 2) l += __shfl_xor_sync(0xffffffffu, l, o);
-                    const int r = 8 * n + 2 * t + e, row = row0 + r;
-                    if (row >= rows) continue;
-                    float by = 1.0f;
-                    if (whole) by = 1.0f / l;
-                    float4 y[D / 32];
-#pragma unroll
-                    for (int j = 0; j < D / 32; ++j)
-                        y[j] = make_float4(part.o[n][2 * j][e] * by, part.o[n][2 * j][e + 2] * by, part.o[n][2 * j + 1][e] * by,
-                                           part.o[n][2 * j + 1][e + 2] * by);
-                    if (!whole) {
-#pragma unroll
-                        for (int j = 0; j < D / 32; ++j) reinterpret_cast<float4 *>(slot + r * (D + 4) + gid * (D / 8))[j] = y[j];
-                        if (gid == 0) *reinterpret_cast<float4 *>(slot + r * (D + 4) + D) = make_float4(l, part.m[n][e], nan ? 1.0f : 0.0f, 0.0f);
-                        continue;
-                    }
+                    const int r = 8 * n + 2 * t + e;
+                    if (row0 + r >= rows) continue;
 #pragma unroll
                     for (int j = 0; j < D / 32; ++j) {
-                        if (seen[n][e] <= 0) y[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                        if (nan && seen[n][e] > 0) y[j] = with_nan(g, b, h, len, row / G, gid * (D / 8) + 4 * j, D, y[j]);
-                        reinterpret_cast<uint2 *>(static_cast<uint16_t *>(g.out) + row_at(row) + gid * (D / 8))[j] =
-                            g.type == QMV_F16 ? make_uint2(pack2<__half>(y[j].x, y[j].y), pack2<__half>(y[j].z, y[j].w))
-                                              : make_uint2(pack2<__nv_bfloat16>(y[j].x, y[j].y), pack2<__nv_bfloat16>(y[j].z, y[j].w));
+                        const float4 y = make_float4(part.o[n][2 * j][e], part.o[n][2 * j][e + 2], part.o[n][2 * j + 1][e], part.o[n][2 * j + 1][e + 2]);
+                        if (whole) {
+                            write_row(g, b, h, len, row0 + r, G, gid * (D / 8) + 4 * j, D, l, nan, y);
+                        } else {
+                            reinterpret_cast<float4 *>(slot + r * (D + 4) + gid * (D / 8))[j] = y;
+                        }
                     }
+                    if (!whole && gid == 0) *reinterpret_cast<float4 *>(slot + r * (D + 4) + D) = make_float4(l, part.m[n][e], nan ? 1.0f : 0.0f, 0.0f);
                 }
             }
         }
-        cut.left -= count;
+        cut.left -= taken;
         cut.at = 0;
         if (++cut.item == items && cut.left > 0) {
             cut.item = 0;
             do {
                 ++cut.b;
-            } while (blocks_of(g, cut.b) == 0);   // ends: there are units left
+            } while (units_of(g, cut.b) == 0);   // ends: there are units left
         }
     }
 }
 
-// The items of which runs have parts. Grid (B * Hkv * row_groups, rows / rows of a CTA): `share`
-// warps a row, each every share-th part.
+// The rows of which runs have parts. A CTA has blockDim / 32 / share rows of all B * pairs * n of them
+// (n: rows of a group), `share` warps a row, each every share-th part. Short code: what a launch runs
+// once takes as long as fetching its instructions does.
 template <int D, int NT>
-__global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ PagedArgs g, int row_groups, int warps, int ctas, int share)
+__global__ void __launch_bounds__(1024) paged_join_kernel(const __grid_constant__ PagedArgs g, int row_groups, int warps, int ctas, int share, int n)
 {
     constexpr int kD4 = D / 4;
-    __shared__ float4 sum_o[8][kD4], sum_l[8];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, G = g.Hq / g.Hkv, rows = g.T * G;
-    const int row_group = static_cast<int>(blockIdx.x) % row_groups, of_b = static_cast<int>(blockIdx.x) / row_groups;
-    const int h = of_b % g.Hkv, b = of_b / g.Hkv, item = h / warps * row_groups + row_group;
-    const int items = (g.Hkv + warps - 1) / warps * row_groups;
+    __shared__ float4 sum_o[32][kD4];
+    __shared__ float4 sum_l[32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, mine = warp % share;
+    const uint32_t pairs = static_cast<uint32_t>(g.Hkv * row_groups), task = blockIdx.x * (blockDim.x / 32 / share) + warp / share;
+    const uint32_t of_row = task / static_cast<uint32_t>(n), b = of_row / pairs, pair = of_row - b * pairs;
+    const int r = static_cast<int>(task - of_row * n), row = static_cast<int>(pair) % row_groups * 8 * NT + r;
+    const int item = static_cast<int>(pair) / warps, items = (static_cast<int>(pairs) + warps - 1) / warps;
     grid_launch_dependents();
     grid_dependency_wait();   // in every CTA: this launch ends after the one before it
-    const int64_t *starts = starts_of<D, NT>(g);
-    const int64_t before = starts[b], blocks = starts[b + 1] - before, units = starts[g.B] * items;
-    if (blocks == 0) return;
-    const int64_t item0 = before * items + blocks * item, item1 = item0 + blocks;
-    // the runs that have units of the item
-    const int64_t q = quotient(units, ctas), long_ones = units - q * ctas;
-    auto run_of = [&](int64_t unit) {
-        return static_cast<int>(unit < long_ones * (q + 1) ? quotient(unit, q + 1) : long_ones + quotient(unit - long_ones * (q + 1), q));
-    };
-    const int run0 = run_of(item0), parts = run_of(item1 - 1) - run0 + 1;
-    if (parts == 1) return;   // one run has all of it
-    const int r = (static_cast<int>(blockIdx.y) * 8 + warp) / share, row = row_group * 8 * NT + r, mine = warp % share;
-    const bool live = r < 8 * NT && row < rows;
-    const bool at_start = q * run0 + min(static_cast<int64_t>(run0), long_ones) == item0;   // the first run starts with the item
-    Joined x;
+    const bool live = b < static_cast<uint32_t>(g.B) && row < g.T * (g.Hq / g.Hkv);
+    int parts = 0;
+    const float *part0 = nullptr;   // this row's part of the item's first run; the further ones are `stride` apart
+    int64_t stride = 0, skip = 0;   // skip: from the slots for a run's first piece to those for its last
     if (live) {
-        auto row_of = [&](int i) { return slot_of<D, NT>(g, run0 + i, i > 0 || at_start, warps, h % warps) + r * (D + 4); };
-#pragma unroll 4
-        for (int i = mine; i < parts; i += share) x.top(*reinterpret_cast<const float4 *>(row_of(i) + D));
-#pragma unroll 4
-        for (int i = mine; i < parts; i += share)
-            x.add(*reinterpret_cast<const float4 *>(row_of(i) + D), lane < kD4 ? reinterpret_cast<const float4 *>(row_of(i))[lane] : x.o);
-        if (lane < kD4) sum_o[warp][lane] = x.o;
-        if (lane == 0) sum_l[warp] = make_float4(x.l, x.m, x.nan, 0.0f);
+        const int64_t *starts = starts_of<D, NT>(g);
+        const int64_t before = starts[b], blocks = starts[b + 1] - before, units = starts[g.B] * items;
+        const int64_t item0 = before * items + blocks * item, q = quotient(units, ctas), long_ones = units - q * ctas;
+        // of runs of q + 1 units, long_ones of them, and then of q: that of a unit, and where it starts
+        auto run_of = [&](int64_t unit, int64_t &start) {
+            const bool l = unit < long_ones * (q + 1);
+            const int64_t rest = l ? unit : unit - long_ones * (q + 1), each = l ? q + 1 : q, run = quotient(rest, each);
+            start = unit - (rest - run * each);
+            return static_cast<int>(run + (l ? 0 : long_ones));
+        };
+        if (blocks > 0) {
+            int64_t start, end;
+            const int run0 = run_of(item0, start);
+            parts = run_of(item0 + blocks - 1, end) - run0 + 1;
+            skip = static_cast<int64_t>(warps) * slot_floats<D, NT>();
+            stride = 2 * skip;
+            part0 = slot_of<D, NT>(g, run0, true, warps, static_cast<int>(pair) % warps) + r * (D + 4);
+            if (start == item0) skip = 0;   // the run starts with the item
+        }
     }
-    __syncthreads();
-    if (!live || mine > 0 || lane >= kD4) return;
-    Joined all;
-    for (int w = 0; w < share; ++w) all.top(sum_l[warp + w]);
-    for (int w = 0; w < share; ++w) all.add(sum_l[warp + w], sum_o[warp + w][lane]);
-    all.write(g, b, h, static_cast<int>(min(static_cast<int64_t>(g.lens[b]), g.max_len)), row, G, 4 * lane, D);
+    float l = 0.0f, m = kLowest, nan = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    // 32 parts at a time: their statistics a lane a part, then their weights to all lanes
+    for (int i0 = mine; parts > 1 && i0 < parts; i0 += 32 * share) {
+        const int i = i0 + lane * share, count = min(32, (parts - i0 + share - 1) / share);
+        float4 st = make_float4(0.0f, kLowest, 0.0f, 0.0f);
+        if (i < parts) st = *reinterpret_cast<const float4 *>(part0 + i * stride + (i > 0 ? 0 : skip) + D);
+        float top = fmaxf(m, st.y);
+#pragma unroll
+        for (int x = 16; x > 0; x /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+        const float by = exp2_fast(m - top), weight = exp2_fast(st.y - top);
+        l = l * by + st.x * weight;   // of this lane's parts; by is 1 but for more than 32
+        o = make_float4(o.x * by, o.y * by, o.z * by, o.w * by);
+        m = top;
+        nan = fmaxf(nan, st.z);
+        const float *x_at = part0 + i0 * stride + 4 * (lane % kD4);
+        int64_t skipped = i0 > 0 ? 0 : skip;
+#pragma unroll 4
+        for (int k = 0; k < count; ++k) {
+            const float4 x = *reinterpret_cast<const float4 *>(x_at + skipped);
+            const float w = __shfl_sync(0xffffffffu, weight, k);
+            x_at += share * stride;
+            skipped = 0;
+            o = make_float4(o.x + x.x * w, o.y + x.y * w, o.z + x.z * w, o.w + x.w * w);
+        }
+    }
+#pragma unroll
+    for (int x = 16; x > 0; x /= 2) {
+        l += __shfl_xor_sync(0xffffffffu, l, x);
+        nan = fmaxf(nan, __shfl_xor_sync(0xffffffffu, nan, x));
+    }
+    if (share > 1) {
+        if (lane < kD4) sum_o[warp][lane] = o;
+        if (lane == 0) sum_l[warp] = make_float4(l, m, nan, 0.0f);
+        __syncthreads();
+        if (mine > 0) return;
+        for (int w = 1; w < share; ++w) m = fmaxf(m, sum_l[warp + w].y);
+        l = 0.0f;
+        o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
+        for (int w = 0; w < share; ++w) {
+            const float4 st = sum_l[warp + w], x = sum_o[warp + w][lane % kD4];
+            const float by = exp2_fast(st.y - m);
+            l += st.x * by;
+            nan = fmaxf(nan, st.z);
+            o = make_float4(o.x + x.x * by, o.y + x.y * by, o.z + x.z * by, o.w + x.w * by);
+        }
+    }
+    if (parts > 1 && lane < kD4)
+        write_row(g, static_cast<int>(b), static_cast<int>(pair) / row_groups, static_cast<int>(min(static_cast<int64_t>(g.lens[b]), g.max_len)), row,
+                  g.Hq / g.Hkv, 4 * lane, D, l, nan != 0.0f, o);
 }
 
 template <int D, int NT>
@@ -750,8 +776,9 @@ cudaError_t launch_typed(const PagedArgs &g, int row_groups, cudaStream_t s)
     using S = Shape<D, NT>;
     static_assert(S::kWarpsSm * S::kOwn <= 224 * 1024, "the warps' memory fits an SM");
     static_assert(2ll * S::kMostWarpsOfRuns * slot_floats<D, NT>() * 4 <= (NT == 1 ? kFewBytes : kMostBytes), "the workspace has every run's parts");
-    const int head_groups = (g.Hkv + kMostWarps - 1) / kMostWarps, warps = (g.Hkv + head_groups - 1) / head_groups;
-    const int64_t items = static_cast<int64_t>(head_groups) * row_groups, blocks = (g.max_len + kBlock - 1) / kBlock;
+    const int64_t pairs = static_cast<int64_t>(g.Hkv) * row_groups, items = (pairs + kMostWarps - 1) / kMostWarps;
+    const int warps = static_cast<int>((pairs + items - 1) / items);
+    const int64_t blocks = (g.max_len + kBlock - 1) / kBlock;
     const int ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kSms * (S::kWarpsSm / warps), items * g.B * blocks / kLeastBlocks)));
     const int smem = warps * S::kOwn;
     cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(paged_kernel<D, NT>), smem);
@@ -768,31 +795,28 @@ cudaError_t launch_typed(const PagedArgs &g, int row_groups, cudaStream_t s)
     if (e != cudaSuccess || ctas == 1) return e;
     // the join starts while the runs still go on, and waits for their end on the device
     const int rows = std::min(8 * NT, g.T * (g.Hq / g.Hkv));
-    int share = 1;
-    while (share < 8 && share * 4 * g.B * items < ctas) share *= 2;   // about four parts a warp
+    const int64_t tasks = g.B * pairs * rows;
+    int share = 1;   // two parts a warp or more, by the mean, and as many warps as the SMs take at once
+    while (share < 32 && 4 * share * g.B * items <= ctas && 2 * share * tasks <= 16 * kSms) share *= 2;
+    const int join_warps = std::max(share, 8);
     cudaLaunchConfig_t join = {};
-    join.blockDim = dim3(256);
-    join.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(g.B) * g.Hkv * row_groups), static_cast<unsigned>((rows * share + 7) / 8));
+    join.blockDim = dim3(static_cast<unsigned>(32 * join_warps));
+    join.gridDim = dim3(static_cast<unsigned>((tasks * share + join_warps - 1) / join_warps));
     join.stream = s;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     join.attrs = attr;
     join.numAttrs = 1;
-    return cudaLaunchKernelEx(&join, paged_join_kernel<D, NT>, g, row_groups, warps, ctas, share);
+    return cudaLaunchKernelEx(&join, paged_join_kernel<D, NT>, g, row_groups, warps, ctas, share, rows);
 }
 
 // Groups of up to 8 NT rows, all of nearly the same number.
 template <int D>
 cudaError_t launch_rows(const PagedArgs &g, cudaStream_t s)
 {
-    constexpr int kMost = D == 64 ? 48 : 32;
+    constexpr int kMost = 16;
     const int rows = g.T * (g.Hq / g.Hkv);
-    const int groups = (rows + kMost - 1) / kMost, each = (rows + groups - 1) / groups;
-    if (each <= 8) return launch_typed<D, 1>(g, groups, s);
-    if (each <= 16) return launch_typed<D, 2>(g, (rows + 15) / 16, s);
-    if (each <= 32) return launch_typed<D, 4>(g, (rows + 31) / 32, s);
-    if constexpr (D == 64) return launch_typed<D, 6>(g, (rows + 47) / 48, s);
-    return cudaErrorInvalidValue;
+    return rows <= 8 ? launch_typed<D, 1>(g, 1, s) : launch_typed<D, 2>(g, (rows + kMost - 1) / kMost, s);
 }
 
 }  // namespace
