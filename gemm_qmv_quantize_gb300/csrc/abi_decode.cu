@@ -48,8 +48,8 @@ qmv_status run_norm_rope(NormRopeArgs g, const uint8_t *axis_of_pair, int axes, 
     if (!g.qkv || !g.q || !g.slots || !g.k_cache || !g.v_cache) return QMV_ERR_NULL;
     if (g.rot > 0 && (!g.positions || !g.table || !axis_of_pair)) return QMV_ERR_NULL;
     if (misaligned(g.qkv, 16) || misaligned(g.q, 16) || misaligned(g.k_cache, 16) || misaligned(g.v_cache, 16) ||
-        misaligned(g.table, 16) || misaligned(g.positions, 4) || misaligned(g.slots, 8) || misaligned(g.q_norm, 4) ||
-        misaligned(g.k_norm, 4) || misaligned(g.k_scale, 4) || misaligned(g.v_scale, 4))
+        misaligned(g.table, 16) || misaligned(g.positions, 4) || misaligned(g.slots, 8) || misaligned(g.q_norm, 16) ||
+        misaligned(g.k_norm, 16) || misaligned(g.k_scale, 4) || misaligned(g.v_scale, 4))
         return QMV_ERR_ALIGN;
     for (int i = 0; i < g.rot / 2; ++i) {
         if (axis_of_pair[i] >= axes) return QMV_ERR_SHAPE;
@@ -130,7 +130,7 @@ qmv_status qmv_norm_rope_append(const float *qkv, const int32_t *positions, cons
     const qmv_status st = norm_rope_shape(type, M, Hq, Hkv, D, rot, axes, n_positions, n_slots, eps, false);
     if (st != QMV_OK || M == 0) return st;
     return run_norm_rope(NormRopeArgs{qkv, positions, table, slots, q_norm, k_norm, q, k_cache, v_cache, nullptr, nullptr,
-                                      n_slots, eps, type, M, Hq, Hkv, D, rot, n_positions, interleaved != 0, {}},
+                                      n_slots, eps, 1.0f / static_cast<float>(D), type, M, Hq, Hkv, D, rot, n_positions, interleaved != 0, {}},
                          axis_of_pair, axes, stream);
 }
 
@@ -144,7 +144,7 @@ qmv_status qmv_rope_append_e4m3(const float *qkv, const int32_t *positions, cons
     if (st != QMV_OK || M == 0) return st;
     if (!k_scale || !v_scale) return QMV_ERR_NULL;
     return run_norm_rope(NormRopeArgs{qkv, positions, table, slots, q_norm, k_norm, q, k_cache, v_cache, k_scale, v_scale,
-                                      n_slots, eps, type, M, Hq, Hkv, D, rot, n_positions, interleaved != 0, {}},
+                                      n_slots, eps, 1.0f / static_cast<float>(D), type, M, Hq, Hkv, D, rot, n_positions, interleaved != 0, {}},
                          axis_of_pair, axes, stream);
 }
 

@@ -52,9 +52,9 @@ struct NormRopeArgs {
     void *q, *k_cache, *v_cache;
     float *k_scale, *v_scale;   // [n_slots / 16][Hkv], or null
     int64_t n_slots;
-    float eps;
+    float eps, one_over_d;
     int type, M, Hq, Hkv, D, rot, n_positions, interleaved;
-    uint8_t axis_of_pair[kMaxRopePairs];
+    alignas(4) uint8_t axis_of_pair[kMaxRopePairs];
 };
 cudaError_t launch_norm_rope(const NormRopeArgs &g, cudaStream_t s);
 

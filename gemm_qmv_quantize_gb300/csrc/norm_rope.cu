@@ -25,7 +25,7 @@ namespace {
 __device__ uint32_t g_norm_rope_error;
 
 constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kTwoRows = 256;   // rows from which a CTA takes two
 
 // The 8 elements e0 .. e0 + 3 and e1 .. e1 + 3 of a head that a lane has.
 struct Unit {
@@ -50,42 +50,69 @@ __device__ __forceinline__ void load8(float (&x)[8], const float *in, const Unit
     x[0] = p.x, x[1] = p.y, x[2] = p.z, x[3] = p.w, x[4] = q.x, x[5] = q.y, x[6] = q.z, x[7] = q.w;
 }
 
-// The norm, over the group of L lanes that has the head.
+// The norm, over the group of L lanes that has the head, where `norm`; w is 1 where not. (All lanes
+// take part: the groups of a warp may have heads of both kinds.)
 template <int L>
-__device__ __forceinline__ void norm8(float (&x)[8], const float (&w)[8], int D, float eps)
+__device__ __forceinline__ void norm8(float (&x)[8], const float (&w)[8], bool norm, const NormRopeArgs &g)
 {
     float sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum = fmaf(x[j], x[j], sum);
 #pragma unroll
     for (int o = L / 2; o > 0; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    const float r = 1.0f / sqrtf(sum / static_cast<float>(D) + eps);
+    const float r = norm ? rsqrtf(fmaf(sum, g.one_over_d, g.eps)) : 1.0f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) x[j] = x[j] * r * w[j];
 }
 
-template <bool kInterleaved>
-__device__ __forceinline__ void turn8(float (&x)[8], const float2 *cs, int i)
-{
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int lo = kInterleaved ? 2 * j : j, hi = kInterleaved ? 2 * j + 1 : j + 4;
-        const float2 t = cs[4 * i + j];
-        const float a = x[lo], b = x[hi];
-        x[lo] = a * t.x - b * t.y;
-        x[hi] = b * t.x + a * t.y;
-    }
-}
+// A unit's four angles, (cos, sin) each.
+struct Angles {
+    float4 a, b;
+};
 
-// Angle `pair` of row m.
-__device__ __forceinline__ float2 angle_of(const NormRopeArgs &g, int m, int pair)
+__device__ __forceinline__ int position_of(const NormRopeArgs &g, int m, int axis)
 {
-    int pos = g.positions[static_cast<int64_t>(g.axis_of_pair[pair]) * g.M + m];
+    int pos = g.positions[static_cast<int64_t>(axis) * g.M + m];
     if (pos < 0 || pos >= g.n_positions) {
         atomicOr(&g_norm_rope_error, kErrIndex);
         pos = pos < 0 ? 0 : g.n_positions - 1;
     }
-    return reinterpret_cast<const float2 *>(g.table)[static_cast<int64_t>(pos) * (g.rot / 2) + pair];
+    return pos;
+}
+
+// Of row m and pairs 4 i .. 4 i + 3. Lanes with the same i of all of a CTA's heads read the same ones: L1
+// serves all but the first. (Through shared memory, with a barrier, 4001 rows took 39 us for 35, and with codes
+// 53 for 40.)
+__device__ __forceinline__ Angles angles_of(const NormRopeArgs &g, int m, int i)
+{
+    const int pairs = g.rot / 2;
+    const float4 *table = reinterpret_cast<const float4 *>(g.table);
+    Angles t;
+    const uint32_t axes = reinterpret_cast<const uint32_t *>(g.axis_of_pair)[i], axis = axes & 0xffu;   // of the four pairs
+    if (axes == axis * 0x01010101u) {
+        const float4 *at = table + (static_cast<int64_t>(position_of(g, m, static_cast<int>(axis))) * pairs + 4 * i) / 2;
+        t.a = __ldg(at), t.b = __ldg(at + 1);
+    } else {
+        float2 c[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            c[j] = __ldg(reinterpret_cast<const float2 *>(g.table) + static_cast<int64_t>(position_of(g, m, static_cast<int>(axes >> (8 * j) & 0xffu))) * pairs + 4 * i + j);
+        t.a = make_float4(c[0].x, c[0].y, c[1].x, c[1].y), t.b = make_float4(c[2].x, c[2].y, c[3].x, c[3].y);
+    }
+    return t;
+}
+
+template <bool kInterleaved>
+__device__ __forceinline__ void turn8(float (&x)[8], const Angles &t)
+{
+    const float2 angles[4] = {make_float2(t.a.x, t.a.y), make_float2(t.a.z, t.a.w), make_float2(t.b.x, t.b.y), make_float2(t.b.z, t.b.w)};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int lo = kInterleaved ? 2 * j : j, hi = kInterleaved ? 2 * j + 1 : j + 4;
+        const float a = x[lo], b = x[hi];
+        x[lo] = a * angles[j].x - b * angles[j].y;
+        x[hi] = b * angles[j].x + a * angles[j].y;
+    }
 }
 
 template <typename T>
@@ -96,42 +123,10 @@ __device__ __forceinline__ void store8(void *base, int64_t head, int D, const Un
     *reinterpret_cast<uint2 *>(out + u.e1) = make_uint2(pack2<T>(x[4], x[5]), pack2<T>(x[6], x[7]));
 }
 
-// kThreads / L heads of row m, from head `first` on, of `heads` (q heads, then k, then v): q to
-// g.q and, in a cache of 16 bits, k and v to their slot.
-template <typename T, bool kInterleaved, int L>
-__device__ __forceinline__ void row_heads(const NormRopeArgs &g, int m, int first, int heads, int64_t slot, float2 *cs)
+__device__ __forceinline__ void load_weight(float (&w)[8], const float *weight, const Unit &u)
 {
-    const int tid = threadIdx.x, pairs = g.rot / 2, i = tid % L, head = first + tid / L;
-    const bool is_v = head >= g.Hq + g.Hkv;
-    const Unit u = unit_of<kInterleaved>(i, g.D, pairs, is_v);
-    const bool live = u.live && head < heads;
-    float x[8] = {}, w[8] = {};
-    if (live) load8(x, g.qkv + (static_cast<int64_t>(m) * (g.Hq + 2 * g.Hkv) + head) * g.D, u);
-    const float *weight = is_v ? nullptr : head < g.Hq ? g.q_norm : g.k_norm;
-    if (live && weight) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = __ldg(weight + (j < 4 ? u.e0 + j : u.e1 + j - 4));
-    }
-    if (tid < pairs) cs[tid] = angle_of(g, m, tid);
-    __syncthreads();
-    if (g.q_norm || g.k_norm) {   // (all lanes take part)
-        float y[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = x[j];
-        norm8<L>(y, w, g.D, g.eps);
-        if (weight) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = y[j];
-        }
-    }
-    if (!live) return;
-    if (u.turn) turn8<kInterleaved>(x, cs, i);
-    if (head < g.Hq) {
-        store8<T>(g.q, static_cast<int64_t>(m) * g.Hq + head, g.D, u, x);
-    } else if (slot >= 0) {
-        const int h = head - g.Hq - (is_v ? g.Hkv : 0);
-        store8<T>(is_v ? g.v_cache : g.k_cache, slot * g.Hkv + h, g.D, u, x);
-    }
+    const float4 p = __ldg(reinterpret_cast<const float4 *>(weight + u.e0)), q = __ldg(reinterpret_cast<const float4 *>(weight + u.e1));
+    w[0] = p.x, w[1] = p.y, w[2] = p.z, w[3] = p.w, w[4] = q.x, w[5] = q.y, w[6] = q.z, w[7] = q.w;
 }
 
 __device__ __forceinline__ int64_t slot_of(const NormRopeArgs &g, int m)
@@ -142,15 +137,52 @@ __device__ __forceinline__ int64_t slot_of(const NormRopeArgs &g, int m)
     return -1;
 }
 
-// Grid (M, CTAs of kThreads / L heads).
-template <typename T, bool kInterleaved, int L>
+// kThreads / L heads of rows m .. m + R - 1, from head `first` on, of `heads` (q heads, then k,
+// then v): q to g.q and, in a cache of 16 bits, k and v to their slots.
+template <typename T, bool kInterleaved, int L, int R>
+__device__ __forceinline__ void row_heads(const NormRopeArgs &g, int m, int first, int heads)
+{
+    const int tid = threadIdx.x, pairs = g.rot / 2, i = tid % L, head = first + tid / L, rows = min(R, g.M - m);
+    const bool is_v = head >= g.Hq + g.Hkv;
+    const Unit u = unit_of<kInterleaved>(i, g.D, pairs, is_v);
+    const bool live = u.live && head < heads;
+    const float *in = g.qkv + (static_cast<int64_t>(m) * (g.Hq + 2 * g.Hkv) + head) * g.D;
+    float x[R][8] = {}, w[8] = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        if (live && r < rows) load8(x[r], in + static_cast<int64_t>(r) * (g.Hq + 2 * g.Hkv) * g.D, u);
+    const float *weight = is_v ? nullptr : head < g.Hq ? g.q_norm : g.k_norm;
+    if (live && weight) load_weight(w, weight, u);
+    Angles t[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        if (live && u.turn && r < rows) t[r] = angles_of(g, m + r, i);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        if (g.q_norm || g.k_norm) norm8<L>(x[r], w, weight != nullptr, g);
+        if (!live || r >= rows) continue;
+        if (u.turn) turn8<kInterleaved>(x[r], t[r]);
+        if (head < g.Hq) {
+            store8<T>(g.q, static_cast<int64_t>(m + r) * g.Hq + head, g.D, u, x[r]);
+        } else {
+            const int64_t slot = slot_of(g, m + r);
+            const int h = head - g.Hq - (is_v ? g.Hkv : 0);
+            if (slot >= 0) store8<T>(is_v ? g.v_cache : g.k_cache, slot * g.Hkv + h, g.D, u, x[r]);
+        }
+    }
+}
+
+// Grid (rows / R, CTAs of kThreads / L heads).
+template <typename T, bool kInterleaved, int L, int R>
 __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ NormRopeArgs g)
 {
-    __shared__ float2 cs[kMaxRopePairs];
     grid_launch_dependents();
     grid_dependency_wait();
-    const int m = blockIdx.x;
-    row_heads<T, kInterleaved, L>(g, m, static_cast<int>(blockIdx.y) * (kThreads / L), g.Hq + 2 * g.Hkv, slot_of(g, m), cs);
+    const int m = static_cast<int>(blockIdx.x) * R;
+    if (threadIdx.x == 0 && blockIdx.y == 0) {
+        for (int r = 0; r < R && m + r < g.M; ++r) (void)slot_of(g, m + r);   // flags what lies outside
+    }
+    row_heads<T, kInterleaved, L, R>(g, m, static_cast<int>(blockIdx.y) * (kThreads / L), g.Hq + 2 * g.Hkv);
 }
 
 // The least e >= -64 with largest <= 448 * 2^e, as the scale 2^e; `largest` the bits of a
@@ -161,131 +193,164 @@ __device__ __forceinline__ float scale_for(uint32_t largest)
     return __uint_as_float(static_cast<uint32_t>(max(e, -64) + 127) << 23);
 }
 
-// The codes of one head of k or of v: a warp a head. Row m is the first of a run of rows whose
-// slots follow one another in one block; the warp takes the run's rows (n of them, at places
-// `offset` .. of the block), so that it alone reads and writes the head's part of the block.
+// The codes of one head of k (task < Hkv) or of v, of the runs that start in rows 16 `window`
+// .. + 15: a run is rows whose slots follow one another in one block, so this CTA alone reads and
+// writes the head's part of the block. A run that starts at the window's last row ends 15 rows
+// later: the CTA looks at 31 rows, a group of L lanes a row or two.
 template <bool kInterleaved, int L>
-__device__ __forceinline__ void block_head(const NormRopeArgs &g, int m, int n, int64_t slot, int task,
-                                           const float2 (*cs)[kMaxRopePairs / 2], bool live_task)
+__device__ __forceinline__ void window_head(const NormRopeArgs &g, int window, int task, uint32_t *run_largest)
 {
-    constexpr int kGroups = 32 / L, kTokens = kScaleTokens / kGroups;   // of a lane
-    const int lane = threadIdx.x & 31, i = lane % L, group = lane / L, pairs = g.rot / 2, D = g.D;
+    constexpr int kGroups = kThreads / L, kEach = 2 * kScaleTokens / kGroups;   // groups of lanes, rows of a group: 2 or 1
+    const int tid = threadIdx.x, lane = tid & 31, i = tid % L, group = tid / L, pairs = g.rot / 2, D = g.D;
+    const int m0 = window * kScaleTokens;
     const bool is_v = task >= g.Hkv;
-    const int h = is_v ? task - g.Hkv : task;
     const Unit u = unit_of<kInterleaved>(i, D, pairs, is_v);
     const int64_t row = static_cast<int64_t>(g.Hq + 2 * g.Hkv) * D;
-    const float *in = g.qkv + static_cast<int64_t>(m) * row + static_cast<int64_t>(g.Hq + task) * D;
-    float x[kTokens][8] = {}, w[8];
+    const float *in = g.qkv + static_cast<int64_t>(m0) * row + static_cast<int64_t>(g.Hq + task) * D;
+    // which rows, in every warp: lane j looks at row m0 + j
+    const int64_t slot = m0 + lane < g.M && lane < 2 * kScaleTokens - 1 ? g.slots[m0 + lane] : -1;
+    const int64_t before = m0 + lane > 0 && m0 + lane < g.M ? g.slots[m0 + lane - 1] : -1;
+    const bool valid = slot >= 0 && slot < g.n_slots;
+    if (slot >= g.n_slots && lane < kScaleTokens && tid < 32 && task == 0) atomicOr(&g_norm_rope_error, kErrIndex);
+    const uint32_t starts = __ballot_sync(0xffffffffu, valid && (before != slot - 1 || slot % kScaleTokens == 0));
+    const uint32_t up_to = starts & (0xffffffffu >> (31 - lane));
+    const int start = up_to && valid ? 31 - __clz(up_to) : -1;   // the row (of 32) that this row's run starts at
+    const int run = start < kScaleTokens ? start : -1;            // a later window's run is not this CTA's
+    const uint32_t mine = __ballot_sync(0xffffffffu, run >= 0);
+    float x[kEach][8] = {}, w[8], had[kEach];
+    int my_run[kEach];
+    int64_t my_slot[kEach];
 #pragma unroll
-    for (int j = 0; j < kTokens; ++j)
-        if (live_task && u.live && group + j * kGroups < n) load8(x[j], in + (group + j * kGroups) * row, u);
-    const int64_t block = slot / kScaleTokens;
-    const int offset = static_cast<int>(slot % kScaleTokens);
-    float *scale_at = (is_v ? g.v_scale : g.k_scale) + block * g.Hkv + h;
-    uint8_t *codes = static_cast<uint8_t *>(is_v ? g.v_cache : g.k_cache) + ((block * kScaleTokens) * g.Hkv + h) * D;
-    const int64_t token = static_cast<int64_t>(g.Hkv) * D;   // bytes from a token to the next
-    const float had = live_task && offset > 0 ? *scale_at : 0.0f;
-    const bool norm = !is_v && g.k_norm;
-    if (norm) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = u.live ? __ldg(g.k_norm + (j < 4 ? u.e0 + j : u.e1 + j - 4)) : 0.0f;
+    for (int k = 0; k < kEach; ++k) {
+        const int j = group + k * kGroups;
+        my_run[k] = __shfl_sync(0xffffffffu, run, j);
+        my_slot[k] = __shfl_sync(0xffffffffu, slot, j);
+        if (my_run[k] >= 0 && u.live) load8(x[k], in + j * row, u);
     }
-    __syncthreads();   // the angles
-    if (!live_task) return;
-    uint32_t largest = 0;
+    float *scales = is_v ? g.v_scale : g.k_scale;
+    const int h = is_v ? task - g.Hkv : task;
+    const bool norm = !is_v && g.k_norm;
 #pragma unroll
-    for (int j = 0; j < kTokens; ++j) {
-        if (j * kGroups >= n) break;
-        if (norm) norm8<L>(x[j], w, D, g.eps);
-        if (u.turn && group + j * kGroups < n) turn8<kInterleaved>(x[j], cs[group + j * kGroups], i);
+    for (int j = 0; j < 8; ++j) w[j] = 1.0f;
+    if (norm && u.live) load_weight(w, g.k_norm, u);
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {   // the scale of tokens that are there before the run
+        const int j = group + k * kGroups;
+        const int64_t first = my_slot[k] - (j - my_run[k]);
+        had[k] = my_run[k] >= 0 && first % kScaleTokens > 0 ? scales[first / kScaleTokens * g.Hkv + h] : 0.0f;
+    }
+    Angles t[kEach];
+#pragma unroll
+    for (int k = 0; k < kEach; ++k)
+        if (u.turn && my_run[k] >= 0) t[k] = angles_of(g, m0 + group + k * kGroups, i);
+    if (tid < kScaleTokens) run_largest[tid] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+        if (!(mine >> (tid / 32 * (32 / L) + k * kGroups) & ((1u << (32 / L)) - 1))) continue;   // no rows for this warp's groups
+        if (norm) norm8<L>(x[k], w, true, g);
+        if (u.turn && my_run[k] >= 0) turn8<kInterleaved>(x[k], t[k]);
+        uint32_t largest = 0;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const uint32_t bits = __float_as_uint(x[j][e]) & 0x7fffffffu;
+            const uint32_t bits = __float_as_uint(x[k][e]) & 0x7fffffffu;
             if (bits < 0x7f800000u) {
                 largest = max(largest, bits);
             } else {
-                x[j][e] = __uint_as_float(0x7fc00000u);   // there is no infinity among the codes
+                x[k][e] = __uint_as_float(0x7fc00000u);   // there is no infinity among the codes
             }
         }
-    }
-    largest = __reduce_max_sync(0xffffffffu, largest);
-    const float scale = fmaxf(scale_for(largest), had), inv = 1.0f / scale;
-    if (had > 0.0f && scale > had) {   // earlier tokens follow: 16 codes a lane
-        const float by = had * inv;
-        for (int c = lane; c < offset * (D / 16); c += 32) {
-            uint4 *at = reinterpret_cast<uint4 *>(codes + (c / (D / 16)) * token + (c % (D / 16)) * 16);
-            uint4 v = *at;
-            uint32_t words[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint32_t lo = e4m3x2_to_f16x2(words[k] & 0xffffu), hi = e4m3x2_to_f16x2(words[k] >> 16);
-                const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&lo)), b = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-                words[k] = e4m3x4(a.x * by, a.y * by, b.x * by, b.y * by);
+        for (int o = L / 2; o > 0; o /= 2) largest = max(largest, __shfl_xor_sync(0xffffffffu, largest, o));
+        if (i == 0 && my_run[k] >= 0) atomicMax(run_largest + my_run[k], largest);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+        const int j = group + k * kGroups;
+        if (my_run[k] < 0) continue;
+        const float scale = fmaxf(scale_for(run_largest[my_run[k]]), had[k]), inv = 1.0f / scale;
+        uint8_t *codes = static_cast<uint8_t *>(is_v ? g.v_cache : g.k_cache);
+        const int64_t token = static_cast<int64_t>(g.Hkv) * D;   // bytes from a token to the next
+        if (j == my_run[k]) {   // the run's first row: its group sees to the scale and the earlier tokens
+            const int64_t block = my_slot[k] / kScaleTokens;
+            if (had[k] > 0.0f && scale > had[k]) {   // 16 codes a lane
+                const int offset = static_cast<int>(my_slot[k] % kScaleTokens), pieces = D / 16;
+                const float by = had[k] * inv;
+                for (int c = i; c < offset * pieces; c += L) {
+                    uint4 *at = reinterpret_cast<uint4 *>(codes + (block * kScaleTokens + c / pieces) * token + h * D + c % pieces * 16);
+                    const uint4 v = *at;
+                    uint32_t words[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        const uint32_t lo = e4m3x2_to_f16x2(words[n] & 0xffffu), hi = e4m3x2_to_f16x2(words[n] >> 16);
+                        const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&lo)), b = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+                        words[n] = e4m3x4(a.x * by, a.y * by, b.x * by, b.y * by);
+                    }
+                    *at = make_uint4(words[0], words[1], words[2], words[3]);
+                }
             }
-            *at = make_uint4(words[0], words[1], words[2], words[3]);
+            if (i == 0) scales[block * g.Hkv + h] = scale;
         }
-    }
-    if (lane == 0) *scale_at = scale;
-    if (!u.live) return;
-#pragma unroll
-    for (int j = 0; j < kTokens; ++j) {
-        const int t = group + j * kGroups;
-        if (t >= n) break;
-        uint8_t *out = codes + (offset + t) * token;
-        *reinterpret_cast<uint32_t *>(out + u.e0) = e4m3x4(x[j][0] * inv, x[j][1] * inv, x[j][2] * inv, x[j][3] * inv);
-        *reinterpret_cast<uint32_t *>(out + u.e1) = e4m3x4(x[j][4] * inv, x[j][5] * inv, x[j][6] * inv, x[j][7] * inv);
+        if (!u.live) continue;
+        uint8_t *out = codes + my_slot[k] * token + h * D;
+        *reinterpret_cast<uint32_t *>(out + u.e0) = e4m3x4(x[k][0] * inv, x[k][1] * inv, x[k][2] * inv, x[k][3] * inv);
+        *reinterpret_cast<uint32_t *>(out + u.e1) = e4m3x4(x[k][4] * inv, x[k][5] * inv, x[k][6] * inv, x[k][7] * inv);
     }
 }
 
-// Grid (M, kv_ctas + CTAs of kThreads / L query heads). The first kv_ctas of a row have a warp
-// for each k and v head; they go on only where the row starts a run.
-template <typename T, bool kInterleaved, int L>
-__global__ void __launch_bounds__(kThreads) rope_e4m3_kernel(const __grid_constant__ NormRopeArgs g, int kv_ctas)
+// Grid: windows * 2 Hkv CTAs of a window's head, then rows / R * q_ctas of kThreads / L query heads.
+template <typename T, bool kInterleaved, int L, int R>
+__global__ void __launch_bounds__(kThreads) rope_e4m3_kernel(const __grid_constant__ NormRopeArgs g, int windows, int q_ctas)
 {
-    __shared__ float2 cs[kScaleTokens][kMaxRopePairs / 2];
+    __shared__ uint32_t run_largest[kScaleTokens];
     grid_launch_dependents();
     grid_dependency_wait();
-    const int m = blockIdx.x, tid = threadIdx.x, pairs = g.rot / 2;
-    if (static_cast<int>(blockIdx.y) >= kv_ctas) {
-        row_heads<T, kInterleaved, L>(g, m, (static_cast<int>(blockIdx.y) - kv_ctas) * (kThreads / L), g.Hq, -1, &cs[0][0]);
-        return;
+    const int kv = windows * 2 * g.Hkv, c = static_cast<int>(blockIdx.x);
+    if (c < kv) {
+        window_head<kInterleaved, L>(g, c / (2 * g.Hkv), c % (2 * g.Hkv), run_largest);
+    } else {
+        row_heads<T, kInterleaved, L, R>(g, (c - kv) / q_ctas * R, (c - kv) % q_ctas * (kThreads / L), g.Hq);
     }
-    const int64_t slot = blockIdx.y == 0 ? slot_of(g, m) : g.slots[m];
-    if (slot < 0 || slot >= g.n_slots) return;
-    if (slot % kScaleTokens != 0 && m > 0 && g.slots[m - 1] == slot - 1) return;   // an earlier row's run
-    const int lane = tid & 31, most = kScaleTokens - static_cast<int>(slot % kScaleTokens);
-    const bool goes_on = lane < most && lane < g.M - m && g.slots[m + lane] == slot + lane;
-    const int n = __ffs(~__ballot_sync(0xffffffffu, goes_on)) - 1;   // at least 1, at most 16
-    for (int a = tid; a < n * pairs; a += kThreads) cs[a / pairs][a % pairs] = angle_of(g, m + a / pairs, a % pairs);
-    const int task = static_cast<int>(blockIdx.y) * kWarps + tid / 32;
-    block_head<kInterleaved, L>(g, m, n, slot, task, cs, task < 2 * g.Hkv);
 }
 
-template <typename T, bool kInterleaved, int L>
+template <typename T, bool kInterleaved, int L, int R>
 cudaError_t launch_typed(const NormRopeArgs &g, cudaStream_t s)
 {
     constexpr int kHeads = kThreads / L;
-    const bool codes = g.k_scale != nullptr;
-    const int kv_ctas = codes ? (2 * g.Hkv + kWarps - 1) / kWarps : 0, heads = codes ? g.Hq : g.Hq + 2 * g.Hkv;
+    const int row_ctas = (g.M + R - 1) / R;
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kThreads);
-    cfg.gridDim = dim3(static_cast<unsigned>(g.M), static_cast<unsigned>(kv_ctas + (heads + kHeads - 1) / kHeads));
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = set_launch_overlap_attr(attr);
     if constexpr (L <= 16) {   // codes: heads of 128 at most
-        if (codes) return cudaLaunchKernelEx(&cfg, rope_e4m3_kernel<T, kInterleaved, L>, g, kv_ctas);
+        if (g.k_scale) {
+            const int windows = (g.M + kScaleTokens - 1) / kScaleTokens, q_ctas = (g.Hq + kHeads - 1) / kHeads;
+            const int64_t grid = static_cast<int64_t>(windows) * 2 * g.Hkv + static_cast<int64_t>(row_ctas) * q_ctas;
+            if (grid > 0x7fffffff) return cudaErrorInvalidValue;
+            cfg.gridDim = dim3(static_cast<unsigned>(grid));
+            return cudaLaunchKernelEx(&cfg, rope_e4m3_kernel<T, kInterleaved, L, R>, g, windows, q_ctas);
+        }
     }
-    return cudaLaunchKernelEx(&cfg, norm_rope_kernel<T, kInterleaved, L>, g);
+    cfg.gridDim = dim3(static_cast<unsigned>(row_ctas), static_cast<unsigned>((g.Hq + 2 * g.Hkv + kHeads - 1) / kHeads));
+    return cudaLaunchKernelEx(&cfg, norm_rope_kernel<T, kInterleaved, L, R>, g);
+}
+
+// Two rows a CTA where there are CTAs enough: weights and addresses are worked out once.
+template <typename T, bool kInterleaved, int L>
+cudaError_t launch_rows(const NormRopeArgs &g, cudaStream_t s)
+{
+    return g.M >= kTwoRows ? launch_typed<T, kInterleaved, L, 2>(g, s) : launch_typed<T, kInterleaved, L, 1>(g, s);
 }
 
 template <typename T, bool kInterleaved>
 cudaError_t launch_lanes(const NormRopeArgs &g, cudaStream_t s)
 {
-    if (g.D <= 64) return launch_typed<T, kInterleaved, 8>(g, s);
-    if (g.D <= 128) return launch_typed<T, kInterleaved, 16>(g, s);
-    return launch_typed<T, kInterleaved, 32>(g, s);
+    if (g.D <= 64) return launch_rows<T, kInterleaved, 8>(g, s);
+    if (g.D <= 128) return launch_rows<T, kInterleaved, 16>(g, s);
+    return launch_rows<T, kInterleaved, 32>(g, s);
 }
 
 }  // namespace

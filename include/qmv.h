@@ -381,7 +381,7 @@ QMV_API qmv_status qmv_penalize_logits(const float *logits, const int32_t *token
  * qmv_rope_append with an RMS norm of each q and k head before it is turned:
  *   x[i] = x[i] / sqrt(sum_j x[j]^2 / D + eps) * q_norm[i]   (k_norm for k heads; v has none)
  * in fp32, squares included (a head with elements of 1e19 or more overflows them).
- *   q_norm, k_norm  fp32 [D], each NULL for no norm; eps 0 or more and finite.
+ *   q_norm, k_norm  fp32 [D], 16-byte aligned, each NULL for no norm; eps 0 or more and finite.
  *   All else as in qmv_rope_append.
  */
 QMV_API qmv_status qmv_norm_rope_append(const float *qkv, const int32_t *positions, const float *table,
