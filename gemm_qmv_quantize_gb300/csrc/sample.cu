@@ -13,11 +13,12 @@
 // same token, and nothing is sorted: the cuts are found by histograms.
 //
 // A row is a cluster's: each CTA keeps a slice of it in shared memory. Pass 1 finds the
-// maximum. Pass 2, where there is a top-k or top-p, a histogram of 1024 bins of t, counts and
-// sums; the first CTA adds them over the cluster and finds the bin that holds a cut; bins of
-// more than 256 tokens are split again by the bits of (logit, index), then the bin's tokens are
-// ranked. Pass 3 sums what is kept, in pieces of 128 tokens, and the piece that u falls to
-// is gone through.
+// maximum. Pass 2, where there is a top-k or top-p, a histogram of 1024 bins of t (counts, and sums
+// where a top-p needs them); the first CTA adds them over the cluster and finds the bin that
+// holds the cut. Where the tokens up to that bin are few, as behind most top-k, they go to the
+// first CTA, which ranks them and draws. Else only the bin's tokens do (bins of more than 256
+// are split again by the bits of (logit, index)); then pass 3 sums what is kept, in pieces of
+// 128 tokens, and the piece that u falls to is gone through.
 #include <algorithm>
 
 #include <cooperative_groups.h>
@@ -41,10 +42,10 @@ constexpr int64_t kMaxSlice = 32768 + 8; // tokens of a CTA
 constexpr uint64_t kOne = 1ull << kFraction, kAll = ~0ull;
 
 struct Found {                 // a bin with a cut in it
-    uint64_t lo, hi;           // the codes of its tokens are in lo .. hi
+    uint64_t lo, hi;           // the codes of its tokens are in lo .. hi; of the first histogram's: its number
     uint64_t need;             // tokens, or weight, up to the cut, of this bin
     uint64_t before;           // weight before the bin
-    uint32_t count;            // its tokens; 0: there is no cut
+    uint32_t count, upto;      // its tokens (0: there is no cut), and those of it and the bins before it
 };
 
 struct alignas(16) Shared {
@@ -52,16 +53,39 @@ struct alignas(16) Shared {
     uint64_t before[kBins + 1];                       // the first histogram's sums, added up (first CTA)
     uint32_t first_count[kBins];
     uint64_t table[256];                              // 2^(40 - j / 256)
-    uint64_t list[kRanked];
+    uint64_t list[2][kRanked];                        // codes that were sent to the first CTA, for each cut
+    uint64_t list_weight[kRanked];
     uint64_t piece[kMaxPieces];
     uint64_t warp_sum[kWarps];
     uint32_t warp_count[kWarps];
     uint64_t total, lo, hi;                           // of this CTA
-    uint64_t cut, upto;
-    Found found;
-    uint32_t top, listed;
-    int token;
+    uint64_t cut[2], upto;
+    Found found[2];
+    uint32_t top, listed[2];
 };
+
+// 2^(40 - j / 256) for j = 0 .. 255, worked out by the compiler: products of 2^(-2^k / 256), each the root of
+// the one before it (Newton's iteration), in doubles.
+struct Table {
+    uint64_t v[256];
+    constexpr Table() : v()
+    {
+        double root[8] = {};
+        double r = 0.5;
+        for (int k = 7; k >= 0; --k) {
+            double x = 1.0;
+            for (int i = 0; i < 40; ++i) x = 0.5 * (x + r / x);
+            root[k] = r = x;
+        }
+        for (int j = 0; j < 256; ++j) {
+            double p = 1099511627776.0;
+            for (int k = 0; k < 8; ++k)
+                if (j >> k & 1) p *= root[k];
+            v[j] = static_cast<uint64_t>(p + 0.5);
+        }
+    }
+};
+__device__ const Table g_table = Table();
 
 // Logits in their order as whole numbers, NaN as -inf and -0 as 0.
 __device__ __forceinline__ float cleaned(float x) { return x != x ? -INFINITY : x + 0.0f; }
@@ -137,24 +161,25 @@ __device__ __forceinline__ void clear_histogram(Shared &s)
 
 // The first CTA: the cluster's histogram, and of it the bin in which the count, or the weight,
 // reaches `need`. First level: kept for later cuts. Bins are [lo + (bin << shift), + 1 << shift).
-__device__ void pick(cg::cluster_group &cluster, Shared &s, bool by_weight, bool first_level, uint64_t need, uint64_t lo,
-                     uint64_t hi, int shift, uint64_t before)
+__device__ void pick(cg::cluster_group &cluster, Shared &s, Found &found, bool weights, bool by_weight, bool first_level, uint64_t need,
+                     uint64_t lo, uint64_t hi, int shift, uint64_t before)
 {
     constexpr int kEach = kBins / kThreads;
-    uint32_t n[kEach], n_sum = 0;
-    uint64_t w[kEach], w_sum = 0;
-    if (threadIdx.x == 0) s.found.count = 0;
-#pragma unroll
-    for (int j = 0; j < kEach; ++j) {
-        const int bin = threadIdx.x * kEach + j;
-        n[j] = 0, w[j] = 0;
-        for (unsigned r = 0; r < cluster.num_blocks(); ++r) {
-            const Shared &o = *cluster.map_shared_rank(&s, r);
-            n[j] += o.count[bin];
-            w[j] += (static_cast<uint64_t>(o.high[bin]) << 32) + o.low[bin];
+    uint32_t n[kEach] = {}, n_sum = 0;
+    uint64_t w[kEach] = {}, w_sum = 0;
+    if (threadIdx.x == 0) found.count = 0;
+#pragma unroll 4
+    for (unsigned r = 0; r < cluster.num_blocks(); ++r) {
+        const Shared &o = *cluster.map_shared_rank(&s, r);
+        const uint2 c = reinterpret_cast<const uint2 *>(o.count)[threadIdx.x];
+        n[0] += c.x, n[1] += c.y;
+        if (weights) {
+            const uint2 l = reinterpret_cast<const uint2 *>(o.low)[threadIdx.x], h = reinterpret_cast<const uint2 *>(o.high)[threadIdx.x];
+            w[0] += (static_cast<uint64_t>(h.x) << 32) + l.x, w[1] += (static_cast<uint64_t>(h.y) << 32) + l.y;
         }
-        n_sum += n[j], w_sum += w[j];
     }
+    static_assert(kEach == 2, "two bins a thread");
+    n_sum = n[0] + n[1], w_sum = w[0] + w[1];
     uint32_t n_at = n_sum;
     uint64_t w_at = w_sum;
     scan(s, n_at, w_at);
@@ -163,19 +188,100 @@ __device__ void pick(cg::cluster_group &cluster, Shared &s, bool by_weight, bool
     for (int j = 0; j < kEach; ++j) {
         const int bin = threadIdx.x * kEach + j;
         if (first_level) s.before[bin] = w_at, s.first_count[bin] = n[j];
+        if (by_weight && first_level) need = 0;   // not known before all sums are
         const uint64_t at = by_weight ? w_at : n_at, with = at + (by_weight ? w[j] : n[j]);
         if (at < need && need <= with) {
-            s.found.count = n[j];
-            s.found.need = need - at;
-            s.found.before = before + w_at;
-            s.found.lo = lo + (static_cast<uint64_t>(bin) << shift);
-            s.found.hi = s.found.lo + ((static_cast<uint64_t>(1) << shift) - 1);
-            if (s.found.hi > hi) s.found.hi = hi;
+            found.count = n[j];
+            found.upto = n_at + n[j];
+            found.need = need - at;
+            found.before = before + w_at;
+            found.lo = lo + (static_cast<uint64_t>(bin) << shift);
+            found.hi = found.lo + ((static_cast<uint64_t>(1) << shift) - 1);
+            if (found.hi > hi) found.hi = hi;
         }
         n_at += n[j], w_at += w[j];
     }
     if (first_level && threadIdx.x == kThreads - 1) s.before[kBins] = w_at;
     __syncthreads();
+}
+
+// The largest whole number not above p w, and whether it is p w; 0 <= p < 1.
+__device__ __forceinline__ uint64_t share_of(float p, uint64_t w, bool &exact)
+{
+    const uint32_t bits = __float_as_uint(p);
+    const int e = static_cast<int>(bits >> 23), sh = 150 - max(e, 1);   // p = mant 2^-sh, sh is 24 at least
+    const uint64_t mant = e ? (bits & 0x7fffffu) | 0x800000u : bits & 0x7fffffu;
+    const uint64_t lo = w * mant, hi = __umul64hi(w, mant);
+    exact = sh < 64 ? (lo & ((static_cast<uint64_t>(1) << sh) - 1)) == 0 : mant == 0;
+    return sh < 64 ? (hi << (64 - sh)) | (lo >> sh) : sh < 128 ? hi >> (sh - 64) : 0;
+}
+// The least whole number not below p w; 0 < p < 1.
+__device__ __forceinline__ uint64_t share_above(float p, uint64_t w)
+{
+    bool exact;
+    const uint64_t y = share_of(p, w, exact);
+    return exact ? y : y + 1;
+}
+// a / b rounded about once: the quotient of both as fp32, and what that leaves.
+__device__ __forceinline__ float ratio(uint64_t a, uint64_t b)
+{
+    const float ah = static_cast<float>(a), bh = static_cast<float>(b), q = ah / bh;
+    const float al = static_cast<float>(static_cast<int64_t>(a - static_cast<uint64_t>(ah))), bl = static_cast<float>(static_cast<int64_t>(b - static_cast<uint64_t>(bh)));
+    return q + (fmaf(-q, bh, ah) + fmaf(-q, bl, al)) / bh;
+}
+// The whole number that a kept token's running sum has to exceed.
+__device__ __forceinline__ uint64_t drawn(float u, uint64_t total)
+{
+    bool exact;
+    return u >= 1.0f ? total - 1 : u > 0.0f ? share_of(u, total, exact) : 0;
+}
+
+__device__ __forceinline__ uint64_t sum_over_cta(Shared &s, uint64_t v)
+{
+    v = warp_sum64(v);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) s.warp_sum[threadIdx.x / 32] = v;
+    __syncthreads();
+    v = 0;
+    for (int i = 0; i < kWarps; ++i) v += s.warp_sum[i];
+    return v;
+}
+
+// The draw from the n codes of s.list[0], among which are the first k, or else all that a top-p keeps,
+// whose share is of `whole`, the sum over the row.
+__device__ void draw_from_list(Shared &s, const SampleArgs &g, const Row &r, int m, int n, int k, bool cut_k, bool cut_p, float top_p, uint64_t whole, uint64_t least, float u)
+{
+    const int tid = threadIdx.x;
+    const uint64_t code = tid < n ? s.list[0][tid] : kAll;
+    const uint64_t w = tid < n ? weight(r, of_key(~static_cast<uint32_t>(code >> 32))) : 0;
+    if (tid < n) s.list_weight[tid] = w;
+    __syncthreads();
+    int rank = 0;
+    uint64_t before = 0;
+    if (tid < n) {
+        for (int j = 0; j < n; ++j) {
+            const bool b = s.list[0][j] < code;
+            rank += b;
+            before += b ? s.list_weight[j] : 0;
+        }
+    }
+    bool kept = tid < n && rank < k;
+    if (cut_p) {
+        const uint64_t sum = sum_over_cta(s, kept ? w : 0);
+        kept = kept && before < share_above(top_p, cut_k ? sum : whole);
+    }
+    kept = kept && w >= least;
+    const uint64_t total = sum_over_cta(s, kept ? w : 0), y = drawn(u, total);
+    if (tid < n) s.list_weight[tid] = kept ? w : 0;
+    __syncthreads();
+    if (!kept) return;
+    const uint32_t index = static_cast<uint32_t>(code);
+    uint64_t at = 0;
+    for (int j = 0; j < n; ++j) at += static_cast<uint32_t>(s.list[0][j]) < index ? s.list_weight[j] : 0;
+    if (at <= y && y < at + w) {
+        g.token[m] = static_cast<int32_t>(index);
+        if (g.prob) g.prob[m] = ratio(w, total);
+    }
 }
 
 // Grid (C, M) in clusters of C. Dynamic shared memory: Shared, then the slice.
@@ -184,13 +290,14 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     extern __shared__ __align__(16) uint8_t smem[];
     Shared &s = *reinterpret_cast<Shared *>(smem);
     float *x = reinterpret_cast<float *>(smem + sizeof(Shared));
+    float4 *x4 = reinterpret_cast<float4 *>(x);
     cg::cluster_group cluster = cg::this_cluster();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32, m = blockIdx.y;
     const unsigned rank = cluster.block_rank(), C = cluster.num_blocks();
     Shared &lead = *cluster.map_shared_rank(&s, 0);
-    for (int j = tid; j < 256; j += kThreads) s.table[j] = static_cast<uint64_t>(__double2ll_rn(exp2(40.0 - j / 256.0)));
+    if (tid < 256) s.table[tid] = g_table.v[tid];
     clear_histogram(s);
-    if (tid == 0) s.top = 0, s.lo = kAll, s.hi = 0, s.listed = 0, s.cut = kAll;
+    if (tid == 0) s.top = 0, s.lo = kAll, s.hi = 0, s.listed[0] = s.listed[1] = 0, s.cut[0] = s.cut[1] = kAll;
     grid_launch_dependents();
     grid_dependency_wait();
     // the slice: 16-byte pieces of the row from the boundary before it on; what is not the row's is -inf
@@ -199,13 +306,13 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     const int all = (g.V + skew + 3) / 4, each = (all + static_cast<int>(C) - 1) / static_cast<int>(C);
     const int from = min(all, static_cast<int>(rank) * each), pieces = min(all, from + each) - from;
     const int index0 = 4 * from - skew;   // of x[0]
-    uint32_t top = 0;
-#pragma unroll 4
+    float most = -INFINITY;
+#pragma unroll 8
     for (int i = tid; i < pieces; i += kThreads) {
         const int at = index0 + 4 * i;
         float4 v;
         if (at >= 0 && at + 4 <= g.V) {
-            v = __ldg(reinterpret_cast<const float4 *>(row + at));
+            v = __ldcs(reinterpret_cast<const float4 *>(row + at));
         } else {
             v.x = at >= 0 && at < g.V ? row[at] : -INFINITY;
             v.y = at + 1 >= 0 && at + 1 < g.V ? row[at + 1] : -INFINITY;
@@ -213,27 +320,26 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
             v.w = at + 3 >= 0 && at + 3 < g.V ? row[at + 3] : -INFINITY;
         }
         v = make_float4(cleaned(v.x), cleaned(v.y), cleaned(v.z), cleaned(v.w));
-        reinterpret_cast<float4 *>(x)[i] = v;
-        top = max(max(top, max(key_of(v.x), key_of(v.y))), max(key_of(v.z), key_of(v.w)));
+        x4[i] = v;
+        most = fmaxf(fmaxf(most, fmaxf(v.x, v.y)), fmaxf(v.z, v.w));
     }
     const float T = g.temperature ? g.temperature[m] : 1.0f, u = g.u[m];
     const float top_p = g.top_p ? g.top_p[m] : 1.0f, min_p = g.min_p ? g.min_p[m] : 0.0f;
     int k = g.top_k ? g.top_k[m] : 0;
     if (k <= 0 || k > g.V) k = g.V;
-    const bool greedy = !(T > 0.0f);
-    if (greedy || top_p <= 0.0f || min_p > 1.0f) k = 1;
-    top = __reduce_max_sync(0xffffffffu, top);
+    if (!(T > 0.0f) || top_p <= 0.0f || min_p > 1.0f) k = 1;
+    uint32_t top = __reduce_max_sync(0xffffffffu, key_of(most));
     __syncthreads();
     if (lane == 0) atomicMax(&s.top, top);
     cluster.sync();
-    for (unsigned r = 0; r < C; ++r) top = max(top, cluster.map_shared_rank(&s, r)->top);
+    for (unsigned q = 0; q < C; ++q) top = max(top, cluster.map_shared_rank(&s, q)->top);
+    // log2(e) / T in two terms, 2^-46 off
+    constexpr float kLog2eHi = 1.44269502e+00f, kLog2eLo = 1.92596299e-08f;
     Row r;
     r.top = of_key(top);
     r.table = s.table;
-    const double c = 1.4426950408889634 / static_cast<double>(T);
-    r.c_hi = static_cast<float>(c);
-    r.c_lo = static_cast<float>(c - static_cast<double>(r.c_hi));
-    const int n = 4 * pieces;
+    r.c_hi = kLog2eHi / T;
+    r.c_lo = T < INFINITY ? (fmaf(-r.c_hi, T, kLog2eHi) + kLog2eLo) / T : 0.0f;
     if (top <= key_of(-INFINITY)) {   // no logit above -inf
         if (rank == 0 && tid == 0) {
             g.token[m] = -1;
@@ -242,189 +348,209 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
         cluster.sync();   // nobody leaves while others read its memory
         return;
     }
+    // f(logit, index) for every token of the slice
+    auto each_token = [&](auto f) {
+        for (int i = tid; i < pieces; i += kThreads) {
+            const float4 v = x4[i];
+            const uint32_t at = static_cast<uint32_t>(index0 + 4 * i);
+            f(v.x, at), f(v.y, at + 1), f(v.z, at + 2), f(v.w, at + 3);
+        }
+    };
+    const float per_t = static_cast<float>(kBins) / kMostT;
+    auto bin_of = [&](float t) { return min(static_cast<int>(t * per_t), kBins - 1); };
+    const uint64_t least = min_p > 0.0f && k > 1 ? (min_p >= 1.0f ? kOne : max(static_cast<unsigned long long>(1), static_cast<unsigned long long>(share_above(min_p, kOne)))) : 1;
     uint64_t cut = kAll;   // the last kept token's code
     const bool cut_p = top_p < 1.0f && k > 1, cut_k = k < g.V && k > 1;
     if (k == 1) {   // the first of the largest
         uint64_t first = kAll;
-        for (int i = tid; i < n; i += kThreads)
-            if (x[i] == r.top) first = min(first, code_of(x[i], static_cast<uint32_t>(index0 + i)));
+        each_token([&](float v, uint32_t at) {
+            if (v == r.top) first = min(static_cast<unsigned long long>(first), static_cast<unsigned long long>(code_of(v, at)));
+        });
         if (first != kAll) atomicMin(reinterpret_cast<unsigned long long *>(&s.lo), first);
         cluster.sync();
-        for (unsigned q = 0; q < C; ++q) cut = min(cut, cluster.map_shared_rank(&s, q)->lo);
-    } else if (cut_p || cut_k) {
-        const float per_t = static_cast<float>(kBins) / kMostT;
-        auto bin_of = [&](float t) { return min(static_cast<int>(t * per_t), kBins - 1); };
-        for (int i = tid; i < n; i += kThreads) {
-            const float t = rough_t(r, x[i]);
-            if (!(t <= kMostT)) continue;
-            const int bin = bin_of(t);
-            atomicAdd(&s.count[bin], 1u);
-            if (cut_p) add64(s, bin, weight(r, x[i]));
+        for (unsigned q = 0; q < C; ++q) {
+            const uint64_t o = cluster.map_shared_rank(&s, q)->lo;
+            if (o < cut) cut = o;
+        }
+        if (rank == 0 && tid == 0) {
+            g.token[m] = static_cast<int32_t>(static_cast<uint32_t>(cut));
+            if (g.prob) g.prob[m] = 1.0f;
         }
         cluster.sync();
-        bool first_level = true;
-        for (int by_weight = cut_k ? 0 : 1; by_weight < (cut_p ? 2 : 1); ++by_weight) {
+        return;
+    }
+    if (cut_p || cut_k) {
+        // Behind a small top-k the tokens up to the cut are most likely few, and weights not needed for more than those.
+        bool weights = cut_p && !(cut_k && k <= kRanked / 2);
+        for (;;) {
+            each_token([&](float v, uint32_t) {
+                const float t = rough_t(r, v);
+                if (!(t <= kMostT)) return;
+                const int bin = bin_of(t);
+                atomicAdd(&s.count[bin], 1u);
+                if (weights) add64(s, bin, weight(r, v));
+            });
+            cluster.sync();
             if (rank == 0) {
-                if (first_level) {   // without a top-k the share is of the whole sum, which is known after this
-                    pick(cluster, s, false, true, static_cast<uint64_t>(k), 0, kAll, 0, 0);
-                    if (tid == 0) s.upto = s.before[kBins];
-                    __syncthreads();
-                }
-                if (by_weight) {
-                    if (tid == 0) {
-                        s.found.count = 0;
-                        const uint64_t all_w = s.upto;
-                        // the least whole number not below top_p all_w
-                        const uint32_t bits = __float_as_uint(top_p);
-                        const int e = static_cast<int>(bits >> 23);
-                        const uint64_t mant = e ? (bits & 0x7fffffu) | 0x800000u : bits & 0x7fffffu;
-                        const int sh = 150 - max(e, 1);   // top_p = mant 2^-sh, 24 at least
-                        const uint64_t lo = all_w * mant, hi = __umul64hi(all_w, mant);
-                        uint64_t y;
-                        if (sh < 64) {
-                            y = (hi << (64 - sh)) | (lo >> sh);
-                            if (lo & ((1ull << sh) - 1)) ++y;
-                        } else {
-                            y = sh < 128 ? (hi >> (sh - 64)) : 0;
-                            if (y < 1) y = 1;
-                        }
-                        s.total = y;
+                pick(cluster, s, s.found[0], weights, !cut_k, true, static_cast<uint64_t>(k), 0, kAll, 0, 0);
+                if (tid == 0) s.upto = s.before[kBins];
+                if (!cut_k) {   // the share of the whole sum
+                    const uint64_t y = share_above(top_p, s.before[kBins]);
+                    uint32_t n = 0;
+                    for (int j = 0; j < kBins / kThreads; ++j) {
+                        const int bin = tid * (kBins / kThreads) + j;
+                        if (s.before[bin] < y) n += s.first_count[bin];   // bins up to the cut's, all of them
                     }
-                    __syncthreads();
-                    const uint64_t y = s.total;
+                    const uint32_t upto = static_cast<uint32_t>(sum_over_cta(s, n));
                     for (int bin = tid; bin < kBins; bin += kThreads) {
-                        if (s.before[bin] < y && y <= s.before[bin + 1]) {
-                            s.found.count = s.first_count[bin];
-                            s.found.need = y - s.before[bin];
-                            s.found.before = s.before[bin];
-                            s.found.lo = static_cast<uint64_t>(bin);
-                        }
+                        if (s.before[bin] >= y || y > s.before[bin + 1]) continue;
+                        s.found[0] = Found{static_cast<uint64_t>(bin), 0, y - s.before[bin], s.before[bin], s.first_count[bin], upto};
                     }
                 }
-                __syncthreads();
-            }
-            first_level = false;
-            cluster.sync();
-            Found f = lead.found;
-            cluster.sync();
-            if (!f.count) continue;
-            // the codes that the bin's tokens span
-            const int bin = static_cast<int>(f.lo);   // the first level's
-            if (tid == 0) s.lo = kAll, s.hi = 0;
-            __syncthreads();
-            uint64_t lo = kAll, hi = 0;
-            for (int i = tid; i < n; i += kThreads) {
-                const float t = rough_t(r, x[i]);
-                if (!(t <= kMostT) || bin_of(t) != bin) continue;
-                const uint64_t code = code_of(x[i], static_cast<uint32_t>(index0 + i));
-                lo = min(lo, code), hi = max(hi, code);
-            }
-            if (lo != kAll) {
-                atomicMin(reinterpret_cast<unsigned long long *>(&s.lo), lo);
-                atomicMax(reinterpret_cast<unsigned long long *>(&s.hi), hi);
             }
             cluster.sync();
-            for (unsigned q = 0; q < C; ++q) {
-                const Shared &o = *cluster.map_shared_rank(&s, q);
-                lo = min(lo, o.lo), hi = max(hi, o.hi);
+            const Found f = lead.found[0];
+            if (f.count && f.upto <= kRanked) {   // few tokens: the first CTA sees to them
+                const int last = static_cast<int>(f.lo);
+                each_token([&](float v, uint32_t at) {
+                    const float t = rough_t(r, v);
+                    if (!(t <= kMostT) || bin_of(t) > last) return;
+                    const uint32_t i = atomicAdd(&lead.listed[0], 1u);
+                    if (i < kRanked) lead.list[0][i] = code_of(v, at);
+                });
+                cluster.sync();
+                if (rank == 0) draw_from_list(s, g, r, m, static_cast<int>(f.upto), k, cut_k, cut_p, top_p, s.upto, least, u);
+                return;   // the others' memory is not read any more
             }
-            f.lo = lo, f.hi = hi;
+            if (weights || !cut_p) break;
+            weights = true;   // more than a few after all
+            clear_histogram(s);
             cluster.sync();
-            while (f.count > kRanked) {
-                const int shift = max(0, 64 - __clzll(f.hi - f.lo) - 10);
-                clear_histogram(s);
-                __syncthreads();
-                for (int i = tid; i < n; i += kThreads) {
-                    const uint64_t code = code_of(x[i], static_cast<uint32_t>(index0 + i));
-                    if (code < f.lo || code > f.hi) continue;
-                    const int b = static_cast<int>((code - f.lo) >> shift);
-                    atomicAdd(&s.count[b], 1u);
-                    if (cut_p) add64(s, b, weight(r, x[i]));
+        }
+        for (int by_weight = cut_k ? 0 : 1; by_weight < (cut_p ? 2 : 1); ++by_weight) {
+            const int which = by_weight && cut_k ? 1 : 0;
+            if (which) {   // a top-p behind a top-k
+                if (rank == 0) {
+                    if (tid == 0) s.found[1].count = 0;
+                    const uint64_t y = share_above(top_p, s.upto);
+                    __syncthreads();
+                    for (int bin = tid; bin < kBins; bin += kThreads) {
+                        if (s.before[bin] >= y || y > s.before[bin + 1]) continue;
+                        s.found[1] = Found{static_cast<uint64_t>(bin), 0, y - s.before[bin], s.before[bin], s.first_count[bin], 0};
+                    }
                 }
                 cluster.sync();
-                if (rank == 0) pick(cluster, s, by_weight, false, f.need, f.lo, f.hi, shift, f.before);
+            }
+            Found f = lead.found[which];
+            if (!f.count) continue;
+            const int bin = static_cast<int>(f.lo);   // the first histogram's
+            const bool split = f.count > kRanked;
+            if (split) {
+                // the codes that the bin's tokens span
+                if (tid == 0) s.lo = kAll, s.hi = 0;
+                __syncthreads();
+                unsigned long long lo = kAll, hi = 0;
+                each_token([&](float v, uint32_t at) {
+                    const float t = rough_t(r, v);
+                    if (!(t <= kMostT) || bin_of(t) != bin) return;
+                    const unsigned long long code = code_of(v, at);
+                    lo = min(lo, code), hi = max(hi, code);
+                });
+                if (lo != kAll) {
+                    atomicMin(reinterpret_cast<unsigned long long *>(&s.lo), lo);
+                    atomicMax(reinterpret_cast<unsigned long long *>(&s.hi), hi);
+                }
                 cluster.sync();
-                f = lead.found;
-                cluster.sync();
+                for (unsigned q = 0; q < C; ++q) {
+                    const Shared &o = *cluster.map_shared_rank(&s, q);
+                    lo = min(lo, static_cast<unsigned long long>(o.lo)), hi = max(hi, static_cast<unsigned long long>(o.hi));
+                }
+                f.lo = lo, f.hi = hi;
+                while (f.count > kRanked) {
+                    const int shift = max(0, 64 - __clzll(static_cast<long long>(f.hi - f.lo)) - 10);
+                    clear_histogram(s);
+                    __syncthreads();
+                    each_token([&](float v, uint32_t at) {
+                        const uint64_t code = code_of(v, at);
+                        if (code < f.lo || code > f.hi) return;
+                        const int b = static_cast<int>((code - f.lo) >> shift);
+                        atomicAdd(&s.count[b], 1u);
+                        if (cut_p) add64(s, b, weight(r, v));
+                    });
+                    cluster.sync();
+                    if (rank == 0) pick(cluster, s, s.found[which], cut_p, by_weight, false, f.need, f.lo, f.hi, shift, f.before);
+                    cluster.sync();
+                    f = lead.found[which];
+                    cluster.sync();
+                }
             }
             // the bin's tokens, in no order, to the first CTA, which ranks them
-            for (int i = tid; i < n; i += kThreads) {
-                const uint64_t code = code_of(x[i], static_cast<uint32_t>(index0 + i));
-                if (code < f.lo || code > f.hi) continue;
-                const uint32_t at = atomicAdd(&lead.listed, 1u);
-                if (at < kRanked) lead.list[at] = code;
-            }
+            each_token([&](float v, uint32_t at) {
+                const uint64_t code = code_of(v, at);
+                if (split) {
+                    if (code < f.lo || code > f.hi) return;
+                } else {
+                    const float t = rough_t(r, v);
+                    if (!(t <= kMostT) || bin_of(t) != bin) return;
+                }
+                const uint32_t i = atomicAdd(&lead.listed[which], 1u);
+                if (i < kRanked) lead.list[which][i] = code;
+            });
             cluster.sync();
             if (rank == 0) {
-                if (tid < static_cast<int>(f.count)) {
-                    const uint64_t code = s.list[tid];
+                const int n = static_cast<int>(f.count);
+                const uint64_t code = tid < n ? s.list[which][tid] : kAll;
+                const uint64_t mine = tid < n && cut_p ? weight(r, of_key(~static_cast<uint32_t>(code >> 32))) : 0;
+                if (tid < n) s.list_weight[tid] = mine;
+                __syncthreads();
+                if (tid < n) {
                     uint64_t rank_of = 0, w_before = 0;
-                    for (uint32_t j = 0; j < f.count; ++j) {
-                        const uint64_t o = s.list[j];
-                        if (o >= code) continue;
-                        ++rank_of;
-                        if (cut_p) w_before += weight(r, of_key(~static_cast<uint32_t>(o >> 32)));
+                    for (int j = 0; j < n; ++j) {
+                        const bool b = s.list[which][j] < code;
+                        rank_of += b;
+                        w_before += b ? s.list_weight[j] : 0;
                     }
-                    const uint64_t mine = cut_p ? weight(r, of_key(~static_cast<uint32_t>(code >> 32))) : 0;
                     const uint64_t at = by_weight ? w_before : rank_of, with = at + (by_weight ? mine : 1);
                     if (at < f.need && f.need <= with) {
-                        s.cut = code;
+                        s.cut[which] = code;
                         s.upto = f.before + w_before + mine;
                     }
                 }
-                __syncthreads();
-                if (tid == 0) s.listed = 0;
             }
             cluster.sync();
-            cut = min(cut, lead.cut);
-            cluster.sync();
+            if (lead.cut[which] < cut) cut = lead.cut[which];
         }
     }
     // what is kept, in pieces of 128 tokens
-    const uint64_t least = min_p > 0.0f && k > 1 ? static_cast<uint64_t>(ceil(static_cast<double>(min_p) * static_cast<double>(kOne))) : 1;
-    auto kept = [&](int i) -> uint64_t {
-        const float v = x[i];
-        if (code_of(v, static_cast<uint32_t>(index0 + i)) > cut) return 0;
+    auto kept = [&](float v, uint32_t at) -> uint64_t {
+        if (code_of(v, at) > cut) return 0;
         const uint64_t w = weight(r, v);
         return w >= least ? w : 0;
     };
     uint64_t mine = 0;
     for (int piece = warp; piece * 32 < pieces; piece += kWarps) {
-        const int i = 4 * (piece * 32 + lane);
+        const int i = piece * 32 + lane;
         uint64_t w = 0;
-        if (i < n) w = kept(i) + kept(i + 1) + kept(i + 2) + kept(i + 3);
+        if (i < pieces) {
+            const float4 v = x4[i];
+            const uint32_t at = static_cast<uint32_t>(index0 + 4 * i);
+            w = kept(v.x, at) + kept(v.y, at + 1) + kept(v.z, at + 2) + kept(v.w, at + 3);
+        }
         w = warp_sum64(w);
         if (lane == 0) s.piece[piece] = w;
         mine += w;
     }
-    __syncthreads();
-    if (lane == 0) s.warp_sum[warp] = mine;
-    __syncthreads();
-    if (tid == 0) {
-        uint64_t total = 0;
-        for (int i = 0; i < kWarps; ++i) total += s.warp_sum[i];
-        s.total = total;
-    }
+    mine = sum_over_cta(s, lane == 0 ? mine : 0);
+    if (tid == 0) s.total = mine;
     cluster.sync();
-    uint64_t before = 0, total = 0, own = 0;
+    uint64_t before = 0, total = 0;
     for (unsigned q = 0; q < C; ++q) {
         const uint64_t w = cluster.map_shared_rank(&s, q)->total;
         if (q < rank) before += w;
-        if (q == rank) own = w;
         total += w;
     }
-    // the largest whole number not above u total; u = mant 2^-sh
-    uint64_t y;
-    if (u >= 1.0f) {
-        y = total - 1;
-    } else {
-        const uint32_t bits = u > 0.0f ? __float_as_uint(u) : 0u;
-        const int e = static_cast<int>(bits >> 23), sh = 150 - max(e, 1);
-        const uint64_t mant = e ? (bits & 0x7fffffu) | 0x800000u : bits & 0x7fffffu;
-        const uint64_t lo = total * mant, hi = __umul64hi(total, mant);
-        y = sh < 64 ? (hi << (64 - sh)) | (lo >> sh) : sh < 128 ? hi >> (sh - 64) : 0;
-    }
-    if (warp == 0 && before <= y && y < before + own) {
+    const uint64_t y = drawn(u, total);
+    if (warp == 0 && before <= y && y < before + mine) {
         uint64_t at = before;
         int piece = 0;
         for (; piece * 32 < pieces; piece += 32) {
@@ -436,18 +562,17 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
             }
             const uint32_t past = __ballot_sync(0xffffffffu, at + upto > y);
             const int in = past ? __ffs(past) - 1 : 31;
-            const uint64_t skip = __shfl_sync(0xffffffffu, upto - (past ? w : 0), in);
-            at += skip;
+            at += __shfl_sync(0xffffffffu, upto - (past ? w : 0), in);
             if (past) {
                 piece += in;
                 break;
             }
         }
-        const int i = 4 * (piece * 32 + lane);
+        const int i = piece * 32 + lane;
         uint64_t w[4] = {0, 0, 0, 0};
-        if (i < n) {
+        if (i < pieces) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = kept(i + j);
+            for (int j = 0; j < 4; ++j) w[j] = kept(x[4 * i + j], static_cast<uint32_t>(index0 + 4 * i + j));
         }
         const uint64_t sum4 = w[0] + w[1] + w[2] + w[3];
         uint64_t upto = sum4;
@@ -460,8 +585,8 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             if (at <= y && y < at + w[j]) {
-                g.token[m] = index0 + i + j;
-                if (g.prob) g.prob[m] = static_cast<float>(static_cast<double>(w[j]) / static_cast<double>(total));
+                g.token[m] = index0 + 4 * i + j;
+                if (g.prob) g.prob[m] = ratio(w[j], total);
             }
             at += w[j];
         }
