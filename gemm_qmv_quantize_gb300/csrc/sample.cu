@@ -48,11 +48,16 @@ struct Found {                 // a bin with a cut in it
     uint32_t count, upto;      // its tokens (0: there is no cut), and those of it and the bins before it
 };
 
+struct alignas(16) Power {     // 2^(40 - j / 256), whole and as fp32
+    uint64_t whole;
+    float rounded;
+};
+
 struct alignas(16) Shared {
     uint32_t count[kBins], low[kBins], high[kBins];   // a histogram: tokens, and sums in two words
     uint64_t before[kBins + 1];                       // the first histogram's sums, added up (first CTA)
     uint32_t first_count[kBins];
-    uint64_t table[256];                              // 2^(40 - j / 256)
+    Power table[256];
     uint64_t list[2][kRanked];                        // codes that were sent to the first CTA, for each cut
     uint64_t list_weight[kRanked];
     uint64_t piece[kMaxPieces];
@@ -64,10 +69,10 @@ struct alignas(16) Shared {
     uint32_t top, listed[2];
 };
 
-// 2^(40 - j / 256) for j = 0 .. 255, worked out by the compiler: products of 2^(-2^k / 256), each the root of
+// The powers for j = 0 .. 255, worked out by the compiler: products of 2^(-2^k / 256), each the root of
 // the one before it (Newton's iteration), in doubles.
 struct Table {
-    uint64_t v[256];
+    Power v[256];
     constexpr Table() : v()
     {
         double root[8] = {};
@@ -81,7 +86,8 @@ struct Table {
             double p = 1099511627776.0;
             for (int k = 0; k < 8; ++k)
                 if (j >> k & 1) p *= root[k];
-            v[j] = static_cast<uint64_t>(p + 0.5);
+            v[j].whole = static_cast<uint64_t>(p + 0.5);
+            v[j].rounded = static_cast<float>(p);
         }
     }
 };
@@ -100,7 +106,7 @@ __device__ __forceinline__ uint64_t code_of(float x, uint32_t index) { return st
 
 struct Row {
     float top, c_hi, c_lo;        // max x; log2(e) / T
-    const uint64_t *table;
+    const Power *table;
 };
 
 // t of a logit, rounded: not below that of a larger logit.
@@ -114,11 +120,13 @@ __device__ __forceinline__ uint64_t weight(const Row &r, float x)
     const float back = r.top - d;   // what d's rounding left: top - x = d + d_lo, exactly
     const float d_lo = (back - x) + (r.top - (d + back));
     const float t_lo = fmaf(d, r.c_hi, -t) + fmaf(d, r.c_lo, d_lo * r.c_hi);
-    const int k = __float2int_rn(t * 256.0f);
-    const float z = ((t - static_cast<float>(k) * (1.0f / 256.0f)) + t_lo) * 0.693147180559945f;
+    constexpr float kMagic = 12582912.0f;   // 1.5 * 2^23: adding it rounds to a whole number, in the low bits
+    const float shifted = fmaf(t, 256.0f, kMagic);
+    const uint32_t k = __float_as_uint(shifted) - __float_as_uint(kMagic);
+    const float z = (fmaf(shifted - kMagic, -1.0f / 256.0f, t) + t_lo) * 0.693147180559945f;
     const float series = z * fmaf(z, fmaf(z, -1.0f / 6.0f, 0.5f), -1.0f);   // e^-z - 1, |z| <= 0.0014
-    const uint64_t at = r.table[k & 255];
-    const uint64_t w = at + static_cast<int64_t>(__float2int_rn(static_cast<float>(at) * series));
+    const Power p = r.table[k & 255u];
+    const uint64_t w = p.whole + static_cast<int64_t>(__float2int_rn(p.rounded * series));
     return (w << (kFraction - 40)) >> (k >> 8);
 }
 
@@ -306,33 +314,36 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     const int all = (g.V + skew + 3) / 4, each = (all + static_cast<int>(C) - 1) / static_cast<int>(C);
     const int from = min(all, static_cast<int>(rank) * each), pieces = min(all, from + each) - from;
     const int index0 = 4 * from - skew;   // of x[0]
-    float most = -INFINITY;
-#pragma unroll 8
-    for (int i = tid; i < pieces; i += kThreads) {
-        const int at = index0 + 4 * i;
-        float4 v;
-        if (at >= 0 && at + 4 <= g.V) {
-            v = __ldcs(reinterpret_cast<const float4 *>(row + at));
-        } else {
-            v.x = at >= 0 && at < g.V ? row[at] : -INFINITY;
-            v.y = at + 1 >= 0 && at + 1 < g.V ? row[at + 1] : -INFINITY;
-            v.z = at + 2 >= 0 && at + 2 < g.V ? row[at + 2] : -INFINITY;
-            v.w = at + 3 >= 0 && at + 3 < g.V ? row[at + 3] : -INFINITY;
+    const int whole0 = max(0, (3 - index0) / 4), whole1 = max(whole0, min(pieces, (g.V - index0) / 4));   // pieces that are the row's
+    for (int i = whole0 + tid; i < whole1; i += kThreads) cp_async_16(x4 + i, row + index0 + 4 * i);
+    auto edge = [&](int i) {
+        for (int j = 0; j < 4; ++j) {
+            const int at = index0 + 4 * i + j;
+            x[4 * i + j] = at >= 0 && at < g.V ? row[at] : -INFINITY;
         }
-        v = make_float4(cleaned(v.x), cleaned(v.y), cleaned(v.z), cleaned(v.w));
-        x4[i] = v;
-        most = fmaxf(fmaxf(most, fmaxf(v.x, v.y)), fmaxf(v.z, v.w));
-    }
+    };
+    if (tid < min(whole0, pieces)) edge(tid);
+    if (tid < pieces - whole1) edge(whole1 + tid);
     const float T = g.temperature ? g.temperature[m] : 1.0f, u = g.u[m];
     const float top_p = g.top_p ? g.top_p[m] : 1.0f, min_p = g.min_p ? g.min_p[m] : 0.0f;
     int k = g.top_k ? g.top_k[m] : 0;
     if (k <= 0 || k > g.V) k = g.V;
     if (!(T > 0.0f) || top_p <= 0.0f || min_p > 1.0f) k = 1;
-    uint32_t top = __reduce_max_sync(0xffffffffu, key_of(most));
+    cp_async_wait_all();
     __syncthreads();
+    float most = -INFINITY;
+#pragma unroll 4
+    for (int i = tid; i < pieces; i += kThreads) {
+        float4 v = x4[i];
+        v = make_float4(cleaned(v.x), cleaned(v.y), cleaned(v.z), cleaned(v.w));
+        x4[i] = v;
+        most = fmaxf(fmaxf(most, fmaxf(v.x, v.y)), fmaxf(v.z, v.w));
+    }
+    uint32_t top = __reduce_max_sync(0xffffffffu, key_of(most));
     if (lane == 0) atomicMax(&s.top, top);
     cluster.sync();
-    for (unsigned q = 0; q < C; ++q) top = max(top, cluster.map_shared_rank(&s, q)->top);
+    // (a lane a CTA: reads of others' memory take a while)
+    top = __reduce_max_sync(0xffffffffu, lane < static_cast<int>(C) ? cluster.map_shared_rank(&s, lane)->top : 0u);
     // log2(e) / T in two terms, 2^-46 off
     constexpr float kLog2eHi = 1.44269502e+00f, kLog2eLo = 1.92596299e-08f;
     Row r;
@@ -368,7 +379,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
         });
         if (first != kAll) atomicMin(reinterpret_cast<unsigned long long *>(&s.lo), first);
         cluster.sync();
-        for (unsigned q = 0; q < C; ++q) {
+        for (unsigned q = 0; rank == 0 && tid == 0 && q < C; ++q) {
             const uint64_t o = cluster.map_shared_rank(&s, q)->lo;
             if (o < cut) cut = o;
         }
@@ -522,8 +533,11 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
         }
     }
     // what is kept, in pieces of 128 tokens
+    // (first what one comparison of fp32 shows: below the last kept logit, or far below min_p)
+    const float cut_x = cut == kAll ? -INFINITY : of_key(~static_cast<uint32_t>(cut >> 32));
+    const float most_t = min_p > 0.0f && min_p < 1.0f ? fminf(kMostT, 0.001f - log2f(min_p)) : kMostT;
     auto kept = [&](float v, uint32_t at) -> uint64_t {
-        if (code_of(v, at) > cut) return 0;
+        if (v < cut_x || !(rough_t(r, v) <= most_t) || code_of(v, at) > cut) return 0;
         const uint64_t w = weight(r, v);
         return w >= least ? w : 0;
     };
@@ -536,21 +550,28 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
             const uint32_t at = static_cast<uint32_t>(index0 + 4 * i);
             w = kept(v.x, at) + kept(v.y, at + 1) + kept(v.z, at + 2) + kept(v.w, at + 3);
         }
-        w = warp_sum64(w);
+        // a sum of 32 weights' low 24 bits, and of what is above, fit 32 bits
+        w = (static_cast<uint64_t>(__reduce_add_sync(0xffffffffu, static_cast<uint32_t>(w >> 24))) << 24) +
+            __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(w) & 0xffffffu);
         if (lane == 0) s.piece[piece] = w;
         mine += w;
     }
     mine = sum_over_cta(s, lane == 0 ? mine : 0);
     if (tid == 0) s.total = mine;
     cluster.sync();
-    uint64_t before = 0, total = 0;
-    for (unsigned q = 0; q < C; ++q) {
-        const uint64_t w = cluster.map_shared_rank(&s, q)->total;
-        if (q < rank) before += w;
-        total += w;
+    if (warp > 0) {
+        cluster.sync();
+        return;
     }
+    uint64_t upto_rank = lane < static_cast<int>(C) ? cluster.map_shared_rank(&s, lane)->total : 0;
+#pragma unroll
+    for (int o = 1; o < 16; o *= 2) {
+        const uint64_t b = shfl_up64(upto_rank, o);
+        if (lane >= o) upto_rank += b;
+    }
+    const uint64_t total = __shfl_sync(0xffffffffu, upto_rank, C - 1), before = __shfl_sync(0xffffffffu, upto_rank, rank) - mine;
     const uint64_t y = drawn(u, total);
-    if (warp == 0 && before <= y && y < before + mine) {
+    if (before <= y && y < before + mine) {
         uint64_t at = before;
         int piece = 0;
         for (; piece * 32 < pieces; piece += 32) {

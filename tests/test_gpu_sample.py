@@ -63,6 +63,13 @@ def test_flat_and_steep(spread, filters):
     check(inputs(3, 20011, spread, seed=int(spread * 100), **filters))
 
 
+@pytest.mark.parametrize("spread", [0.0, 0.001, 0.02])
+def test_a_small_top_k_among_many_alike(spread):
+    """The bin with the cut holds more tokens than are ranked at once."""
+    check(inputs(4, 20011, spread, top_k=100, top_p=0.9, seed=11))
+    check(inputs(4, 20011, spread, top_k=100, min_p=0.5, seed=12))
+
+
 @pytest.mark.parametrize("V", [7, 300, 9000])
 def test_ties_go_to_the_lowest_index(V):
     """Logits of few distinct values: cuts fall among equals. Sums of equal weights are exact here."""
