@@ -66,7 +66,7 @@ struct alignas(16) Shared {
     uint64_t total, lo, hi;                           // of this CTA
     uint64_t cut[2], upto;
     Found found[2];
-    uint32_t top, listed[2];
+    uint32_t top, listed[2], counted;                 // counted: tokens of the first histogram (first CTA)
 };
 
 // The powers for j = 0 .. 255, worked out by the compiler: products of 2^(-2^k / 256), each the root of
@@ -209,7 +209,7 @@ __device__ void pick(cg::cluster_group &cluster, Shared &s, Found &found, bool w
         }
         n_at += n[j], w_at += w[j];
     }
-    if (first_level && threadIdx.x == kThreads - 1) s.before[kBins] = w_at;
+    if (first_level && threadIdx.x == kThreads - 1) s.before[kBins] = w_at, s.counted = n_at;
     __syncthreads();
 }
 
@@ -405,6 +405,8 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
             if (rank == 0) {
                 pick(cluster, s, s.found[0], weights, !cut_k, true, static_cast<uint64_t>(k), 0, kAll, 0, 0);
                 if (tid == 0) s.upto = s.before[kBins];
+                // fewer tokens of any weight than k, and few: the last bin is taken for the cut's
+                if (tid == 0 && cut_k && !s.found[0].count && s.counted <= kRanked) s.found[0] = Found{kBins - 1, 0, 0, 0, s.counted, s.counted};
                 if (!cut_k) {   // the share of the whole sum
                     const uint64_t y = share_above(top_p, s.before[kBins]);
                     uint32_t n = 0;

@@ -70,6 +70,11 @@ def test_a_small_top_k_among_many_alike(spread):
     check(inputs(4, 20011, spread, top_k=100, min_p=0.5, seed=12))
 
 
+@pytest.mark.parametrize("filters", [dict(top_k=50), dict(top_k=50, top_p=0.95), dict(top_k=5000, top_p=0.9), dict(top_p=0.999999), {}])
+def test_fewer_tokens_of_any_weight_than_top_k(filters):
+    check(inputs(6, 30000, 60.0, seed=13, **filters))
+
+
 @pytest.mark.parametrize("V", [7, 300, 9000])
 def test_ties_go_to_the_lowest_index(V):
     """Logits of few distinct values: cuts fall among equals. Sums of equal weights are exact here."""
