@@ -66,7 +66,7 @@ struct alignas(16) Shared {
     uint64_t total, lo, hi;                           // of this CTA
     uint64_t cut[2], upto;
     Found found[2];
-    uint32_t top, listed[2], counted;                 // counted: tokens of the first histogram (first CTA)
+    uint32_t top, bottom, listed[2], counted;                 // counted: tokens of the first histogram (first CTA)
 };
 
 // The powers for j = 0 .. 255, worked out by the compiler: products of 2^(-2^k / 256), each the root of
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     Shared &lead = *cluster.map_shared_rank(&s, 0);
     if (tid < 256) s.table[tid] = g_table.v[tid];
     clear_histogram(s);
-    if (tid == 0) s.top = 0, s.lo = kAll, s.hi = 0, s.listed[0] = s.listed[1] = 0, s.cut[0] = s.cut[1] = kAll;
+    if (tid == 0) s.top = 0, s.bottom = 0xffffffffu, s.lo = kAll, s.hi = 0, s.listed[0] = s.listed[1] = 0, s.cut[0] = s.cut[1] = kAll;
     grid_launch_dependents();
     grid_dependency_wait();
     // the slice: 16-byte pieces of the row from the boundary before it on; what is not the row's is -inf
@@ -331,19 +331,22 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     if (!(T > 0.0f) || top_p <= 0.0f || min_p > 1.0f) k = 1;
     cp_async_wait_all();
     __syncthreads();
-    float most = -INFINITY;
+    float most = -INFINITY, lowest = INFINITY;   // lowest: above -inf
 #pragma unroll 4
     for (int i = tid; i < pieces; i += kThreads) {
         float4 v = x4[i];
         v = make_float4(cleaned(v.x), cleaned(v.y), cleaned(v.z), cleaned(v.w));
         x4[i] = v;
         most = fmaxf(fmaxf(most, fmaxf(v.x, v.y)), fmaxf(v.z, v.w));
+        const auto above = [](float a) { return a > -INFINITY ? a : INFINITY; };
+        lowest = fminf(fminf(lowest, fminf(above(v.x), above(v.y))), fminf(above(v.z), above(v.w)));
     }
-    uint32_t top = __reduce_max_sync(0xffffffffu, key_of(most));
-    if (lane == 0) atomicMax(&s.top, top);
+    uint32_t top = __reduce_max_sync(0xffffffffu, key_of(most)), bottom = __reduce_min_sync(0xffffffffu, key_of(lowest));
+    if (lane == 0) atomicMax(&s.top, top), atomicMin(&s.bottom, bottom);
     cluster.sync();
     // (a lane a CTA: reads of others' memory take a while)
     top = __reduce_max_sync(0xffffffffu, lane < static_cast<int>(C) ? cluster.map_shared_rank(&s, lane)->top : 0u);
+    bottom = __reduce_min_sync(0xffffffffu, lane < static_cast<int>(C) ? cluster.map_shared_rank(&s, lane)->bottom : 0xffffffffu);
     // log2(e) / T in two terms, 2^-46 off
     constexpr float kLog2eHi = 1.44269502e+00f, kLog2eLo = 1.92596299e-08f;
     Row r;
@@ -367,7 +370,8 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
             f(v.x, at), f(v.y, at + 1), f(v.z, at + 2), f(v.w, at + 3);
         }
     };
-    const float per_t = static_cast<float>(kBins) / kMostT;
+    // The histogram spans what the row's logits do, a vocabulary of nearly equal ones too.
+    const float span = fminf(kMostT, fmaxf(1.001f * rough_t(r, of_key(bottom)), 1e-6f)), per_t = static_cast<float>(kBins) / span;
     auto bin_of = [&](float t) { return min(static_cast<int>(t * per_t), kBins - 1); };
     const uint64_t least = min_p > 0.0f && k > 1 ? (min_p >= 1.0f ? kOne : max(static_cast<unsigned long long>(1), static_cast<unsigned long long>(share_above(min_p, kOne)))) : 1;
     uint64_t cut = kAll;   // the last kept token's code
@@ -396,7 +400,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
         for (;;) {
             each_token([&](float v, uint32_t) {
                 const float t = rough_t(r, v);
-                if (!(t <= kMostT)) return;
+                if (!(t <= span)) return;
                 const int bin = bin_of(t);
                 atomicAdd(&s.count[bin], 1u);
                 if (weights) add64(s, bin, weight(r, v));
@@ -427,7 +431,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
                 const int last = static_cast<int>(f.lo);
                 each_token([&](float v, uint32_t at) {
                     const float t = rough_t(r, v);
-                    if (!(t <= kMostT) || bin_of(t) > last) return;
+                    if (!(t <= span) || bin_of(t) > last) return;
                     const uint32_t i = atomicAdd(&lead.listed[0], 1u);
                     if (i < kRanked) lead.list[0][i] = code_of(v, at);
                 });
@@ -465,7 +469,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
                 unsigned long long lo = kAll, hi = 0;
                 each_token([&](float v, uint32_t at) {
                     const float t = rough_t(r, v);
-                    if (!(t <= kMostT) || bin_of(t) != bin) return;
+                    if (!(t <= span) || bin_of(t) != bin) return;
                     const unsigned long long code = code_of(v, at);
                     lo = min(lo, code), hi = max(hi, code);
                 });
@@ -504,7 +508,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
                     if (code < f.lo || code > f.hi) return;
                 } else {
                     const float t = rough_t(r, v);
-                    if (!(t <= kMostT) || bin_of(t) != bin) return;
+                    if (!(t <= span) || bin_of(t) != bin) return;
                 }
                 const uint32_t i = atomicAdd(&lead.listed[which], 1u);
                 if (i < kRanked) lead.list[which][i] = code;
