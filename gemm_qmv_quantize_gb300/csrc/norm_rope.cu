@@ -13,7 +13,8 @@
 //
 // A group of L lanes (8, 16 or 32: the power of two that holds D / 8) has a head of a token,
 // a lane 8 of its elements: 4 pairs of the rotated part, or 8 elements beyond it. Bound by
-// the bytes.
+// the bytes and by what a lane executes for them: 4001 tokens of 40 + 8 + 8 heads of 128 take 35 us in 16
+// bits (4.9 TB/s) and 40 us as codes (4.1).
 #include "decode_device.cuh"
 #include "decode_ops.h"
 #include "qmv.h"

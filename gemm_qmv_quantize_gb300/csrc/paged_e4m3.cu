@@ -12,12 +12,21 @@
 // binary16, exactly, on their way from shared memory into the product. P^T is S^T transposed in registers.
 //
 // Numerics: q is held in binary16 (bfloat16 rows are scaled by a power of two that brings
-// their largest element to 2^14 or more: elements 2^-28 of it and less lose bits); S, the softmax's
-// statistics, and O are fp32. A column's running maxima are two: m of z = c sk S for the
-// denominator l = sum 2^(z - m), and m' of z + log2 sv for the numerator, whose terms
-// 2^(z + log2 sv - m') are rounded to binary16, the product's operand: with a maximum of its
-// own the largest term is near 1, whatever the scales of the blocks. Both follow the true
-// maxima with a slack of 2^8, so that O is rescaled rarely.
+// their largest element to 2^14 or more: elements 2^-28 of it and less lose bits); S, the
+// softmax's statistics and O are fp32. The running maximum of a column is that of z + log2 sv, z = c sk S:
+// the terms 2^(z + log2 sv - m) of the numerator, which are rounded to binary16, the
+// product's operand, are then near 1 where they are largest, whatever the scales of the blocks.
+// The denominator's are 2^(z - m), in fp32, whose range holds them. m follows the true maximum
+// with a slack of 2^8, so that O is rescaled rarely. P's rounding adds a quarter to the error of a plain
+// form in fp32 (2.6e-4 of the outputs for 2.1e-4 in binary16; none that shows in bfloat16).
+//
+// Bound by the cache's bytes: 64 requests of up to 16384 tokens, 40 query heads over 8 key heads of
+// 128, take 165 us, 6.6 TB/s. What it took to get there, us: a CTA an item 482; equal runs of blocks over
+// all SMs 223; key heads of the same blocks side by side, and copies of whole rows (half rows
+// were as many requests to L2 again, which bound it), 174; scores of the next block beside this
+// one's softmax, starting on an item counted as blocks 165. The smaller the call, the more of it
+// is starting and joining: 12 us or so, much of that fetching instructions, which is why what runs
+// once is written short and not unrolled.
 #include <algorithm>
 #include <cmath>
 
@@ -36,7 +45,7 @@ __device__ uint32_t g_paged_error;
 
 constexpr int kBlock = kScaleTokens;    // keys a step of a warp
 constexpr int kMostWarps = 8;           // of a CTA, a key head each
-constexpr int64_t kFewBytes = 22ll << 20, kMostBytes = 44ll << 20;   // of the workspace's slots
+constexpr int64_t kFewBytes = 11ll << 20, kMostBytes = 22ll << 20;   // of the workspace's slots, with 8 rows and 16
 constexpr int kSms = 152;
 constexpr int kStartUnits = 8;          // what starting on an item costs, in blocks of a warp's
 constexpr int kLeastBlocks = 2;         // of a run, where there are few
@@ -51,8 +60,9 @@ struct Ring {
     static constexpr int kBytes = 32 * kBlock * D / 16;   // keys and values of a block: 2 * 16 * D
 };
 
-// Warps an SM, by the registers that NT row tiles of O take, and stages of a warp's ring, by the
-// shared memory that is left beside q's operands.
+// Warps an SM, and stages of a warp's ring, by the shared memory that is left beside q's operands:
+// 8 warps with six stages. (16 with three end at the same time where there is much, 166 us for 165, but have twice
+// the parts: 75 us for 54 with one request of 131072 tokens. A block of 64 dimensions is half the bytes.)
 template <int D, int NT>
 struct Shape {
     static constexpr int kWarpsSm = D == 128 ? 8 : 16;
@@ -810,13 +820,14 @@ cudaError_t launch_typed(const PagedArgs &g, int row_groups, cudaStream_t s)
     return cudaLaunchKernelEx(&join, paged_join_kernel<D, NT>, g, row_groups, warps, ctas, share, rows);
 }
 
-// Groups of up to 8 NT rows, all of nearly the same number.
+// Groups of 8 rows, or of up to 16: where there are more, further warps take them beside each other, and
+// find the keys in L2. (25 rows of 8 requests in one group of 32: 43 us for 26; of 64 requests of up to 8191
+// tokens, bound by the products' instructions, 236 for 225. 40 rows of 64 dimensions in one of 48: 56 for 33.)
 template <int D>
 cudaError_t launch_rows(const PagedArgs &g, cudaStream_t s)
 {
-    constexpr int kMost = 16;
     const int rows = g.T * (g.Hq / g.Hkv);
-    return rows <= 8 ? launch_typed<D, 1>(g, 1, s) : launch_typed<D, 2>(g, (rows + kMost - 1) / kMost, s);
+    return rows <= 8 ? launch_typed<D, 1>(g, 1, s) : launch_typed<D, 2>(g, (rows + 15) / 16, s);
 }
 
 }  // namespace

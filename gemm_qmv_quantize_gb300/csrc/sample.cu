@@ -19,6 +19,11 @@
 // first CTA, which ranks them and draws. Else only the bin's tokens do (bins of more than 256
 // are split again by the bits of (logit, index)); then pass 3 sums what is kept, in pieces of
 // 128 tokens, and the piece that u falls to is gone through.
+//
+// Bound by what it executes: 96 rows of 151936, four in five with a top-k of 50, take 61 us (the logits'
+// bytes 8.6), eight rows with a top-p alone 29, one of 32000 with a top-k 9. A weight is 35
+// instructions, a token of the histogram two or three atomics. (CTAs of 16 to a row, or 4, or of 1024 threads: 103, 93
+// and 98 us for what then took 70; sums by 64-bit atomics of shared memory 72 for 57.)
 #include <algorithm>
 
 #include <cooperative_groups.h>
