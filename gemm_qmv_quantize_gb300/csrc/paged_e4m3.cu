@@ -25,11 +25,12 @@
 // all SMs 223; key heads of the same blocks side by side, and copies of whole rows (half rows
 // were as many requests to L2 again, which bound it), 174; scores of the next block beside this
 // one's softmax, starting on an item counted as blocks 165. The smaller the call, the more of it
-// is starting and joining: 12 us or so, much of that fetching instructions, which is why what runs
+// is starting and joining: 12 us or so (8 where clusters have the items), much of that fetching instructions, which is why what runs
 // once is written short and not unrolled.
 #include <algorithm>
 #include <cmath>
 
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -37,6 +38,8 @@
 #include "decode_ops.h"
 #include "qmv.h"
 #include "qmv_device.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace qmv {
 namespace {
@@ -49,6 +52,9 @@ constexpr int64_t kFewBytes = 11ll << 20, kMostBytes = 22ll << 20;   // of the w
 constexpr int kSms = 152;
 constexpr int kStartUnits = 8;          // what starting on an item costs, in blocks of a warp's
 constexpr int kLeastBlocks = 2;         // of a run, where there are few
+// Blocks a CTA up to which a cluster has an item: one launch for two. 560 keys of one request 8.5 us for
+// 11.1, 12 requests of 1000 keys 12.4 for 16.8; one of 2000 keys, the most there is for one, 12.6 for 12.3.
+constexpr int kClusterBlocks = 8;
 constexpr int kBatch = 32;              // blocks whose page and scales a warp looks up at a time, a lane a block
 constexpr float kSlack = 8.0f;
 constexpr float kLowest = -3.402823466e38f;   // a maximum of no scores: the difference to it is never NaN
@@ -560,6 +566,27 @@ __device__ __noinline__ float4 with_nan(const PagedArgs &g, int b, int h, int le
     return o;
 }
 
+template <int D, int NT>
+__device__ __forceinline__ void put(const Part<D, NT> &r, float *slot, int lane)
+{
+    const int gid = lane / 4, t = lane % 4;
+    const bool nan = __any_sync(0xffffffffu, r.nan != 0);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float l = r.l[n][e];
+#pragma unroll
+            for (int o = 4; o < 32; o *= 2) l += __shfl_xor_sync(0xffffffffu, l, o);
+            float *row = slot + (8 * n + 2 * t + e) * (D + 4);
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j)
+                reinterpret_cast<float4 *>(row + gid * (D / 8))[j] = make_float4(r.o[n][2 * j][e], r.o[n][2 * j][e + 2], r.o[n][2 * j + 1][e], r.o[n][2 * j + 1][e + 2]);
+            if (gid == 0) *reinterpret_cast<float4 *>(row + D) = make_float4(l, r.m[n][e], nan ? 1.0f : 0.0f, 0.0f);
+        }
+    }
+}
+
 // Four outputs of row `row` of a key head, from their sums over V and the denominator l.
 __device__ __forceinline__ void write_row(const PagedArgs &g, int b, int h, int len, int row, int G, int d, int D, float l, bool nan, float4 o)
 {
@@ -583,6 +610,51 @@ template <int D, int NT>
 __device__ __forceinline__ int64_t *starts_of(const PagedArgs &g)
 {
     return reinterpret_cast<int64_t *>(static_cast<float *>(g.workspace) + 2ll * Shape<D, NT>::kMostWarpsOfRuns * slot_floats<D, NT>());
+}
+
+// A warp's part of an item: `count` blocks from block `at` on of request b, against 8 NT rows of
+// key head h from row0 on.
+template <int D, int NT>
+__device__ __forceinline__ void add_item(Part<D, NT> &part, const PagedArgs &g, Queries<D, NT> &q, uint32_t ring, int b, int h, int row0,
+                                 int len, int at, int count, int lane)
+{
+    const int gid = lane / 4, t = lane % 4, G = g.Hq / g.Hkv, rows = g.T * G;
+    int seen[NT][2];
+    Place p;
+    p.token = static_cast<int64_t>(g.Hkv) * D;
+    p.k = static_cast<const uint8_t *>(g.k) + h * D;
+    p.v = static_cast<const uint8_t *>(g.v) + h * D;
+    p.ks = g.ks + h;
+    p.vs = g.vs + h;
+    p.table = g.table + static_cast<int64_t>(b) * g.table_pages;
+    p.pages = g.n_pages;
+    p.page_shift = 31 - __clz(g.page);
+    p.Hkv = g.Hkv;
+    p.len = len;
+    p.first_seen = len - g.T + 1;
+    auto row_at = [&](int r) { return ((static_cast<int64_t>(b) * g.T + r / G) * g.Hq + static_cast<int64_t>(h) * G + r % G) * D; };
+    uint32_t words[D / 8];   // the first row tile's, on their way while the pages are looked up
+    fetch_q<D>(words, static_cast<const uint16_t *>(g.q) + (row0 + gid < rows ? row_at(row0 + gid) : 0), row0 + gid < rows, t);
+    Walk<D, NT> walk(p, ring, lane, at, count);
+    float c[NT][2];
+    part.nan = 0;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const float back = set_q<D, NT>(q, n, words, g.type);
+        const int next = row0 + 8 * (n + 1) + gid;
+        if (n + 1 < NT) fetch_q<D>(words, static_cast<const uint16_t *>(g.q) + (next < rows ? row_at(next) : 0), next < rows, t);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int r = row0 + 8 * n + 2 * t + e;
+            c[n][e] = g.scale * kLog2e * __shfl_sync(0xffffffffu, back, (2 * t + e) * 4);
+            seen[n][e] = r < rows ? p.first_seen + r / G : 0;
+            part.l[n][e] = 0.0f;
+            part.m[n][e] = kLowest;
+        }
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) part.o[n][j][0] = part.o[n][j][1] = part.o[n][j][2] = part.o[n][j][3] = 0.0f;
+    }
+    walk.add(part, q, c, seen);
 }
 
 // A run a CTA. row_groups: groups of 8 NT query rows.
@@ -614,42 +686,7 @@ __global__ void __launch_bounds__(32 * kMostWarps, Shape<D, NT>::kWarpsSm / kMos
         const int len = len_of(g, b), units = units_of(g, b), taken = static_cast<int>(min(units - cut.at, cut.left));
         const int at = max(static_cast<int>(cut.at) - kStartUnits, 0), count = max(static_cast<int>(cut.at) + taken - kStartUnits, 0) - at;
         if (pair < pairs) {
-            Place p;
-            p.token = static_cast<int64_t>(g.Hkv) * D;
-            p.k = static_cast<const uint8_t *>(g.k) + h * D;
-            p.v = static_cast<const uint8_t *>(g.v) + h * D;
-            p.ks = g.ks + h;
-            p.vs = g.vs + h;
-            p.table = g.table + static_cast<int64_t>(b) * g.table_pages;
-            p.pages = g.n_pages;
-            p.page_shift = 31 - __clz(g.page);
-            p.Hkv = g.Hkv;
-            p.len = len;
-            p.first_seen = len - g.T + 1;
-            auto row_at = [&](int r) { return ((static_cast<int64_t>(b) * g.T + r / G) * g.Hq + static_cast<int64_t>(h) * G + r % G) * D; };
-            uint32_t words[D / 8];   // the first row tile's, on their way while the pages are looked up
-            fetch_q<D>(words, static_cast<const uint16_t *>(g.q) + (row0 + gid < rows ? row_at(row0 + gid) : 0), row0 + gid < rows, t);
-            Walk<D, NT> walk(p, my_ring, lane, at, count);
-            float c[NT][2];
-            int seen[NT][2];
-            part.nan = 0;
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const float back = set_q<D, NT>(q, n, words, g.type);
-                const int next = row0 + 8 * (n + 1) + gid;
-                if (n + 1 < NT) fetch_q<D>(words, static_cast<const uint16_t *>(g.q) + (next < rows ? row_at(next) : 0), next < rows, t);
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int r = row0 + 8 * n + 2 * t + e;
-                    c[n][e] = g.scale * kLog2e * __shfl_sync(0xffffffffu, back, (2 * t + e) * 4);
-                    seen[n][e] = r < rows ? p.first_seen + r / G : 0;
-                    part.l[n][e] = 0.0f;
-                    part.m[n][e] = kLowest;
-                }
-#pragma unroll
-                for (int j = 0; j < D / 16; ++j) part.o[n][j][0] = part.o[n][j][1] = part.o[n][j][2] = part.o[n][j][3] = 0.0f;
-            }
-            walk.add(part, q, c, seen);
+            add_item<D, NT>(part, g, q, my_ring, b, h, row0, len, at, count, lane);
             // the output, or a part
             const bool whole = taken == units, nan = __any_sync(0xffffffffu, part.nan != 0);
             float *slot = slot_of<D, NT>(g, static_cast<int>(blockIdx.x), first, warps, warp);
@@ -780,6 +817,69 @@ __global__ void __launch_bounds__(1024) paged_join_kernel(const __grid_constant_
                   g.Hq / g.Hkv, 4 * lane, D, l, nan != 0.0f, o);
 }
 
+// Few and short requests: a cluster an item, its CTAs equal shares of the item's blocks, joined in their
+// shared memory. One launch, and no search for where a run begins.
+template <int D, int NT>
+__global__ void __launch_bounds__(32 * kMostWarps) paged_cluster_kernel(const __grid_constant__ PagedArgs g, int row_groups)
+{
+    extern __shared__ __align__(128) uint8_t smem[];
+    cg::cluster_group cluster = cg::this_cluster();
+    const int R = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, warps = blockDim.x / 32;
+    const int G = g.Hq / g.Hkv, rows = g.T * G, pairs = g.Hkv * row_groups, items = (pairs + warps - 1) / warps;
+    const int of = static_cast<int>(blockIdx.x) / R, b = of / items, pair = of % items * warps + warp;
+    const int h = pair / row_groups, row0 = pair % row_groups * 8 * NT;
+    uint8_t *own = smem + warp * Shape<D, NT>::kOwn;
+    grid_launch_dependents();
+    grid_dependency_wait();
+    if (g.lens[b] > g.max_len && rank == 0 && threadIdx.x == 0) atomicOr(&g_paged_error, kErrIndex);
+    const int len = len_of(g, b), blocks = (len + kBlock - 1) / kBlock;
+    const int at = blocks * rank / R, count = blocks * (rank + 1) / R - at;
+    float *slot = reinterpret_cast<float *>(own);   // over the ring
+    if (pair < pairs) {
+        Part<D, NT> part{};
+        Queries<D, NT> q;
+        q.base = smem_addr(own) + Shape<D, NT>::kStages * Ring<D>::kBytes + lane * 8;
+        add_item<D, NT>(part, g, q, smem_addr(own), b, h, row0, len, at, count, lane);
+        __syncwarp();
+        put<D, NT>(part, slot, lane);
+    }
+    cluster.sync();
+    constexpr int kD4 = D / 4;
+    // a row a warp: rows rank, rank + R, .. of the warp's pair
+    for (int r = rank; pair < pairs && r < 8 * NT && row0 + r < rows; r += R) {
+        const float *row = slot + r * (D + 4);
+        const float4 st = lane < R ? *reinterpret_cast<const float4 *>(cluster.map_shared_rank(const_cast<float *>(row) + D, lane)) : make_float4(0.0f, kLowest, 0.0f, 0.0f);
+        float top = st.y;
+#pragma unroll
+        for (int x = 16; x > 0; x /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+        const float weight = exp2_fast(st.y - top);
+        float l = st.x * weight, nan = st.z;
+#pragma unroll
+        for (int x = 16; x > 0; x /= 2) {
+            l += __shfl_xor_sync(0xffffffffu, l, x);
+            nan = fmaxf(nan, __shfl_xor_sync(0xffffffffu, nan, x));
+        }
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+        for (int k = 0; k < R; ++k) {
+            const float4 x = reinterpret_cast<const float4 *>(cluster.map_shared_rank(const_cast<float *>(row), k))[lane % kD4];
+            const float w = __shfl_sync(0xffffffffu, weight, k);
+            o = make_float4(o.x + x.x * w, o.y + x.y * w, o.z + x.z * w, o.w + x.w * w);
+        }
+        if (lane < kD4) write_row(g, b, h, len, row0 + r, G, 4 * lane, D, l, nan != 0.0f, o);
+    }
+    cluster.sync();   // nobody leaves while others read its memory
+}
+
+// CTAs of a cluster for each of `items` of up to `blocks` blocks, or 0. (16 to a cluster only for four items: more
+// such clusters wait for one another's places, 9.7 us for 15.6 with 8 requests.)
+int cluster_for(int64_t items, int64_t blocks)
+{
+    const int R = items <= 4 ? 16 : 8;
+    return items * R <= 128 && blocks <= kClusterBlocks * R ? R : 0;
+}
+
 template <int D, int NT>
 cudaError_t launch_typed(const PagedArgs &g, int row_groups, cudaStream_t s)
 {
@@ -791,15 +891,27 @@ cudaError_t launch_typed(const PagedArgs &g, int row_groups, cudaStream_t s)
     const int64_t blocks = (g.max_len + kBlock - 1) / kBlock;
     const int ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kSms * (S::kWarpsSm / warps), items * g.B * blocks / kLeastBlocks)));
     const int smem = warps * S::kOwn;
-    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(paged_kernel<D, NT>), smem);
-    if (e != cudaSuccess) return e;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(static_cast<unsigned>(32 * warps));
-    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = s;
     cfg.attrs = attr;
+    const int R = cluster_for(items * g.B, blocks);
+    if (R > 0) {
+        cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(paged_cluster_kernel<D, NT>), smem);
+        if (e == cudaSuccess && R > 8) e = cudaFuncSetAttribute(paged_cluster_kernel<D, NT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = static_cast<unsigned>(R);
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.gridDim = dim3(static_cast<unsigned>(items * g.B * R));
+        cfg.numAttrs = 1 + set_launch_overlap_attr(attr + 1);
+        return cudaLaunchKernelEx(&cfg, paged_cluster_kernel<D, NT>, g, row_groups);
+    }
+    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(paged_kernel<D, NT>), smem);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
     cfg.numAttrs = set_launch_overlap_attr(attr);
     e = cudaLaunchKernelEx(&cfg, paged_kernel<D, NT>, g, row_groups);
     if (e != cudaSuccess || ctas == 1) return e;

@@ -107,6 +107,49 @@ def test_nan_of_later_tokens_does_not_reach_earlier_rows(T, n, D):
         assert bool(torch.isnan(got[0, first:, 3:, where if name == "v_cache" else slice(None)]).all())
 
 
+def widened(args, keys=4096):
+    """The same call with a bound of the lengths for which the work is split in runs over all SMs."""
+    page, (B, width) = args["k_cache"].shape[1], args["table"].shape
+    return {**args, "table": torch.cat([args["table"], args["table"][:, :1].expand(B, max(0, keys // page - width))], 1).contiguous()}
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("T,n", [(5, 70), (5, 64), (3, 3), (20, 500), (2, 1700)])
+def test_nan_of_later_tokens_with_a_long_bound(T, n, D):
+    args = widened(inputs(3, T, 6, 2, D, [n, n + 1, 4000], 16, seed=4))
+    clean = check(args)
+    for token, name, where in ((n - 1, "v_cache", slice(3, 9)), (n - T + 1, "v_cache", slice(0, D)), (n - 1, "k_cache", slice(0, 1))):
+        if token < 0:
+            continue
+        bad = {**args, name: args[name].clone()}
+        bad[name].view(torch.uint8)[int(args["table"][0, token // 16]), token % 16, 1, where] = 0xff
+        got = check(bad)
+        first = max(0, token - (n - T))
+        assert torch.equal(got[0, :first], clean[0, :first]) and torch.equal(got[1:], clean[1:])
+        assert bool(torch.isnan(got[0, first:, 3:, where if name == "v_cache" else slice(None)]).all())
+
+
+@pytest.mark.parametrize("B,T,Hq,Hkv,D,lens,page,type_", [
+    (1, 1, 8, 1, 128, [5], 16, "f16"), (3, 2, 40, 8, 128, [0, 1, 2], 32, "bf16"), (4, 3, 6, 3, 64, [17, 0, 900, 33], 64, "f16"),
+    (2, 40, 4, 2, 64, [39, 41], 16, "bf16"), (6, 1, 30, 10, 128, [16, 32, 48, 1, 15, 3000], 16, "f16"), (40, 1, 8, 8, 64, [7] * 39 + [2500], 32, "f16"),
+    (300, 1, 2, 1, 128, [30 + i % 90 for i in range(300)], 16, "bf16"), (1, 1, 64, 16, 64, [4096], 256, "f16")])
+def test_short_lengths_with_a_long_bound(B, T, Hq, Hkv, D, lens, page, type_):
+    check(widened(inputs(B, T, Hq, Hkv, D, lens, page, type_, seed=B + D)), type_)
+
+
+def test_special_queries_and_lengths_with_a_long_bound():
+    args = widened(inputs(3, 4, 4, 2, 64, [0, 2, 4], 16, seed=10))
+    got = check(args)
+    assert bool((got[0] == 0).all()) and bool((got[1, :2] == 0).all())
+    args = widened(inputs(2, 2, 6, 2, 128, [60, 61], 16, seed=11))
+    clean = run(args)
+    args["q"][0, 1, 2, 7], args["q"][1, 0, 5, 9] = math.nan, math.inf
+    got = run(args)
+    assert bool(torch.isnan(got[0, 1, 2]).all()) and bool(torch.isnan(got[1, 0, 5]).all())
+    got[0, 1, 2], got[1, 0, 5] = clean[0, 1, 2], clean[1, 0, 5]
+    assert torch.equal(got, clean)
+
+
 def test_scales_of_all_sizes():
     """Blocks whose scales are far apart: small values under a large softmax weight and the reverse."""
     args = inputs(2, 1, 8, 2, 128, [400, 90], 16, seed=5)
