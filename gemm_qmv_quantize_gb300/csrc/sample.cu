@@ -38,12 +38,13 @@ namespace qmv {
 namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kBins = 1024;
+constexpr int kBins = kThreads;
 constexpr int kRanked = 256;             // tokens that are ranked by comparing each with each
 constexpr int kFraction = 44;            // bits of a weight below the point
 constexpr float kMostT = 45.0f;          // from there on a weight is 0
-constexpr int kMaxPieces = 512;          // of 128 tokens, of a CTA's slice
 constexpr int64_t kMaxSlice = 32768 + 8; // tokens of a CTA
+constexpr int kPiece = 64, kMaxPieces = (kMaxSlice / kWarps + kPiece) / kPiece;   // of a warp's share of the slice
+constexpr int kListed = 320;             // tokens of a warp's list
 constexpr uint64_t kOne = 1ull << kFraction, kAll = ~0ull;
 
 struct Found {                 // a bin with a cut in it
@@ -53,22 +54,18 @@ struct Found {                 // a bin with a cut in it
     uint32_t count, upto;      // its tokens (0: there is no cut), and those of it and the bins before it
 };
 
-struct alignas(16) Power {     // 2^(40 - j / 256), whole and as fp32
-    uint64_t whole;
-    float rounded;
-};
-
 struct alignas(16) Shared {
     uint32_t count[kBins], low[kBins], high[kBins];   // a histogram: tokens, and sums in two words
     uint64_t before[kBins + 1];                       // the first histogram's sums, added up (first CTA)
     uint32_t first_count[kBins];
-    Power table[256];
+    uint64_t power[256];                              // 2^(44 - j / 256), of 2^4
     uint64_t list[2][kRanked];                        // codes that were sent to the first CTA, for each cut
     uint64_t list_weight[kRanked];
-    uint64_t piece[kMaxPieces];
+    uint64_t piece[kWarps][kMaxPieces];
+    uint16_t listed_token[kWarps][kListed];           // of its share
     uint64_t warp_sum[kWarps];
     uint32_t warp_count[kWarps];
-    uint64_t total, lo, hi;                           // of this CTA
+    uint64_t total, lo, hi;                           // of this CTA (total: of all weights, then of what is kept)
     uint64_t cut[2], upto;
     Found found[2];
     uint32_t top, bottom, listed[2], counted;                 // counted: tokens of the first histogram (first CTA)
@@ -77,7 +74,7 @@ struct alignas(16) Shared {
 // The powers for j = 0 .. 255, worked out by the compiler: products of 2^(-2^k / 256), each the root of
 // the one before it (Newton's iteration), in doubles.
 struct Table {
-    Power v[256];
+    uint64_t v[256];
     constexpr Table() : v()
     {
         double root[8] = {};
@@ -91,18 +88,16 @@ struct Table {
             double p = 1099511627776.0;
             for (int k = 0; k < 8; ++k)
                 if (j >> k & 1) p *= root[k];
-            v[j].whole = static_cast<uint64_t>(p + 0.5);
-            v[j].rounded = static_cast<float>(p);
+            v[j] = static_cast<uint64_t>(p + 0.5) << (kFraction - 40);
         }
     }
 };
 __device__ const Table g_table = Table();
 
-// Logits in their order as whole numbers, NaN as -inf and -0 as 0.
-__device__ __forceinline__ float cleaned(float x) { return x != x ? -INFINITY : x + 0.0f; }
+// Logits in their order as whole numbers, -0 as 0. (NaN have neither a place nor a weight: their t compares false.)
 __device__ __forceinline__ uint32_t key_of(float x)
 {
-    const uint32_t b = __float_as_uint(x);
+    const uint32_t b = __float_as_uint(x + 0.0f);
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 __device__ __forceinline__ float of_key(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); }
@@ -111,7 +106,7 @@ __device__ __forceinline__ uint64_t code_of(float x, uint32_t index) { return st
 
 struct Row {
     float top, c_hi, c_lo;        // max x; log2(e) / T
-    const Power *table;
+    const uint64_t *power;
 };
 
 // t of a logit, rounded: not below that of a larger logit.
@@ -119,20 +114,19 @@ __device__ __forceinline__ float rough_t(const Row &r, float x) { return x == r.
 
 __device__ __forceinline__ uint64_t weight(const Row &r, float x)
 {
-    if (x == r.top) return kOne;
     const float d = r.top - x, t = d * r.c_hi;
-    if (!(t <= kMostT)) return 0;   // and what is NaN
     const float back = r.top - d;   // what d's rounding left: top - x = d + d_lo, exactly
     const float d_lo = (back - x) + (r.top - (d + back));
-    const float t_lo = fmaf(d, r.c_hi, -t) + fmaf(d, r.c_lo, d_lo * r.c_hi);
+    const float t_lo = fmaf(d_lo, r.c_hi, fmaf(d, r.c_lo, fmaf(d, r.c_hi, -t)));
     constexpr float kMagic = 12582912.0f;   // 1.5 * 2^23: adding it rounds to a whole number, in the low bits
-    const float shifted = fmaf(t, 256.0f, kMagic);
+    const float shifted = fmaf(fminf(t, kMostT), 256.0f, kMagic);
     const uint32_t k = __float_as_uint(shifted) - __float_as_uint(kMagic);
-    const float z = (fmaf(shifted - kMagic, -1.0f / 256.0f, t) + t_lo) * 0.693147180559945f;
-    const float series = z * fmaf(z, fmaf(z, -1.0f / 6.0f, 0.5f), -1.0f);   // e^-z - 1, |z| <= 0.0014
-    const Power p = r.table[k & 255u];
-    const uint64_t w = p.whole + static_cast<int64_t>(__float2int_rn(p.rounded * series));
-    return (w << (kFraction - 40)) >> (k >> 8);
+    const float z = fmaf(shifted - kMagic, -1.0f / 256.0f, t) + t_lo;   // |z| <= 0.002
+    constexpr float kLn2 = 0.693147180559945f;
+    const float series = z * fmaf(z, fmaf(z, -512.0f / 6.0f * kLn2 * kLn2 * kLn2, 256.0f * kLn2 * kLn2), -512.0f * kLn2);   // 2^9 (2^-z - 1)
+    const uint64_t p = r.power[k & 255u];
+    const uint64_t w = p + static_cast<int64_t>(__float2int_rn(__uint2float_rn(static_cast<uint32_t>(p >> (kFraction - 31))) * series)) * (1 << (kFraction - 40));
+    return x == r.top ? kOne : t <= kMostT ? w >> (k >> 8) : 0;   // (t can be NaN)
 }
 
 __device__ __forceinline__ void add64(Shared &s, int bin, uint64_t w)
@@ -177,44 +171,34 @@ __device__ __forceinline__ void clear_histogram(Shared &s)
 __device__ void pick(cg::cluster_group &cluster, Shared &s, Found &found, bool weights, bool by_weight, bool first_level, uint64_t need,
                      uint64_t lo, uint64_t hi, int shift, uint64_t before)
 {
-    constexpr int kEach = kBins / kThreads;
-    uint32_t n[kEach] = {}, n_sum = 0;
-    uint64_t w[kEach] = {}, w_sum = 0;
+    const int bin = threadIdx.x;
+    uint32_t n = 0;
+    uint64_t w = 0;
     if (threadIdx.x == 0) found.count = 0;
 #pragma unroll 4
     for (unsigned r = 0; r < cluster.num_blocks(); ++r) {
         const Shared &o = *cluster.map_shared_rank(&s, r);
-        const uint2 c = reinterpret_cast<const uint2 *>(o.count)[threadIdx.x];
-        n[0] += c.x, n[1] += c.y;
-        if (weights) {
-            const uint2 l = reinterpret_cast<const uint2 *>(o.low)[threadIdx.x], h = reinterpret_cast<const uint2 *>(o.high)[threadIdx.x];
-            w[0] += (static_cast<uint64_t>(h.x) << 32) + l.x, w[1] += (static_cast<uint64_t>(h.y) << 32) + l.y;
-        }
+        n += o.count[bin];
+        if (weights) w += (static_cast<uint64_t>(o.high[bin]) << 32) + o.low[bin];
     }
-    static_assert(kEach == 2, "two bins a thread");
-    n_sum = n[0] + n[1], w_sum = w[0] + w[1];
-    uint32_t n_at = n_sum;
-    uint64_t w_at = w_sum;
-    scan(s, n_at, w_at);
-    n_at -= n_sum, w_at -= w_sum;
-#pragma unroll
-    for (int j = 0; j < kEach; ++j) {
-        const int bin = threadIdx.x * kEach + j;
-        if (first_level) s.before[bin] = w_at, s.first_count[bin] = n[j];
-        if (by_weight && first_level) need = 0;   // not known before all sums are
-        const uint64_t at = by_weight ? w_at : n_at, with = at + (by_weight ? w[j] : n[j]);
-        if (at < need && need <= with) {
-            found.count = n[j];
-            found.upto = n_at + n[j];
-            found.need = need - at;
-            found.before = before + w_at;
-            found.lo = lo + (static_cast<uint64_t>(bin) << shift);
-            found.hi = found.lo + ((static_cast<uint64_t>(1) << shift) - 1);
-            if (found.hi > hi) found.hi = hi;
-        }
-        n_at += n[j], w_at += w[j];
+    uint32_t n_with = n;
+    uint64_t w_with = w;
+    scan(s, n_with, w_with);
+    if (first_level) {
+        s.before[bin] = w_with - w, s.first_count[bin] = n;
+        if (bin == kBins - 1) s.before[kBins] = w_with, s.counted = n_with;
+        if (by_weight) need = 0;   // not known before all sums are
     }
-    if (first_level && threadIdx.x == kThreads - 1) s.before[kBins] = w_at, s.counted = n_at;
+    const uint64_t with = by_weight ? w_with : n_with, at = with - (by_weight ? w : n);
+    if (at < need && need <= with) {
+        found.count = n;
+        found.upto = n_with;
+        found.need = need - at;
+        found.before = before + w_with - w;
+        found.lo = lo + (static_cast<uint64_t>(bin) << shift);
+        found.hi = found.lo + ((static_cast<uint64_t>(1) << shift) - 1);
+        if (found.hi > hi) found.hi = hi;
+    }
     __syncthreads();
 }
 
@@ -308,7 +292,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32, m = blockIdx.y;
     const unsigned rank = cluster.block_rank(), C = cluster.num_blocks();
     Shared &lead = *cluster.map_shared_rank(&s, 0);
-    if (tid < 256) s.table[tid] = g_table.v[tid];
+    if (tid < 256) s.power[tid] = g_table.v[tid];
     clear_histogram(s);
     if (tid == 0) s.top = 0, s.bottom = 0xffffffffu, s.lo = kAll, s.hi = 0, s.listed[0] = s.listed[1] = 0, s.cut[0] = s.cut[1] = kAll;
     grid_launch_dependents();
@@ -339,9 +323,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     float most = -INFINITY, lowest = INFINITY;   // lowest: above -inf
 #pragma unroll 4
     for (int i = tid; i < pieces; i += kThreads) {
-        float4 v = x4[i];
-        v = make_float4(cleaned(v.x), cleaned(v.y), cleaned(v.z), cleaned(v.w));
-        x4[i] = v;
+        const float4 v = x4[i];
         most = fmaxf(fmaxf(most, fmaxf(v.x, v.y)), fmaxf(v.z, v.w));
         const auto above = [](float a) { return a > -INFINITY ? a : INFINITY; };
         lowest = fminf(fminf(lowest, fminf(above(v.x), above(v.y))), fminf(above(v.z), above(v.w)));
@@ -356,7 +338,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     constexpr float kLog2eHi = 1.44269502e+00f, kLog2eLo = 1.92596299e-08f;
     Row r;
     r.top = of_key(top);
-    r.table = s.table;
+    r.power = s.power;
     r.c_hi = kLog2eHi / T;
     r.c_lo = T < INFINITY ? (fmaf(-r.c_hi, T, kLog2eHi) + kLog2eLo) / T : 0.0f;
     if (top <= key_of(-INFINITY)) {   // no logit above -inf
@@ -367,20 +349,24 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
         cluster.sync();   // nobody leaves while others read its memory
         return;
     }
-    // f(logit, index) for every token of the slice
+    const bool cut_p = top_p < 1.0f && k > 1, cut_k = k < g.V && k > 1;
+    // The histogram spans what the row's logits do, a vocabulary of nearly equal ones too.
+    float span = fminf(kMostT, fmaxf(1.001f * rough_t(r, of_key(bottom)), 1e-6f));
+    // A warp's share of the slice, or a list of those of its tokens that can count, in their order
+    const int share = (pieces + 3) / 4, first = warp * share;
+    int tokens = max(0, min(share, 4 * pieces - first));
+    bool listed = false;
+    const uint16_t *list = s.listed_token[warp];
+    // f(logit, index) for each of them
     auto each_token = [&](auto f) {
-        for (int i = tid; i < pieces; i += kThreads) {
-            const float4 v = x4[i];
-            const uint32_t at = static_cast<uint32_t>(index0 + 4 * i);
-            f(v.x, at), f(v.y, at + 1), f(v.z, at + 2), f(v.w, at + 3);
+#pragma unroll 4
+        for (int j = lane; j < tokens; j += 32) {
+            const int i = first + (listed ? list[j] : j);
+            f(x[i], static_cast<uint32_t>(index0 + i));
         }
     };
-    // The histogram spans what the row's logits do, a vocabulary of nearly equal ones too.
-    const float span = fminf(kMostT, fmaxf(1.001f * rough_t(r, of_key(bottom)), 1e-6f)), per_t = static_cast<float>(kBins) / span;
-    auto bin_of = [&](float t) { return min(static_cast<int>(t * per_t), kBins - 1); };
     const uint64_t least = min_p > 0.0f && k > 1 ? (min_p >= 1.0f ? kOne : max(static_cast<unsigned long long>(1), static_cast<unsigned long long>(share_above(min_p, kOne)))) : 1;
     uint64_t cut = kAll;   // the last kept token's code
-    const bool cut_p = top_p < 1.0f && k > 1, cut_k = k < g.V && k > 1;
     if (k == 1) {   // the first of the largest
         uint64_t first = kAll;
         each_token([&](float v, uint32_t at) {
@@ -399,17 +385,46 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
         cluster.sync();
         return;
     }
+    uint64_t whole = 0;   // all weights, where a top-p is of them
+    if (cut_p && !cut_k) {
+        uint64_t sum = 0;
+        each_token([&](float v, uint32_t) { sum += weight(r, v); });
+        sum = sum_over_cta(s, sum);
+        if (tid == 0) s.total = sum;
+        cluster.sync();
+        whole = warp_sum64(lane < static_cast<int>(C) ? cluster.map_shared_rank(&s, lane)->total : 0);
+        // Together, the tokens that are V / (1 - p) times lighter than the whole are behind the cut.
+        span = fminf(span, log2f(static_cast<float>(g.V) * static_cast<float>(kOne) / ((1.0f - top_p) * static_cast<float>(whole))) + 0.01f);
+        int n = 0;
+#pragma unroll 4
+        for (int j = lane; j - lane < tokens; j += 32) {
+            const bool in = j < tokens && rough_t(r, x[first + j]) <= span;
+            const uint32_t who = __ballot_sync(0xffffffffu, in);
+            const int at = n + __popc(who & ((1u << lane) - 1));
+            if (in && at < kListed) s.listed_token[warp][at] = static_cast<uint16_t>(j);
+            n += __popc(who);
+        }
+        __syncwarp();
+        listed = n <= kListed;
+        if (listed) tokens = n;
+    }
+    const float per_t = static_cast<float>(kBins) / span;
+    auto bin_of = [&](float t) { return min(static_cast<int>(t * per_t), kBins - 1); };
     if (cut_p || cut_k) {
-        // Behind a small top-k the tokens up to the cut are most likely few, and weights not needed for more than those.
-        bool weights = cut_p && !(cut_k && k <= kRanked / 2);
+        // Behind a small top-k, the histogram is of the threads' largest logits alone: as many of them as k are in
+        // some first bins, so at least that many tokens are, and most likely few more. Those go to the first CTA.
+        bool few = cut_k && k <= kRanked / 2;
         for (;;) {
-            each_token([&](float v, uint32_t) {
+            const bool weights = cut_p && !few;
+            auto count = [&](float v, uint32_t) {
                 const float t = rough_t(r, v);
                 if (!(t <= span)) return;
                 const int bin = bin_of(t);
                 atomicAdd(&s.count[bin], 1u);
                 if (weights) add64(s, bin, weight(r, v));
-            });
+            };
+            if (few) count(most, 0);
+            else each_token(count);
             cluster.sync();
             if (rank == 0) {
                 pick(cluster, s, s.found[0], weights, !cut_k, true, static_cast<uint64_t>(k), 0, kAll, 0, 0);
@@ -417,36 +432,47 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
                 // fewer tokens of any weight than k, and few: the last bin is taken for the cut's
                 if (tid == 0 && cut_k && !s.found[0].count && s.counted <= kRanked) s.found[0] = Found{kBins - 1, 0, 0, 0, s.counted, s.counted};
                 if (!cut_k) {   // the share of the whole sum
-                    const uint64_t y = share_above(top_p, s.before[kBins]);
-                    uint32_t n = 0;
-                    for (int j = 0; j < kBins / kThreads; ++j) {
-                        const int bin = tid * (kBins / kThreads) + j;
-                        if (s.before[bin] < y) n += s.first_count[bin];   // bins up to the cut's, all of them
-                    }
-                    const uint32_t upto = static_cast<uint32_t>(sum_over_cta(s, n));
-                    for (int bin = tid; bin < kBins; bin += kThreads) {
-                        if (s.before[bin] >= y || y > s.before[bin + 1]) continue;
-                        s.found[0] = Found{static_cast<uint64_t>(bin), 0, y - s.before[bin], s.before[bin], s.first_count[bin], upto};
-                    }
+                    const uint64_t y = share_above(top_p, whole);
+                    const uint32_t upto = static_cast<uint32_t>(sum_over_cta(s, s.before[tid] < y ? s.first_count[tid] : 0));   // bins up to the cut's, all of them
+                    if (s.before[tid] < y && y <= s.before[tid + 1])
+                        s.found[0] = Found{static_cast<uint64_t>(tid), 0, y - s.before[tid], s.before[tid], s.first_count[tid], upto};
+                    if (tid == 0) s.upto = whole;
                 }
             }
             cluster.sync();
             const Found f = lead.found[0];
-            if (f.count && f.upto <= kRanked) {   // few tokens: the first CTA sees to them
+            if (f.count && (few || f.upto <= kRanked)) {   // few tokens: the first CTA sees to them
                 const int last = static_cast<int>(f.lo);
-                each_token([&](float v, uint32_t at) {
+                auto send = [&](float v, uint32_t at) {
                     const float t = rough_t(r, v);
                     if (!(t <= span) || bin_of(t) > last) return;
                     const uint32_t i = atomicAdd(&lead.listed[0], 1u);
                     if (i < kRanked) lead.list[0][i] = code_of(v, at);
-                });
+                };
+                if (listed) {
+                    each_token(send);
+                } else {
+#pragma unroll 2
+                    for (int i = tid; i < pieces; i += kThreads) {
+                        const float4 v = x4[i];
+                        const float t = rough_t(r, fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
+                        if (!(t <= span) || bin_of(t) > last) continue;
+                        const uint32_t at = static_cast<uint32_t>(index0 + 4 * i);
+                        send(v.x, at), send(v.y, at + 1), send(v.z, at + 2), send(v.w, at + 3);
+                    }
+                }
                 cluster.sync();
-                if (rank == 0) draw_from_list(s, g, r, m, static_cast<int>(f.upto), k, cut_k, cut_p, top_p, s.upto, least, u);
-                return;   // the others' memory is not read any more
+                const uint32_t n = few ? lead.listed[0] : f.upto;
+                if (few) cluster.sync();   // all have read it
+                if (n <= kRanked) {
+                    if (rank == 0) draw_from_list(s, g, r, m, static_cast<int>(n), k, cut_k, cut_p, top_p, s.upto, least, u);
+                    return;   // the others' memory is not read any more
+                }
             }
-            if (weights || !cut_p) break;
-            weights = true;   // more than a few after all
+            if (!few) break;
+            few = false;   // more than a few after all
             clear_histogram(s);
+            if (tid == 0) s.listed[0] = 0;
             cluster.sync();
         }
         for (int by_weight = cut_k ? 0 : 1; by_weight < (cut_p ? 2 : 1); ++by_weight) {
@@ -456,10 +482,8 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
                     if (tid == 0) s.found[1].count = 0;
                     const uint64_t y = share_above(top_p, s.upto);
                     __syncthreads();
-                    for (int bin = tid; bin < kBins; bin += kThreads) {
-                        if (s.before[bin] >= y || y > s.before[bin + 1]) continue;
-                        s.found[1] = Found{static_cast<uint64_t>(bin), 0, y - s.before[bin], s.before[bin], s.first_count[bin], 0};
-                    }
+                    if (s.before[tid] < y && y <= s.before[tid + 1])
+                        s.found[1] = Found{static_cast<uint64_t>(tid), 0, y - s.before[tid], s.before[tid], s.first_count[tid], 0};
                 }
                 cluster.sync();
             }
@@ -489,7 +513,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
                 }
                 f.lo = lo, f.hi = hi;
                 while (f.count > kRanked) {
-                    const int shift = max(0, 64 - __clzll(static_cast<long long>(f.hi - f.lo)) - 10);
+                    const int shift = max(0, 64 - __clzll(static_cast<long long>(f.hi - f.lo)) - 9);
                     clear_histogram(s);
                     __syncthreads();
                     each_token([&](float v, uint32_t at) {
@@ -543,7 +567,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
             if (lead.cut[which] < cut) cut = lead.cut[which];
         }
     }
-    // what is kept, in pieces of 128 tokens
+    // what is kept, in pieces
     // (first what one comparison of fp32 shows: below the last kept logit, or far below min_p)
     const float cut_x = cut == kAll ? -INFINITY : of_key(~static_cast<uint32_t>(cut >> 32));
     const float most_t = min_p > 0.0f && min_p < 1.0f ? fminf(kMostT, 0.001f - log2f(min_p)) : kMostT;
@@ -552,75 +576,48 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
         const uint64_t w = weight(r, v);
         return w >= least ? w : 0;
     };
+    auto kept_at = [&](int j) -> uint64_t {
+        if (j >= tokens) return 0;
+        const int i = first + (listed ? list[j] : j);
+        return kept(x[i], static_cast<uint32_t>(index0 + i));
+    };
     uint64_t mine = 0;
-    for (int piece = warp; piece * 32 < pieces; piece += kWarps) {
-        const int i = piece * 32 + lane;
-        uint64_t w = 0;
-        if (i < pieces) {
-            const float4 v = x4[i];
-            const uint32_t at = static_cast<uint32_t>(index0 + 4 * i);
-            w = kept(v.x, at) + kept(v.y, at + 1) + kept(v.z, at + 2) + kept(v.w, at + 3);
-        }
-        // a sum of 32 weights' low 24 bits, and of what is above, fit 32 bits
+    for (int p = 0; p * kPiece < tokens; ++p) {
+        uint64_t w = kept_at(p * kPiece + lane) + kept_at(p * kPiece + 32 + lane);
+        // a sum of 64 weights' low 24 bits, and of what is above, fit 32 bits
         w = (static_cast<uint64_t>(__reduce_add_sync(0xffffffffu, static_cast<uint32_t>(w >> 24))) << 24) +
             __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(w) & 0xffffffu);
-        if (lane == 0) s.piece[piece] = w;
+        if (lane == 0) s.piece[warp][p] = w;
         mine += w;
     }
-    mine = sum_over_cta(s, lane == 0 ? mine : 0);
-    if (tid == 0) s.total = mine;
+    const uint64_t of_cta = sum_over_cta(s, lane == 0 ? mine : 0);
+    if (tid == 0) s.total = of_cta;
     cluster.sync();
-    if (warp > 0) {
-        cluster.sync();
-        return;
-    }
-    uint64_t upto_rank = lane < static_cast<int>(C) ? cluster.map_shared_rank(&s, lane)->total : 0;
-#pragma unroll
-    for (int o = 1; o < 16; o *= 2) {
-        const uint64_t b = shfl_up64(upto_rank, o);
-        if (lane >= o) upto_rank += b;
-    }
-    const uint64_t total = __shfl_sync(0xffffffffu, upto_rank, C - 1), before = __shfl_sync(0xffffffffu, upto_rank, rank) - mine;
-    const uint64_t y = drawn(u, total);
-    if (before <= y && y < before + mine) {
-        uint64_t at = before;
-        int piece = 0;
-        for (; piece * 32 < pieces; piece += 32) {
-            uint64_t w = (piece + lane) * 32 < pieces ? s.piece[piece + lane] : 0, upto = w;
-#pragma unroll
-            for (int o = 1; o < 32; o *= 2) {
-                const uint64_t b = shfl_up64(upto, o);
-                if (lane >= o) upto += b;
-            }
-            const uint32_t past = __ballot_sync(0xffffffffu, at + upto > y);
-            const int in = past ? __ffs(past) - 1 : 31;
-            at += __shfl_sync(0xffffffffu, upto - (past ? w : 0), in);
-            if (past) {
-                piece += in;
-                break;
-            }
-        }
-        const int i = piece * 32 + lane;
-        uint64_t w[4] = {0, 0, 0, 0};
-        if (i < pieces) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = kept(x[4 * i + j], static_cast<uint32_t>(index0 + 4 * i + j));
-        }
-        const uint64_t sum4 = w[0] + w[1] + w[2] + w[3];
-        uint64_t upto = sum4;
+    // (inclusive sums over a warp's lanes)
+    auto scanned = [&](uint64_t v) {
 #pragma unroll
         for (int o = 1; o < 32; o *= 2) {
-            const uint64_t b = shfl_up64(upto, o);
-            if (lane >= o) upto += b;
+            const uint64_t b = shfl_up64(v, o);
+            if (lane >= o) v += b;
         }
-        at += upto - sum4;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (at <= y && y < at + w[j]) {
-                g.token[m] = index0 + 4 * i + j;
-                if (g.prob) g.prob[m] = ratio(w[j], total);
+        return v;
+    };
+    const uint64_t upto_rank = scanned(lane < static_cast<int>(C) ? cluster.map_shared_rank(&s, lane)->total : 0);
+    const uint64_t total = __shfl_sync(0xffffffffu, upto_rank, C - 1), y = drawn(u, total);
+    uint64_t at = __shfl_sync(0xffffffffu, upto_rank, rank) - of_cta;
+    for (int i = 0; i < warp; ++i) at += s.warp_sum[i];
+    if (at <= y && y < at + mine) {
+        __syncwarp();
+        int p = 0;
+        for (; y >= at + s.piece[warp][p]; ++p) at += s.piece[warp][p];
+#pragma unroll 1
+        for (int j = p * kPiece + lane; j < (p + 1) * kPiece; j += 32) {
+            const uint64_t w = kept_at(j), upto = scanned(w);
+            if (at + upto - w <= y && y < at + upto) {
+                g.token[m] = index0 + first + (listed ? list[j] : j);
+                if (g.prob) g.prob[m] = ratio(w, total);
             }
-            at += w[j];
+            at += __shfl_sync(0xffffffffu, upto, 31);
         }
     }
     cluster.sync();   // nobody leaves while others read its memory
