@@ -8,22 +8,27 @@
 // The choice has to be the one of exact arithmetic: tokens' shares of the sum are as small as
 // 1e-7 or less, where sums in fp32 would move the borders between them by whole tokens. So weights are
 // whole numbers, 2^44 for the largest token: t to 2^-33 or so by a two-term difference and
-// product, 2^-t from a table of 256 and a short series, 2^-32 off its value; below 2^-44
+// product, 2^-t from a table of 256 and a short series, some 2^-32 off its value; below 2^-44
 // they are 0. Sums of whole numbers are exact, in any order, so the same call gives the
 // same token, and nothing is sorted: the cuts are found by histograms.
 //
 // A row is a cluster's: each CTA keeps a slice of it in shared memory. Pass 1 finds the
-// maximum. Pass 2, where there is a top-k or top-p, a histogram of 1024 bins of t (counts, and sums
-// where a top-p needs them); the first CTA adds them over the cluster and finds the bin that
-// holds the cut. Where the tokens up to that bin are few, as behind most top-k, they go to the
-// first CTA, which ranks them and draws. Else only the bin's tokens do (bins of more than 256
-// are split again by the bits of (logit, index)); then pass 3 sums what is kept, in pieces of
-// 128 tokens, and the piece that u falls to is gone through.
+// maximum. A small top-k: a histogram of 512 bins of t of the threads' largest logits alone shows a
+// bin up to which there are k tokens or more; those up to it go to the first CTA, which ranks
+// them and draws. A top-p alone: all weights are summed; tokens so light that all of them together would
+// not reach beyond 1 - p are behind the cut, the others' places go to lists, a warp each. Then, or with a
+// larger top-k, a histogram of counts and sums of weights, added over the cluster by the first CTA, finds the
+// bin that holds the cut. Where the tokens up to that bin are few they too go to the
+// first CTA, which draws. Else only the bin's tokens do (bins of more than 256
+// are split again by the bits of (logit, index)); then the last pass sums what is kept, in pieces of
+// 64 tokens, and the piece that u falls to is gone through.
 //
-// Bound by what it executes: 96 rows of 151936, four in five with a top-k of 50, take 61 us (the logits'
-// bytes 8.6), eight rows with a top-p alone 29, one of 32000 with a top-k 9. A weight is 35
-// instructions, a token of the histogram two or three atomics. (CTAs of 16 to a row, or 4, or of 1024 threads: 103, 93
-// and 98 us for what then took 70; sums by 64-bit atomics of shared memory 72 for 57.)
+// Bound by what it executes: 96 rows of 151936, four in five with a top-k of 50, take 52 us (the logits'
+// bytes 8.6), eight rows with a top-p alone 25, one of 32000 with a top-k 9. A weight is some 45
+// instructions with its place in a table, a token of the histogram two or three atomics more: with a
+// histogram of all tokens that was 61, 29 and 9 us. (CTAs of 16 to a row, or 4, or of 1024 threads: 103, 93
+// and 98 us for what then took 70; 16 for up to four rows 5 % faster, for eight 6 % slower; sums by
+// 64-bit atomics of shared memory 72 for 57.)
 #include <algorithm>
 
 #include <cooperative_groups.h>
@@ -351,18 +356,23 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     }
     const bool cut_p = top_p < 1.0f && k > 1, cut_k = k < g.V && k > 1;
     // The histogram spans what the row's logits do, a vocabulary of nearly equal ones too.
-    float span = fminf(kMostT, fmaxf(1.001f * rough_t(r, of_key(bottom)), 1e-6f));
+    const float range = 1.001f * rough_t(r, of_key(bottom));
+    float span = fminf(kMostT, fmaxf(range, 1e-6f));
     // A warp's share of the slice, or a list of those of its tokens that can count, in their order
-    const int share = (pieces + 3) / 4, first = warp * share;
+    const int share = 4 * ((pieces + kWarps - 1) / kWarps), first = warp * share;
     int tokens = max(0, min(share, 4 * pieces - first));
     bool listed = false;
     const uint16_t *list = s.listed_token[warp];
     // f(logit, index) for each of them
     auto each_token = [&](auto f) {
-#pragma unroll 4
-        for (int j = lane; j < tokens; j += 32) {
-            const int i = first + (listed ? list[j] : j);
-            f(x[i], static_cast<uint32_t>(index0 + i));
+        if (listed) {
+            for (int j = lane; j < tokens; j += 32) f(x[first + list[j]], static_cast<uint32_t>(index0 + first + list[j]));
+            return;
+        }
+        for (int i = first + 4 * lane; i < first + tokens; i += 128) {
+            const float4 v = *reinterpret_cast<const float4 *>(x + i);
+            const uint32_t at = static_cast<uint32_t>(index0 + i);
+            f(v.x, at), f(v.y, at + 1), f(v.z, at + 2), f(v.w, at + 3);
         }
     };
     const uint64_t least = min_p > 0.0f && k > 1 ? (min_p >= 1.0f ? kOne : max(static_cast<unsigned long long>(1), static_cast<unsigned long long>(share_above(min_p, kOne)))) : 1;
@@ -385,8 +395,12 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
         cluster.sync();
         return;
     }
-    uint64_t whole = 0;   // all weights, where a top-p is of them
-    if (cut_p && !cut_k) {
+    uint64_t whole = 0;   // all weights, where lists are made
+    // Lists pay where most tokens are left out: by the row's range, as wide as that of normal logits of which a quarter is
+    // listed. 32 rows of 151936 normal logits of standard deviation 3, 3.5 and 4, top-p 0.9: 55, 39 and 36 us for 59, 47 and
+    // 41 without; 2 and 2.5, where lists would not hold them, 77 and 74 for 64 and 62.
+    const bool listing = cut_p && !cut_k && range > 23.0f - 3.6f * log2f(1.0f - top_p);
+    if (listing) {
         uint64_t sum = 0;
         each_token([&](float v, uint32_t) { sum += weight(r, v); });
         sum = sum_over_cta(s, sum);
@@ -432,6 +446,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
                 // fewer tokens of any weight than k, and few: the last bin is taken for the cut's
                 if (tid == 0 && cut_k && !s.found[0].count && s.counted <= kRanked) s.found[0] = Found{kBins - 1, 0, 0, 0, s.counted, s.counted};
                 if (!cut_k) {   // the share of the whole sum
+                    if (!listing) whole = s.before[kBins];
                     const uint64_t y = share_above(top_p, whole);
                     const uint32_t upto = static_cast<uint32_t>(sum_over_cta(s, s.before[tid] < y ? s.first_count[tid] : 0));   // bins up to the cut's, all of them
                     if (s.before[tid] < y && y <= s.before[tid + 1])
@@ -441,7 +456,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
             }
             cluster.sync();
             const Found f = lead.found[0];
-            if (f.count && (few || f.upto <= kRanked)) {   // few tokens: the first CTA sees to them
+            if (f.count && f.upto <= kRanked) {   // few tokens: the first CTA sees to them
                 const int last = static_cast<int>(f.lo);
                 auto send = [&](float v, uint32_t at) {
                     const float t = rough_t(r, v);

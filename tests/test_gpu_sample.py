@@ -31,23 +31,42 @@ def run(args, **kw):
 
 def check(args):
     token, prob = run(args)
+    V = args["logits"].shape[1]
     of = lambda name, m, none: none if args[name] is None else args[name][m].item()  # noqa: E731
     for m in range(len(token)):
-        ids, w = cache8_ref.kept(args["logits"][m], of("temperature", m, 1.0), of("top_k", m, 0), of("top_p", m, 1.0), of("min_p", m, 0.0))
         got = int(token[m])
-        if len(ids) == 0:
-            assert got == -1 and float(prob[m]) == 0
-            continue
-        at = (ids == got).nonzero()
-        assert at.numel() == 1, (m, got, len(ids))
-        at = int(at)
-        upto = torch.cumsum(w, 0)
-        total = float(upto[-1])
-        target = min(max(float(args["u"][m]), 0.0), 1 - 2.0 ** -24) * total
-        near = 2.0 ** -31 * total + 2.0 ** -44 * len(ids)
-        assert float(upto[at] - w[at]) - near <= target < float(upto[at]) + near, (m, got)
-        assert abs(float(prob[m]) - float(w[at]) / total) <= 2.0 ** -23 * float(w[at]) / total + 2.0 ** -40, m
+        wrong = []
+        # A top-p's border is p S, and both S and the sum before a token are within e = 2^-31 + 2^-44 V of S (which is
+        # 1 at least) of their values: they compare as at some p' with |p' - p| <= e (1 + p). So a token that is on the border but
+        # for that is kept or not; equal heavy tokens, whose sums meet p S exactly but for tokens of 2^-49, are.
+        p = of("top_p", m, 1.0)
+        e = (2.0 ** -31 + 2.0 ** -44 * V) * (1 + p)
+        for top_p in (p, p - e, p + e) if 0 < p < 1 else (p,):
+            ids, w = cache8_ref.kept(args["logits"][m], of("temperature", m, 1.0), of("top_k", m, 0), top_p, of("min_p", m, 0.0))
+            wrong.append(not_drawn(ids, w, got, float(prob[m]), float(args["u"][m])))
+            if wrong[-1] is None:
+                break
+        assert wrong[-1] is None, (m, got, wrong)
     return token
+
+
+def not_drawn(ids, w, got, prob, u):
+    """Why the token is not the one that u falls to among the tokens ids of weights w, or None."""
+    if len(ids) == 0:
+        return None if got == -1 and prob == 0 else "no token is kept"
+    at = (ids == got).nonzero()
+    if at.numel() != 1:
+        return f"not among the {len(ids)} kept"
+    at = int(at)
+    upto = torch.cumsum(w, 0)
+    total = float(upto[-1])
+    target = min(max(u, 0.0), 1 - 2.0 ** -24) * total
+    near = 2.0 ** -31 * total + 2.0 ** -44 * len(ids)
+    if not float(upto[at] - w[at]) - near <= target < float(upto[at]) + near:
+        return f"{target} is not in {float(upto[at] - w[at])} .. {float(upto[at])}"
+    if not abs(prob - float(w[at]) / total) <= 2.0 ** -23 * float(w[at]) / total + 2.0 ** -40:
+        return f"probability {prob}, not {float(w[at]) / total}"
+    return None
 
 
 @pytest.mark.parametrize("filters", [{}, dict(top_k=5), dict(top_p=0.8), dict(min_p=0.1), dict(top_k=50, top_p=0.95),
@@ -175,6 +194,46 @@ def test_rows_that_start_anywhere():
         args = inputs(7, 4099, top_k=100, top_p=0.9, seed=8)
         args["logits"] = whole[skew:skew + 7 * 4099].view(7, 4099)
         check(args)
+
+
+@pytest.mark.parametrize("V", [37, 8191, 70001])
+@pytest.mark.parametrize("spread", [2.0, 4.0, 8.0, 30.0])
+def test_a_top_p_alone_of_narrow_and_wide_rows(spread, V):
+    for top_p in (0.2, 0.9, 0.99, 0.9999):
+        check(inputs(3, V, spread, top_p=top_p, min_p=0.001 if spread == 8.0 else None, seed=int(spread) + V))
+
+
+@pytest.mark.parametrize("top_p", [0.5, 0.95, 0.9999])
+def test_wide_rows_whose_tokens_are_nearly_all_alike(top_p):
+    """Some light tokens make the range wide, though all but those count; or a few heavy ones, and a cut far among the others."""
+    args = inputs(4, 20011, 0.01, top_p=top_p, temperature=False, seed=14)
+    x = args["logits"]
+    x[:3, 5:20011:4000] = -60.0
+    x[1, ::2], x[1, 1::7] = -math.inf, math.nan
+    x[2] = torch.where(x[2] > -1, 0.0, x[2])
+    x[2, 11::13] = -0.0
+    x[3] = torch.where(torch.arange(20011, device="cuda") % 1000 == 17, 9.0, x[3] - 25.0)
+    check(args)
+
+
+def test_special_logits_of_wide_rows():
+    args = inputs(5, 9001, 6.0, top_p=0.9, temperature=False, seed=15)
+    x = args["logits"]
+    x[0, ::3] = math.nan
+    x[1, 1::2] = -math.inf
+    x[2, [4, 8000]] = math.inf
+    x[3, :8000] = -80.0
+    x[4, 77] = torch.finfo(torch.float32).max
+    check(args)
+
+
+def test_threads_largest_logits_in_a_few_places():
+    """As many large logits as top_k in the parts of few threads; all of them in one."""
+    args = inputs(3, 50001, 0.1, top_k=60, top_p=0.97, seed=16)
+    args["logits"][0, 4096:4196] += 9.0
+    args["logits"][1, 48000:48300] += 5.0
+    args["logits"][2, :4] += 20.0
+    check(args)
 
 
 def test_a_large_vocabulary():
