@@ -13,8 +13,10 @@
 //
 // A group of L lanes (8, 16 or 32: the power of two that holds D / 8) has a head of a token,
 // a lane 8 of its elements: 4 pairs of the rotated part, or 8 elements beyond it. Bound by
-// the bytes and by what a lane executes for them: 4001 tokens of 40 + 8 + 8 heads of 128 take 35 us in 16
-// bits (4.9 TB/s) and 40 us as codes (4.1).
+// the bytes and by what a lane executes for them: 4001 tokens of 40 + 8 + 8 heads of 128 take 30 us in 16
+// bits (5.8 TB/s) and 40 us as codes (4.1).
+#include <algorithm>
+
 #include "decode_device.cuh"
 #include "decode_ops.h"
 #include "qmv.h"
@@ -26,7 +28,14 @@ namespace {
 __device__ uint32_t g_norm_rope_error;
 
 constexpr int kThreads = 256;
-constexpr int kTwoRows = 256;   // rows from which a CTA takes two
+constexpr int kTwoRows = 256;   // rows from which a CTA takes two, with codes
+// Rows from which CTAs go through many, in 16 bits: 1000 rows of 56 heads 10.2 us for 10.3 by a CTA a row, 4001 29.8 for
+// 35.6 by CTAs of two; 512 alike, 256 4.4 for 3.7. (With codes, q in such a launch of its own 41 us for 40 with 4005 rows.)
+constexpr int kStreamRows = 1000;
+// CTAs of so many threads, all on the SMs at once; a CTA's rows that are on their way and the one it works on. (4 or 3 for 2
+// stages 31.6 and 29.9 us for 29.7; 256 threads 32.7, 64 30.1.)
+constexpr int kStreamThreads = 128, kStreamCtas = 152 * 8, kStages = 2;
+using Ring = float4[kStages][2][kStreamThreads];
 
 // The 8 elements e0 .. e0 + 3 and e1 .. e1 + 3 of a head that a lane has.
 struct Unit {
@@ -71,14 +80,22 @@ struct Angles {
     float4 a, b;
 };
 
-__device__ __forceinline__ int position_of(const NormRopeArgs &g, int m, int axis)
+__device__ __forceinline__ int position_inside(const NormRopeArgs &g, int pos)
 {
-    int pos = g.positions[static_cast<int64_t>(axis) * g.M + m];
     if (pos < 0 || pos >= g.n_positions) {
         atomicOr(&g_norm_rope_error, kErrIndex);
         pos = pos < 0 ? 0 : g.n_positions - 1;
     }
     return pos;
+}
+
+__device__ __forceinline__ int position_of(const NormRopeArgs &g, int m, int axis) { return position_inside(g, g.positions[static_cast<int64_t>(axis) * g.M + m]); }
+
+// Of a position and pairs 4 i .. 4 i + 3.
+__device__ __forceinline__ Angles angles_at(const NormRopeArgs &g, int pos, int i)
+{
+    const float4 *at = reinterpret_cast<const float4 *>(g.table) + (static_cast<int64_t>(pos) * (g.rot / 2) + 4 * i) / 2;
+    return Angles{__ldg(at), __ldg(at + 1)};
 }
 
 // Of row m and pairs 4 i .. 4 i + 3. Lanes with the same i of all of a CTA's heads read the same ones: L1
@@ -87,12 +104,10 @@ __device__ __forceinline__ int position_of(const NormRopeArgs &g, int m, int axi
 __device__ __forceinline__ Angles angles_of(const NormRopeArgs &g, int m, int i)
 {
     const int pairs = g.rot / 2;
-    const float4 *table = reinterpret_cast<const float4 *>(g.table);
     Angles t;
     const uint32_t axes = reinterpret_cast<const uint32_t *>(g.axis_of_pair)[i], axis = axes & 0xffu;   // of the four pairs
     if (axes == axis * 0x01010101u) {
-        const float4 *at = table + (static_cast<int64_t>(position_of(g, m, static_cast<int>(axis))) * pairs + 4 * i) / 2;
-        t.a = __ldg(at), t.b = __ldg(at + 1);
+        t = angles_at(g, position_of(g, m, static_cast<int>(axis)), i);
     } else {
         float2 c[4];
 #pragma unroll
@@ -130,12 +145,22 @@ __device__ __forceinline__ void load_weight(float (&w)[8], const float *weight, 
     w[0] = p.x, w[1] = p.y, w[2] = p.z, w[3] = p.w, w[4] = q.x, w[5] = q.y, w[6] = q.z, w[7] = q.w;
 }
 
-__device__ __forceinline__ int64_t slot_of(const NormRopeArgs &g, int m)
+// A slot, or -1 for one that lies outside.
+__device__ __forceinline__ int64_t slot_inside(const NormRopeArgs &g, int64_t slot)
 {
-    const int64_t slot = g.slots[m];
     if (slot < g.n_slots) return slot;
-    if (threadIdx.x == 0) atomicOr(&g_norm_rope_error, kErrIndex);
+    atomicOr(&g_norm_rope_error, kErrIndex);
     return -1;
+}
+
+template <typename T>
+__device__ __forceinline__ void put_head(const NormRopeArgs &g, int m, int head, bool is_v, int64_t slot, const Unit &u, const float (&x)[8])
+{
+    if (head < g.Hq) {
+        store8<T>(g.q, static_cast<int64_t>(m) * g.Hq + head, g.D, u, x);
+    } else if (slot >= 0) {
+        store8<T>(is_v ? g.v_cache : g.k_cache, slot * g.Hkv + head - g.Hq - (is_v ? g.Hkv : 0), g.D, u, x);
+    }
 }
 
 // kThreads / L heads of rows m .. m + R - 1, from head `first` on, of `heads` (q heads, then k,
@@ -163,27 +188,84 @@ __device__ __forceinline__ void row_heads(const NormRopeArgs &g, int m, int firs
         if (g.q_norm || g.k_norm) norm8<L>(x[r], w, weight != nullptr, g);
         if (!live || r >= rows) continue;
         if (u.turn) turn8<kInterleaved>(x[r], t[r]);
-        if (head < g.Hq) {
-            store8<T>(g.q, static_cast<int64_t>(m + r) * g.Hq + head, g.D, u, x[r]);
-        } else {
-            const int64_t slot = slot_of(g, m + r);
-            const int h = head - g.Hq - (is_v ? g.Hkv : 0);
-            if (slot >= 0) store8<T>(is_v ? g.v_cache : g.k_cache, slot * g.Hkv + h, g.D, u, x[r]);
-        }
+        put_head<T>(g, m + r, head, is_v, head < g.Hq ? 0 : slot_inside(g, g.slots[m + r]), u, x[r]);
     }
 }
 
-// Grid (rows / R, CTAs of kThreads / L heads).
-template <typename T, bool kInterleaved, int L, int R>
+// The same of rows m, m + step, .., kStreamThreads / L heads: each lane copies its own pieces of the next rows to shared memory, and
+// has the row's angles on their way, while it works on a row.
+template <typename T, bool kInterleaved, int L>
+__device__ __forceinline__ void stream_heads(const NormRopeArgs &g, int m, int step, int first, Ring &ring)
+{
+    const int tid = threadIdx.x, pairs = g.rot / 2, i = tid % L, head = first + tid / L;
+    const bool is_v = head >= g.Hq + g.Hkv;
+    const Unit u = unit_of<kInterleaved>(i, g.D, pairs, is_v);
+    const bool live = u.live && head < g.Hq + 2 * g.Hkv, turn = live && u.turn, normed = g.q_norm || g.k_norm;
+    const float *weight = is_v ? nullptr : head < g.Hq ? g.q_norm : g.k_norm;
+    float w[8] = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
+    if (live && weight) load_weight(w, weight, u);
+    const int64_t row = static_cast<int64_t>(g.Hq + 2 * g.Hkv) * g.D;
+    const float *in = g.qkv + static_cast<int64_t>(head) * g.D;
+    auto copy = [&](int at, int stage) {
+        if (live && at < g.M) {
+            cp_async_16(&ring[stage][0][tid], in + at * row + u.e0);
+            cp_async_16(&ring[stage][1][tid], in + at * row + u.e1);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int j = 0; j < kStages - 1; ++j) copy(m + j * step, j);
+    // of the four pairs; where they are of one axis, the position is there a row before the angles are asked for
+    const uint32_t axes = turn ? reinterpret_cast<const uint32_t *>(g.axis_of_pair)[i] : 0, axis = axes & 0xffu;
+    const bool one_axis = axes == axis * 0x01010101u, cached = live && head >= g.Hq;
+    const int *positions = g.positions + static_cast<int64_t>(axis) * g.M;
+    Angles next;
+    if (turn) next = angles_of(g, m, i);
+    int next_position = turn && m + step < g.M ? positions[m + step] : 0;
+    int64_t next_slot = cached ? g.slots[m] : 0;
+    int stage = 0;
+#pragma unroll 1
+    for (; m < g.M; m += step) {
+        copy(m + (kStages - 1) * step, (stage + kStages - 1) % kStages);
+        const Angles t = next;
+        const int64_t slot = next_slot;
+        const int position = next_position;
+        if (m + step < g.M) {
+            if (turn) next = one_axis ? angles_at(g, position_inside(g, position), i) : angles_of(g, m + step, i);
+            if (cached) next_slot = g.slots[m + step];
+            if (turn && m + 2 * step < g.M) next_position = positions[m + 2 * step];
+        }
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+        float x[8] = {};
+        if (live) {
+            const float4 p = ring[stage][0][tid], q = ring[stage][1][tid];
+            x[0] = p.x, x[1] = p.y, x[2] = p.z, x[3] = p.w, x[4] = q.x, x[5] = q.y, x[6] = q.z, x[7] = q.w;
+        }
+        stage = (stage + 1) % kStages;
+        if (normed) norm8<L>(x, w, weight != nullptr, g);
+        if (turn) turn8<kInterleaved>(x, t);
+        if (live) put_head<T>(g, m, head, is_v, cached ? slot_inside(g, slot) : 0, u, x);
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+// Grid (rows, CTAs of kThreads / L heads).
+template <typename T, bool kInterleaved, int L>
 __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ NormRopeArgs g)
 {
     grid_launch_dependents();
     grid_dependency_wait();
-    const int m = static_cast<int>(blockIdx.x) * R;
-    if (threadIdx.x == 0 && blockIdx.y == 0) {
-        for (int r = 0; r < R && m + r < g.M; ++r) (void)slot_of(g, m + r);   // flags what lies outside
-    }
-    row_heads<T, kInterleaved, L, R>(g, m, static_cast<int>(blockIdx.y) * (kThreads / L), g.Hq + 2 * g.Hkv);
+    row_heads<T, kInterleaved, L, 1>(g, static_cast<int>(blockIdx.x), static_cast<int>(blockIdx.y) * (kThreads / L), g.Hq + 2 * g.Hkv);
+}
+
+// Grid (CTAs that the rows go to in turn, CTAs of kStreamThreads / L heads).
+template <typename T, bool kInterleaved, int L>
+__global__ void __launch_bounds__(kStreamThreads, kStreamCtas / 152) norm_rope_stream_kernel(const __grid_constant__ NormRopeArgs g)
+{
+    __shared__ Ring ring;
+    grid_launch_dependents();
+    grid_dependency_wait();
+    stream_heads<T, kInterleaved, L>(g, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), static_cast<int>(blockIdx.y) * (kStreamThreads / L), ring);
 }
 
 // The least e >= -64 with largest <= 448 * 2^e, as the scale 2^e; `largest` the bits of a
@@ -315,11 +397,10 @@ __global__ void __launch_bounds__(kThreads) rope_e4m3_kernel(const __grid_consta
     }
 }
 
-template <typename T, bool kInterleaved, int L, int R>
+template <typename T, bool kInterleaved, int L>
 cudaError_t launch_typed(const NormRopeArgs &g, cudaStream_t s)
 {
-    constexpr int kHeads = kThreads / L;
-    const int row_ctas = (g.M + R - 1) / R;
+    constexpr int kHeads = kThreads / L, kStreamHeads = kStreamThreads / L;
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kThreads);
@@ -328,30 +409,32 @@ cudaError_t launch_typed(const NormRopeArgs &g, cudaStream_t s)
     cfg.numAttrs = set_launch_overlap_attr(attr);
     if constexpr (L <= 16) {   // codes: heads of 128 at most
         if (g.k_scale) {
+            const int rows = g.M >= kTwoRows ? 2 : 1;
             const int windows = (g.M + kScaleTokens - 1) / kScaleTokens, q_ctas = (g.Hq + kHeads - 1) / kHeads;
-            const int64_t grid = static_cast<int64_t>(windows) * 2 * g.Hkv + static_cast<int64_t>(row_ctas) * q_ctas;
+            const int64_t grid = static_cast<int64_t>(windows) * 2 * g.Hkv + static_cast<int64_t>((g.M + rows - 1) / rows) * q_ctas;
             if (grid > 0x7fffffff) return cudaErrorInvalidValue;
             cfg.gridDim = dim3(static_cast<unsigned>(grid));
-            return cudaLaunchKernelEx(&cfg, rope_e4m3_kernel<T, kInterleaved, L, R>, g, windows, q_ctas);
+            return rows == 2 ? cudaLaunchKernelEx(&cfg, rope_e4m3_kernel<T, kInterleaved, L, 2>, g, windows, q_ctas)
+                             : cudaLaunchKernelEx(&cfg, rope_e4m3_kernel<T, kInterleaved, L, 1>, g, windows, q_ctas);
         }
     }
-    cfg.gridDim = dim3(static_cast<unsigned>(row_ctas), static_cast<unsigned>((g.Hq + 2 * g.Hkv + kHeads - 1) / kHeads));
-    return cudaLaunchKernelEx(&cfg, norm_rope_kernel<T, kInterleaved, L, R>, g);
-}
-
-// Two rows a CTA where there are CTAs enough: weights and addresses are worked out once.
-template <typename T, bool kInterleaved, int L>
-cudaError_t launch_rows(const NormRopeArgs &g, cudaStream_t s)
-{
-    return g.M >= kTwoRows ? launch_typed<T, kInterleaved, L, 2>(g, s) : launch_typed<T, kInterleaved, L, 1>(g, s);
+    const int heads = g.Hq + 2 * g.Hkv;
+    if (g.M >= kStreamRows) {
+        const int head_ctas = (heads + kStreamHeads - 1) / kStreamHeads;
+        cfg.blockDim = dim3(kStreamThreads);
+        cfg.gridDim = dim3(static_cast<unsigned>(std::min(g.M, std::max(1, kStreamCtas / head_ctas))), static_cast<unsigned>(head_ctas));
+        return cudaLaunchKernelEx(&cfg, norm_rope_stream_kernel<T, kInterleaved, L>, g);
+    }
+    cfg.gridDim = dim3(static_cast<unsigned>(g.M), static_cast<unsigned>((heads + kHeads - 1) / kHeads));
+    return cudaLaunchKernelEx(&cfg, norm_rope_kernel<T, kInterleaved, L>, g);
 }
 
 template <typename T, bool kInterleaved>
 cudaError_t launch_lanes(const NormRopeArgs &g, cudaStream_t s)
 {
-    if (g.D <= 64) return launch_rows<T, kInterleaved, 8>(g, s);
-    if (g.D <= 128) return launch_rows<T, kInterleaved, 16>(g, s);
-    return launch_rows<T, kInterleaved, 32>(g, s);
+    if (g.D <= 64) return launch_typed<T, kInterleaved, 8>(g, s);
+    if (g.D <= 128) return launch_typed<T, kInterleaved, 16>(g, s);
+    return launch_typed<T, kInterleaved, 32>(g, s);
 }
 
 }  // namespace
