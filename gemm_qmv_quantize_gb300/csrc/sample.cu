@@ -468,7 +468,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
                     each_token(send);
                 } else {
 #pragma unroll 2
-                    for (int i = tid; i < pieces; i += kThreads) {
+                    for (int i = first / 4 + lane; i < (first + tokens) / 4; i += 32) {
                         const float4 v = x4[i];
                         const float t = rough_t(r, fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
                         if (!(t <= span) || bin_of(t) > last) continue;

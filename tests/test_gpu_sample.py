@@ -216,6 +216,20 @@ def test_wide_rows_whose_tokens_are_nearly_all_alike(top_p):
     check(args)
 
 
+@pytest.mark.parametrize("dense_first", [True, False])
+def test_some_shares_with_lists_and_some_without(dense_first):
+    """Ten heavy tokens, all that are kept; half of the others, 2000 on end, just heavy enough to be listed, more than lists hold."""
+    V = 70001
+    args = inputs(4, V, 0.02, top_p=0.99, temperature=False, seed=17)
+    x = args["logits"]
+    half = torch.arange(V, device="cuda") // 2000 % 2 == 0
+    x += torch.where(half == dense_first, -13.3, -40.0)
+    x[:, 5] = -60.0
+    x[:, 3001:V:7000] = 0.0
+    token = check(args)
+    assert bool((token % 7000 == 3001).all())
+
+
 def test_special_logits_of_wide_rows():
     args = inputs(5, 9001, 6.0, top_p=0.9, temperature=False, seed=15)
     x = args["logits"]
