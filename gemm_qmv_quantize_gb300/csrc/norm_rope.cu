@@ -28,10 +28,11 @@ namespace {
 __device__ uint32_t g_norm_rope_error;
 
 constexpr int kThreads = 256;
-constexpr int kTwoRows = 256;   // rows from which a CTA takes two, with codes
-// Rows from which CTAs go through many, in 16 bits: 1000 rows of 56 heads 10.2 us for 10.3 by a CTA a row, 4001 29.8 for
-// 35.6 by CTAs of two; 512 alike, 256 4.4 for 3.7. (With codes, q in such a launch of its own 41 us for 40 with 4005 rows.)
-constexpr int kStreamRows = 1000;
+constexpr int kTwoRows = 256;   // rows from which a CTA takes two: 512 of 56 heads 5.7 us for 6.1
+// Rows a CTA from which CTAs that fill the SMs go through them, in 16 bits. 4001 rows of 56 heads (23 each) 29.8 us for 35.6 by
+// CTAs of two rows, 1000 (6) 10.3 for 10.4; 1000 of 10 heads (2) 4.7 for 3.5, 8000 (13) 17.9 for 17.6. (With codes, q
+// in such a launch of its own 41 us for 40 with 4005 rows.)
+constexpr int kStreamRows = 6;
 // CTAs of so many threads, all on the SMs at once; a CTA's rows that are on their way and the one it works on. (4 or 3 for 2
 // stages 31.6 and 29.9 us for 29.7; 256 threads 32.7, 64 30.1.)
 constexpr int kStreamThreads = 128, kStreamCtas = 152 * 8, kStages = 2;
@@ -249,13 +250,13 @@ __device__ __forceinline__ void stream_heads(const NormRopeArgs &g, int m, int s
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-// Grid (rows, CTAs of kThreads / L heads).
-template <typename T, bool kInterleaved, int L>
+// Grid (rows / R, CTAs of kThreads / L heads).
+template <typename T, bool kInterleaved, int L, int R>
 __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ NormRopeArgs g)
 {
     grid_launch_dependents();
     grid_dependency_wait();
-    row_heads<T, kInterleaved, L, 1>(g, static_cast<int>(blockIdx.x), static_cast<int>(blockIdx.y) * (kThreads / L), g.Hq + 2 * g.Hkv);
+    row_heads<T, kInterleaved, L, R>(g, static_cast<int>(blockIdx.x) * R, static_cast<int>(blockIdx.y) * (kThreads / L), g.Hq + 2 * g.Hkv);
 }
 
 // Grid (CTAs that the rows go to in turn, CTAs of kStreamThreads / L heads).
@@ -401,6 +402,7 @@ template <typename T, bool kInterleaved, int L>
 cudaError_t launch_typed(const NormRopeArgs &g, cudaStream_t s)
 {
     constexpr int kHeads = kThreads / L, kStreamHeads = kStreamThreads / L;
+    const int rows = g.M >= kTwoRows ? 2 : 1, row_ctas = (g.M - 1) / rows + 1;
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kThreads);
@@ -409,24 +411,24 @@ cudaError_t launch_typed(const NormRopeArgs &g, cudaStream_t s)
     cfg.numAttrs = set_launch_overlap_attr(attr);
     if constexpr (L <= 16) {   // codes: heads of 128 at most
         if (g.k_scale) {
-            const int rows = g.M >= kTwoRows ? 2 : 1;
             const int windows = (g.M + kScaleTokens - 1) / kScaleTokens, q_ctas = (g.Hq + kHeads - 1) / kHeads;
-            const int64_t grid = static_cast<int64_t>(windows) * 2 * g.Hkv + static_cast<int64_t>((g.M + rows - 1) / rows) * q_ctas;
+            const int64_t grid = static_cast<int64_t>(windows) * 2 * g.Hkv + static_cast<int64_t>(row_ctas) * q_ctas;
             if (grid > 0x7fffffff) return cudaErrorInvalidValue;
             cfg.gridDim = dim3(static_cast<unsigned>(grid));
             return rows == 2 ? cudaLaunchKernelEx(&cfg, rope_e4m3_kernel<T, kInterleaved, L, 2>, g, windows, q_ctas)
                              : cudaLaunchKernelEx(&cfg, rope_e4m3_kernel<T, kInterleaved, L, 1>, g, windows, q_ctas);
         }
     }
-    const int heads = g.Hq + 2 * g.Hkv;
-    if (g.M >= kStreamRows) {
-        const int head_ctas = (heads + kStreamHeads - 1) / kStreamHeads;
+    const int heads = g.Hq + 2 * g.Hkv, stream_head_ctas = (heads + kStreamHeads - 1) / kStreamHeads;
+    const int at_once = std::max(1, kStreamCtas / stream_head_ctas);   // rows
+    if (g.M / at_once >= kStreamRows) {
         cfg.blockDim = dim3(kStreamThreads);
-        cfg.gridDim = dim3(static_cast<unsigned>(std::min(g.M, std::max(1, kStreamCtas / head_ctas))), static_cast<unsigned>(head_ctas));
+        cfg.gridDim = dim3(static_cast<unsigned>(at_once), static_cast<unsigned>(stream_head_ctas));
         return cudaLaunchKernelEx(&cfg, norm_rope_stream_kernel<T, kInterleaved, L>, g);
     }
-    cfg.gridDim = dim3(static_cast<unsigned>(g.M), static_cast<unsigned>((heads + kHeads - 1) / kHeads));
-    return cudaLaunchKernelEx(&cfg, norm_rope_kernel<T, kInterleaved, L>, g);
+    cfg.gridDim = dim3(static_cast<unsigned>(row_ctas), static_cast<unsigned>((heads + kHeads - 1) / kHeads));
+    return rows == 2 ? cudaLaunchKernelEx(&cfg, norm_rope_kernel<T, kInterleaved, L, 2>, g)
+                     : cudaLaunchKernelEx(&cfg, norm_rope_kernel<T, kInterleaved, L, 1>, g);
 }
 
 template <typename T, bool kInterleaved>
