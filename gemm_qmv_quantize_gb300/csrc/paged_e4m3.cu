@@ -14,11 +14,12 @@
 // Numerics: q is held in binary16 (bfloat16 rows are scaled by a power of two that brings
 // their largest element to 2^14 or more: elements 2^-28 of it and less lose bits); S, the
 // softmax's statistics and O are fp32. The running maximum of a column is that of z + log2 sv, z = c sk S:
-// the terms 2^(z + log2 sv - m) of the numerator, which are rounded to binary16, the
-// product's operand, are then near 1 where they are largest, whatever the scales of the blocks.
+// the terms 2^(z + log2 sv - m) of the numerator are then near 1 where they are largest, whatever the
+// scales of the blocks. Each goes into the products as two binary16, itself rounded and what that left: 2^-22 of
+// it, or 2^-25 of the row's largest, is lost. (Rounded once, outputs differed from a plain form's in fp32 by 2.5e-4 for 6e-6 now, and
+// were 2.6e-4 off for 2.1e-4, binary16's own rounding. It costs nothing that shows with 8 rows a key head, 30 us for 29 with 40.)
 // The denominator's are 2^(z - m), in fp32, whose range holds them. m follows the true maximum
-// with a slack of 2^8, so that O is rescaled rarely. P's rounding adds a quarter to the error of a plain
-// form in fp32 (2.6e-4 of the outputs for 2.1e-4 in binary16; none that shows in bfloat16).
+// with a slack of 2^8, so that O is rescaled rarely.
 //
 // Bound by the cache's bytes: 64 requests of up to 16384 tokens, 40 query heads over 8 key heads of
 // 128, take 165 us, 6.6 TB/s. What it took to get there, us: a CTA an item 482; equal runs of blocks over
@@ -305,13 +306,18 @@ __device__ __forceinline__ void add_block(Part<D, NT> &r, float (&s)[NT][4], con
             }
         }
     }
-    uint32_t p[NT][2];
+    uint32_t p[NT][2], rest[NT][2];   // the terms, and what their rounding left
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) r.l[n][e & 1] += exp2_fast(u[n][e] - lv);
-        p[n][0] = transpose8x8(half2_bits(exp2_fast(u[n][0]), exp2_fast(u[n][1])));
-        p[n][1] = transpose8x8(half2_bits(exp2_fast(u[n][2]), exp2_fast(u[n][3])));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float a = exp2_fast(u[n][2 * i]), b = exp2_fast(u[n][2 * i + 1]);
+            const __half2 h = __floats2half2_rn(a, b);
+            p[n][i] = transpose8x8(*reinterpret_cast<const uint32_t *>(&h));
+            rest[n][i] = transpose8x8(half2_bits(a - __low2float(h), b - __high2float(h)));
+        }
     }
 #pragma unroll
     for (int w = 0; w < D / 32; ++w) {
@@ -327,6 +333,8 @@ __device__ __forceinline__ void add_block(Part<D, NT> &r, float (&s)[NT][4], con
         for (int n = 0; n < NT; ++n) {
             mma_16816(r.o[n][2 * w], a0, a1, a2, a3, p[n][0], p[n][1]);
             mma_16816(r.o[n][2 * w + 1], b0, b1, b2, b3, p[n][0], p[n][1]);
+            mma_16816(r.o[n][2 * w], a0, a1, a2, a3, rest[n][0], rest[n][1]);
+            mma_16816(r.o[n][2 * w + 1], b0, b1, b2, b3, rest[n][0], rest[n][1]);
         }
     }
 }
