@@ -353,13 +353,14 @@ __device__ __forceinline__ void window_head(const NormRopeArgs &g, int window, i
     for (int k = 0; k < kEach; ++k) {
         const int j = group + k * kGroups;
         if (my_run[k] < 0) continue;
+        if (!(had[k] >= 0.0f && had[k] < INFINITY)) had[k] = NAN;   // no scale: what it is of becomes NaN
         const float scale = fmaxf(scale_for(run_largest[my_run[k]]), had[k]), inv = 1.0f / scale;
         uint8_t *codes = static_cast<uint8_t *>(is_v ? g.v_cache : g.k_cache);
         const int64_t token = static_cast<int64_t>(g.Hkv) * D;   // bytes from a token to the next
         if (j == my_run[k]) {   // the run's first row: its group sees to the scale and the earlier tokens
             const int64_t block = my_slot[k] / kScaleTokens;
-            if (had[k] > 0.0f && scale > had[k]) {   // 16 codes a lane
-                const int offset = static_cast<int>(my_slot[k] % kScaleTokens), pieces = D / 16;
+            const int offset = static_cast<int>(my_slot[k] % kScaleTokens), pieces = D / 16;
+            if (offset > 0 && scale != had[k]) {   // 16 codes a lane
                 const float by = had[k] * inv;
                 for (int c = i; c < offset * pieces; c += L) {
                     uint4 *at = reinterpret_cast<uint4 *>(codes + (block * kScaleTokens + c / pieces) * token + h * D + c % pieces * 16);

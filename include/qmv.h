@@ -404,7 +404,8 @@ QMV_API qmv_status qmv_norm_rope_append(const float *qkv, const int32_t *positio
  *            call's new tokens in the block is above 448 times, nor less than the scale
  *            that kept tokens have. Where it grows, their codes are multiplied by the old
  *            scale over the new one and rounded again: exact for codes that stay at 2^-6
- *            or above, within 2^-10 new scales for the others.
+ *            or above, within 2^-10 new scales for the others. So the codes of a scale of 0 become 0,
+ *            and those of one that is negative, infinite or NaN become NaN.
  *   code     value / scale rounded to the nearest, ties to even. There are no infinities:
  *            they become NaN, as NaN does.
  *   Rows of a call with slots of one block follow one another, in the slots' order and
