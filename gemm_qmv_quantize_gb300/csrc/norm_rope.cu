@@ -21,6 +21,7 @@
 #include "decode_ops.h"
 #include "qmv.h"
 #include "qmv_device.cuh"
+#include "rows.h"
 
 namespace qmv {
 namespace {
@@ -193,10 +194,10 @@ __device__ __forceinline__ void row_heads(const NormRopeArgs &g, int m, int firs
     }
 }
 
-// The same of rows m, m + step, .., kStreamThreads / L heads: each lane copies its own pieces of the next rows to shared memory, and
+// The same of a CTA's rows in turn, kStreamThreads / L heads: each lane copies its own pieces of the next rows to shared memory, and
 // has the row's angles on their way, while it works on a row.
 template <typename T, bool kInterleaved, int L>
-__device__ __forceinline__ void stream_heads(const NormRopeArgs &g, int m, int step, int first, Ring &ring)
+__device__ __forceinline__ void stream_heads(const NormRopeArgs &g, RowsInTurn at, int first, Ring &ring)
 {
     const int tid = threadIdx.x, pairs = g.rot / 2, i = tid % L, head = first + tid / L;
     const bool is_v = head >= g.Hq + g.Hkv;
@@ -207,34 +208,34 @@ __device__ __forceinline__ void stream_heads(const NormRopeArgs &g, int m, int s
     if (live && weight) load_weight(w, weight, u);
     const int64_t row = static_cast<int64_t>(g.Hq + 2 * g.Hkv) * g.D;
     const float *in = g.qkv + static_cast<int64_t>(head) * g.D;
-    auto copy = [&](int at, int stage) {
-        if (live && at < g.M) {
-            cp_async_16(&ring[stage][0][tid], in + at * row + u.e0);
-            cp_async_16(&ring[stage][1][tid], in + at * row + u.e1);
+    auto copy = [&](int n, int stage) {
+        if (live && at.ahead(n)) {
+            cp_async_16(&ring[stage][0][tid], in + at.row(n) * row + u.e0);
+            cp_async_16(&ring[stage][1][tid], in + at.row(n) * row + u.e1);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 #pragma unroll
-    for (int j = 0; j < kStages - 1; ++j) copy(m + j * step, j);
+    for (int j = 0; j < kStages - 1; ++j) copy(j, j);
     // of the four pairs; where they are of one axis, the position is there a row before the angles are asked for
     const uint32_t axes = turn ? reinterpret_cast<const uint32_t *>(g.axis_of_pair)[i] : 0, axis = axes & 0xffu;
     const bool one_axis = axes == axis * 0x01010101u, cached = live && head >= g.Hq;
     const int *positions = g.positions + static_cast<int64_t>(axis) * g.M;
     Angles next;
-    if (turn) next = angles_of(g, m, i);
-    int next_position = turn && m + step < g.M ? positions[m + step] : 0;
-    int64_t next_slot = cached ? g.slots[m] : 0;
+    if (turn) next = angles_of(g, at.row(0), i);
+    int next_position = turn && at.ahead(1) ? positions[at.row(1)] : 0;
+    int64_t next_slot = cached ? g.slots[at.row(0)] : 0;
     int stage = 0;
 #pragma unroll 1
-    for (; m < g.M; m += step) {
-        copy(m + (kStages - 1) * step, (stage + kStages - 1) % kStages);
+    for (; at.ahead(0); at.next()) {
+        copy(kStages - 1, (stage + kStages - 1) % kStages);
         const Angles t = next;
         const int64_t slot = next_slot;
         const int position = next_position;
-        if (m + step < g.M) {
-            if (turn) next = one_axis ? angles_at(g, position_inside(g, position), i) : angles_of(g, m + step, i);
-            if (cached) next_slot = g.slots[m + step];
-            if (turn && m + 2 * step < g.M) next_position = positions[m + 2 * step];
+        if (at.ahead(1)) {
+            if (turn) next = one_axis ? angles_at(g, position_inside(g, position), i) : angles_of(g, at.row(1), i);
+            if (cached) next_slot = g.slots[at.row(1)];
+            if (turn && at.ahead(2)) next_position = positions[at.row(2)];
         }
         asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
         float x[8] = {};
@@ -245,7 +246,7 @@ __device__ __forceinline__ void stream_heads(const NormRopeArgs &g, int m, int s
         stage = (stage + 1) % kStages;
         if (normed) norm8<L>(x, w, weight != nullptr, g);
         if (turn) turn8<kInterleaved>(x, t);
-        if (live) put_head<T>(g, m, head, is_v, cached ? slot_inside(g, slot) : 0, u, x);
+        if (live) put_head<T>(g, at.row(0), head, is_v, cached ? slot_inside(g, slot) : 0, u, x);
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
@@ -266,7 +267,7 @@ __global__ void __launch_bounds__(kStreamThreads, kStreamCtas / 152) norm_rope_s
     __shared__ Ring ring;
     grid_launch_dependents();
     grid_dependency_wait();
-    stream_heads<T, kInterleaved, L>(g, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), static_cast<int>(blockIdx.y) * (kStreamThreads / L), ring);
+    stream_heads<T, kInterleaved, L>(g, RowsInTurn{blockIdx.x, static_cast<int>(gridDim.x), g.M - static_cast<int>(blockIdx.x)}, static_cast<int>(blockIdx.y) * (kStreamThreads / L), ring);
 }
 
 // The least e >= -64 with largest <= 448 * 2^e, as the scale 2^e; `largest` the bits of a
@@ -292,8 +293,9 @@ __device__ __forceinline__ void window_head(const NormRopeArgs &g, int window, i
     const int64_t row = static_cast<int64_t>(g.Hq + 2 * g.Hkv) * D;
     const float *in = g.qkv + static_cast<int64_t>(m0) * row + static_cast<int64_t>(g.Hq + task) * D;
     // which rows, in every warp: lane j looks at row m0 + j
-    const int64_t slot = m0 + lane < g.M && lane < 2 * kScaleTokens - 1 ? g.slots[m0 + lane] : -1;
-    const int64_t before = m0 + lane > 0 && m0 + lane < g.M ? g.slots[m0 + lane - 1] : -1;
+    const bool there = row_ahead(m0, lane, g.M);
+    const int64_t slot = there && lane < 2 * kScaleTokens - 1 ? g.slots[m0 + lane] : -1;
+    const int64_t before = there && m0 + lane > 0 ? g.slots[m0 + lane - 1] : -1;
     const bool valid = slot >= 0 && slot < g.n_slots;
     if (slot >= g.n_slots && lane < kScaleTokens && tid < 32 && task == 0) atomicOr(&g_norm_rope_error, kErrIndex);
     const uint32_t starts = __ballot_sync(0xffffffffu, valid && (before != slot - 1 || slot % kScaleTokens == 0));
@@ -403,7 +405,7 @@ template <typename T, bool kInterleaved, int L>
 cudaError_t launch_typed(const NormRopeArgs &g, cudaStream_t s)
 {
     constexpr int kHeads = kThreads / L, kStreamHeads = kStreamThreads / L;
-    const int rows = g.M >= kTwoRows ? 2 : 1, row_ctas = (g.M - 1) / rows + 1;
+    const int rows = g.M >= kTwoRows ? 2 : 1, row_ctas = groups_of(g.M, rows);
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kThreads);
@@ -412,7 +414,7 @@ cudaError_t launch_typed(const NormRopeArgs &g, cudaStream_t s)
     cfg.numAttrs = set_launch_overlap_attr(attr);
     if constexpr (L <= 16) {   // codes: heads of 128 at most
         if (g.k_scale) {
-            const int windows = (g.M + kScaleTokens - 1) / kScaleTokens, q_ctas = (g.Hq + kHeads - 1) / kHeads;
+            const int windows = groups_of(g.M, kScaleTokens), q_ctas = (g.Hq + kHeads - 1) / kHeads;
             const int64_t grid = static_cast<int64_t>(windows) * 2 * g.Hkv + static_cast<int64_t>(row_ctas) * q_ctas;
             if (grid > 0x7fffffff) return cudaErrorInvalidValue;
             cfg.gridDim = dim3(static_cast<unsigned>(grid));
