@@ -59,7 +59,9 @@ constexpr int kClusterBlocks = 8;
 constexpr int kBatch = 32;              // blocks whose page and scales a warp looks up at a time, a lane a block
 constexpr float kSlack = 8.0f;
 constexpr float kLowest = -3.402823466e38f;   // a maximum of no scores: the difference to it is never NaN
-constexpr float kLeastLog = -100.0f;          // log2 of the least scale, and of 0
+// log2 of a scale of 0; smaller ones are taken for 0. A row's denominator is up to 2^(8 + 81) for each of 2^30 keys, where all scales are as
+// small: that fits fp32.
+constexpr float kLeastLog = -81.0f;
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D>

@@ -428,7 +428,8 @@ QMV_API qmv_status qmv_rope_append_e4m3(const float *qkv, const int32_t *positio
  *            B T Hq up to 2^31 - 1, D = 64 or 128, Hkv dividing Hq.
  *   k_cache, v_cache uint8 [n_pages][page][Hkv][D], page a power of two, 16..256, 16-byte
  *            aligned; k_scale, v_scale fp32 [n_pages][page / 16][Hkv]: 0 or, for values to
- *            count in full, 2^-100 .. 2^90.
+ *            count in full, 2^-80 .. 2^90. A v_scale of 2^-81 or less counts as 0, as one that is
+ *            negative or NaN does, of either.
  *   table    int32 [B][table_pages]; lens int32 [B] (at most max_len, a bound the caller
  *            knows, itself at most table_pages * page and 2^30; a longer one is cut to
  *            max_len and sets bit 2). A page outside the cache reads as zeros (bit 2).

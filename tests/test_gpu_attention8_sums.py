@@ -39,3 +39,36 @@ def test_terms_are_held_closer_than_binary16(D, T, G, long_bound):
     k = cache8_ref.values(args["k_cache"], args["k_scale"]).abs().amax(dim=(0, 1, 2))   # [D]
     most = float((args["q"].double().abs() @ k).max()) * D ** -0.5
     check(args, "f16", D ** -0.5, most)
+
+
+def close(got, args, scale):
+    """bfloat16 outputs of any size: half a step, and the terms' errors as above with scores of magnitude 2^5 at most."""
+    o, bound, _ = cache8_ref.attention(*(args[n] for n in ("q", "k_cache", "v_cache", "k_scale", "v_scale", "table", "lens")), scale)
+    assert bool((o != 0).any()) and bool(((got.double() - o).abs() <= 2.0 ** -8 * o.abs() + (2.0 ** -12 + 2.0 ** -15) * bound).all())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("exponent", [-80, -64, 90])
+def test_ends_of_the_scales_range(exponent, D):
+    for lens in ([600, 17], [600, 4000]):        # by clusters, and in runs
+        args = inputs(2, 1, 8, 2, D, lens, 16, "bf16", seed=31)
+        args["k_scale"].fill_(2.0 ** -9)
+        args["v_scale"].fill_(2.0 ** exponent)
+        close(run(args), args, D ** -0.5)
+
+
+@pytest.mark.parametrize("small", [2.0 ** -81, 2.0 ** -90, 2.0 ** -100, 1e-45, -1.0, float("-inf"), float("nan")])
+def test_scales_that_count_as_0(small):
+    """Of values, those below the range and no scales at all; of keys, the latter."""
+    for lens in ([600, 17], [600, 4000]):
+        args = inputs(2, 2, 8, 2, 128, lens, 16, "bf16", seed=32)
+        args["v_scale"][::3] = 0
+        if not small > 0:
+            args["k_scale"][::2] = 0
+        expected = run(args)
+        args["v_scale"][::3] = small
+        if not small > 0:
+            args["k_scale"][::2] = small
+        assert torch.equal(run(args), expected)
+        args["v_scale"].fill_(small)
+        assert bool((run(args) == 0).all())
