@@ -14,12 +14,12 @@
 // Numerics: q is held in binary16 (bfloat16 rows are scaled by a power of two that brings
 // their largest element to 2^14 or more: elements 2^-28 of it and less lose bits); S, the
 // softmax's statistics and O are fp32. The running maximum of a column is that of z + log2 sv, z = c sk S:
-// the terms 2^(z + log2 sv - m) of the numerator are then near 1 where they are largest, whatever the
+// the terms 2^(z + log2 sv - m) of the numerator are then of one size where they are largest, whatever the
 // scales of the blocks. Each goes into the products as two binary16, itself rounded and what that left: 2^-22 of
-// it, or 2^-25 of the row's largest, is lost. (Rounded once, outputs differed from a plain form's in fp32 by 2.5e-4 for 6e-6 now, and
+// it, or 2^-32 of the row's largest, is lost. (Rounded once, outputs differed from a plain form's in fp32 by 2.5e-4 for 6e-6 now, and
 // were 2.6e-4 off for 2.1e-4, binary16's own rounding. It costs nothing that shows with 8 rows a key head, 30 us for 29 with 40.)
-// The denominator's are 2^(z - m), in fp32, whose range holds them. m follows the true maximum
-// with a slack of 2^8, so that O is rescaled rarely.
+// The denominator's are 2^(z - m), in fp32, whose range holds them. m is the true maximum less 7, and follows it
+// with a slack of 2^8, so that O is rescaled rarely: the largest terms are 2^7 .. 2^15, binary16's range ends at 2^16.
 //
 // Bound by the cache's bytes: 64 requests of up to 16384 tokens, 40 query heads over 8 key heads of
 // 128, take 165 us, 6.6 TB/s. What it took to get there, us: a CTA an item 482; equal runs of blocks over
@@ -57,9 +57,9 @@ constexpr int kLeastBlocks = 2;         // of a run, where there are few
 // 11.1, 12 requests of 1000 keys 12.4 for 16.8; one of 2000 keys, the most there is for one, 12.6 for 12.3.
 constexpr int kClusterBlocks = 8;
 constexpr int kBatch = 32;              // blocks whose page and scales a warp looks up at a time, a lane a block
-constexpr float kSlack = 8.0f;
+constexpr float kLift = 7.0f, kSlack = 15.0f;   // log2 of the largest term when m is set, and at most
 constexpr float kLowest = -3.402823466e38f;   // a maximum of no scores: the difference to it is never NaN
-// log2 of a scale of 0; smaller ones are taken for 0. A row's denominator is up to 2^(8 + 81) for each of 2^30 keys, where all scales are as
+// log2 of a scale of 0; smaller ones are taken for 0. A row's denominator is up to 2^(15 + 81) for each of 2^30 keys, where all scales are as
 // small: that fits fp32.
 constexpr float kLeastLog = -81.0f;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -295,7 +295,7 @@ __device__ __forceinline__ void add_block(Part<D, NT> &r, float (&s)[NT][4], con
                 float top = fmaxf(s[n][e], s[n][e + 2]);
 #pragma unroll
                 for (int o = 4; o < 32; o *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                const float m = fmaxf(r.m[n][e], fmaf(top, ck, lv)), by = exp2_fast(r.m[n][e] - m);
+                const float m = fmaxf(r.m[n][e], fmaf(top, ck, lv) - kLift), by = exp2_fast(r.m[n][e] - m);
                 r.m[n][e] = m;
                 r.l[n][e] *= by;
                 u[n][e] = fmaf(s[n][e], ck, lv - m);

@@ -438,7 +438,7 @@ QMV_API qmv_status qmv_rope_append_e4m3(const float *qkv, const int32_t *positio
  *   scale    finite and positive.
  *   q is held in binary16: of a bfloat16 row, scaled by a power of two, elements smaller
  *   than 2^-28 of the row's largest lose bits. The terms of the sum over V are held to 2^-22 of themselves, or to
- *   2^-25 of the row's largest.
+ *   2^-32 of the row's largest.
  *   Workspace: qmv_paged_attention_e4m3_workspace(...) bytes (negative: QMV_ERR_SHAPE).
  */
 QMV_API int64_t qmv_paged_attention_e4m3_workspace(int B, int T, int Hq, int Hkv, int D, int64_t max_len);

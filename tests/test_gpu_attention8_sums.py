@@ -7,6 +7,8 @@ most D / 16 + 2 = 10 additions to a sum, each within 2^-22 of the magnitudes' su
 a term and, at most as much, in the denominator; exponentials and the terms' two parts, 2^-20 together; a
 warp's additions of blocks, at most 40 here, 2^-22 each in either sum, 2^-15.7 together.
 """
+import math
+
 import pytest
 import torch
 
@@ -72,3 +74,26 @@ def test_scales_that_count_as_0(small):
         assert torch.equal(run(args), expected)
         args["v_scale"].fill_(small)
         assert bool((run(args) == 0).all())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("weight,code,n", [(18.0, 448.0, 4001), (18.0, 448.0, 200), (20.0, 448.0, 9000)])
+def test_many_light_terms_beside_a_heavy_one(weight, code, n, D):
+    """The first key weighs e^18 or e^20 (2^26, 2^29) times what each other one does and has values of 0: the outputs
+    are the others', none of which is dropped for being light: a term is within 2^-32 of the largest, half of binary16's least
+    step for the 2^7 that the largest is at least."""
+    args = inputs(1, 1, 2, 1, D, [n], 16, seed=33)
+    for name in ("k_cache", "v_cache"):
+        args[name].view(torch.uint8).zero_()
+    for name in ("k_scale", "v_scale"):
+        args[name].fill_(1.0)
+    at = int(args["table"][0, 0])
+    args["q"].zero_()
+    args["q"][..., 0] = 1.0
+    args["k_cache"][at, 0, 0, 0] = weight
+    args["v_cache"].copy_(torch.full_like(args["v_cache"].float(), code).to(E4M3))
+    args["v_cache"].view(torch.uint8)[at, 0].zero_()
+    got = run(args, scale=1.0).double()
+    o = cache8_ref.attention(*(args[n_] for n_ in ("q", "k_cache", "v_cache", "k_scale", "v_scale", "table", "lens")), 1.0)[0]
+    step = 2.0 ** -32 * math.exp(weight)     # of a term
+    assert bool(((got - o).abs() <= (2.0 ** -11 + 2.0 ** -15 + step) * o + 2.0 ** -25).all()), (float(got.min()), float(o.min()))
