@@ -258,19 +258,18 @@ __device__ __forceinline__ void add_block(Part<D, NT> &r, float (&s)[NT][4], con
             for (int e = 0; e < 4; ++e)
                 if (key0 + gid + (e >> 1) * 8 >= seen[n][e & 1]) s[n][e] = -INFINITY;   // (c is positive)
         }
-        // Values behind the last token are cleared, whatever lies there. Of keys that not every
-        // row sees, NaN is cleared (0 x NaN is NaN), and the rows that see it get it when they are
-        // written.
+        // Values behind the last token are cleared, whatever lies there; of a scale of 0, all but NaN, which
+        // stays NaN. Of keys that not every row sees, NaN is cleared (0 x NaN is NaN), and the rows that see it
+        // get it when they are written.
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int key = key0 + 2 * t + i % 2 + 8 * (i / 2);
-            const uint32_t keep = key < len && !zero ? ~0u : 0u;
+            const uint32_t there = key < len ? ~0u : 0u, some = key >= first_seen ? ~0u : 0u;
 #pragma unroll
             for (int w = 0; w < D / 32; ++w) {
-                v[i][w] &= keep;
-                const uint32_t nan = key >= first_seen ? nan_bytes(v[i][w]) : 0u;
-                v[i][w] &= ~((nan >> 7) * 0xffu);
-                r.nan |= nan;
+                const uint32_t nan = nan_bytes(v[i][w]) & there, bytes = (nan >> 7) * 0xffu;
+                v[i][w] &= (zero ? bytes : there) & ~(bytes & some);
+                r.nan |= nan & some;
             }
         }
     }
