@@ -161,14 +161,14 @@ __device__ __forceinline__ Found find(const Place &p, int block, bool any)
     Found f{-1, 0.0f, 0.0f};
     if (!any) return f;
     const int per_page = p.page_shift - 4;
-    const int page = __ldg(p.table + (block >> per_page));
+    const int page = p.table[block >> per_page];
     if (page < 0 || page >= p.pages) {
         atomicOr(&g_paged_error, kErrIndex);
         return f;
     }
     f.block = (static_cast<int64_t>(page) << per_page) + (block & ((1 << per_page) - 1));
-    f.ks = __ldg(p.ks + f.block * p.Hkv);
-    f.vs = __ldg(p.vs + f.block * p.Hkv);
+    f.ks = p.ks[f.block * p.Hkv];   // (no read-only loads: an append that this launch overlapped with may have written them)
+    f.vs = p.vs[f.block * p.Hkv];
     return f;
 }
 
