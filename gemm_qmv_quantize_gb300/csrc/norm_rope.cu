@@ -30,9 +30,10 @@ __device__ uint32_t g_norm_rope_error;
 
 constexpr int kThreads = 256;
 constexpr int kTwoRows = 256;   // rows from which a CTA takes two: 512 of 56 heads 5.7 us for 6.1
-// Rows a CTA from which CTAs that fill the SMs go through them, in 16 bits. 4001 rows of 56 heads (23 each) 29.8 us for 35.6 by
-// CTAs of two rows, 1000 (6) 10.3 for 10.4; 1000 of 10 heads (2) 4.7 for 3.5, 8000 (13) 17.9 for 17.6. (With codes, q
-// in such a launch of its own 41 us for 40 with 4005 rows.)
+// Rows a CTA, rounded down, from which CTAs that fill the SMs go through them, in 16 bits: with 56 heads from 1038 rows on, with
+// 10 from 3648. 4001 rows of 56 heads (23 each) 29.8 us for 35.6 by CTAs of two rows, 1000 (5, or 6 for most) 10.3 for
+// 10.4; at the border 1037 rows by CTAs of two 10.2 us, 1038 streamed 10.6, 1200 11.6. 1000 of 10 heads (1) 4.7 for 3.5, 8000 (13) 17.9
+// for 17.6; at the border 8.4 and 9.1. (With codes, q in such a launch of its own 41 us for 40 with 4005 rows.)
 constexpr int kStreamRows = 6;
 // CTAs of so many threads, all on the SMs at once; a CTA's rows that are on their way and the one it works on. (4 or 3 for 2
 // stages 31.6 and 29.9 us for 29.7; 256 threads 32.7, 64 30.1.)
