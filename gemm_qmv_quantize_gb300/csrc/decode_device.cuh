@@ -1,5 +1,5 @@
 // decode_device.cuh -- device helpers that the decode step's operators share: rounding to
-// the 16-bit types and to E4M3.
+// the 16-bit types and to E4M3, and sizes that several go by.
 #pragma once
 
 #include <cstdint>
@@ -33,6 +33,7 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d)
     return static_cast<uint32_t>(lo) | static_cast<uint32_t>(hi) << 16;
 }
 
+constexpr int kSms = 152;
 constexpr int kScaleTokens = 16;   // consecutive places of a cache of codes that share a scale, for each head
 
 }  // namespace qmv

@@ -37,7 +37,7 @@ constexpr int kTwoRows = 256;   // rows from which a CTA takes two: 512 of 56 he
 constexpr int kStreamRows = 6;
 // CTAs of so many threads, all on the SMs at once; a CTA's rows that are on their way and the one it works on. (4 or 3 for 2
 // stages 31.6 and 29.9 us for 29.7; 256 threads 32.7, 64 30.1.)
-constexpr int kStreamThreads = 128, kStreamCtas = 152 * 8, kStages = 2;
+constexpr int kStreamThreads = 128, kStreamCtas = kSms * 8, kStages = 2;
 using Ring = float4[kStages][2][kStreamThreads];
 
 // The 8 elements e0 .. e0 + 3 and e1 .. e1 + 3 of a head that a lane has.
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
 
 // Grid (CTAs that the rows go to in turn, CTAs of kStreamThreads / L heads).
 template <typename T, bool kInterleaved, int L>
-__global__ void __launch_bounds__(kStreamThreads, kStreamCtas / 152) norm_rope_stream_kernel(const __grid_constant__ NormRopeArgs g)
+__global__ void __launch_bounds__(kStreamThreads, kStreamCtas / kSms) norm_rope_stream_kernel(const __grid_constant__ NormRopeArgs g)
 {
     __shared__ Ring ring;
     grid_launch_dependents();

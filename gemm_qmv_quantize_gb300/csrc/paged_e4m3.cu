@@ -50,7 +50,6 @@ __device__ uint32_t g_paged_error;
 constexpr int kBlock = kScaleTokens;    // keys a step of a warp
 constexpr int kMostWarps = 8;           // of a CTA, a key head each
 constexpr int64_t kFewBytes = 11ll << 20, kMostBytes = 22ll << 20;   // of the workspace's slots, with 8 rows and 16
-constexpr int kSms = 152;
 constexpr int kStartUnits = 8;          // what starting on an item costs, in blocks of a warp's
 constexpr int kLeastBlocks = 2;         // of a run, where there are few
 // Blocks a CTA up to which a cluster has an item: one launch for two. 560 keys of one request 8.5 us for
@@ -78,7 +77,7 @@ struct Shape {
     static constexpr int kQueries = NT == 1 ? 0 : NT * D * 16;   // bytes a warp
     static constexpr int kFit = (216 * 1024 / kWarpsSm - kQueries) / (32 * D), kStages = kFit < 3 ? 3 : kFit > 6 ? 6 : kFit;
     static constexpr int kOwn = kStages * 32 * D + kQueries;     // a warp's shared memory
-    static constexpr int kMostWarpsOfRuns = 152 * kWarpsSm;
+    static constexpr int kMostWarpsOfRuns = kSms * kWarpsSm;
 };
 
 __device__ __forceinline__ void cp_async_16_zfill(uint32_t dst, const void *src, bool there)
@@ -493,8 +492,7 @@ __device__ __forceinline__ Cut cut_of(const PagedArgs &g, int c, int ctas, int i
             total += all;
         }
         const int64_t start = (base + before) * items;
-        if (start <= from && from < start + mine * items && from < to)
-{
+        if (start <= from && from < start + mine * items && from < to) {
             const int64_t item = quotient(from - start, mine);
             *shared = Cut{b0 + tid, static_cast<int>(item), from - start - item * mine, to - from, from, units};
         }
