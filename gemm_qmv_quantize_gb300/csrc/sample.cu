@@ -30,6 +30,7 @@
 // and 98 us for what then took 70; 16 for up to four rows 5 % faster, for eight 6 % slower; sums by
 // 64-bit atomics of shared memory 72 for 57.)
 #include <algorithm>
+#include <cfloat>
 
 #include <cooperative_groups.h>
 
@@ -322,7 +323,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     const float top_p = g.top_p ? g.top_p[m] : 1.0f, min_p = g.min_p ? g.min_p[m] : 0.0f;
     int k = g.top_k ? g.top_k[m] : 0;
     if (k <= 0 || k > g.V) k = g.V;
-    if (!(T > 0.0f) || top_p <= 0.0f || min_p > 1.0f) k = 1;
+    if (!(T >= FLT_MIN) || top_p <= 0.0f || min_p > 1.0f) k = 1;   // (log2(e) / T is finite)
     cp_async_wait_all();
     __syncthreads();
     float most = -INFINITY, lowest = INFINITY;   // lowest: above -inf

@@ -461,9 +461,10 @@ QMV_API qmv_status qmv_paged_attention_e4m3(const void *q, const void *k_cache, 
  * Sums are whole numbers of 2^-44 of the largest weight, each weight within 2^-32 of its
  * value and those below 2^-44 zero.
  *   logits   fp32 [M][V], M = 0..65535, V = 1..524288. NaN counts as -inf; a row without
- *            a logit above -inf gives token -1 and prob 0; +inf weighs 1, all else beside it 0.
+ *            a logit above -inf gives token -1 and prob 0; +inf weighs 1, all else beside it 0. A
+ *            logit further below the largest than fp32 reaches (2^128) weighs 0.
  *   u        fp32 [M]; below 0 or NaN counts as 0, 1 or more as just below 1.
- *   temperature fp32 [M], NULL for 1; one that is not above 0 takes the first token.
+ *   temperature fp32 [M], NULL for 1; one below 2^-126 (0, negative, subnormal) or NaN takes the first token.
  *   top_k int32 [M], top_p, min_p fp32 [M], each NULL for none; top_k of 0 or less or above
  *            V, top_p of 1 or more, min_p of 0 or less, and NaN are none; top_p of 0 or
  *            less and min_p above 1 keep the first token alone.
