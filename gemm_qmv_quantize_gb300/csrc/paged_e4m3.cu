@@ -55,6 +55,10 @@ constexpr int kLeastBlocks = 2;         // of a run, where there are few
 // Blocks a CTA up to which a cluster has an item: one launch for two. 560 keys of one request 8.5 us for
 // 11.1, 12 requests of 1000 keys 12.4 for 16.8; one of 2000 keys, the most there is for one, 12.6 for 12.3.
 constexpr int kClusterBlocks = 8;
+// Blocks after which a warp leaves its part in the workspace and begins a new one, which the first is added to in fp32: the products truncate their
+// sums to fp32, and with values of one sign a sum over n blocks is 5e-8 n too small (152 requests of 65536 keys 4e-4, of 1048576 6.7e-3;
+// now 3e-5). A launch whose runs may have so many of one item has the code for it: 24 requests of up to 131072 keys take 514 us for 513.
+constexpr int kFold = 512;
 constexpr int kBatch = 32;              // blocks whose page and scales a warp looks up at a time, a lane a block
 constexpr float kLift = 7.0f, kSlack = 15.0f;   // log2 of the largest term when m is set, and at most
 constexpr float kLowest = -3.402823466e38f;   // a maximum of no scores: the difference to it is never NaN
@@ -594,6 +598,33 @@ __device__ __forceinline__ void put(const Part<D, NT> &r, float *slot, int lane)
     }
 }
 
+// Adds a part that `put` has left in a slot, by the same warp.
+template <int D, int NT>
+__device__ __forceinline__ void add_put(Part<D, NT> &r, const float *slot, int lane)
+{
+    const int gid = lane / 4, t = lane % 4;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float *row = slot + (8 * n + 2 * t + e) * (D + 4);
+            const float4 st = *reinterpret_cast<const float4 *>(row + D);
+            const float m = fmaxf(r.m[n][e], st.y), by = exp2_fast(r.m[n][e] - m), weight = exp2_fast(st.y - m);
+            r.m[n][e] = m;
+            r.l[n][e] = r.l[n][e] * by + (gid == 0 ? st.x * weight : 0.0f);
+            if (st.z != 0.0f) r.nan = 1;
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j) {
+                const float4 x = reinterpret_cast<const float4 *>(row + gid * (D / 8))[j];
+                r.o[n][2 * j][e] = r.o[n][2 * j][e] * by + x.x * weight;
+                r.o[n][2 * j][e + 2] = r.o[n][2 * j][e + 2] * by + x.y * weight;
+                r.o[n][2 * j + 1][e] = r.o[n][2 * j + 1][e] * by + x.z * weight;
+                r.o[n][2 * j + 1][e + 2] = r.o[n][2 * j + 1][e + 2] * by + x.w * weight;
+            }
+        }
+    }
+}
+
 // Four outputs of row `row` of a key head, from their sums over V and the denominator l.
 __device__ __forceinline__ void write_row(const PagedArgs &g, int b, int h, int len, int row, int G, int d, int D, float l, bool nan, float4 o)
 {
@@ -664,8 +695,8 @@ __device__ __forceinline__ void add_item(Part<D, NT> &part, const PagedArgs &g, 
     walk.add(part, q, c, seen);
 }
 
-// A run a CTA. row_groups: groups of 8 NT query rows.
-template <int D, int NT>
+// A run a CTA. row_groups: groups of 8 NT query rows. kLong: of an item, a run can have more than kFold blocks.
+template <int D, int NT, bool kLong>
 __global__ void __launch_bounds__(32 * kMostWarps, Shape<D, NT>::kWarpsSm / kMostWarps) paged_kernel(const __grid_constant__ PagedArgs g, int row_groups)
 {
     extern __shared__ __align__(128) uint8_t smem[];
@@ -693,10 +724,23 @@ __global__ void __launch_bounds__(32 * kMostWarps, Shape<D, NT>::kWarpsSm / kMos
         const int len = len_of(g, b), units = units_of(g, b), taken = static_cast<int>(min(units - cut.at, cut.left));
         const int at = max(static_cast<int>(cut.at) - kStartUnits, 0), count = max(static_cast<int>(cut.at) + taken - kStartUnits, 0) - at;
         if (pair < pairs) {
-            add_item<D, NT>(part, g, q, my_ring, b, h, row0, len, at, count, lane);
+            float *slot = slot_of<D, NT>(g, static_cast<int>(blockIdx.x), first, warps, warp);
+            if constexpr (kLong) {
+#pragma unroll 1
+                for (int done = 0;;) {
+                    const int n = min(count - done, kFold);
+                    add_item<D, NT>(part, g, q, my_ring, b, h, row0, len, at + done, n, lane);
+                    if (done > 0) add_put<D, NT>(part, slot, lane);
+                    __syncwarp();   // all have read the slot
+                    if ((done += n) == count) break;
+                    put<D, NT>(part, slot, lane);
+                    __syncwarp();
+                }
+            } else {
+                add_item<D, NT>(part, g, q, my_ring, b, h, row0, len, at, count, lane);
+            }
             // the output, or a part
             const bool whole = taken == units, nan = __any_sync(0xffffffffu, part.nan != 0);
-            float *slot = slot_of<D, NT>(g, static_cast<int>(blockIdx.x), first, warps, warp);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -916,11 +960,12 @@ cudaError_t launch_typed(const PagedArgs &g, int row_groups, cudaStream_t s)
         cfg.numAttrs = 1 + set_launch_overlap_attr(attr + 1);
         return cudaLaunchKernelEx(&cfg, paged_cluster_kernel<D, NT>, g, row_groups);
     }
-    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(paged_kernel<D, NT>), smem);
+    const auto kernel = std::min<int64_t>(blocks, items * g.B * (blocks + kStartUnits) / ctas + 1) > kFold ? paged_kernel<D, NT, true> : paged_kernel<D, NT, false>;
+    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(kernel), smem);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(static_cast<unsigned>(ctas));
     cfg.numAttrs = set_launch_overlap_attr(attr);
-    e = cudaLaunchKernelEx(&cfg, paged_kernel<D, NT>, g, row_groups);
+    e = cudaLaunchKernelEx(&cfg, kernel, g, row_groups);
     if (e != cudaSuccess || ctas == 1) return e;
     // the join starts while the runs still go on, and waits for their end on the device
     const int rows = std::min(8 * NT, g.T * (g.Hq / g.Hkv));

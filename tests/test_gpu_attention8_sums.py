@@ -14,7 +14,7 @@ import torch
 
 import cache8_ref
 from cache8_ref import E4M3
-from test_gpu_paged_attention_e4m3 import TYPES, inputs, run, widened
+from test_gpu_paged_attention_e4m3 import TYPES, inputs, near, run, widened
 
 pytestmark = pytest.mark.gpu
 
@@ -97,3 +97,56 @@ def test_many_light_terms_beside_a_heavy_one(weight, code, n, D):
     o = cache8_ref.attention(*(args[n_] for n_ in ("q", "k_cache", "v_cache", "k_scale", "v_scale", "table", "lens")), 1.0)[0]
     step = 2.0 ** -32 * math.exp(weight)     # of a term
     assert bool(((got - o).abs() <= (2.0 ** -11 + 2.0 ** -15 + step) * o + 2.0 ** -25).all()), (float(got.min()), float(o.min()))
+
+
+def long_runs(B, Hq, Hkv, D, lens, pages, type_="f16", T=1, seed=61):
+    """Requests over a few pages again and again, so many of them that a run is a request's."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    args = inputs(1, T, Hq, Hkv, D, [256 * pages], 256, type_, seed=seed, spare=0)
+    width = (max(lens) + 255) // 256
+    args["table"] = torch.randint(0, pages, (B, width), generator=g, device="cuda", dtype=torch.int32)
+    args["q"] = torch.randn((B, T, Hq, D), generator=g, device="cuda").to(args["q"].dtype)
+    args["lens"] = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    return args
+
+
+@pytest.mark.parametrize("D,Hq,B", [(128, 8, 152), (128, 128, 152), (64, 8, 304)])
+def test_long_sums_of_one_sign_are_not_cut(D, Hq, B):
+    """4096 blocks a run, values that are all positive: what the products truncate adds up in one direction (4e-4 of the
+    outputs). The mean over 1024 and more outputs of (got - o) / o: each output's rounding is within 2^-11 and of either
+    sign, so the mean's is within 2^-11 / 32 but for 1 in 10^3; a part of 512 blocks is at most 1024 truncations of 2^-24, half
+    of that in the mean, too small: 2^-15; sums in fp32, 2^-17."""
+    args = long_runs(B, Hq, 8, D, [65536] * B, 4)
+    args["table"] = (torch.arange(256, device="cuda", dtype=torch.int32) % 4).expand(B, 256).contiguous()
+    args["q"] = args["q"][:1].expand(B, 1, Hq, D).contiguous()
+    args["k_scale"].fill_(2.0 ** -10)
+    args["v_cache"] = args["v_cache"].float().abs().to(E4M3)
+    o, bound, _ = cache8_ref.attention(args["q"][:1], args["k_cache"], args["v_cache"], args["k_scale"], args["v_scale"], args["table"][:1],
+                                       torch.tensor([1024]), D ** -0.5)
+    off = (run(args).double() - o) / o
+    assert float(off.abs().max()) <= 2.0 ** -11 + 2.0 ** -14 + 2.0 ** -15
+    assert abs(float(off.mean())) <= 2.0 ** -16 + 2.0 ** -15 + 2.0 ** -17, float(off.mean())
+
+
+@pytest.mark.parametrize("T,Hq,type_", [(1, 8, "f16"), (3, 8, "bf16"), (2, 64, "f16")])
+def test_runs_of_several_parts(T, Hq, type_):
+    """Lengths about two parts and more of 512 blocks, scales that differ from page to page, and NaN in a newest token."""
+    B = 160
+    args = long_runs(B, Hq, 8, 128, [17000 - 53 * b for b in range(B)], 96, type_, T, seed=62)
+    g = torch.Generator(device="cuda").manual_seed(63)
+    for n in ("k_scale", "v_scale"):
+        args[n] = torch.exp2(torch.randint(-11, -4, args[n].shape, generator=g, device="cuda").float())
+    n = int(args["lens"][7])
+    own, at = args["table"][7].tolist(), (n - 1) // 256
+    got = run(args)
+    some = [0, 7, 80, B - 1]
+    near(got[some], {k: v[some].contiguous() if k in ("q", "table", "lens") else v for k, v in args.items()}, type_, 128 ** -0.5)
+    if T > 1:                                       # a page of request 7's own, with NaN in its newest token
+        for name in ("k_cache", "v_cache", "k_scale", "v_scale"):
+            args[name] = torch.cat([args[name].view(torch.uint8), args[name].view(torch.uint8)[own[at]:own[at] + 1]]).view(args[name].dtype)
+        args["table"][7, at] = 96
+        args["v_cache"].view(torch.uint8)[96, (n - 1) % 256, 2, 9] = 0x7f
+        bad = run(args)
+        G = Hq // 8
+        assert bool(torch.isnan(bad[7, T - 1, 2 * G:3 * G, 9]).all()) and int(torch.isnan(bad).sum()) == G
+        assert torch.equal(torch.where(torch.isnan(bad), got, bad), got)
