@@ -17,17 +17,19 @@
 // the terms 2^(z + log2 sv - m) of the numerator are then of one size where they are largest, whatever the
 // scales of the blocks. Each goes into the products as two binary16, itself rounded and what that left: 2^-22 of
 // it, or 2^-32 of the row's largest, is lost. (Rounded once, outputs differed from a plain form's in fp32 by 2.5e-4 for 6e-6 now, and
-// were 2.6e-4 off for 2.1e-4, binary16's own rounding. It costs nothing that shows with 8 rows a key head, 30 us for 29 with 40.)
+// were 2.6e-4 off for 2.1e-4, binary16's own rounding. With 5 rows a key head of 128 that costs nothing that shows, where the products' instructions
+// bound a call up to a tenth: 40 rows of heads of 64 30 us for 28.6, 64 requests of 16384 keys and 16 rows of 64 143 for 129.)
 // The denominator's are 2^(z - m), in fp32, whose range holds them. m is the true maximum less 7, and follows it
 // with a slack of 2^8, so that O is rescaled rarely: the largest terms are 2^7 .. 2^15, binary16's range ends at 2^16.
 //
 // Bound by the cache's bytes: 64 requests of up to 16384 tokens, 40 query heads over 8 key heads of
-// 128, take 165 us, 6.6 TB/s. What it took to get there, us: a CTA an item 482; equal runs of blocks over
+// 128, take 164 to 166 us on the boxes seen, 6.6 TB/s. What it took to get there, us: a CTA an item 482; equal runs of blocks over
 // all SMs 223; key heads of the same blocks side by side, and copies of whole rows (half rows
 // were as many requests to L2 again, which bound it), 174; scores of the next block beside this
 // one's softmax, starting on an item counted as blocks 165. The smaller the call, the more of it
-// is starting and joining: 12 us or so (8 where clusters have the items), much of that fetching instructions, which is why what runs
-// once is written short and not unrolled.
+// is starting and joining: 12 us or so (8 where clusters have the items), a chain of lengths, pages, scales, codes and parts that wait for
+// one another. Of the cycles between a warp's instructions in a cluster 27 % are at barriers, 18 fixed latencies, 16 reads of memory and 7 the
+// fetching of instructions; in a join 37 % reads.
 #include <algorithm>
 #include <cmath>
 
@@ -53,11 +55,12 @@ constexpr int64_t kFewBytes = 11ll << 20, kMostBytes = 22ll << 20;   // of the w
 constexpr int kStartUnits = 8;          // what starting on an item costs, in blocks of a warp's
 constexpr int kLeastBlocks = 2;         // of a run, where there are few
 // Blocks a CTA up to which a cluster has an item: one launch for two. 560 keys of one request 8.5 us for
-// 11.1, 12 requests of 1000 keys 12.4 for 16.8; one of 2000 keys, the most there is for one, 12.6 for 12.3.
+// 11.1, 12 requests of 1000 keys 12.3 for 16.8; one of 2000 keys, the most there is for one, 12.6 for 12.3.
 constexpr int kClusterBlocks = 8;
 // Blocks after which a warp leaves its part in the workspace and begins a new one, which the first is added to in fp32: the products truncate their
 // sums to fp32, and with values of one sign a sum over n blocks is 5e-8 n too small (152 requests of 65536 keys 4e-4, of 1048576 6.7e-3;
-// now 3e-5). A launch whose runs may have so many of one item has the code for it: 24 requests of up to 131072 keys take 514 us for 513.
+// now 3e-5). A launch whose runs may have so many of one item has the code for it: 24 requests of up to 131072 keys take 511 us for 506
+// (in all launches 169 us for 165.5 with 64 requests of up to 16384, 33 for 30 with 40 rows of heads of 64).
 constexpr int kFold = 512;
 constexpr int kBatch = 32;              // blocks whose page and scales a warp looks up at a time, a lane a block
 constexpr float kLift = 7.0f, kSlack = 15.0f;   // log2 of the largest term when m is set, and at most
@@ -378,7 +381,7 @@ struct Walk {
         cp_async_commit();
     }
     // Block j's softmax and values beside block j + 1's scores, whose instructions do not wait for
-    // one another. (One loop, so that its code, which each launch fetches anew, is there once.)
+    // one another. (One loop, so that its code is there once.)
     template <typename Q>
     __device__ __forceinline__ void add(Part<D, NT> &r, const Q &q, const float (&c)[NT][2], const int (&seen)[NT][2])
     {
@@ -775,8 +778,7 @@ __global__ void __launch_bounds__(32 * kMostWarps, Shape<D, NT>::kWarpsSm / kMos
 }
 
 // The rows of which runs have parts. A CTA has blockDim / 32 / share rows of all B * pairs * n of them
-// (n: rows of a group), `share` warps a row, each every share-th part. Short code: what a launch runs
-// once takes as long as fetching its instructions does.
+// (n: rows of a group), `share` warps a row, each every share-th part.
 template <int D, int NT>
 __global__ void __launch_bounds__(1024) paged_join_kernel(const __grid_constant__ PagedArgs g, int row_groups, int warps, int ctas, int share, int n)
 {
@@ -985,8 +987,8 @@ cudaError_t launch_typed(const PagedArgs &g, int row_groups, cudaStream_t s)
 }
 
 // Groups of 8 rows, or of up to 16: where there are more, further warps take them beside each other, and
-// find the keys in L2. (25 rows of 8 requests in one group of 32: 43 us for 26; of 64 requests of up to 8191
-// tokens, bound by the products' instructions, 236 for 225. 40 rows of 64 dimensions in one of 48: 56 for 33.)
+// find the keys in L2. (With terms of one binary16: 25 rows of 8 requests in one group of 32 43 us for 26; of 64 requests of up to 8191
+// tokens, bound by the products' instructions, 236 for 225 (228 now). 40 rows of 64 dimensions in one of 48 56 for 33 (30 now).)
 template <int D>
 cudaError_t launch_rows(const PagedArgs &g, cudaStream_t s)
 {

@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     // 41 without; 2 and 2.5, where lists would not hold them, 77 and 74 for 64 and 62. The range is that of all logits above -inf, so
     // masks of a finite value make any row wide: at 2, with one token masked by -1e9 76 us for 62, with half of them 64 (-inf 61), with
     // 98 of 100 masked by -1e4 31. (A pass that leaves them out of the range: 62 .. 66 in the first two, but 34 in the
-    // last, 37 for 33 at 4, and for rows without masks 26.7 us for 25.9 with eight and 53 for 52 with 96, its instructions being fetched.)
+    // last, 37 for 33 at 4, and for rows without masks 26.7 us for 25.9 with eight and 53 for 52 with 96.)
     const bool listing = cut_p && !cut_k && range > 23.0f - 3.6f * log2f(1.0f - top_p);
     if (listing) {
         uint64_t sum = 0;
