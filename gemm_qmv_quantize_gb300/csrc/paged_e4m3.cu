@@ -23,7 +23,7 @@
 // with a slack of 2^8, so that O is rescaled rarely: the largest terms are 2^7 .. 2^15, binary16's range ends at 2^16.
 //
 // Bound by the cache's bytes: 64 requests of up to 16384 tokens, 40 query heads over 8 key heads of
-// 128, take 164 to 166 us on the boxes seen, 6.6 TB/s. What it took to get there, us: a CTA an item 482; equal runs of blocks over
+// 128, take 164 to 166 us, by the GPU, 6.6 TB/s. What it took to get there, us: a CTA an item 482; equal runs of blocks over
 // all SMs 223; key heads of the same blocks side by side, and copies of whole rows (half rows
 // were as many requests to L2 again, which bound it), 174; scores of the next block beside this
 // one's softmax, starting on an item counted as blocks 165. The smaller the call, the more of it
