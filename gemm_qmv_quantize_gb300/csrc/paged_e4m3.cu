@@ -59,7 +59,8 @@ constexpr int kLeastBlocks = 2;         // of a run, where there are few
 constexpr int kClusterBlocks = 8;
 // Blocks after which a warp leaves its part in the workspace and begins a new one, which the first is added to in fp32: the products truncate their
 // sums to fp32, and with values of one sign a sum over n blocks is 5e-8 n too small (152 requests of 65536 keys 4e-4, of 1048576 6.7e-3;
-// now 3e-5). A launch whose runs may have so many of one item has the code for it: 24 requests of up to 131072 keys take 511 us for 506
+// now 3e-5). A launch whose runs may have so many of one item has the code for it: 24 requests of up to 131072 keys take 511 us for 506,
+// 64 of 2000 with that bound 45 for 44 (16 rows of 64: 48 for 46)
 // (in all launches 169 us for 165.5 with 64 requests of up to 16384, 33 for 30 with 40 rows of heads of 64).
 constexpr int kFold = 512;
 constexpr int kBatch = 32;              // blocks whose page and scales a warp looks up at a time, a lane a block
@@ -628,6 +629,22 @@ __device__ __forceinline__ void add_put(Part<D, NT> &r, const float *slot, int l
     }
 }
 
+// Adds those of an item's parts that are in the slot, and leaves all in it, if more follow.
+template <int D, int NT>
+__device__ __forceinline__ void fold(Part<D, NT> &r, float *slot, int lane, bool before, bool after)
+{
+    if (before) add_put<D, NT>(r, slot, lane);
+    __syncwarp();   // all have read the slot
+    if (after) put<D, NT>(r, slot, lane);
+    __syncwarp();
+}
+template <int D, int NT>
+__device__ __noinline__ Part<D, NT> fold_called(Part<D, NT> r, float *slot, int lane, bool before, bool after)
+{
+    fold<D, NT>(r, slot, lane, before, after);
+    return r;
+}
+
 // Four outputs of row `row` of a key head, from their sums over V and the denominator l.
 __device__ __forceinline__ void write_row(const PagedArgs &g, int b, int h, int len, int row, int G, int d, int D, float l, bool nan, float4 o)
 {
@@ -733,11 +750,14 @@ __global__ void __launch_bounds__(32 * kMostWarps, Shape<D, NT>::kWarpsSm / kMos
                 for (int done = 0;;) {
                     const int n = min(count - done, kFold);
                     add_item<D, NT>(part, g, q, my_ring, b, h, row0, len, at + done, n, lane);
-                    if (done > 0) add_put<D, NT>(part, slot, lane);
-                    __syncwarp();   // all have read the slot
+                    // Heads of 64 have 128 registers a thread, of which the loop is left more where this is called: 64 requests of
+                    // 2000 keys, 16 rows, 48 us for 53. (With 128, and 5 rows, 24 requests of up to 131072 keys 532 called, 517 not.)
+                    if constexpr (D == 64) {
+                        if (count > kFold) part = fold_called<D, NT>(part, slot, lane, done > 0, done + n < count);
+                    } else {
+                        fold<D, NT>(part, slot, lane, done > 0, done + n < count);
+                    }
                     if ((done += n) == count) break;
-                    put<D, NT>(part, slot, lane);
-                    __syncwarp();
                 }
             } else {
                 add_item<D, NT>(part, g, q, my_ring, b, h, row0, len, at, count, lane);
