@@ -60,8 +60,8 @@ constexpr int kClusterBlocks = 8;
 // Blocks after which a warp leaves its part in the workspace and begins a new one, which the first is added to in fp32: the products truncate their
 // sums to fp32, and with values of one sign a sum over n blocks is 5e-8 n too small (152 requests of 65536 keys 4e-4, of 1048576 6.7e-3;
 // now 3e-5). A launch whose runs may have so many of one item has the code for it: 24 requests of up to 131072 keys take 511 us for 506,
-// 64 of 2000 with that bound 45 for 44 (16 rows of 64: 48 for 46)
-// (in all launches 169 us for 165.5 with 64 requests of up to 16384, 33 for 30 with 40 rows of heads of 64).
+// 64 of 2000 with that bound 45 for 44 (16 rows of 64: 48 for 46). In all launches it would be 169 us for 165.5 with 64 requests of up to 16384
+// keys, and 33 for 30 with 40 rows of heads of 64.
 constexpr int kFold = 512;
 constexpr int kBatch = 32;              // blocks whose page and scales a warp looks up at a time, a lane a block
 constexpr float kLift = 7.0f, kSlack = 15.0f;   // log2 of the largest term when m is set, and at most

@@ -128,11 +128,11 @@ def test_long_sums_of_one_sign_are_not_cut(D, Hq, B):
     assert abs(float(off.mean())) <= 2.0 ** -16 + 2.0 ** -15 + 2.0 ** -17, float(off.mean())
 
 
-@pytest.mark.parametrize("T,Hq,type_", [(1, 8, "f16"), (3, 8, "bf16"), (2, 64, "f16")])
-def test_runs_of_several_parts(T, Hq, type_):
+@pytest.mark.parametrize("T,Hq,type_,D", [(1, 8, "f16", 128), (3, 8, "bf16", 128), (2, 64, "f16", 128), (2, 8, "bf16", 64), (3, 64, "f16", 64)])
+def test_runs_of_several_parts(T, Hq, type_, D):
     """Lengths about two parts and more of 512 blocks, scales that differ from page to page, and NaN in a newest token."""
-    B = 160
-    args = long_runs(B, Hq, 8, 128, [17000 - 53 * b for b in range(B)], 96, type_, T, seed=62)
+    B = 160 if D == 128 else 320
+    args = long_runs(B, Hq, 8, D, [17000 - 53 * (b % 160) for b in range(B)], 96, type_, T, seed=62)
     g = torch.Generator(device="cuda").manual_seed(63)
     for n in ("k_scale", "v_scale"):
         args[n] = torch.exp2(torch.randint(-11, -4, args[n].shape, generator=g, device="cuda").float())
@@ -140,7 +140,7 @@ def test_runs_of_several_parts(T, Hq, type_):
     own, at = args["table"][7].tolist(), (n - 1) // 256
     got = run(args)
     some = [0, 7, 80, B - 1]
-    near(got[some], {k: v[some].contiguous() if k in ("q", "table", "lens") else v for k, v in args.items()}, type_, 128 ** -0.5)
+    near(got[some], {k: v[some].contiguous() if k in ("q", "table", "lens") else v for k, v in args.items()}, type_, D ** -0.5)
     if T > 1:                                       # a page of request 7's own, with NaN in its newest token
         for name in ("k_cache", "v_cache", "k_scale", "v_scale"):
             args[name] = torch.cat([args[name].view(torch.uint8), args[name].view(torch.uint8)[own[at]:own[at] + 1]]).view(args[name].dtype)
